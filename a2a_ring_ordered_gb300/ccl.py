@@ -39,6 +39,20 @@ class A2APlan(ctypes.Structure):
                 ("launches", ctypes.c_int), ("tile_bytes", ctypes.c_uint)]
 
 
+class AdamWTensor(ctypes.Structure):
+    """ccl_adamw_tensor_t."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("n", ctypes.c_size_t)]
+
+
+class AdamWHyper(ctypes.Structure):
+    """ccl_adamw_hyper_t."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_uint64),
+                ("grad_scale", ctypes.c_void_p)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -80,6 +94,15 @@ def _load() -> ctypes.CDLL:
         "ccl_moe_dispatch": (st, [pp, pp, vp, pp, i32, sz, i32, i32, sz, i32, pp, ctypes.POINTER(sz),
                                   pp, pp, vp]),
         "ccl_moe_combine": (st, [pp, ctypes.POINTER(sz), pp, pp, vp, pp, i32, sz, i32, i32, sz, pp, vp]),
+        "ccl_moe_sort": (st, [pp, ctypes.POINTER(sz), i32, i32, i32, ctypes.POINTER(ctypes.c_int32), pp, pp, vp]),
+        "ccl_moe_to_experts": (st, [pp, pp, ctypes.POINTER(sz), i32, i32, sz, i32, pp, ctypes.POINTER(sz), vp]),
+        "ccl_moe_from_experts": (st, [pp, ctypes.POINTER(sz), pp, pp, ctypes.POINTER(sz), i32, i32, sz, i32, pp, vp]),
+        "ccl_moe_from_experts_grad": (st, [pp, pp, ctypes.POINTER(sz), pp, pp, ctypes.POINTER(sz), i32, i32, sz, i32,
+                                           pp, pp, vp]),
+        "ccl_moe_product": (st, [pp, pp, pp, ctypes.POINTER(sz), i32, i32, sz, sz, pp, vp]),
+        "ccl_moe_product_grad_input": (st, [pp, pp, pp, ctypes.POINTER(sz), i32, i32, sz, sz, pp, vp]),
+        "ccl_moe_product_grad_weight": (st, [pp, pp, pp, ctypes.POINTER(sz), i32, i32, sz, sz, i32, pp, vp]),
+        "ccl_adamw_step": (st, [ctypes.POINTER(AdamWTensor), sz, i32, i32, i32, ctypes.POINTER(AdamWHyper), vp]),
         "ccl_plan_buckets": (st, [ctypes.POINTER(sz), sz, sz, sz, ctypes.POINTER(ctypes.c_uint32),
                                   ctypes.POINTER(sz), ctypes.POINTER(sz), ctypes.POINTER(sz)]),
         "ccl_ring_allreduce_literal": (st, [pp, pp, i32, sz, i32, i32, ctypes.POINTER(u64), vp, sz, vp]),
@@ -635,6 +658,253 @@ def ccl_moe_combine(y, expert_ids, weights, counts, slots, num_experts: int, out
                                _ptr_array([t.data_ptr() for t in slots]), p, tokens, k, num_experts,
                                hidden, _ptr_array([t.data_ptr() for t in out]),
                                _stream(stream, out[0].device)), "ccl_moe_combine")
+
+
+# --------------------------------------------------- MoE: a rank's own experts
+def _sizes(values):
+    return (ctypes.c_size_t * len(values))(*values)
+
+
+def _pointers(ts):
+    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+
+
+def _ranks(ts, name: str, p: int, dtype, rows=None, width=None) -> list[torch.Tensor]:
+    """The p rank buffers of an argument, of one dtype; where given, rank r has
+    rows[r] rows of `width` elements."""
+    ts = _tensors(ts, name)
+    if len(ts) != p:
+        raise ValueError(f"{name} must hold {p} rank buffers, got {len(ts)}")
+    if ts[0].dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {ts[0].dtype}")
+    if rows is not None:
+        for r, t in enumerate(ts):
+            if t.numel() != rows[r] * width:
+                raise ValueError(f"{name}[{r}] has {t.numel()} elements, expected {rows[r]} x {width}")
+    return ts
+
+
+def _choices(rows, name: str = "rows"):
+    """(buffers, tokens of each rank, k) of a list of (tokens, k) int32 tensors."""
+    rows = _tensors(rows, name)
+    if rows[0].dtype != torch.int32:
+        raise ValueError(f"{name} must be int32, got {rows[0].dtype}")
+    k = rows[0].shape[1] if rows[0].dim() == 2 else 1
+    for r, t in enumerate(rows):
+        if t.dim() > 2 or (t.shape[1] if t.dim() == 2 else 1) != k:
+            raise ValueError(f"{name}[{r}] must be (tokens, {k})")
+    return rows, [t.shape[0] for t in rows], k
+
+
+def _row_buffers(ts, name: str, p: int, dtype=None):
+    """(buffers, rows of each rank, width) of a list of (rows, width) tensors."""
+    ts = _tensors(ts, name)
+    if len(ts) != p:
+        raise ValueError(f"{name} must hold {p} rank buffers, got {len(ts)}")
+    if dtype is not None and ts[0].dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {ts[0].dtype}")
+    for r, t in enumerate(ts):
+        if t.dim() != 2 or t.shape[1] != ts[0].shape[1]:
+            raise ValueError(f"{name}[{r}] must be (rows, {ts[0].shape[-1]})")
+    return ts, [t.shape[0] for t in ts], ts[0].shape[1]
+
+
+def ccl_moe_sort(expert_ids, num_experts: int, offsets, rows, first_expert=None, stream=None) -> None:
+    """expert_ids[r] ((tokens, k) int32) -> offsets[r] (num_experts + 1 int32) and
+    rows[r] ((tokens, k) int32: the row of each choice in expert order, -1 for
+    an id outside [first_expert[r], first_expert[r] + num_experts))."""
+    ids, tokens, k = _choices(expert_ids, "expert_ids")
+    p = len(ids)
+    offsets = _ranks(offsets, "offsets", p, torch.int32, [num_experts + 1] * p, 1)
+    rows = _ranks(rows, "rows", p, torch.int32, tokens, k)
+    first = None
+    if first_expert is not None:
+        if len(first_expert) != p:
+            raise ValueError(f"first_expert must hold {p} numbers")
+        first = (ctypes.c_int32 * p)(*first_expert)
+    _check(LIB.ccl_moe_sort(_pointers(ids), _sizes(tokens), p, k, num_experts, first, _pointers(offsets),
+                            _pointers(rows), _stream(stream, ids[0].device)), "ccl_moe_sort")
+
+
+def ccl_moe_to_experts(x, rows, sorted, stream=None) -> None:
+    """sorted[r][rows[r][t, j]] = x[r][t]: the tokens' rows in expert order."""
+    rows, tokens, k = _choices(rows)
+    p = len(rows)
+    sorted, cap, hidden = _row_buffers(sorted, "sorted", p)
+    x = _ranks(x, "x", p, sorted[0].dtype, tokens, hidden)
+    _check(LIB.ccl_moe_to_experts(_pointers(x), _pointers(rows), _sizes(tokens), p, k, hidden, _dtype_code(x[0]),
+                                  _pointers(sorted), _sizes(cap), _stream(stream, rows[0].device)),
+           "ccl_moe_to_experts")
+
+
+def ccl_moe_from_experts(y, rows, weights, out, stream=None) -> None:
+    """out[r][t] = sum_j weights[r][t, j] * y[r][rows[r][t, j]] in fp32, rounded
+    once; weights None adds the rows as they are (the gradient of
+    ccl_moe_to_experts)."""
+    rows, tokens, k = _choices(rows)
+    p = len(rows)
+    y, cap, hidden = _row_buffers(y, "y", p)
+    out = _ranks(out, "out", p, y[0].dtype, tokens, hidden)
+    if weights is not None:
+        weights = _pointers(_ranks(weights, "weights", p, torch.float32, tokens, k))
+    _check(LIB.ccl_moe_from_experts(_pointers(y), _sizes(cap), _pointers(rows), weights, _sizes(tokens), p, k, hidden,
+                                    _dtype_code(y[0]), _pointers(out), _stream(stream, rows[0].device)),
+           "ccl_moe_from_experts")
+
+
+def ccl_moe_from_experts_grad(dout, y, rows, weights, dy=None, dweights=None, stream=None) -> None:
+    """The gradient of ccl_moe_from_experts: dy[r][row] = weights * dout[r][t]
+    and dweights[r][t, j] = <y[r][row], dout[r][t]>; either may be None (y too,
+    when dweights is)."""
+    rows, tokens, k = _choices(rows)
+    p = len(rows)
+    if dy is None and dweights is None:
+        raise ValueError("dy or dweights must be given")
+    if dweights is not None and y is None:
+        raise ValueError("dweights needs y")
+    expert_rows = y if y is not None else dy
+    expert_rows, cap, hidden = _row_buffers(expert_rows, "y" if y is not None else "dy", p)
+    dtype = expert_rows[0].dtype
+    dout = _ranks(dout, "dout", p, dtype, tokens, hidden)
+    if y is not None:
+        y = expert_rows
+    if dy is not None:
+        dy = _ranks(dy, "dy", p, dtype, cap, hidden)
+    if weights is not None:
+        weights = _pointers(_ranks(weights, "weights", p, torch.float32, tokens, k))
+    if dweights is not None:
+        dweights = _pointers(_ranks(dweights, "dweights", p, torch.float32, tokens, k))
+    _check(LIB.ccl_moe_from_experts_grad(_pointers(dout), None if y is None else _pointers(y), _sizes(cap),
+                                         _pointers(rows), weights, _sizes(tokens), p, k, hidden,
+                                         _dtype_code(dout[0]), None if dy is None else _pointers(dy), dweights,
+                                         _stream(stream, rows[0].device)), "ccl_moe_from_experts_grad")
+
+
+def _weights(ts, name: str, p: int, dtype=torch.bfloat16):
+    """(buffers, experts, n, contract) of a list of (experts, n, contract) tensors."""
+    ts = _tensors(ts, name)
+    if len(ts) != p:
+        raise ValueError(f"{name} must hold {p} rank buffers, got {len(ts)}")
+    if dtype is not None and ts[0].dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {ts[0].dtype}")
+    for r, t in enumerate(ts):
+        if t.dim() != 3 or t.shape != ts[0].shape:
+            raise ValueError(f"{name}[{r}] must be (experts, n, contract), alike on every rank")
+    return ts, *ts[0].shape
+
+
+def ccl_moe_product(x, offsets, w, y, stream=None) -> None:
+    """y[rows of e] = x[rows of e] @ w[e].T for every expert e: x[r] (rows, contract),
+    w[r] (experts, n, contract), y[r] (rows, n), bf16; offsets[r] from ccl_moe_sort."""
+    x, rows, contract = _row_buffers(x, "x", len(x), torch.bfloat16)
+    p = len(x)
+    w, experts, n, depth = _weights(w, "w", p)
+    if depth != contract:
+        raise ValueError(f"w has {depth} columns, x {contract}")
+    y = _ranks(y, "y", p, torch.bfloat16, rows, n)
+    offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
+    _check(LIB.ccl_moe_product(_pointers(x), _pointers(offsets), _pointers(w), _sizes(rows), p, experts, n, contract,
+                               _pointers(y), _stream(stream, x[0].device)), "ccl_moe_product")
+
+
+def ccl_moe_product_grad_input(dy, offsets, w, dx, stream=None) -> None:
+    """dx[rows of e] = dy[rows of e] @ w[e]: the gradient of ccl_moe_product for x."""
+    dy, rows, n = _row_buffers(dy, "dy", len(dy), torch.bfloat16)
+    p = len(dy)
+    w, experts, height, contract = _weights(w, "w", p)
+    if height != n:
+        raise ValueError(f"w has {height} rows, dy {n} columns")
+    dx = _ranks(dx, "dx", p, torch.bfloat16, rows, contract)
+    offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
+    _check(LIB.ccl_moe_product_grad_input(_pointers(dy), _pointers(offsets), _pointers(w), _sizes(rows), p, experts, n,
+                                          contract, _pointers(dx), _stream(stream, dy[0].device)),
+           "ccl_moe_product_grad_input")
+
+
+def ccl_moe_product_grad_weight(dy, x, offsets, dw, stream=None) -> None:
+    """dw[e] = dy[rows of e].T @ x[rows of e], fp32 or bf16 (zeros for an expert
+    without rows): the gradient of ccl_moe_product for w."""
+    dy, rows, n = _row_buffers(dy, "dy", len(dy), torch.bfloat16)
+    p = len(dy)
+    dw, experts, height, contract = _weights(dw, "dw", p, None)
+    if height != n:
+        raise ValueError(f"dw has {height} rows, dy {n} columns")
+    x = _ranks(x, "x", p, torch.bfloat16, rows, contract)
+    offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
+    _check(LIB.ccl_moe_product_grad_weight(_pointers(dy), _pointers(x), _pointers(offsets), _sizes(rows), p, experts,
+                                           n, contract, _dtype_code(dw[0]), _pointers(dw),
+                                           _stream(stream, dy[0].device)), "ccl_moe_product_grad_weight")
+
+
+# ------------------------------------------------------------------------ AdamW
+class AdamWTable:
+    """The tensors of an AdamW step, checked and packed once; it holds them, so
+    their addresses stay good for as long as the table is used.
+
+    params fp32 or bf16; grads fp32 or bf16; exp_avg and exp_avg_sq fp32, or
+    8-bit codes (float8_e4m3fn or uint8) with exp_avg_scale and
+    exp_avg_sq_scale (fp32, one per 128 elements); copies bf16 or None.
+    """
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None, copies=None):
+        fields = {"param": params, "grad": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
+                  "exp_avg_scale": exp_avg_scale, "exp_avg_sq_scale": exp_avg_sq_scale, "copy": copies}
+        fields = {k: list(v) for k, v in fields.items() if v is not None}
+        self.tensors = fields
+        count = len(fields["param"])
+        if count == 0:
+            raise ValueError("no tensors")
+        kinds = {k: v[0].dtype for k, v in fields.items() if v}
+        self.state_bits = 8 if kinds.get("exp_avg") in (torch.float8_e4m3fn, torch.uint8) else 32
+        state = (torch.float8_e4m3fn, torch.uint8) if self.state_bits == 8 else (torch.float32,)
+        either = (torch.float32, torch.bfloat16)
+        wanted = {"param": either, "grad": either, "exp_avg": state, "exp_avg_sq": state, "copy": (torch.bfloat16,),
+                  "exp_avg_scale": (torch.float32,), "exp_avg_sq_scale": (torch.float32,)}
+        if self.state_bits == 8 and ("exp_avg_scale" not in fields or "exp_avg_sq_scale" not in fields):
+            raise ValueError("8-bit states need exp_avg_scale and exp_avg_sq_scale")
+        if self.state_bits == 32 and ("exp_avg_scale" in fields or "exp_avg_sq_scale" in fields):
+            raise ValueError("fp32 states have no scales")
+        if "copy" in fields and kinds["param"] != torch.float32:
+            raise ValueError("copies are written beside fp32 parameters only")
+        self.device = fields["param"][0].device
+        spans = []
+        for name, ts in fields.items():
+            if len(ts) != count:
+                raise ValueError(f"{name}: {len(ts)} tensors, expected {count}")
+            for i, t in enumerate(ts):
+                n = fields["param"][i].numel()
+                want = -(-n // 128) if name.endswith("scale") else n
+                if not t.is_cuda or t.device != self.device or not t.is_contiguous():
+                    raise ValueError(f"{name}[{i}] must be a contiguous tensor on {self.device}")
+                if t.dtype not in wanted[name] or t.dtype != ts[0].dtype:
+                    raise ValueError(f"{name}[{i}] has dtype {t.dtype}")
+                if t.numel() != want:
+                    raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {want}")
+                if want:
+                    spans.append((t.data_ptr(), t.data_ptr() + want * t.element_size(), f"{name}[{i}]"))
+        spans.sort()
+        for a, b in zip(spans, spans[1:]):
+            if b[0] < a[1]:
+                raise ValueError(f"{b[2]} overlaps {a[2]}")
+        self.param_code, self.grad_code = _DTYPES[kinds["param"]], _DTYPES[kinds["grad"]]
+        self.count = count
+        self.array = (AdamWTensor * count)()
+        for i, entry in enumerate(self.array):
+            for name, ts in fields.items():
+                setattr(entry, name, ts[i].data_ptr())
+            entry.n = fields["param"][i].numel()
+
+
+def ccl_adamw_step(table: AdamWTable, step: int, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
+                   weight_decay: float = 0.01, grad_scale=None, stream=None) -> None:
+    """One AdamW step over the table's tensors; `step` counts from 1, grad_scale
+    is a one-element fp32 CUDA tensor that multiplies every gradient."""
+    if grad_scale is not None and (not grad_scale.is_cuda or grad_scale.dtype != torch.float32 or grad_scale.numel() != 1):
+        raise ValueError("grad_scale must be one fp32 number on the GPU")
+    hyper = AdamWHyper(lr, betas[0], betas[1], eps, weight_decay, step,
+                       None if grad_scale is None else grad_scale.data_ptr())
+    _check(LIB.ccl_adamw_step(table.array, table.count, table.param_code, table.grad_code, table.state_bits,
+                              ctypes.byref(hyper), _stream(stream, table.device)), "ccl_adamw_step")
 
 
 # ------------------------------------------------ Ulysses head <-> sequence

@@ -12,22 +12,10 @@
 #include <mutex>
 
 #include <cuda.h>  // driver types only (CUcontext, CUresult); nothing links the driver
-#include <nvtx3/nvToolsExt.h>
 
 #include "ccl_internal.h"
 
 namespace ccl {
-
-// An NVTX range named after the entry point, so that a profiler's timeline
-// (ncu --nvtx, Nsight Systems) groups each call's kernels under its name.
-// Without an attached tool a push/pop costs a few nanoseconds.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-#define CCL_TRACE() ::ccl::NvtxRange ccl_trace_range_(__func__)
 
 static std::atomic<uint64_t> g_launches{0};
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }

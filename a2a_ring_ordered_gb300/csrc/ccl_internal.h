@@ -8,9 +8,22 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <nvtx3/nvToolsExt.h>
+
 #include "../../include/ccl.h"
 
 namespace ccl {
+
+// An NVTX range named after the entry point, so that a profiler's timeline
+// (ncu --nvtx, Nsight Systems) groups each call's kernels under its name.
+// Without an attached tool a push/pop costs a few nanoseconds.
+struct NvtxRange {
+  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+  ~NvtxRange() { nvtxRangePop(); }
+  NvtxRange(const NvtxRange&) = delete;
+  NvtxRange& operator=(const NvtxRange&) = delete;
+};
+#define CCL_TRACE() ::ccl::NvtxRange ccl_trace_range_(__func__)
 
 // ------------------------------------------------ fused fold (AR / RS / bucket)
 enum FoldMode : int {
@@ -208,6 +221,81 @@ static_assert(sizeof(MoeCombineArgs) <= 4096, "MoE combine parameters exceed 4 K
 cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t s);
 cudaError_t launch_moe_dispatch(const MoeDispatchArgs& a, bool fp8, cudaStream_t s);
 cudaError_t launch_moe_combine(const MoeCombineArgs& a, cudaStream_t s);
+
+// ------------------------------------------------- MoE: a rank's own experts
+constexpr int kSortMaxExperts = 1024;
+struct MoeSortArgs {
+  const int32_t* ids[kMoeMaxRanks];  // tokens * k expert ids per rank
+  int32_t* offsets[kMoeMaxRanks];    // out: num_experts + 1 row starts
+  int32_t* rows[kMoeMaxRanks];       // out: row of each (token, choice), or -1
+  uint32_t items[kMoeMaxRanks];      // tokens * k
+  int32_t first[kMoeMaxRanks];       // first expert id of the rank
+  int p, num_experts;
+};
+struct MoeRowsArgs {  // to_experts, from_experts and its gradient
+  const void* x[kMoeMaxRanks];         // token rows read (to_experts: x; the gradient: dout)
+  const void* y[kMoeMaxRanks];         // expert rows read
+  const int32_t* rows[kMoeMaxRanks];
+  const float* weights[kMoeMaxRanks];  // weights[0] NULL: ones
+  void* out[kMoeMaxRanks];             // expert rows (to_experts, dy) or token rows (from_experts) written
+  float* dweights[kMoeMaxRanks];
+  uint32_t tokens[kMoeMaxRanks];
+  uint32_t cap[kMoeMaxRanks];          // expert rows that the rank's buffer holds
+  uint64_t hidden;                     // elements per row
+  int p, k;
+};
+static_assert(sizeof(MoeSortArgs) <= 4096, "MoE sort parameters exceed 4 KB");
+static_assert(sizeof(MoeRowsArgs) <= 4096, "MoE row parameters exceed 4 KB");
+cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s);
+// `align`: the largest of 16, 4 and 2 that divides every row address
+cudaError_t launch_moe_to_experts(int dt, int align, const MoeRowsArgs& a, cudaStream_t s);
+cudaError_t launch_moe_from_experts(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s);
+cudaError_t launch_moe_from_experts_grad(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s);
+
+// The experts' products.  With rows r of an expert's segment: forward sums
+// a[r][c] * b[e][o][c] over c, grad_input a[r][c] * b[e][c][o] over c,
+// grad_weight a[r][m] * b[r][o] over r.
+enum ProductKind : int { kProductForward = 0, kProductGradInput = 1, kProductGradWeight = 2 };
+struct ProductArgs {
+  const void* a[kMoeMaxRanks];
+  const void* b[kMoeMaxRanks];
+  void* out[kMoeMaxRanks];
+  const int32_t* offsets[kMoeMaxRanks];
+  uint32_t rows[kMoeMaxRanks];
+  uint64_t n, contract;
+  int p, num_experts;
+};
+cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------------------ AdamW
+constexpr int kAdamwBlock = 128;           // elements that share a scale in an 8-bit state
+constexpr uint32_t kAdamwChunk = 4096;     // elements of a tensor per CTA
+struct AdamwTensor {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy;
+  uint64_t n;
+};
+template <int CAP>
+struct AdamwArgsT {
+  static constexpr int kCap = CAP;
+  AdamwTensor t[CAP];
+  uint32_t chunk0[CAP + 1];  // first chunk of each tensor; chunk0[count] = the launch's chunks
+  int count;
+  float beta1, one_minus_beta1, beta2, one_minus_beta2, decay, step_size, root_scale, eps;
+  uint32_t dither;           // step * 2654435769 mod 2^32
+  const float* grad_scale;
+};
+using AdamwSmall = AdamwArgsT<56>;
+using AdamwLarge = AdamwArgsT<440>;
+static_assert(sizeof(AdamwSmall) <= 4096, "AdamW parameters exceed 4 KB");
+static_assert(sizeof(AdamwLarge) <= 32764, "AdamW parameters exceed 32,764 bytes");
+cudaError_t launch_adamw(int param_dt, int grad_dt, int bits, bool copy, const AdamwSmall& a, cudaStream_t s);
+cudaError_t launch_adamw(int param_dt, int grad_dt, int bits, bool copy, const AdamwLarge& a, cudaStream_t s);
 
 // Records one successful kernel launch (ccl_kernel_launch_count).
 void note_launch();

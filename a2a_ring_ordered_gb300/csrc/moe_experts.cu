@@ -1,0 +1,414 @@
+// moe_experts.cu -- a rank's tokens in the order of its experts, and back.
+//
+// Row of (token t, choice j), with e its expert among the rank's own:
+//   row(t, j) = #{(t', j') of an expert before e}
+//             + #{(t', j') before (t, j) in token-choice order, of expert e},
+// a stable counting sort.  Then sorted[row(t, j)] = x[t] (to_experts),
+// out[t] = sum_j w[t][j] y[row(t, j)] (from_experts), and the gradient of the
+// latter, dy[row(t, j)] = w[t][j] dout[t], dw[t][j] = <y[row(t, j)], dout[t]>.
+// All of them move rows and are bound by HBM.
+#include <cooperative_groups.h>
+
+#include "device_common.cuh"
+
+namespace ccl {
+namespace {
+
+constexpr int kSortMaxCluster = 8;       // portable cluster size
+constexpr int kSortUnroll = 4;           // id loads in flight per lane
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+// The expert of an item among the rank's own, or -1.
+__device__ __forceinline__ int sort_expert(const int32_t* ids, uint32_t i, uint32_t hi, int first, int experts) {
+  if (i >= hi) return -1;
+  const int64_t e = static_cast<int64_t>(ids[i]) - first;
+  return (e >= 0 && e < experts) ? static_cast<int>(e) : -1;
+}
+
+// One cluster of CTAs per rank (grid x = CTA in the cluster, grid y = rank).
+// CTA c owns a contiguous range of the rank's items and warp w of it a
+// contiguous part of that, so walking parts in order keeps the sort stable.
+//  1. Each warp counts its part's items per expert in its own row of
+//     hist (lanes of equal expert found by __match_any_sync, the first of
+//     them adds the group), so nothing is atomic.
+//  2. A column of hist becomes the running count of the warps before; the
+//     CTAs' totals are exchanged through distributed shared memory; a scan
+//     over the experts gives every expert its first row.
+//  3. The warp walks its part again: row = hist entry + rank among the lanes
+//     of the same expert, and the entry moves on by the group.
+__global__ void moe_sort_kernel(const __grid_constant__ MoeSortArgs a) {
+  namespace cg = cooperative_groups;
+  extern __shared__ uint32_t smem[];
+  const int E = a.num_experts;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  uint32_t* hist = smem;             // [warps][E]
+  uint32_t* total = hist + warps * E;  // [E]: this CTA's items of each expert
+  uint32_t* base = total + E;          // [E]: first row of the CTA's items of each expert
+  __shared__ uint32_t warp_sum[32];
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t c = cluster.block_rank(), ctas = cluster.num_blocks();
+  const int r = blockIdx.y;
+  for (int i = tid; i < warps * E; i += blockDim.x) hist[i] = 0;
+  pdl_enter();
+  const int32_t* ids = a.ids[r];
+  const int first = a.first[r];
+  const uint32_t items = a.items[r];
+  // items per warp: whole groups of 32 lanes
+  const uint32_t parts = ctas * warps;
+  const uint32_t part = ((items + parts - 1) / parts + 31) / 32 * 32;
+  const uint64_t lo64 = static_cast<uint64_t>(c * warps + warp) * part;
+  const uint32_t lo = lo64 < items ? static_cast<uint32_t>(lo64) : items;
+  const uint32_t hi = items - lo < part ? items : lo + part;
+  uint32_t* mine = hist + warp * E;
+  __syncthreads();
+
+  for (uint32_t b = lo; b < hi; b += 32 * kSortUnroll) {
+    int e[kSortUnroll];
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) e[u] = sort_expert(ids, b + 32 * u + lane, hi, first, E);
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+      const unsigned same = __match_any_sync(kAll, e[u]);
+      if (e[u] >= 0 && lane == __ffs(same) - 1) mine[e[u]] += __popc(same);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += blockDim.x) {
+    uint32_t run = 0;
+    for (int w = 0; w < warps; ++w) {
+      const uint32_t v = hist[w * E + e];
+      hist[w * E + e] = run;
+      run += v;
+    }
+    total[e] = run;
+  }
+  cluster.sync();
+  // experts in blocks of blockDim.x: this thread's expert, its rows in all
+  // CTAs and in the CTAs before this one, then a scan over the threads
+  uint32_t carry = 0;
+  for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+    const int e = e0 + tid;
+    uint32_t all = 0, before = 0;
+    if (e < E) {
+      for (uint32_t q = 0; q < ctas; ++q) {
+        const uint32_t v = cluster.map_shared_rank(total, q)[e];
+        all += v;
+        before += q < c ? v : 0;
+      }
+    }
+    uint32_t incl = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    uint32_t start = carry, round = 0;
+    for (int w = 0; w < warps; ++w) {
+      const uint32_t v = warp_sum[w];
+      start += w < warp ? v : 0;
+      round += v;
+    }
+    start += incl - all;
+    carry += round;
+    if (e < E) {
+      base[e] = start + before;
+      if (c == 0) a.offsets[r][e] = static_cast<int32_t>(start);
+    }
+    __syncthreads();
+  }
+  if (c == 0 && tid == 0) a.offsets[r][E] = static_cast<int32_t>(carry);
+  cluster.barrier_arrive();  // the other CTAs may still read this one's totals
+
+  int32_t* rows = a.rows[r];
+  for (uint32_t b = lo; b < hi; b += 32 * kSortUnroll) {
+    int e[kSortUnroll];
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) e[u] = sort_expert(ids, b + 32 * u + lane, hi, first, E);
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+      const uint32_t i = b + 32 * u + lane;
+      const unsigned same = __match_any_sync(kAll, e[u]);
+      const uint32_t before = __popc(same & ((1u << lane) - 1u));
+      const uint32_t at = e[u] >= 0 ? mine[e[u]] : 0;
+      __syncwarp();
+      if (e[u] >= 0 && before == 0) mine[e[u]] = at + __popc(same);
+      __syncwarp();
+      if (i < hi) rows[i] = e[u] >= 0 ? static_cast<int32_t>(base[e[u]] + at + before) : -1;
+    }
+  }
+  cluster.barrier_wait();
+}
+
+// ------------------------------------------------------------------ rows
+// Raw copies of B bytes (16, 4 or 2).
+template <int B>
+struct Raw {
+  using T = uint32_t;
+};
+template <>
+struct Raw<16> {
+  using T = uint4;
+};
+template <int B>
+__device__ __forceinline__ typename Raw<B>::T ld_raw(const char* p) {
+  if constexpr (B == 16) return ld_once16(p);
+  else if constexpr (B == 4) return ld_once4(p);
+  else return ld_once2(p);
+}
+template <int B>
+__device__ __forceinline__ void st_raw(char* p, typename Raw<B>::T v) {
+  if constexpr (B == 16) st_stream16(p, v);
+  else if constexpr (B == 4) st_stream4(p, v);
+  else st_stream2(p, v);
+}
+
+// The row of a choice, or -1 where it has none in the buffer.
+__device__ __forceinline__ int64_t row_of(const int32_t* rows, uint64_t item, uint32_t cap) {
+  const int32_t row = __ldg(rows + item);
+  return (row >= 0 && static_cast<uint32_t>(row) < cap) ? row : -1;
+}
+
+// A rank's (token, vector) pairs are one flat range (grid y = rank); each
+// vector is read once and written to the token's k rows.
+template <int B, int U>
+__global__ void __launch_bounds__(kThreads) moe_to_experts_kernel(const __grid_constant__ MoeRowsArgs a, uint32_t nv) {
+  pdl_enter();
+  const int r = blockIdx.y, k = a.k;
+  const uint64_t total = static_cast<uint64_t>(a.tokens[r]) * nv;
+  const uint64_t row_bytes = static_cast<uint64_t>(nv) * B;
+  const uint64_t f0 = (static_cast<uint64_t>(blockIdx.x) * U) * kThreads + threadIdx.x;
+  if (f0 >= total) return;
+  const char* x = static_cast<const char*>(a.x[r]);
+  typename Raw<B>::T w[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (f0 + u * kThreads < total) w[u] = ld_raw<B>(x + (f0 + u * kThreads) * B);
+  char* out = static_cast<char*>(a.out[r]);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint64_t f = f0 + u * kThreads;
+    if (f >= total) continue;
+    const uint64_t t = f / nv, v = f - t * nv;
+    for (int j = 0; j < k; ++j) {
+      const int64_t row = row_of(a.rows[r], t * k + j, a.cap[r]);
+      if (row >= 0) st_raw<B>(out + row * row_bytes + v * B, w[u]);
+    }
+  }
+}
+
+// The same flat range; the k rows' loads are issued (8 at a time) before any
+// is added.
+template <int DT, int VEC>
+__global__ void __launch_bounds__(kThreads) moe_from_experts_kernel(const __grid_constant__ MoeRowsArgs a, uint32_t nv) {
+  constexpr int W = (VEC * Elem<DT>::kBytes + 3) / 4;
+  pdl_enter();
+  const int r = blockIdx.y, k = a.k;
+  const uint64_t total = static_cast<uint64_t>(a.tokens[r]) * nv;
+  const uint64_t f = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (f >= total) return;
+  const uint64_t t = f / nv, v = f - t * nv;
+  const float* weights = a.weights[r];
+  float acc[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
+  bool have = false;
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    uint32_t raw[8][W];
+    int64_t row[8];
+    float wt[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      row[b] = j0 + b < k ? row_of(a.rows[r], t * k + j0 + b, a.cap[r]) : -1;
+      wt[b] = (weights != nullptr && j0 + b < k) ? __ldg(weights + t * k + j0 + b) : 1.0f;
+    }
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+      if (row[b] >= 0) load_raw<DT, VEC>(a.y[r], row[b] * a.hidden + v * VEC, raw[b]);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      if (row[b] < 0) continue;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float prod = __fmul_rn(wt[b], widen<DT>(raw[b], e));
+        acc[e] = have ? __fadd_rn(acc[e], prod) : prod;
+      }
+      have = true;
+    }
+  }
+  uint32_t w[W];
+  pack_out<DT, VEC>(acc, w);
+  store_raw<DT, VEC>(a.out[r], t * a.hidden + v * VEC, w);
+}
+
+// `tpt` threads (a power of two, 32..256) per token walk its vectors: dout is
+// read once for 8 choices, each y vector once, each dy vector written once.
+// The dot products are added per thread, then in a warp's fixed shuffle tree,
+// then warp by warp.
+template <int DT, int VEC>
+__global__ void __launch_bounds__(kThreads) moe_from_experts_grad_kernel(const __grid_constant__ MoeRowsArgs a,
+                                                                        uint32_t nv, int tpt) {
+  constexpr int W = (VEC * Elem<DT>::kBytes + 3) / 4;
+  __shared__ float part[kThreads / 32][8];
+  pdl_enter();
+  const int r = blockIdx.y, k = a.k;
+  const int group = threadIdx.x / tpt, in = threadIdx.x - group * tpt, lane = threadIdx.x & 31;
+  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * (kThreads / tpt) + group;
+  if (static_cast<uint64_t>(blockIdx.x) * (kThreads / tpt) >= a.tokens[r]) return;
+  const bool live = t < a.tokens[r];
+  const float* weights = a.weights[r];
+  void* dy = a.out[r];
+  float* dw = a.dweights[r];
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    int64_t row[8];
+    float wt[8], dot[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      row[b] = (live && j0 + b < k) ? row_of(a.rows[r], t * k + j0 + b, a.cap[r]) : -1;
+      wt[b] = (live && weights != nullptr && j0 + b < k) ? __ldg(weights + t * k + j0 + b) : 1.0f;
+      dot[b] = 0.0f;
+    }
+    for (uint32_t v = in; live && v < nv; v += tpt) {
+      uint32_t d[W], y[8][W];
+      load_raw<DT, VEC>(a.x[r], t * a.hidden + static_cast<uint64_t>(v) * VEC, d);
+      if (dw != nullptr) {
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+          if (row[b] >= 0) load_raw<DT, VEC>(a.y[r], row[b] * a.hidden + static_cast<uint64_t>(v) * VEC, y[b]);
+      }
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if (row[b] < 0) continue;
+        float o[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float de = widen<DT>(d, e);
+          o[e] = __fmul_rn(wt[b], de);
+          if (dw != nullptr) dot[b] = fmaf(widen<DT>(y[b], e), de, dot[b]);
+        }
+        if (dy != nullptr) {
+          uint32_t w[W];
+          pack_out<DT, VEC>(o, w);
+          store_raw<DT, VEC>(dy, row[b] * a.hidden + static_cast<uint64_t>(v) * VEC, w);
+        }
+      }
+    }
+    if (dw == nullptr) continue;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) dot[b] += __shfl_xor_sync(kAll, dot[b], o);
+    }
+    if (lane == 0) {
+#pragma unroll
+      for (int b = 0; b < 8; ++b) part[threadIdx.x >> 5][b] = dot[b];
+    }
+    __syncthreads();
+    if (live && in < 8 && j0 + in < k) {
+      float sum = 0.0f;
+      for (int w = 0; w < tpt / 32; ++w) sum += part[group * (tpt / 32) + w][in];
+      dw[t * k + j0 + in] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+uint32_t most_tokens(const MoeRowsArgs& a) {
+  uint32_t m = 0;
+  for (int r = 0; r < a.p; ++r) m = a.tokens[r] > m ? a.tokens[r] : m;
+  return m;
+}
+
+template <typename... Params>
+cudaError_t launch_rows(void (*kernel)(Params...), uint64_t ctas, int p, cudaStream_t s, Params... params) {
+  if (ctas > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(p));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = CCL_PDL ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, params...);
+  if (err == cudaSuccess) note_launch();
+  return err;
+}
+
+template <int B>
+cudaError_t launch_copy(int elem, const MoeRowsArgs& a, cudaStream_t s) {
+  constexpr int U = 4;
+  const uint32_t nv = static_cast<uint32_t>(a.hidden * elem / B);
+  const uint64_t total = static_cast<uint64_t>(most_tokens(a)) * nv;
+  return launch_rows(moe_to_experts_kernel<B, U>, (total + kThreads * U - 1) / (kThreads * U), a.p, s, a, nv);
+}
+
+template <int DT, int VEC>
+cudaError_t launch_back(const MoeRowsArgs& a, cudaStream_t s) {
+  const uint32_t nv = static_cast<uint32_t>(a.hidden / VEC);
+  const uint64_t total = static_cast<uint64_t>(most_tokens(a)) * nv;
+  return launch_rows(moe_from_experts_kernel<DT, VEC>, (total + kThreads - 1) / kThreads, a.p, s, a, nv);
+}
+
+template <int DT, int VEC>
+cudaError_t launch_back_grad(const MoeRowsArgs& a, cudaStream_t s) {
+  const uint32_t nv = static_cast<uint32_t>(a.hidden / VEC);
+  int tpt = 32;
+  while (tpt < kThreads && static_cast<uint32_t>(tpt) < nv) tpt *= 2;
+  const uint64_t per = kThreads / tpt;
+  return launch_rows(moe_from_experts_grad_kernel<DT, VEC>, (most_tokens(a) + per - 1) / per, a.p, s, a, nv, tpt);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
+  uint32_t most = 0;
+  for (int r = 0; r < a.p; ++r) most = a.items[r] > most ? a.items[r] : most;
+  // a warp's part is at least 32 lanes x kSortUnroll items while that leaves
+  // no CTA of 32 warps without work; then more CTAs
+  constexpr uint32_t kPerWarp = 32 * kSortUnroll, kPerCta = kPerWarp * 32;
+  const uint32_t ctas = most <= kPerCta ? 1 : (most + kPerCta - 1) / kPerCta >= kSortMaxCluster ? kSortMaxCluster : (most + kPerCta - 1) / kPerCta;
+  uint32_t warps = (most + kPerWarp - 1) / kPerWarp;
+  warps = warps < 8 ? 8 : warps > 32 ? 32 : warps;
+  const size_t smem = (static_cast<size_t>(warps) + 2) * a.num_experts * sizeof(uint32_t);
+  cudaError_t err = cudaSuccess;
+  if (smem > 48 * 1024) err = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, static_cast<unsigned>(a.p));
+  cfg.blockDim = dim3(warps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = CCL_PDL ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, moe_sort_kernel, a);
+  if (err == cudaSuccess) note_launch();
+  return err;
+}
+
+cudaError_t launch_moe_to_experts(int dt, int align, const MoeRowsArgs& a, cudaStream_t s) {
+  const int elem = dt == kF32 ? 4 : 2;
+  return align == 16 ? launch_copy<16>(elem, a, s) : align == 4 ? launch_copy<4>(elem, a, s) : launch_copy<2>(elem, a, s);
+}
+
+cudaError_t launch_moe_from_experts(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s) {
+  if (dt == kF32) return vec ? launch_back<kF32, 4>(a, s) : launch_back<kF32, 1>(a, s);
+  return vec ? launch_back<kBF16, 8>(a, s) : launch_back<kBF16, 1>(a, s);
+}
+
+cudaError_t launch_moe_from_experts_grad(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s) {
+  if (dt == kF32) return vec ? launch_back_grad<kF32, 4>(a, s) : launch_back_grad<kF32, 1>(a, s);
+  return vec ? launch_back_grad<kBF16, 8>(a, s) : launch_back_grad<kBF16, 1>(a, s);
+}
+
+}  // namespace ccl

@@ -393,6 +393,127 @@ ccl_status_t ccl_moe_combine(const void* const* y, const size_t* y_rows,
                              size_t tokens, int k, int num_experts, size_t hidden, void* const* out,
                              void* stream);
 
+/* --------------------------------------------- MoE: a rank's own experts
+ * The local half of an MoE layer, between dispatch and combine ("Networks and
+ * Collective Communication" section 7.4 stops at the exchange): a rank's rows
+ * are brought into the order of its experts, multiplied by each expert's
+ * weights, and brought back; every call has its gradient.  p <= 64 virtual
+ * ranks, 1 <= k <= 16, tokens[r] * k < 2^31.
+ *
+ * ccl_moe_sort: expert_ids[r] (device, tokens[r]*k int32, token-major) ->
+ *   offsets[r] (device, num_experts+1 int32: expert e's rows are offsets[e] ..
+ *   offsets[e+1]-1) and rows[r] (device, tokens[r]*k int32: the row of each
+ *   (token, choice), by expert, then token, then choice; -1 for an id outside
+ *   [first, first + num_experts)).  first_expert (HOST, p entries, NULL: all
+ *   0) is each rank's first id.  num_experts <= 1024.  One launch.  After
+ *   ccl_moe_dispatch, recv_expert with k = 1 is the expert_ids.
+ * ccl_moe_to_experts: sorted[r][rows[r][t*k+j]] = x[r][t], `hidden` elements
+ *   of dt (bf16 or fp32); a copy.  sorted_rows (HOST, p) is each sorted[r]'s
+ *   capacity: rows past it are not written, nor is any row that no choice has.
+ * ccl_moe_from_experts: out[r][t] = sum_j weights[r][t*k+j] *
+ *   y[r][rows[r][t*k+j]] in fp32, products and sums rounded in choice order
+ *   (no fused multiply-add), rounded once to dt; a choice whose row is -1 or
+ *   not below y_rows[r] adds nothing, a token without any gets zeros.
+ *   weights NULL: plain sum, which is the gradient of ccl_moe_to_experts.
+ * ccl_moe_from_experts_grad: dy[r][row] = weights * dout[r][t] (rounded once
+ *   to dt) and dweights[r][t*k+j] = sum_h y[r][row][h] * dout[r][t][h] in fp32
+ *   (0 for a choice without a row).  Either output may be NULL; y may be NULL
+ *   when dweights is.  weights NULL: ones.  Every sum has a fixed order.
+ * No output may overlap an input or another output of its rank. */
+ccl_status_t ccl_moe_sort(const int32_t* const* expert_ids, const size_t* tokens, int p, int k,
+                          int num_experts, const int32_t* first_expert, int32_t* const* offsets,
+                          int32_t* const* rows, void* stream);
+
+ccl_status_t ccl_moe_to_experts(const void* const* x, const int32_t* const* rows, const size_t* tokens,
+                                int p, int k, size_t hidden, ccl_dtype_t dt, void* const* sorted,
+                                const size_t* sorted_rows, void* stream);
+
+ccl_status_t ccl_moe_from_experts(const void* const* y, const size_t* y_rows, const int32_t* const* rows,
+                                  const float* const* weights, const size_t* tokens, int p, int k,
+                                  size_t hidden, ccl_dtype_t dt, void* const* out, void* stream);
+
+ccl_status_t ccl_moe_from_experts_grad(const void* const* dout, const void* const* y, const size_t* y_rows,
+                                       const int32_t* const* rows, const float* const* weights,
+                                       const size_t* tokens, int p, int k, size_t hidden, ccl_dtype_t dt,
+                                       void* const* dy, float* const* dweights, void* stream);
+
+/* The experts' products.  Rank r holds `rows[r]` rows in expert order,
+ * offsets[r] (device) as ccl_moe_sort gives them, and weights w[r] of
+ * num_experts x n x contract elements.  With R_e the rows of expert e:
+ *   ccl_moe_product             y[R_e]  = x[R_e] * w_e^T    (rows x n)
+ *   ccl_moe_product_grad_input  dx[R_e] = dy[R_e] * w_e     (rows x contract)
+ *   ccl_moe_product_grad_weight dw_e    = dy[R_e]^T * x[R_e] (n x contract;
+ *                               zeros for an expert without rows)
+ * Everything is bf16, row-major and contiguous, except dw, which is dw_dt
+ * (CCL_F32, as gradient buckets hold it, or CCL_BF16).  Products are summed
+ * in fp32 in an order fixed by the sizes and rounded once.  Rows that no
+ * expert has (below offsets[0], from offsets[num_experts] on) are not written;
+ * offsets beyond rows[r] are cut to it.  num_experts <= 1024.  The ranks may
+ * share one w; no output may overlap an input or another output. */
+ccl_status_t ccl_moe_product(const void* const* x, const int32_t* const* offsets, const void* const* w,
+                             const size_t* rows, int p, int num_experts, size_t n, size_t contract,
+                             void* const* y, void* stream);
+
+ccl_status_t ccl_moe_product_grad_input(const void* const* dy, const int32_t* const* offsets,
+                                        const void* const* w, const size_t* rows, int p, int num_experts,
+                                        size_t n, size_t contract, void* const* dx, void* stream);
+
+ccl_status_t ccl_moe_product_grad_weight(const void* const* dy, const void* const* x,
+                                         const int32_t* const* offsets, const size_t* rows, int p,
+                                         int num_experts, size_t n, size_t contract, ccl_dtype_t dw_dt,
+                                         void* const* dw, void* stream);
+
+/* ------------------------------------------------------------------ AdamW
+ * One AdamW step over many tensors, behind the gradient buckets
+ * (ccl_bucket_allreduce_scale_cast's bf16 averages are its gradients).  For
+ * each element, every operation in fp32 and rounded by itself:
+ *   g = grad (* *grad_scale, where that is given: a DEVICE float, such as a
+ *       clipping factor, so that no host wait is needed)
+ *   m = m * beta1 + g * (1 - beta1)
+ *   v = v * beta2 + (g * g) * (1 - beta2)
+ *   param = param * (1 - lr * weight_decay)
+ *           - (m / (sqrt(v) * (1 - beta2^step)^-1/2 + eps)) * (lr / (1 - beta1^step))
+ * (the factors are worked out in double and rounded to fp32).  param is fp32
+ * or bf16 (rounded once), grad fp32 or bf16; copy (fp32 param only, may be
+ * NULL) receives param rounded to bf16.
+ *   state_bits 32: exp_avg = m and exp_avg_sq = v, fp32; no scales.
+ *   state_bits 8:  e4m3 codes with one fp32 scale per 128 elements of the
+ *     tensor (the last block may be shorter): exp_avg holds m, exp_avg_sq
+ *     holds sqrt(v); value = code * scale, scale = amax * fp32(1 / 448) over
+ *     the block's finite values, and what is coded is x * (448 * (1 / amax))
+ *     (scale 1 and codes 0 where that amax is at most 2^-100).  The update
+ *     uses the new m and v before they are coded.  m's code rounds to nearest
+ *     even.  sqrt(v) moves by far less than a code's spacing in a
+ *     step, so nearest rounding would hold it still for ever: its code rounds
+ *     up where the distance to the code below, in units of the spacing, plus
+ *     a threshold reaches 1, the threshold being the top 20 bits of
+ *     (i * 1779033703 + step * 2654435769) mod 2^32, i the element's index in
+ *     its tensor: over any run of steps a code is right on average.  A
+ *     nonzero v never gets code 0; values that are not finite are held as NaN.
+ * tensors is a HOST array, read before the call returns; step counts from 1.
+ * One launch for up to 440 tensors.  No buffer may overlap another (checked
+ * within each tensor). */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;     /* state_bits 8: ceil(n / 128) entries */
+  float* exp_avg_sq_scale;  /* likewise */
+  void* copy;               /* bf16, or NULL */
+  size_t n;
+} ccl_adamw_tensor_t;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  uint64_t step;
+  const float* grad_scale; /* device, or NULL */
+} ccl_adamw_hyper_t;
+
+ccl_status_t ccl_adamw_step(const ccl_adamw_tensor_t* tensors, size_t count, ccl_dtype_t param_dt,
+                            ccl_dtype_t grad_dt, int state_bits, const ccl_adamw_hyper_t* hyper,
+                            void* stream);
+
 /* ------------------------------------------------------- literal ring engine
  * Executes the ring schedule as written: the reduce-scatter phase's p-1 steps
  * (rank r sends its partial of chunk (r-s-1) mod p to rank r+1, which adds its
