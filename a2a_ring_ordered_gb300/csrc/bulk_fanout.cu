@@ -231,6 +231,9 @@ cudaError_t read_device_error(unsigned int* flag, bool clear) {
     const unsigned int zero = 0;
     err = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
   }
+  unsigned int product = 0;
+  if (err == cudaSuccess) err = read_product_error(&product, clear);
+  *flag |= product;
   return err;
 }
 

@@ -252,9 +252,8 @@ cudaError_t launch_moe_to_experts(int dt, int align, const MoeRowsArgs& a, cudaS
 cudaError_t launch_moe_from_experts(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s);
 cudaError_t launch_moe_from_experts_grad(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s);
 
-// The experts' products.  With rows r of an expert's segment: forward sums
-// a[r][c] * b[e][o][c] over c, grad_input a[r][c] * b[e][c][o] over c,
-// grad_weight a[r][m] * b[r][o] over r.
+// The experts' products.  b holds the rows (x, or dy for the gradients), a the
+// weights, or x for the weights' gradient.
 enum ProductKind : int { kProductForward = 0, kProductGradInput = 1, kProductGradWeight = 2 };
 struct ProductArgs {
   const void* a[kMoeMaxRanks];
@@ -265,6 +264,8 @@ struct ProductArgs {
   uint64_t n, contract;
   int p, num_experts;
 };
+// The products' device error word, as read_device_error's.
+cudaError_t read_product_error(unsigned int* flag, bool clear);
 cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& a, cudaStream_t s);
 
 // ------------------------------------------------------------------ AdamW

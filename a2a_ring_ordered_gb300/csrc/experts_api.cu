@@ -305,14 +305,14 @@ ccl_status_t product(int kind, const void* const* first, const char* first_name,
       EXPERTS_TRY(check_buffer(first_name, r, first[r], 2));
       EXPERTS_TRY(check_buffer(second_name, r, second[r], 2));
     }
-    a.a[r] = rows[r] != 0 ? first[r] : nullptr;
-    a.b[r] = rows[r] != 0 ? second[r] : nullptr;
+    a.b[r] = rows[r] != 0 ? first[r] : nullptr;
+    a.a[r] = rows[r] != 0 ? second[r] : nullptr;
     a.out[r] = out[r];
     a.offsets[r] = offsets[r];
     a.rows[r] = static_cast<uint32_t>(rows[r]);
     const uint64_t in_cols = kind == kProductForward ? contract : n, out_cols = kind == kProductForward ? n : contract;
-    spans.add(a.a[r], rows[r] * in_cols * 2, false);
-    spans.add(a.b[r], weights_out ? rows[r] * contract * 2 : weight * 2, false);
+    spans.add(a.b[r], rows[r] * in_cols * 2, false);
+    spans.add(a.a[r], weights_out ? rows[r] * contract * 2 : weight * 2, false);
     spans.add(offsets[r], (static_cast<uint64_t>(num_experts) + 1) * 4, false);
     spans.add(out[r], weights_out ? weight * e : rows[r] * out_cols * 2, true);
   }

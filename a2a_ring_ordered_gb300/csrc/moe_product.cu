@@ -1,93 +1,662 @@
-// moe_product.cu -- the experts' products: each expert's rows times its
-// weights, and the gradients for the rows and for the weights.
+// moe_product.cu -- the experts' products on the fifth-generation tensor cores.
+//
+// Rank's rows are sorted by expert; with R_e the rows of expert e,
+//   forward      y[R_e]  = x[R_e] w_e^T     out[row][n] = sum_k w[e][n][k] x[row][k]
+//   grad_input   dx[R_e] = dy[R_e] w_e      out[row][k] = sum_n w[e][n][k] dy[row][n]
+//   grad_weight  dw_e    = dy[R_e]^T x[R_e] out[n][k]   = sum_row x[row][k] dy[row][n]
+// One kernel computes all three as D[m][c] = sum_q A[m][q] B[c][q], with m the
+// output's contiguous axis (a TMEM lane per m, so a warp's stores are
+// contiguous whatever the alignment) and c the rows (or n): the tensor core's
+// N, which may be any multiple of 32.  An expert's rows are cut into equal
+// tiles of at most 256, so a ragged expert wastes less than 32 columns, and a
+// handful of rows costs a handful of columns: the weights' stream bounds it.
+//
+// A pair of CTAs (one cluster) owns a 256 x 256 tile at a time, a persistent
+// grid of one pair per two SMs: each CTA stages 128 rows of A and half of B's
+// columns (tcgen05.mma.cta_group::2 reads both halves, which halves shared
+// memory traffic for B), in stages of 64 contraction elements.  Roles by warp:
+//   0-3  epilogue: TMEM -> registers -> global, double buffered (2 x 256
+//        columns) against the next tile's products
+//   4    TMA: one thread issues the stage's bulk tensor copies
+//   5    MMA: one thread of the even CTA issues for the pair
+//   6-9  loaders: what TMA cannot do -- operands that do not sit on 16 bytes,
+//        and grad_weight's last rows, which must read as zero where the next
+//        expert begins -- by whole 16-byte loads, shifted and masked
+// Every wait is bounded: one that runs out sets the device error word.
+#include <cuda.h>  // CUtensorMap and its enums; nothing links the driver
+
 #include "device_common.cuh"
+#include "realign.cuh"
 
 namespace ccl {
 namespace {
 
-constexpr int kTile = 64, kStep = 16;
+constexpr int kTile = 256;         // outputs per pair: 256 x at most 256
+constexpr int kStep = 64;          // contraction elements per stage (128 bytes: one swizzle row)
+constexpr int kStages = 6;
+constexpr int kOperandBytes = 128 * kStep * 2;  // one CTA's share of A or B in a stage
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kMaxGroups = 2048;   // (rank, expert) pairs per launch
+constexpr int kLaunchRanks = 8;    // keeps the parameter block under 4 KB
+constexpr int kProductThreads = 320;
+constexpr int kLoaderThreads = 128;
+constexpr int kSmallBox = 16;      // rows of B's small box
+constexpr uint32_t kTmemColumns = 512;
+constexpr long long kWaitCycles = 1ll << 32;  // two seconds
 
-// 64 x 64 tile of one expert's product, 4 x 4 outputs per thread, operands
-// staged element by element in shared memory as fp32.  grid.x walks the
-// output columns, grid.y the row tiles of all experts (each expert starts
-// tiles of its own; the weights' gradient has the same tiles for each),
-// grid.z the ranks.
+__device__ unsigned int g_product_error;  // nonzero: a bounded wait ran out
+
+struct PairArgs {
+  CUtensorMap a[kLaunchRanks], b[kLaunchRanks], b_small[kLaunchRanks];
+  const void* pa[kLaunchRanks];
+  const void* pb[kLaunchRanks];
+  void* out[kLaunchRanks];
+  const int32_t* offsets[kLaunchRanks];
+  uint32_t rows[kLaunchRanks];
+  uint32_t n, contract;
+  int p, num_experts;
+  int tma_a, tma_b;
+};
+static_assert(sizeof(PairArgs) <= 4096, "product parameters exceed 4 KB");
+
+struct Shared {
+  alignas(8) uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t tmem_full[2];
+  uint64_t tmem_empty[2];
+  uint32_t tmem;
+  uint32_t dead;
+  uint32_t scan[kProductThreads / 32];
+  uint32_t first[kMaxGroups + 1];  // row tiles before each (rank, expert)
+  int32_t lo[kMaxGroups];          // its first row
+  int32_t count[kMaxGroups];       // and its rows
+};
+constexpr size_t kSmemBytes = 1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(Shared);
+static_assert(kSmemBytes <= 227 * 1024, "product shared memory");
+
+// ------------------------------------------------------------------ barriers
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// The TMA thread has written nothing itself: its arrivals order nothing.  (A
+// release at cluster scope waits for all of the thread's memory operations,
+// which held every stage back by a microsecond.)
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_tx(uint32_t cluster_bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
+               : "memory");
+}
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  return done != 0;
+}
+// False once this or another wait of the CTA ran out.  CLUSTER: what the other
+// CTA's threads wrote before they arrived is seen behind it.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
+  if (mbar_try<CLUSTER>(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try<CLUSTER>(bar, parity)) {
+    if (*dead) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *dead = 1;
+      atomicExch(&g_product_error, 1u);
+      return false;
+    }
+  }
+  return true;
+}
+
+// ------------------------------------------------------------ tensor memory
+__device__ __forceinline__ uint64_t descriptor(uint32_t addr, uint32_t lead_bytes) {
+  // 128-byte swizzle; 1024 bytes between groups of 8 lines
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(lead_bytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+      "%4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+      : "memory");
+}
+
+// -------------------------------------------------------------------- tiles
+struct Tile {
+  int rank, expert;
+  int lo;       // first row of the expert
+  int depth;    // contraction elements
+  int c0;       // first column: a row of the rank, or an n
+  int cols;     // columns that are stored
+  int width;    // columns that are computed: a multiple of 32
+  int m0;       // first m of the pair
+};
+
+template <int KIND>
+__device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int groups, uint64_t index, uint32_t mt) {
+  const uint32_t rt = static_cast<uint32_t>(index / mt);
+  Tile t;
+  t.m0 = static_cast<int>(index - static_cast<uint64_t>(rt) * mt) * kTile;
+  int g;
+  if constexpr (KIND == kProductGradWeight) {
+    const uint32_t nt = (a.n + kTile - 1) / kTile;
+    g = static_cast<int>(rt / nt);
+    t.c0 = static_cast<int>(rt - g * nt) * kTile;
+    t.cols = min(kTile, static_cast<int>(a.n) - t.c0);
+    t.depth = s.count[g];
+  } else {
+    int lo = 0, hi = groups - 1;  // the last group that begins at or before rt
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.first[mid] <= rt) lo = mid;
+      else hi = mid - 1;
+    }
+    g = lo;
+    const int rows = s.count[g], tiles = (rows + kTile - 1) / kTile;
+    const int each = ((rows + tiles - 1) / tiles + 31) & ~31;
+    const int at = static_cast<int>(rt - s.first[g]) * each;
+    t.c0 = s.lo[g] + at;
+    t.cols = min(each, rows - at);
+    t.depth = static_cast<int>(KIND == kProductForward ? a.contract : a.n);
+  }
+  t.lo = s.lo[g];
+  t.rank = g / a.num_experts;
+  t.expert = g - t.rank * a.num_experts;
+  t.width = (t.cols + 31) & ~31;
+  return t;
+}
+
+// ------------------------------------------------------------------ loaders
+// Up to 8 elements at p, zero behind them, by whole 16-byte granules that hold
+// at least one of them.
+__device__ __forceinline__ uint4 load_unit(const __nv_bfloat16* p, int valid) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (valid <= 0) return v;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p), base = at & ~static_cast<uintptr_t>(15);
+  const int delta = static_cast<int>(at - base);
+  const uint4 g0 = __ldg(reinterpret_cast<const uint4*>(base));
+  uint4 g1 = make_uint4(0, 0, 0, 0);
+  if (delta + 2 * valid > 16) g1 = __ldg(reinterpret_cast<const uint4*>(base + 16));
+  v = delta == 0 ? g0 : realign16(g0, g1, delta);
+  if (valid < 8) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < valid ? w[i] : 2 * i < valid ? (w[i] & 0xFFFFu) : 0u;
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+
+// A barrier among the loaders, and whether any of them says so.
+__device__ __forceinline__ bool any_loader(bool x) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "n"(kLoaderThreads)
+      : "memory");
+  return r != 0;
+}
+
+// Fills `lines` lines of 64 elements (8 swizzled units each): line l starts at
+// base + l * ld and holds valid(l) elements.
+template <typename Start, typename Valid>
+__device__ __forceinline__ void fill_lines(char* dst, int lines, int tid, Start start, Valid valid) {
+  for (int i = tid; i < lines * 8; i += kLoaderThreads) {
+    const int l = i >> 3, u = i & 7;
+    const uint4 v = load_unit(start(l) + u * 8, min(valid(l) - u * 8, 8));
+    *reinterpret_cast<uint4*>(dst + l * 128 + ((u ^ (l & 7)) << 4)) = v;
+  }
+}
+
+// ------------------------------------------------------------------- kernel
 template <int KIND, int OUT>
-__global__ void __launch_bounds__(kThreads) product_simple_kernel(const __grid_constant__ ProductArgs a) {
-  __shared__ float as[kStep][kTile + 1], bs[kStep][kTile + 1];
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+    product_kernel(const __grid_constant__ PairArgs a) {
+  constexpr bool kAColumns = KIND != kProductForward;     // A's contiguous axis is m
+  constexpr bool kBColumns = KIND == kProductGradWeight;  // B's contiguous axis is c
+  extern __shared__ char dynamic[];
+  char* stages = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
+  Shared& s = *reinterpret_cast<Shared*>(stages + static_cast<size_t>(kStages) * kStageBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t cta = blockIdx.x & 1;
+  const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const bool loaders = kBColumns || !a.tma_a || !a.tma_b;
+  const int groups = a.p * a.num_experts;
+  const uint32_t M = KIND == kProductForward ? a.n : a.contract;  // the output's contiguous axis
+  const uint32_t mt = (M + kTile - 1) / kTile;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&s.full[i]), loaders ? 4 : 2);  // from both CTAs: the TMA thread, the loaders
+      mbar_init(smem_addr(&s.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&s.tmem_full[i]), 1);
+      mbar_init(smem_addr(&s.tmem_empty[i]), 8);  // the epilogue's warps of both CTAs
+    }
+    s.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)),
+                 "r"(kTmemColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
   pdl_enter();
-  const int r = blockIdx.z, E = a.num_experts;
-  const int32_t* off = a.offsets[r];
-  const int64_t rows = a.rows[r], N = a.n, K = a.contract;
-  int e = 0;
-  int64_t tile = blockIdx.y, lo = 0, hi = 0;
-  const int64_t wt = (N + kTile - 1) / kTile;
-  for (; e < E; ++e) {  // the expert of this tile
-    lo = min(max(static_cast<int64_t>(off[e]), int64_t{0}), rows);
-    hi = min(max(static_cast<int64_t>(off[e + 1]), lo), rows);
-    const int64_t tiles = KIND == kProductGradWeight ? wt : (hi - lo + kTile - 1) / kTile;
-    if (tile < tiles) break;
-    tile -= tiles;
-  }
-  if (e == E) return;
-  const int64_t m0 = tile * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int64_t M = KIND == kProductGradWeight ? N : hi - lo;
-  const int64_t cols = KIND == kProductForward ? N : K;
-  const int64_t depth = KIND == kProductForward ? K : KIND == kProductGradInput ? N : hi - lo;
-  const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(a.a[r]);
-  const __nv_bfloat16* B = static_cast<const __nv_bfloat16*>(a.b[r]);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < depth; k0 += kStep) {
-    for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-      // consecutive threads along the operand's contiguous axis
-      const int ak = KIND == kProductGradWeight ? i / kTile : i % kStep, am = KIND == kProductGradWeight ? i % kTile : i / kStep;
-      float v = 0.0f;
-      if (m0 + am < M && k0 + ak < depth)
-        v = __bfloat162float(KIND == kProductGradWeight ? A[(lo + k0 + ak) * N + m0 + am] : A[(lo + m0 + am) * depth + k0 + ak]);
-      as[ak][am] = v;
-      const int bk = KIND == kProductForward ? i % kStep : i / kTile, bn = KIND == kProductForward ? i / kStep : i % kTile;
-      v = 0.0f;
-      if (n0 + bn < cols && k0 + bk < depth)
-        v = __bfloat162float(KIND == kProductForward     ? B[(e * N + n0 + bn) * K + k0 + bk]
-                             : KIND == kProductGradInput ? B[(e * N + k0 + bk) * K + n0 + bn]
-                                                         : B[(lo + k0 + bk) * K + n0 + bn]);
-      bs[bk][bn] = v;
+
+  // rows of every (rank, expert), cut to what the buffer holds, and a running
+  // count of their row tiles: each thread counts a run of groups, then a scan
+  {
+    const int per = (groups + kProductThreads - 1) / kProductThreads;
+    const int g0 = min(tid * per, groups), g1 = min(g0 + per, groups);
+    uint32_t mine = 0;
+    for (int g = g0; g < g1; ++g) {
+      const int r = g / a.num_experts, e = g - r * a.num_experts;
+      const int rows = static_cast<int>(a.rows[r]);
+      const int32_t* off = a.offsets[r];
+      const int lo = rows == 0 ? 0 : min(max(off[e], 0), rows);
+      const int hi = rows == 0 ? 0 : min(max(off[e + 1], lo), rows);
+      s.lo[g] = lo;
+      s.count[g] = hi - lo;
+      mine += (hi - lo + kTile - 1) / kTile;
     }
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) s.scan[warp] = incl;
     __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < kStep; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[kk][ty * 4 + i], bs[kk][tx + 16 * j], acc[i][j]);
-    __syncthreads();
+    uint32_t run = incl - mine;
+    for (int w = 0; w < warp; ++w) run += s.scan[w];
+    for (int g = g0; g < g1; ++g) {
+      s.first[g] = run;
+      run += (s.count[g] + kTile - 1) / kTile;
+    }
+    if (tid == kProductThreads - 1) s.first[groups] = run;
   }
-  for (int i = 0; i < 4; ++i) {
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i, n = n0 + tx + 16 * j;
-      if (m >= M || n >= cols) continue;
-      const int64_t at = ((KIND == kProductGradWeight ? e * N : lo) + m) * cols + n;
-      if constexpr (OUT == kF32) static_cast<float*>(a.out[r])[at] = acc[i][j];
-      else static_cast<__nv_bfloat16*>(a.out[r])[at] = __float2bfloat16_rn(acc[i][j]);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = s.tmem;
+  const uint64_t tiles = (KIND == kProductGradWeight ? static_cast<uint64_t>(groups) * ((a.n + kTile - 1) / kTile)
+                                                     : static_cast<uint64_t>(s.first[groups])) * mt;
+  volatile uint32_t* dead = &s.dead;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------------ TMA
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+        const Tile t = tile_at<KIND>(a, s, groups, i, mt);
+        const int steps = (t.depth + kStep - 1) / kStep;
+        const int half = t.width >> 1;
+        const int c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
+        const bool wide = half > 64;
+        for (int k = 0; k < steps; ++k, ++it) {
+          const uint32_t st = it % kStages;
+          if (!mbar_wait(smem_addr(&s.empty[st]), ((it / kStages) & 1) ^ 1, dead)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = in_cta(smem_addr(&s.full[st]), 0);
+          const bool tail = kBColumns && (k + 1) * kStep > t.depth;  // the loaders' stage
+          const bool do_a = a.tma_a && !tail, do_b = a.tma_b && !tail;
+          uint32_t bytes = do_a ? kOperandBytes : 0;
+          if (do_b) bytes += kBColumns ? (half + 63) / 64 * (kStep * 128) : wide ? kOperandBytes : (half + kSmallBox - 1) / kSmallBox * (kSmallBox * 128);
+          if (bytes == 0) {
+            mbar_arrive_relaxed(bar);
+            continue;
+          }
+          mbar_arrive_tx(bar, bytes);
+          const uint32_t sa = smem_addr(stages + static_cast<size_t>(st) * kStageBytes), sb = sa + kOperandBytes;
+          if (do_a) {
+            if constexpr (!kAColumns) {
+              tma3(sa, &a.a[t.rank], k * kStep, m, t.expert, bar);
+            } else {
+              const int y = KIND == kProductGradInput ? k * kStep : t.lo + k * kStep;
+              const int z = KIND == kProductGradInput ? t.expert : 0;
+              tma3(sa, &a.a[t.rank], m, y, z, bar);
+              tma3(sa + kStep * 128, &a.a[t.rank], m + 64, y, z, bar);
+            }
+          }
+          if (do_b) {
+            if constexpr (kBColumns) {
+              for (int q = 0; q * 64 < half; ++q) tma3(sb + q * kStep * 128, &a.b[t.rank], c + q * 64, t.lo + k * kStep, 0, bar);
+            } else if (wide) {
+              tma3(sb, &a.b[t.rank], k * kStep, c, 0, bar);
+            } else {
+              for (int q = 0; q * kSmallBox < half; ++q)
+                tma3(sb + q * kSmallBox * 128, &a.b_small[t.rank], k * kStep, c + q * kSmallBox, 0, bar);
+            }
+          }
+        }
+      }
+      // every stage given back: no signal of the tensor core is on its way to
+      // a CTA that has left
+      for (uint32_t j = 0; ok && j < kStages; ++j, ++it)
+        ok = mbar_wait(smem_addr(&s.empty[it % kStages]), ((it / kStages) & 1) ^ 1, dead);
+      if (*dead) {  // copies in flight still write this CTA's shared memory
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1ll << 22)) {
+        }
+      }
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------------ MMA
+    if (cta == 0 && lane == 0) {
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (uint64_t i = pair; ok && i < tiles; i += pairs, ++n) {
+        const Tile t = tile_at<KIND>(a, s, groups, i, mt);
+        const int steps = (t.depth + kStep - 1) / kStep;
+        const uint32_t buf = n & 1;
+        if (!mbar_wait(smem_addr(&s.tmem_empty[buf]), ((n >> 1) & 1) ^ 1, dead)) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t d = tmem + buf * kTile;
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAColumns ? 1u << 15 : 0u) | (kBColumns ? 1u << 16 : 0u) |
+                               (static_cast<uint32_t>(t.width >> 3) << 17) | (16u << 24);
+        for (int k = 0; k < steps; ++k, ++it) {
+          const uint32_t st = it % kStages;
+          const uint32_t bar = smem_addr(&s.full[st]), parity = (it / kStages) & 1;
+          if (!(loaders ? mbar_wait<true>(bar, parity, dead) : mbar_wait(bar, parity, dead))) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t sa = smem_addr(stages + static_cast<size_t>(st) * kStageBytes), sb = sa + kOperandBytes;
+          const int parts = min(kStep, t.depth - k * kStep + 15) / 16;  // of 16 contraction elements
+          const uint64_t da = descriptor(sa, kAColumns ? kStep * 128 : 16), db = descriptor(sb, kBColumns ? kStep * 128 : 16);
+          for (int q = 0; q < parts; ++q)
+            mma(d, da + q * (kAColumns ? 2048 >> 4 : 32 >> 4), db + q * (kBColumns ? 2048 >> 4 : 32 >> 4), idesc, (k | q) != 0);
+          commit_pair(smem_addr(&s.empty[st]));
+        }
+        if (ok) commit_pair(smem_addr(&s.tmem_full[buf]));
+      }
+    }
+  } else if (warp >= 6) {
+    // -------------------------------------------------------------- loaders
+    if (loaders) {
+      const int ltid = tid - 6 * 32;
+      uint32_t it = 0;
+      bool ok = true;
+      for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+        const Tile t = tile_at<KIND>(a, s, groups, i, mt);
+        const int steps = (t.depth + kStep - 1) / kStep;
+        const int half = t.width >> 1;
+        const int64_t c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
+        const int64_t N = a.n, K = a.contract, rows = a.rows[t.rank];
+        const __nv_bfloat16* pa = static_cast<const __nv_bfloat16*>(a.pa[t.rank]);
+        const __nv_bfloat16* pb = static_cast<const __nv_bfloat16*>(a.pb[t.rank]);
+        for (int k = 0; k < steps; ++k, ++it) {
+          const uint32_t st = it % kStages;
+          const bool tail = kBColumns && (k + 1) * kStep > t.depth;
+          const bool do_a = !a.tma_a || tail, do_b = !a.tma_b || tail;
+          const bool here = mbar_wait(smem_addr(&s.empty[st]), ((it / kStages) & 1) ^ 1, dead);
+          const int left = t.depth - k * kStep;  // contraction elements from here
+          char* sa = stages + static_cast<size_t>(st) * kStageBytes;
+          char* sb = sa + kOperandBytes;
+          if (here && do_a) {
+            if constexpr (KIND == kProductForward) {
+              const __nv_bfloat16* w = pa + static_cast<int64_t>(t.expert) * N * K + k * kStep;
+              fill_lines(sa, 128, ltid, [&](int l) { return w + (m + l) * K; },
+                         [&](int l) { return m + l < N ? min(left, kStep) : 0; });
+            } else {
+              const __nv_bfloat16* w = KIND == kProductGradInput ? pa + (static_cast<int64_t>(t.expert) * N + k * kStep) * K
+                                                                 : pa + (static_cast<int64_t>(t.lo) + k * kStep) * K;
+              fill_lines(sa, 128, ltid, [&](int l) { return w + static_cast<int64_t>(l & 63) * K + m + (l & 64); },
+                         [&](int l) { return (l & 63) < left ? static_cast<int>(min(max(K - m - (l & 64), int64_t{0}), int64_t{64})) : 0; });
+            }
+          }
+          if (here && do_b) {
+            if constexpr (!kBColumns) {
+              const int64_t ld = KIND == kProductForward ? K : N;
+              const __nv_bfloat16* x = pb + c * ld + k * kStep;
+              fill_lines(sb, half, ltid, [&](int l) { return x + l * ld; },
+                         [&](int l) { return c + l < rows ? min(left, kStep) : 0; });
+            } else {
+              const __nv_bfloat16* d = pb + (static_cast<int64_t>(t.lo) + k * kStep) * N + c;
+              fill_lines(sb, (half + 63) / 64 * 64, ltid, [&](int l) { return d + static_cast<int64_t>(l & 63) * N + (l & 64); },
+                         [&](int l) { return (l & 63) < left ? static_cast<int>(min(max(N - c - (l & 64), int64_t{0}), int64_t{64})) : 0; });
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (any_loader(!here)) {  // one answer for all of them
+            ok = false;
+            break;
+          }
+          if (ltid == 0) mbar_arrive(in_cta(smem_addr(&s.full[st]), 0));
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- epilogue
+    uint32_t n = 0;
+    for (uint64_t i = pair; i < tiles; i += pairs, ++n) {
+      const Tile t = tile_at<KIND>(a, s, groups, i, mt);
+      const uint32_t buf = n & 1;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_full[buf]), (n >> 1) & 1, dead))) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t m = t.m0 + cta * 128 + warp * 32 + lane;
+      const uint64_t at = (KIND == kProductGradWeight ? static_cast<uint64_t>(t.expert) * a.n + t.c0 : static_cast<uint64_t>(t.c0)) * M + m;
+      constexpr int kBytes = Elem<OUT>::kBytes;
+      char* out = static_cast<char*>(a.out[t.rank]) + at * kBytes;
+      const uint32_t from = tmem + buf * kTile + (static_cast<uint32_t>(warp) << 21);  // lane = 32 * warp
+      for (int c = 0; c < t.width; c += 32) {
+        uint32_t v[32];
+        if (t.depth > 0) {
+          tmem_load32(from + c, v);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0;
+        }
+        if (m < M) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (c + j < t.cols) {
+              char* p = out + static_cast<uint64_t>(c + j) * M * kBytes;
+              if constexpr (OUT == kF32) *reinterpret_cast<uint32_t*>(p) = v[j];
+              else *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(__uint_as_float(v[j]));
+            }
+          }
+        }
+        __syncwarp();
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(in_cta(smem_addr(&s.tmem_empty[buf]), 0));
     }
   }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  // neither CTA leaves while the other may still signal its barriers
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (warp == 5) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns));
+  }
+}
+
+// ---------------------------------------------------------------- host side
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// A [depth][height][width] bf16 tensor in boxes of 64 elements x `box` lines.
+bool encode(CUtensorMap* map, const void* p, uint64_t width, uint64_t height, uint64_t depth, uint32_t box) {
+  const EncodeFn fn = encoder();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {width, height, depth};
+  const cuuint64_t strides[2] = {width * 2, width * height * 2};
+  const cuuint32_t boxes[3] = {kStep, box, 1}, ones[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, boxes, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether TMA can read rows of `width` bf16 elements at p.
+bool on_grid(const void* p, uint64_t width) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && width % 8 == 0; }
+
+template <int KIND, int OUT>
+cudaError_t launch_pairs(const PairArgs& a, uint64_t most_tiles, cudaStream_t s) {
+  // per host thread and device: the attribute belongs to the context
+  static thread_local int ready_dev = -1;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev != ready_dev) {
+    err = cudaFuncSetAttribute(product_kernel<KIND, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (err != cudaSuccess) return err;
+    ready_dev = dev;
+  }
+  uint64_t pairs = static_cast<uint64_t>(current_sm_count() / 2);
+  if (most_tiles < pairs) pairs = most_tiles;
+  if (pairs == 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kProductThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = CCL_PDL ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, product_kernel<KIND, OUT>, a);
+  if (err == cudaSuccess) note_launch();
+  return err;
 }
 
 }  // namespace
 
-cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& a, cudaStream_t s) {
-  uint64_t most = 0;
-  for (int r = 0; r < a.p; ++r) most = a.rows[r] > most ? a.rows[r] : most;
-  const uint64_t cols = kind == kProductForward ? a.n : a.contract;
-  const uint64_t gy = kind == kProductGradWeight ? a.num_experts * ((a.n + kTile - 1) / kTile) : (most + kTile - 1) / kTile + a.num_experts;
-  const dim3 grid(static_cast<unsigned>((cols + kTile - 1) / kTile), static_cast<unsigned>(gy), static_cast<unsigned>(a.p));
-  cudaError_t err = kind == kProductForward     ? launch_kernel(product_simple_kernel<kProductForward, kBF16>, grid, dim3(kThreads), s, a)
-                    : kind == kProductGradInput ? launch_kernel(product_simple_kernel<kProductGradInput, kBF16>, grid, dim3(kThreads), s, a)
-                    : out_dt == kF32            ? launch_kernel(product_simple_kernel<kProductGradWeight, kF32>, grid, dim3(kThreads), s, a)
-                                                : launch_kernel(product_simple_kernel<kProductGradWeight, kBF16>, grid, dim3(kThreads), s, a);
-  if (err == cudaSuccess) note_launch();
+cudaError_t read_product_error(unsigned int* flag, bool clear) {
+  cudaError_t err = cudaMemcpyFromSymbol(flag, g_product_error, sizeof(unsigned int));
+  if (err == cudaSuccess && clear && *flag != 0) {
+    const unsigned int zero = 0;
+    err = cudaMemcpyToSymbol(g_product_error, &zero, sizeof(zero));
+  }
   return err;
+}
+
+cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& args, cudaStream_t s) {
+  const int E = args.num_experts;
+  const int most_ranks = kMaxGroups / E < kLaunchRanks ? kMaxGroups / E : kLaunchRanks;
+  const uint64_t n = args.n, k = args.contract;
+  for (int r0 = 0; r0 < args.p; r0 += most_ranks) {
+    PairArgs a = {};
+    a.p = args.p - r0 < most_ranks ? args.p - r0 : most_ranks;
+    a.num_experts = E;
+    a.n = static_cast<uint32_t>(n);
+    a.contract = static_cast<uint32_t>(k);
+    const uint64_t a_width = k, b_width = kind == kProductForward ? k : n;
+    a.tma_a = a.tma_b = 1;
+    uint64_t rows = 0;
+    for (int i = 0; i < a.p; ++i) {
+      a.pa[i] = args.a[r0 + i];
+      a.pb[i] = args.b[r0 + i];
+      a.out[i] = args.out[r0 + i];
+      a.offsets[i] = args.offsets[r0 + i];
+      a.rows[i] = args.rows[r0 + i];
+      rows += (a.rows[i] + kTile - 1) / kTile + (a.rows[i] != 0 ? E : 0);
+      if (a.rows[i] == 0) continue;
+      a.tma_a = a.tma_a && on_grid(a.pa[i], a_width);
+      a.tma_b = a.tma_b && on_grid(a.pb[i], b_width);
+    }
+    for (int i = 0; i < a.p; ++i) {
+      if (a.rows[i] == 0) continue;
+      bool ok = true;
+      if (a.tma_a) {
+        ok = kind == kProductForward     ? encode(&a.a[i], a.pa[i], k, n, E, 128)
+             : kind == kProductGradInput ? encode(&a.a[i], a.pa[i], k, n, E, kStep)
+                                         : encode(&a.a[i], a.pa[i], k, a.rows[i], 1, kStep);
+      }
+      if (ok && a.tma_b) {
+        ok = kind == kProductGradWeight ? encode(&a.b[i], a.pb[i], n, a.rows[i], 1, kStep)
+                                        : encode(&a.b[i], a.pb[i], b_width, a.rows[i], 1, 128) &&
+                                              encode(&a.b_small[i], a.pb[i], b_width, a.rows[i], 1, kSmallBox);
+      }
+      if (!ok) return cudaErrorInvalidValue;
+    }
+    const uint64_t mt = ((kind == kProductForward ? n : k) + kTile - 1) / kTile;
+    const uint64_t most_tiles = (kind == kProductGradWeight ? static_cast<uint64_t>(a.p) * E * ((n + kTile - 1) / kTile) : rows) * mt;
+    const cudaError_t err = kind == kProductForward     ? launch_pairs<kProductForward, kBF16>(a, most_tiles, s)
+                            : kind == kProductGradInput ? launch_pairs<kProductGradInput, kBF16>(a, most_tiles, s)
+                            : out_dt == kF32            ? launch_pairs<kProductGradWeight, kF32>(a, most_tiles, s)
+                                                        : launch_pairs<kProductGradWeight, kBF16>(a, most_tiles, s);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace ccl
