@@ -19,7 +19,7 @@
 //        columns) against the next tile's products
 //   4    TMA: one thread issues the stage's bulk tensor copies
 //   5    MMA: one thread of the even CTA issues for the pair
-//   6-9  loaders: what TMA cannot do -- operands that do not sit on 16 bytes,
+//   6-13 loaders: what TMA cannot do -- operands that do not sit on 16 bytes,
 //        and grad_weight's last rows, which must read as zero where the next
 //        expert begins -- by whole 16-byte loads, shifted and masked
 // Every wait is bounded: one that runs out sets the device error word.
@@ -38,8 +38,8 @@ constexpr int kOperandBytes = 128 * kStep * 2;  // one CTA's share of A or B in 
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMaxGroups = 2048;   // (rank, expert) pairs per launch
 constexpr int kLaunchRanks = 8;    // keeps the parameter block under 4 KB
-constexpr int kProductThreads = 320;
-constexpr int kLoaderThreads = 128;
+constexpr int kLoaderThreads = 256;
+constexpr int kProductThreads = 192 + kLoaderThreads;
 constexpr int kSmallBox = 16;      // rows of B's small box
 constexpr uint32_t kTmemColumns = 512;
 constexpr long long kWaitCycles = 1ll << 32;  // two seconds
@@ -62,6 +62,7 @@ static_assert(sizeof(PairArgs) <= 4096, "product parameters exceed 4 KB");
 struct Shared {
   alignas(8) uint64_t full[kStages];
   uint64_t empty[kStages];
+  uint64_t go[kStages];  // the TMA thread to the loaders: the stage is free and theirs to fill
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint32_t tmem;
@@ -98,6 +99,9 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_bar) {
 __device__ __forceinline__ void mbar_arrive_tx(uint32_t cluster_bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
                : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_own(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
@@ -248,14 +252,25 @@ __device__ __forceinline__ bool any_loader(bool x) {
   return r != 0;
 }
 
-// Fills `lines` lines of 64 elements (8 swizzled units each): line l starts at
-// base + l * ld and holds valid(l) elements.
+// Fills `lines` lines (a multiple of 16) of 64 elements, 8 swizzled units
+// each: line l starts at start(l) and holds valid(l) elements.  A thread's
+// loads are issued kBatch units at a time before any is stored.
 template <typename Start, typename Valid>
 __device__ __forceinline__ void fill_lines(char* dst, int lines, int tid, Start start, Valid valid) {
-  for (int i = tid; i < lines * 8; i += kLoaderThreads) {
-    const int l = i >> 3, u = i & 7;
-    const uint4 v = load_unit(start(l) + u * 8, min(valid(l) - u * 8, 8));
-    *reinterpret_cast<uint4*>(dst + l * 128 + ((u ^ (l & 7)) << 4)) = v;
+  constexpr int kBatch = 4;
+  const int u = tid & 7;  // kLoaderThreads is a multiple of 8: a thread keeps its unit of the line
+  for (int l0 = tid >> 3; l0 < lines; l0 += kBatch * (kLoaderThreads / 8)) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int l = l0 + b * (kLoaderThreads / 8);
+      v[b] = load_unit(start(l) + u * 8, l < lines ? min(valid(l) - u * 8, 8) : 0);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int l = l0 + b * (kLoaderThreads / 8);
+      if (l < lines) *reinterpret_cast<uint4*>(dst + l * 128 + ((u ^ (l & 7)) << 4)) = v[b];
+    }
   }
 }
 
@@ -280,6 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&s.full[i]), loaders ? 4 : 2);  // from both CTAs: the TMA thread, the loaders
       mbar_init(smem_addr(&s.empty[i]), 1);
+      mbar_init(smem_addr(&s.go[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&s.tmem_full[i]), 1);
@@ -359,6 +375,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
           const bool do_a = a.tma_a && !tail, do_b = a.tma_b && !tail;
           uint32_t bytes = do_a ? kOperandBytes : 0;
           if (do_b) bytes += kBColumns ? (half + 63) / 64 * (kStep * 128) : wide ? kOperandBytes : (half + kSmallBox - 1) / kSmallBox * (kSmallBox * 128);
+          if (loaders) {
+            if (do_a && do_b) mbar_arrive_relaxed(bar);  // in the loaders' place
+            else mbar_arrive_own(smem_addr(&s.go[st]));
+          }
           if (bytes == 0) {
             mbar_arrive_relaxed(bar);
             continue;
@@ -414,7 +434,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         for (int k = 0; k < steps; ++k, ++it) {
           const uint32_t st = it % kStages;
           const uint32_t bar = smem_addr(&s.full[st]), parity = (it / kStages) & 1;
-          if (!(loaders ? mbar_wait<true>(bar, parity, dead) : mbar_wait(bar, parity, dead))) {
+          const bool loaded = !a.tma_a || !a.tma_b || (kBColumns && (k + 1) * kStep > t.depth);
+          if (!(loaded ? mbar_wait<true>(bar, parity, dead) : mbar_wait(bar, parity, dead))) {
             ok = false;
             break;
           }
@@ -434,6 +455,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     if (loaders) {
       const int ltid = tid - 6 * 32;
       uint32_t it = 0;
+      // parity of each stage's next `go`.  The loaders skip stages, so they
+      // could not follow `empty` by its parity: several of its phases may pass
+      // between two of theirs, while `go` moves on only once they have filled.
+      uint32_t parity = 0;
       bool ok = true;
       for (uint64_t i = pair; ok && i < tiles; i += pairs) {
         const Tile t = tile_at<KIND>(a, s, groups, i, mt);
@@ -447,7 +472,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
           const uint32_t st = it % kStages;
           const bool tail = kBColumns && (k + 1) * kStep > t.depth;
           const bool do_a = !a.tma_a || tail, do_b = !a.tma_b || tail;
-          const bool here = mbar_wait(smem_addr(&s.empty[st]), ((it / kStages) & 1) ^ 1, dead);
+          if (!do_a && !do_b) continue;
+          const bool here = mbar_wait(smem_addr(&s.go[st]), (parity >> st) & 1, dead);
+          parity ^= 1u << st;
           const int left = t.depth - k * kStep;  // contraction elements from here
           char* sa = stages + static_cast<size_t>(st) * kStageBytes;
           char* sb = sa + kOperandBytes;

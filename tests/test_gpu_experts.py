@@ -234,7 +234,8 @@ def test_gates_gradient_against_differences(lib):
 # ends and between, single rows, widths off every grid, deep and wide
 PRODUCTS = [([1], 1, 1), ([0, 3, 0], 8, 16), ([5, 0, 130, 1, 64], 72, 200), ([128, 128], 128, 128), ([300], 264, 520),
             ([7, 250, 33, 0], 77, 131), ([129, 1, 127], 384, 64), ([17] * 9, 136, 1032), ([0, 0], 64, 64),
-            ([1] * 40, 256, 512), ([1000, 24], 512, 256), ([2, 515], 1024, 2056), ([64, 200], 130, 66)]
+            ([1] * 40, 256, 512), ([1000, 24], 512, 256), ([2, 515], 1024, 2056), ([64, 200], 130, 66),
+            ([1400, 70, 1000, 3, 641, 129], 1288, 1544), ([833, 65, 1090], 1281, 1403)]
 
 
 def product_inputs(rng, counts, n, k, whole):
