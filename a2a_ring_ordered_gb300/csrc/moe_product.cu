@@ -90,18 +90,11 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// The TMA thread has written nothing itself: its arrivals order nothing.  (A
-// release at cluster scope waits for all of the thread's memory operations,
-// which held every stage back by a microsecond.)
-__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+__device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_tx(uint32_t cluster_bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_own(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mbar_arrive_own(uint32_t bar, uint32_t count = 1) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
@@ -173,6 +166,24 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int x
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
       : "memory");
 }
+
+// One lane of the warp, the same for every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
+}
+
+// A place in the ring of stages and the parity of the pass over it.
+struct Ring {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 // -------------------------------------------------------------------- tiles
 struct Tile {
@@ -293,7 +304,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(&s.full[i]), loaders ? 4 : 2);  // from both CTAs: the TMA thread, the loaders
+      // of the even CTA: its TMA thread, and both CTAs' loaders
+      mbar_init(smem_addr(&s.full[i]), loaders ? 3 : 1);
       mbar_init(smem_addr(&s.empty[i]), 1);
       mbar_init(smem_addr(&s.go[i]), 1);
     }
@@ -355,106 +367,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 
   if (warp == 4) {
     // ------------------------------------------------------------------ TMA
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (uint64_t i = pair; ok && i < tiles; i += pairs) {
-        const Tile t = tile_at<KIND>(a, s, groups, i, mt);
-        const int steps = (t.depth + kStep - 1) / kStep;
-        const int half = t.width >> 1;
-        const int c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
-        const bool wide = half > 64;
-        for (int k = 0; k < steps; ++k, ++it) {
-          const uint32_t st = it % kStages;
-          if (!mbar_wait(smem_addr(&s.empty[st]), ((it / kStages) & 1) ^ 1, dead)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = in_cta(smem_addr(&s.full[st]), 0);
-          const bool tail = kBColumns && (k + 1) * kStep > t.depth;  // the loaders' stage
+    // The whole warp walks the stages, so that addresses and coordinates are
+    // uniform; one lane issues.
+    const bool issuer = elect_one();
+    Ring ring;
+    const uint32_t even = in_cta(smem_addr(s.full), 0);
+    const uint32_t own = smem_addr(s.full), empty = smem_addr(s.empty), data = smem_addr(stages);
+    bool ok = true;
+    for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+      const Tile t = tile_at<KIND>(a, s, groups, i, mt);
+      const int half = t.width >> 1;
+      const int c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
+      const int boxes = kBColumns ? (half + 63) / 64 : half > 64 ? 1 : (half + kSmallBox - 1) / kSmallBox;
+      const uint32_t box_bytes = kBColumns ? kStep * 128 : half > 64 ? kOperandBytes : kSmallBox * 128;
+      const CUtensorMap* map_a = &a.a[t.rank];
+      const CUtensorMap* map_b = !kBColumns && half <= 64 ? &a.b_small[t.rank] : &a.b[t.rank];
+      const int z = KIND == kProductGradWeight ? 0 : t.expert;
+      for (int k = 0; k < t.depth; k += kStep) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead))) {
+          ok = false;
+          break;
+        }
+        if (issuer) {
+          // the even CTA's barrier counts both CTAs' copies; its own TMA
+          // thread alone arrives, for the bytes of both
+          const uint32_t bar = even + 8 * ring.stage;
+          const bool tail = kBColumns && k + kStep > t.depth;  // the loaders' stage
           const bool do_a = a.tma_a && !tail, do_b = a.tma_b && !tail;
-          uint32_t bytes = do_a ? kOperandBytes : 0;
-          if (do_b) bytes += kBColumns ? (half + 63) / 64 * (kStep * 128) : wide ? kOperandBytes : (half + kSmallBox - 1) / kSmallBox * (kSmallBox * 128);
-          if (loaders) {
-            if (do_a && do_b) mbar_arrive_relaxed(bar);  // in the loaders' place
-            else mbar_arrive_own(smem_addr(&s.go[st]));
+          if (loaders && !(do_a && do_b)) mbar_arrive_own(smem_addr(&s.go[ring.stage]));
+          if (cta == 0) {
+            if (loaders && do_a && do_b) mbar_arrive_own(own + 8 * ring.stage, 2);  // in the loaders' place
+            mbar_arrive_tx(own + 8 * ring.stage, 2 * ((do_a ? kOperandBytes : 0) + (do_b ? boxes * box_bytes : 0)));
           }
-          if (bytes == 0) {
-            mbar_arrive_relaxed(bar);
-            continue;
-          }
-          mbar_arrive_tx(bar, bytes);
-          const uint32_t sa = smem_addr(stages + static_cast<size_t>(st) * kStageBytes), sb = sa + kOperandBytes;
+          const uint32_t sa = data + ring.stage * kStageBytes, sb = sa + kOperandBytes;
           if (do_a) {
             if constexpr (!kAColumns) {
-              tma3(sa, &a.a[t.rank], k * kStep, m, t.expert, bar);
+              tma3(sa, map_a, k, m, z, bar);
             } else {
-              const int y = KIND == kProductGradInput ? k * kStep : t.lo + k * kStep;
-              const int z = KIND == kProductGradInput ? t.expert : 0;
-              tma3(sa, &a.a[t.rank], m, y, z, bar);
-              tma3(sa + kStep * 128, &a.a[t.rank], m + 64, y, z, bar);
+              const int y = KIND == kProductGradInput ? k : t.lo + k;
+              tma3(sa, map_a, m, y, z, bar);
+              tma3(sa + kStep * 128, map_a, m + 64, y, z, bar);
             }
           }
           if (do_b) {
             if constexpr (kBColumns) {
-              for (int q = 0; q * 64 < half; ++q) tma3(sb + q * kStep * 128, &a.b[t.rank], c + q * 64, t.lo + k * kStep, 0, bar);
-            } else if (wide) {
-              tma3(sb, &a.b[t.rank], k * kStep, c, 0, bar);
+              tma3(sb, map_b, c, t.lo + k, 0, bar);
+              if (boxes > 1) tma3(sb + kStep * 128, map_b, c + 64, t.lo + k, 0, bar);
             } else {
-              for (int q = 0; q * kSmallBox < half; ++q)
-                tma3(sb + q * kSmallBox * 128, &a.b_small[t.rank], k * kStep, c + q * kSmallBox, 0, bar);
+              tma3(sb, map_b, k, c, 0, bar);
+              for (int q = 1; q < boxes; ++q) tma3(sb + q * kSmallBox * 128, map_b, k, c + q * kSmallBox, 0, bar);
             }
           }
         }
+        ring.next();
       }
-      // every stage given back: no signal of the tensor core is on its way to
-      // a CTA that has left
-      for (uint32_t j = 0; ok && j < kStages; ++j, ++it)
-        ok = mbar_wait(smem_addr(&s.empty[it % kStages]), ((it / kStages) & 1) ^ 1, dead);
-      if (*dead) {  // copies in flight still write this CTA's shared memory
-        const long long t0 = clock64();
-        while (clock64() - t0 < (1ll << 22)) {
-        }
+    }
+    // every stage given back: no signal of the tensor core is on its way to a
+    // CTA that has left
+    for (int j = 0; ok && j < kStages; ++j, ring.next())
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead));
+    if (!ok) {  // copies in flight still write this CTA's shared memory
+      const long long t0 = clock64();
+      while (clock64() - t0 < (1ll << 22)) {
       }
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------------ MMA
-    if (cta == 0 && lane == 0) {
-      uint32_t it = 0, n = 0;
+    if (cta == 0) {
+      const bool issuer = elect_one();
+      Ring ring;
+      uint32_t n = 0;
+      const uint32_t full = smem_addr(s.full), empty = smem_addr(s.empty);
+      // descriptors of stage 0; a stage, and 16 contraction elements, further on
+      const uint64_t a0 = descriptor(smem_addr(stages), kAColumns ? kStep * 128 : 16);
+      const uint64_t b0 = descriptor(smem_addr(stages) + kOperandBytes, kBColumns ? kStep * 128 : 16);
+      constexpr uint64_t kNextA = (kAColumns ? 2048 : 32) >> 4, kNextB = (kBColumns ? 2048 : 32) >> 4;
       bool ok = true;
       for (uint64_t i = pair; ok && i < tiles; i += pairs, ++n) {
         const Tile t = tile_at<KIND>(a, s, groups, i, mt);
-        const int steps = (t.depth + kStep - 1) / kStep;
         const uint32_t buf = n & 1;
-        if (!mbar_wait(smem_addr(&s.tmem_empty[buf]), ((n >> 1) & 1) ^ 1, dead)) break;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_empty[buf]), ((n >> 1) & 1) ^ 1, dead))) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t d = tmem + buf * kTile;
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAColumns ? 1u << 15 : 0u) | (kBColumns ? 1u << 16 : 0u) |
                                (static_cast<uint32_t>(t.width >> 3) << 17) | (16u << 24);
-        for (int k = 0; k < steps; ++k, ++it) {
-          const uint32_t st = it % kStages;
-          const uint32_t bar = smem_addr(&s.full[st]), parity = (it / kStages) & 1;
-          const bool loaded = !a.tma_a || !a.tma_b || (kBColumns && (k + 1) * kStep > t.depth);
-          if (!(loaded ? mbar_wait<true>(bar, parity, dead) : mbar_wait(bar, parity, dead))) {
+        for (int k = 0; k < t.depth; k += kStep) {
+          const bool loaded = !a.tma_a || !a.tma_b || (kBColumns && k + kStep > t.depth);
+          const uint32_t bar = full + 8 * ring.stage;
+          if (!__all_sync(0xFFFFFFFFu, loaded ? mbar_wait<true>(bar, ring.phase, dead) : mbar_wait(bar, ring.phase, dead))) {
             ok = false;
             break;
           }
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t sa = smem_addr(stages + static_cast<size_t>(st) * kStageBytes), sb = sa + kOperandBytes;
-          const int parts = min(kStep, t.depth - k * kStep + 15) / 16;  // of 16 contraction elements
-          const uint64_t da = descriptor(sa, kAColumns ? kStep * 128 : 16), db = descriptor(sb, kBColumns ? kStep * 128 : 16);
-          for (int q = 0; q < parts; ++q)
-            mma(d, da + q * (kAColumns ? 2048 >> 4 : 32 >> 4), db + q * (kBColumns ? 2048 >> 4 : 32 >> 4), idesc, (k | q) != 0);
-          commit_pair(smem_addr(&s.empty[st]));
+          if (issuer) {
+            const uint64_t da = a0 + ring.stage * (kStageBytes >> 4), db = b0 + ring.stage * (kStageBytes >> 4);
+            const int left = t.depth - k;  // contraction elements from here
+            mma(d, da, db, idesc, k != 0);
+            if (left > 16) mma(d, da + kNextA, db + kNextB, idesc, 1);
+            if (left > 32) mma(d, da + 2 * kNextA, db + 2 * kNextB, idesc, 1);
+            if (left > 48) mma(d, da + 3 * kNextA, db + 3 * kNextB, idesc, 1);
+            commit_pair(empty + 8 * ring.stage);
+          }
+          ring.next();
         }
-        if (ok) commit_pair(smem_addr(&s.tmem_full[buf]));
+        if (ok && issuer) commit_pair(smem_addr(&s.tmem_full[buf]));
+        __syncwarp();
       }
     }
   } else if (warp >= 6) {
     // -------------------------------------------------------------- loaders
     if (loaders) {
       const int ltid = tid - 6 * 32;
-      uint32_t it = 0;
+      Ring ring;
       // parity of each stage's next `go`.  The loaders skip stages, so they
       // could not follow `empty` by its parity: several of its phases may pass
       // between two of theirs, while `go` moves on only once they have filled.
@@ -462,30 +486,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
       bool ok = true;
       for (uint64_t i = pair; ok && i < tiles; i += pairs) {
         const Tile t = tile_at<KIND>(a, s, groups, i, mt);
-        const int steps = (t.depth + kStep - 1) / kStep;
         const int half = t.width >> 1;
         const int64_t c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
         const int64_t N = a.n, K = a.contract, rows = a.rows[t.rank];
         const __nv_bfloat16* pa = static_cast<const __nv_bfloat16*>(a.pa[t.rank]);
         const __nv_bfloat16* pb = static_cast<const __nv_bfloat16*>(a.pb[t.rank]);
-        for (int k = 0; k < steps; ++k, ++it) {
-          const uint32_t st = it % kStages;
-          const bool tail = kBColumns && (k + 1) * kStep > t.depth;
+        for (int k = 0; k < t.depth; k += kStep, ring.next()) {
+          const uint32_t st = ring.stage;
+          const bool tail = kBColumns && k + kStep > t.depth;
           const bool do_a = !a.tma_a || tail, do_b = !a.tma_b || tail;
           if (!do_a && !do_b) continue;
           const bool here = mbar_wait(smem_addr(&s.go[st]), (parity >> st) & 1, dead);
           parity ^= 1u << st;
-          const int left = t.depth - k * kStep;  // contraction elements from here
+          const int left = t.depth - k;  // contraction elements from here
           char* sa = stages + static_cast<size_t>(st) * kStageBytes;
           char* sb = sa + kOperandBytes;
           if (here && do_a) {
             if constexpr (KIND == kProductForward) {
-              const __nv_bfloat16* w = pa + static_cast<int64_t>(t.expert) * N * K + k * kStep;
+              const __nv_bfloat16* w = pa + static_cast<int64_t>(t.expert) * N * K + k;
               fill_lines(sa, 128, ltid, [&](int l) { return w + (m + l) * K; },
                          [&](int l) { return m + l < N ? min(left, kStep) : 0; });
             } else {
-              const __nv_bfloat16* w = KIND == kProductGradInput ? pa + (static_cast<int64_t>(t.expert) * N + k * kStep) * K
-                                                                 : pa + (static_cast<int64_t>(t.lo) + k * kStep) * K;
+              const __nv_bfloat16* w = KIND == kProductGradInput ? pa + (static_cast<int64_t>(t.expert) * N + k) * K
+                                                                 : pa + (static_cast<int64_t>(t.lo) + k) * K;
               fill_lines(sa, 128, ltid, [&](int l) { return w + static_cast<int64_t>(l & 63) * K + m + (l & 64); },
                          [&](int l) { return (l & 63) < left ? static_cast<int>(min(max(K - m - (l & 64), int64_t{0}), int64_t{64})) : 0; });
             }
@@ -493,11 +516,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
           if (here && do_b) {
             if constexpr (!kBColumns) {
               const int64_t ld = KIND == kProductForward ? K : N;
-              const __nv_bfloat16* x = pb + c * ld + k * kStep;
+              const __nv_bfloat16* x = pb + c * ld + k;
               fill_lines(sb, half, ltid, [&](int l) { return x + l * ld; },
                          [&](int l) { return c + l < rows ? min(left, kStep) : 0; });
             } else {
-              const __nv_bfloat16* d = pb + (static_cast<int64_t>(t.lo) + k * kStep) * N + c;
+              const __nv_bfloat16* d = pb + (static_cast<int64_t>(t.lo) + k) * N + c;
               fill_lines(sb, (half + 63) / 64 * 64, ltid, [&](int l) { return d + static_cast<int64_t>(l & 63) * N + (l & 64); },
                          [&](int l) { return (l & 63) < left ? static_cast<int>(min(max(N - c - (l & 64), int64_t{0}), int64_t{64})) : 0; });
             }
