@@ -26,7 +26,6 @@
 #include <cuda.h>  // CUtensorMap and its enums; nothing links the driver
 
 #include "device_common.cuh"
-#include "realign.cuh"
 
 namespace ccl {
 namespace {
@@ -62,7 +61,7 @@ static_assert(sizeof(PairArgs) <= 4096, "product parameters exceed 4 KB");
 struct Shared {
   alignas(8) uint64_t full[kStages];
   uint64_t empty[kStages];
-  uint64_t go[kStages];  // the TMA thread to the loaders: the stage is free and theirs to fill
+  uint64_t go[kStages];  // to the loaders: the stage is free to fill, or its last rows have landed
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint32_t tmem;
@@ -231,24 +230,35 @@ __device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int 
 }
 
 // ------------------------------------------------------------------ loaders
-// Up to 8 elements at p, zero behind them, by whole 16-byte granules that hold
-// at least one of them.
-__device__ __forceinline__ uint4 load_unit(const __nv_bfloat16* p, int valid) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (valid <= 0) return v;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p), base = at & ~static_cast<uintptr_t>(15);
-  const int delta = static_cast<int>(at - base);
-  const uint4 g0 = __ldg(reinterpret_cast<const uint4*>(base));
-  uint4 g1 = make_uint4(0, 0, 0, 0);
-  if (delta + 2 * valid > 16) g1 = __ldg(reinterpret_cast<const uint4*>(base + 16));
-  v = delta == 0 ? g0 : realign16(g0, g1, delta);
-  if (valid < 8) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < valid ? w[i] : 2 * i < valid ? (w[i] & 0xFFFFu) : 0u;
-    v = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+// The 16 bytes at p, or zeros.
+__device__ __forceinline__ uint4 load16_if(uintptr_t p, bool take) {
+  uint4 v;
+  asm("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
+      " @p ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(static_cast<uint32_t>(take)));
   return v;
+}
+
+// Bytes [at % 16, at % 16 + 16) of the pair (lo, hi), of which the first
+// `valid` bf16 elements are kept and the others are zero.
+__device__ __forceinline__ uint4 shift_unit(const uint4 lo, const uint4 hi, uint32_t at, int valid) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (at & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (at & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] = __funnelshift_r(w[i], w[i + 1], (at & 2) * 8);
+    o[i] = 2 * i + 1 < valid ? o[i] : 2 * i < valid ? (o[i] & 0xFFFFu) : 0u;
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // A barrier among the loaders, and whether any of them says so.
@@ -263,26 +273,40 @@ __device__ __forceinline__ bool any_loader(bool x) {
   return r != 0;
 }
 
-// Fills `lines` lines (a multiple of 16) of 64 elements, 8 swizzled units
-// each: line l starts at start(l) and holds valid(l) elements.  A thread's
-// loads are issued kBatch units at a time before any is stored.
-template <typename Start, typename Valid>
-__device__ __forceinline__ void fill_lines(char* dst, int lines, int tid, Start start, Valid valid) {
-  constexpr int kBatch = 4;
-  const int u = tid & 7;  // kLoaderThreads is a multiple of 8: a thread keeps its unit of the line
-  for (int l0 = tid >> 3; l0 < lines; l0 += kBatch * (kLoaderThreads / 8)) {
-    uint4 v[kBatch];
+// Fills lines [lo, hi) of a stage, 8 swizzled units of 8 elements each;
+// unit(l, u, p) says how many elements of a unit there are and points p at
+// them.  They come as the whole 16-byte granules that hold at least one of
+// them, kBatch units' loads issued before any is stored.
+template <typename Unit>
+__device__ __forceinline__ void fill_lines(char* dst, int lo, int hi, int tid, Unit unit) {
+  constexpr int kBatch = 4, kApart = kLoaderThreads / 8;
+  const int u = tid & 7;
+  for (int l0 = lo + (tid >> 3); l0 < hi; l0 += kBatch * kApart) {
+    uint4 g0[kBatch], g1[kBatch];
+    uint32_t at[kBatch];
+    int valid[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int l = l0 + b * (kLoaderThreads / 8);
-      v[b] = load_unit(start(l) + u * 8, l < lines ? min(valid(l) - u * 8, 8) : 0);
+      const __nv_bfloat16* p;
+      valid[b] = unit(l0 + b * kApart, u, p);
+      if (l0 + b * kApart >= hi) valid[b] = 0;
+      const uintptr_t from = reinterpret_cast<uintptr_t>(p), base = from & ~static_cast<uintptr_t>(15);
+      at[b] = static_cast<uint32_t>(from - base);
+      g0[b] = load16_if(base, valid[b] > 0);
+      g1[b] = load16_if(base + 16, valid[b] > 0 && at[b] + 2 * valid[b] > 16);
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int l = l0 + b * (kLoaderThreads / 8);
-      if (l < lines) *reinterpret_cast<uint4*>(dst + l * 128 + ((u ^ (l & 7)) << 4)) = v[b];
+      const int l = l0 + b * kApart;
+      if (l < hi) *reinterpret_cast<uint4*>(dst + l * 128 + ((u ^ (l & 7)) << 4)) = shift_unit(g0[b], g1[b], at[b], valid[b]);
     }
   }
+}
+
+// Zeros in the lines of contraction rows from `left` on: line l holds row l mod 64.
+__device__ __forceinline__ void clear_lines(char* dst, int lines, int left, int tid) {
+  for (int i = tid; i < lines * 8; i += kLoaderThreads)
+    if (((i >> 3) & 63) >= left) *reinterpret_cast<uint4*>(dst + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
 // ------------------------------------------------------------------- kernel
@@ -391,14 +415,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         if (issuer) {
           // the even CTA's barrier counts both CTAs' copies; its own TMA
           // thread alone arrives, for the bytes of both
-          const uint32_t bar = even + 8 * ring.stage;
-          const bool tail = kBColumns && k + kStep > t.depth;  // the loaders' stage
-          const bool do_a = a.tma_a && !tail, do_b = a.tma_b && !tail;
-          if (loaders && !(do_a && do_b)) mbar_arrive_own(smem_addr(&s.go[ring.stage]));
+          uint32_t bar = even + 8 * ring.stage;
+          const bool tail = kBColumns && k + kStep > t.depth;
+          const bool do_a = a.tma_a, do_b = a.tma_b;
+          const uint32_t bytes = (do_a ? kOperandBytes : 0) + (do_b ? boxes * box_bytes : 0);
+          const bool loaded = tail || !do_a || !do_b;  // the loaders have a part in the stage
+          const uint32_t go = smem_addr(&s.go[ring.stage]);
+          if (loaded) mbar_arrive_tx(go, tail ? bytes : 0);
           if (cta == 0) {
-            if (loaders && do_a && do_b) mbar_arrive_own(own + 8 * ring.stage, 2);  // in the loaders' place
-            mbar_arrive_tx(own + 8 * ring.stage, 2 * ((do_a ? kOperandBytes : 0) + (do_b ? boxes * box_bytes : 0)));
+            if (loaders && !loaded) mbar_arrive_own(own + 8 * ring.stage, 2);  // in the loaders' place
+            mbar_arrive_tx(own + 8 * ring.stage, tail ? 0 : 2 * bytes);
           }
+          if (tail) bar = go;  // the loaders clear what lies behind the last row
           const uint32_t sa = data + ring.stage * kStageBytes, sb = sa + kOperandBytes;
           if (do_a) {
             if constexpr (!kAColumns) {
@@ -494,35 +522,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         for (int k = 0; k < t.depth; k += kStep, ring.next()) {
           const uint32_t st = ring.stage;
           const bool tail = kBColumns && k + kStep > t.depth;
-          const bool do_a = !a.tma_a || tail, do_b = !a.tma_b || tail;
-          if (!do_a && !do_b) continue;
+          if (a.tma_a && a.tma_b && !tail) continue;
           const bool here = mbar_wait(smem_addr(&s.go[st]), (parity >> st) & 1, dead);
           parity ^= 1u << st;
           const int left = t.depth - k;  // contraction elements from here
           char* sa = stages + static_cast<size_t>(st) * kStageBytes;
           char* sb = sa + kOperandBytes;
-          if (here && do_a) {
-            if constexpr (KIND == kProductForward) {
-              const __nv_bfloat16* w = pa + static_cast<int64_t>(t.expert) * N * K + k;
-              fill_lines(sa, 128, ltid, [&](int l) { return w + (m + l) * K; },
-                         [&](int l) { return m + l < N ? min(left, kStep) : 0; });
+          // lines of the stage: A's 128, then B's; each is 64 elements, `valid` of which are in the product
+          const int lines_b = kBColumns ? (half + 63) & ~63 : half;
+          const int l_lo = a.tma_a ? 128 : 0, l_hi = a.tma_b ? 128 : 128 + lines_b;
+          const auto unit = [&](int l, int u, const __nv_bfloat16*& p) {  // elements of unit u of line l, and where
+            int valid;
+            if (l < 128) {
+              if constexpr (KIND == kProductForward) {
+                p = pa + (static_cast<int64_t>(t.expert) * N + m + l) * K + k;
+                valid = m + l < N ? left : 0;
+              } else {
+                const int64_t row = KIND == kProductGradInput ? static_cast<int64_t>(t.expert) * N + k : static_cast<int64_t>(t.lo) + k;
+                p = pa + (row + (l & 63)) * K + m + (l & 64);
+                valid = (l & 63) < left ? static_cast<int>(min(K - m - (l & 64), int64_t{64})) : 0;
+              }
             } else {
-              const __nv_bfloat16* w = KIND == kProductGradInput ? pa + (static_cast<int64_t>(t.expert) * N + k) * K
-                                                                 : pa + (static_cast<int64_t>(t.lo) + k) * K;
-              fill_lines(sa, 128, ltid, [&](int l) { return w + static_cast<int64_t>(l & 63) * K + m + (l & 64); },
-                         [&](int l) { return (l & 63) < left ? static_cast<int>(min(max(K - m - (l & 64), int64_t{0}), int64_t{64})) : 0; });
+              l -= 128;
+              if constexpr (kBColumns) {
+                p = pb + (static_cast<int64_t>(t.lo) + k + (l & 63)) * N + c + (l & 64);
+                valid = (l & 63) < left ? static_cast<int>(min(N - c - (l & 64), int64_t{64})) : 0;
+              } else {
+                p = pb + (c + l) * (KIND == kProductForward ? K : N) + k;
+                valid = c + l < rows ? left : 0;
+              }
             }
-          }
-          if (here && do_b) {
-            if constexpr (!kBColumns) {
-              const int64_t ld = KIND == kProductForward ? K : N;
-              const __nv_bfloat16* x = pb + c * ld + k;
-              fill_lines(sb, half, ltid, [&](int l) { return x + l * ld; },
-                         [&](int l) { return c + l < rows ? min(left, kStep) : 0; });
-            } else {
-              const __nv_bfloat16* d = pb + (static_cast<int64_t>(t.lo) + k) * N + c;
-              fill_lines(sb, (half + 63) / 64 * 64, ltid, [&](int l) { return d + static_cast<int64_t>(l & 63) * N + (l & 64); },
-                         [&](int l) { return (l & 63) < left ? static_cast<int>(min(max(N - c - (l & 64), int64_t{0}), int64_t{64})) : 0; });
+            p += u * 8;
+            return max(min(valid, 64) - u * 8, 0);
+          };
+          if (here) {
+            fill_lines(sa, l_lo, l_hi, ltid, unit);
+            if (tail) {  // rows behind the expert's last: the next expert's, or nobody's
+              if (a.tma_a) clear_lines(sa, 128, left, ltid);
+              if (a.tma_b) clear_lines(sb, lines_b, left, ltid);
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
