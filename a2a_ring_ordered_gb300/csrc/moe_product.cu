@@ -15,11 +15,11 @@
 // grid of one pair per two SMs: each CTA stages 128 rows of A and half of B's
 // columns (tcgen05.mma.cta_group::2 reads both halves, which halves shared
 // memory traffic for B), in stages of 64 contraction elements.  Roles by warp:
-//   0-3  epilogue: TMEM -> registers -> global, double buffered (2 x 256
+//   0-7  epilogue: TMEM -> registers -> global, double buffered (2 x 256
 //        columns) against the next tile's products
-//   4    TMA: one thread issues the stage's bulk tensor copies
-//   5    MMA: one thread of the even CTA issues for the pair
-//   6-13 loaders: what TMA cannot do -- operands that do not sit on 16 bytes,
+//   8    TMA: one thread issues the stage's bulk tensor copies
+//   9    MMA: one thread of the even CTA issues for the pair
+//   10-17 loaders: what TMA cannot do -- operands that do not sit on 16 bytes,
 //        and grad_weight's last rows, which must read as zero where the next
 //        expert begins -- by whole 16-byte loads, shifted and masked
 // Every wait is bounded: one that runs out sets the device error word.
@@ -38,7 +38,9 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMaxGroups = 2048;   // (rank, expert) pairs per launch
 constexpr int kLaunchRanks = 8;    // keeps the parameter block under 4 KB
 constexpr int kLoaderThreads = 256;
-constexpr int kProductThreads = 192 + kLoaderThreads;
+constexpr int kEpilogueWarps = 8;  // two per 32 TMEM lanes
+constexpr int kTmaWarp = kEpilogueWarps, kMmaWarp = kTmaWarp + 1, kLoaderWarp = kMmaWarp + 1;
+constexpr int kProductThreads = kLoaderWarp * 32 + kLoaderThreads;
 constexpr int kSmallBox = 16;      // rows of B's small box
 constexpr uint32_t kTmemColumns = 512;
 constexpr long long kWaitCycles = 1ll << 32;  // two seconds
@@ -335,12 +337,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&s.tmem_full[i]), 1);
-      mbar_init(smem_addr(&s.tmem_empty[i]), 8);  // the epilogue's warps of both CTAs
+      mbar_init(smem_addr(&s.tmem_empty[i]), 2 * kEpilogueWarps);  // the epilogue's warps of both CTAs
     }
     s.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s.tmem)),
                  "r"(kTmemColumns)
                  : "memory");
@@ -389,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                                                      : static_cast<uint64_t>(s.first[groups])) * mt;
   volatile uint32_t* dead = &s.dead;
 
-  if (warp == 4) {
+  if (warp == kTmaWarp) {
     // ------------------------------------------------------------------ TMA
     // The whole warp walks the stages, so that addresses and coordinates are
     // uniform; one lane issues.
@@ -459,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
       while (clock64() - t0 < (1ll << 22)) {
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA
     if (cta == 0) {
       const bool issuer = elect_one();
@@ -502,10 +504,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         __syncwarp();
       }
     }
-  } else if (warp >= 6) {
+  } else if (warp >= kLoaderWarp) {
     // -------------------------------------------------------------- loaders
     if (loaders) {
-      const int ltid = tid - 6 * 32;
+      const int ltid = tid - kLoaderWarp * 32;
       Ring ring;
       // parity of each stage's next `go`.  The loaders skip stages, so they
       // could not follow `empty` by its parity: several of its phases may pass
@@ -579,12 +581,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
       const uint32_t buf = n & 1;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_full[buf]), (n >> 1) & 1, dead))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t m = t.m0 + cta * 128 + warp * 32 + lane;
+      const uint32_t quarter = warp & 3;  // the 32 lanes that this warp can read
+      const uint32_t m = t.m0 + cta * 128 + quarter * 32 + lane;
       const uint64_t at = (KIND == kProductGradWeight ? static_cast<uint64_t>(t.expert) * a.n + t.c0 : static_cast<uint64_t>(t.c0)) * M + m;
       constexpr int kBytes = Elem<OUT>::kBytes;
       char* out = static_cast<char*>(a.out[t.rank]) + at * kBytes;
-      const uint32_t from = tmem + buf * kTile + (static_cast<uint32_t>(warp) << 21);  // lane = 32 * warp
-      for (int c = 0; c < t.width; c += 32) {
+      const uint32_t from = tmem + buf * kTile + (quarter << 21);  // lane 32 * quarter
+      for (int c = (warp >> 2) * 32; c < t.width; c += kEpilogueWarps / 4 * 32) {
         uint32_t v[32];
         if (t.depth > 0) {
           tmem_load32(from + c, v);
@@ -615,7 +618,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
   __syncthreads();
   // neither CTA leaves while the other may still signal its barriers
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns));
   }
