@@ -57,6 +57,7 @@ struct PairArgs {
   uint32_t n, contract;
   int p, num_experts;
   int tma_a, tma_b;
+  int whole_a, whole_b;  // the operand's contiguous axis is whole chunks of 64: both of a stage in one copy
 };
 static_assert(sizeof(PairArgs) <= 4096, "product parameters exceed 4 KB");
 
@@ -160,11 +161,11 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
         "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t cluster_bar) {
+__device__ __forceinline__ void tma(uint32_t dst, const CUtensorMap* map, int x, int line, int chunk, int z, uint32_t cluster_bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
-      "%4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+      "%4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(line), "r"(chunk), "r"(z), "r"(cluster_bar)
       : "memory");
 }
 
@@ -197,6 +198,9 @@ struct Tile {
   int m0;       // first m of the pair
 };
 
+// The same value in every lane, and known to be.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 template <int KIND>
 __device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int groups, uint64_t index, uint32_t mt) {
   const uint32_t rt = static_cast<uint32_t>(index / mt);
@@ -224,9 +228,13 @@ __device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int 
     t.cols = min(each, rows - at);
     t.depth = static_cast<int>(KIND == kProductForward ? a.contract : a.n);
   }
-  t.lo = s.lo[g];
-  t.rank = g / a.num_experts;
-  t.expert = g - t.rank * a.num_experts;
+  t.lo = uniform(s.lo[g]);
+  t.rank = uniform(g / a.num_experts);
+  t.expert = uniform(g - t.rank * a.num_experts);
+  t.m0 = uniform(t.m0);
+  t.c0 = uniform(t.c0);
+  t.cols = uniform(t.cols);
+  t.depth = uniform(t.depth);
   t.width = (t.cols + 31) & ~31;
   return t;
 }
@@ -309,6 +317,42 @@ __device__ __forceinline__ void fill_lines(char* dst, int lo, int hi, int tid, U
 __device__ __forceinline__ void clear_lines(char* dst, int lines, int left, int tid) {
   for (int i = tid; i < lines * 8; i += kLoaderThreads)
     if (((i >> 3) & 63) >= left) *reinterpret_cast<uint4*>(dst + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// ----------------------------------------------------------------- epilogue
+// This lane's column of the tile in 32 rows of the output, `ld` bytes apart:
+// v[j] goes to p + j * ld while j < count.  `even` (bf16): neighbouring lanes
+// swap halves of two rows, so that the even lane holds two outputs of row j
+// and the odd one two of row j + 1, and half as many stores carry them.
+template <int OUT, bool ALL>
+__device__ __forceinline__ void store_rows(char* p, uint64_t ld, const uint32_t* v, int count, bool live, bool even) {
+  if constexpr (OUT == kF32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (live && (ALL || j < count)) *reinterpret_cast<uint32_t*>(p + j * ld) = v[j];
+  } else {
+    const int odd = threadIdx.x & 1;
+    if (even) {
+      p += odd * (ld - 2);
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+        const uint32_t mine = *reinterpret_cast<const uint32_t*>(&h);
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+        const uint32_t both = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+        if (live && (ALL || j + odd < count)) *reinterpret_cast<uint32_t*>(p + j * ld) = both;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (live && (ALL || j < count)) *reinterpret_cast<__nv_bfloat16*>(p + j * ld) = __float2bfloat16_rn(__uint_as_float(v[j]));
+    }
+  }
+}
+template <int OUT>
+__device__ __forceinline__ void store_columns(char* p, uint64_t ld, const uint32_t* v, int count, bool live, bool even) {
+  if (count >= 32) store_rows<OUT, true>(p, ld, v, count, live, even);
+  else store_rows<OUT, false>(p, ld, v, count, live, even);
 }
 
 // ------------------------------------------------------------------- kernel
@@ -408,6 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
       const uint32_t box_bytes = kBColumns ? kStep * 128 : half > 64 ? kOperandBytes : kSmallBox * 128;
       const CUtensorMap* map_a = &a.a[t.rank];
       const CUtensorMap* map_b = !kBColumns && half <= 64 ? &a.b_small[t.rank] : &a.b[t.rank];
+      const CUtensorMap* map_small = &a.b_small[t.rank];
       const int z = KIND == kProductGradWeight ? 0 : t.expert;
       for (int k = 0; k < t.depth; k += kStep) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead))) {
@@ -432,20 +477,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
           const uint32_t sa = data + ring.stage * kStageBytes, sb = sa + kOperandBytes;
           if (do_a) {
             if constexpr (!kAColumns) {
-              tma3(sa, map_a, k, m, z, bar);
+              tma(sa, map_a, k, m, 0, z, bar);
             } else {
-              const int y = KIND == kProductGradInput ? k : t.lo + k;
-              tma3(sa, map_a, m, y, z, bar);
-              tma3(sa + kStep * 128, map_a, m + 64, y, z, bar);
+              const int line = KIND == kProductGradInput ? k : t.lo + k;
+              if (a.whole_a) {
+                tma(sa, map_a, 0, line, m >> 6, z, bar);
+              } else {
+                tma(sa, map_a, m, line, 0, z, bar);
+                tma(sa + kStep * 128, map_a, m + 64, line, 0, z, bar);
+              }
             }
           }
           if (do_b) {
             if constexpr (kBColumns) {
-              tma3(sb, map_b, c, t.lo + k, 0, bar);
-              if (boxes > 1) tma3(sb + kStep * 128, map_b, c + 64, t.lo + k, 0, bar);
+              if (a.whole_b && boxes > 1) {
+                tma(sb, map_b, 0, t.lo + k, c >> 6, 0, bar);
+              } else {
+                tma(sb, map_small, c, t.lo + k, 0, 0, bar);
+                if (boxes > 1) tma(sb + kStep * 128, map_small, c + 64, t.lo + k, 0, 0, bar);
+              }
             } else {
-              tma3(sb, map_b, k, c, 0, bar);
-              for (int q = 1; q < boxes; ++q) tma3(sb + q * kSmallBox * 128, map_b, k, c + q * kSmallBox, 0, bar);
+              tma(sb, map_b, k, c, 0, 0, bar);
+              for (int q = 1; q < boxes; ++q) tma(sb + q * kSmallBox * 128, map_b, k, c + q * kSmallBox, 0, 0, bar);
             }
           }
         }
@@ -585,6 +638,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
       const uint32_t m = t.m0 + cta * 128 + quarter * 32 + lane;
       const uint64_t at = (KIND == kProductGradWeight ? static_cast<uint64_t>(t.expert) * a.n + t.c0 : static_cast<uint64_t>(t.c0)) * M + m;
       constexpr int kBytes = Elem<OUT>::kBytes;
+      // bf16 outputs two by two: where every row starts on four bytes
+      const bool even = OUT == kBF16 && (M & 1) == 0 && (reinterpret_cast<uintptr_t>(a.out[t.rank]) & 3) == 0;
       char* out = static_cast<char*>(a.out[t.rank]) + at * kBytes;
       const uint32_t from = tmem + buf * kTile + (quarter << 21);  // lane 32 * quarter
       for (int c = (warp >> 2) * 32; c < t.width; c += kEpilogueWarps / 4 * 32) {
@@ -596,16 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0;
         }
-        if (m < M) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (c + j < t.cols) {
-              char* p = out + static_cast<uint64_t>(c + j) * M * kBytes;
-              if constexpr (OUT == kF32) *reinterpret_cast<uint32_t*>(p) = v[j];
-              else *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(__uint_as_float(v[j]));
-            }
-          }
-        }
+        store_columns<OUT>(out + static_cast<uint64_t>(c) * M * kBytes, static_cast<uint64_t>(M) * kBytes, v, t.cols - c, m < M, even);
         __syncwarp();
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -643,14 +689,16 @@ EncodeFn encoder() {
   return fn;
 }
 
-// A [depth][height][width] bf16 tensor in boxes of 64 elements x `box` lines.
-bool encode(CUtensorMap* map, const void* p, uint64_t width, uint64_t height, uint64_t depth, uint32_t box) {
+// A [depth][height][width] bf16 tensor in boxes of `lines` lines x 64 elements;
+// `chunks` > 1: the width, a multiple of 64, as an axis of its own in chunks of
+// 64, so many of them per box.
+bool encode(CUtensorMap* map, const void* p, uint64_t width, uint64_t height, uint64_t depth, uint32_t lines, uint32_t chunks = 1) {
   const EncodeFn fn = encoder();
   if (fn == nullptr) return false;
-  const cuuint64_t dims[3] = {width, height, depth};
-  const cuuint64_t strides[2] = {width * 2, width * height * 2};
-  const cuuint32_t boxes[3] = {kStep, box, 1}, ones[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, boxes, ones,
+  const cuuint64_t dims[4] = {chunks > 1 ? 64 : width, height, chunks > 1 ? width / 64 : 1, depth};
+  const cuuint64_t strides[3] = {width * 2, chunks > 1 ? 128 : width * height * 2, width * height * 2};
+  const cuuint32_t boxes[4] = {kStep, lines, chunks, 1}, ones[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, boxes, ones,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -711,6 +759,8 @@ cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& args, cu
     a.contract = static_cast<uint32_t>(k);
     const uint64_t a_width = k, b_width = kind == kProductForward ? k : n;
     a.tma_a = a.tma_b = 1;
+    a.whole_a = a_width % 64 == 0 && a_width >= 128;
+    a.whole_b = b_width % 64 == 0 && b_width >= 128;
     uint64_t rows = 0;
     for (int i = 0; i < a.p; ++i) {
       a.pa[i] = args.a[r0 + i];
@@ -728,13 +778,16 @@ cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& args, cu
       bool ok = true;
       if (a.tma_a) {
         ok = kind == kProductForward     ? encode(&a.a[i], a.pa[i], k, n, E, 128)
-             : kind == kProductGradInput ? encode(&a.a[i], a.pa[i], k, n, E, kStep)
-                                         : encode(&a.a[i], a.pa[i], k, a.rows[i], 1, kStep);
+             : kind == kProductGradInput ? encode(&a.a[i], a.pa[i], k, n, E, kStep, a.whole_a ? 2 : 1)
+                                         : encode(&a.a[i], a.pa[i], k, a.rows[i], 1, kStep, a.whole_a ? 2 : 1);
       }
       if (ok && a.tma_b) {
-        ok = kind == kProductGradWeight ? encode(&a.b[i], a.pb[i], n, a.rows[i], 1, kStep)
-                                        : encode(&a.b[i], a.pb[i], b_width, a.rows[i], 1, 128) &&
-                                              encode(&a.b_small[i], a.pb[i], b_width, a.rows[i], 1, kSmallBox);
+        if (kind == kProductGradWeight)
+          ok = encode(&a.b_small[i], a.pb[i], n, a.rows[i], 1, kStep) &&
+               (!a.whole_b || encode(&a.b[i], a.pb[i], n, a.rows[i], 1, kStep, 2));
+        else
+          ok = encode(&a.b[i], a.pb[i], b_width, a.rows[i], 1, 128) &&
+               encode(&a.b_small[i], a.pb[i], b_width, a.rows[i], 1, kSmallBox);
       }
       if (!ok) return cudaErrorInvalidValue;
     }
