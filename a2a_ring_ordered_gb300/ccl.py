@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from typing import Sequence
 
 import torch
@@ -94,14 +95,14 @@ def _load() -> ctypes.CDLL:
         "ccl_moe_dispatch": (st, [pp, pp, vp, pp, i32, sz, i32, i32, sz, i32, pp, ctypes.POINTER(sz),
                                   pp, pp, vp]),
         "ccl_moe_combine": (st, [pp, ctypes.POINTER(sz), pp, pp, vp, pp, i32, sz, i32, i32, sz, pp, vp]),
-        "ccl_moe_sort": (st, [pp, ctypes.POINTER(sz), i32, i32, i32, ctypes.POINTER(ctypes.c_int32), pp, pp, vp]),
-        "ccl_moe_to_experts": (st, [pp, pp, ctypes.POINTER(sz), i32, i32, sz, i32, pp, ctypes.POINTER(sz), vp]),
-        "ccl_moe_from_experts": (st, [pp, ctypes.POINTER(sz), pp, pp, ctypes.POINTER(sz), i32, i32, sz, i32, pp, vp]),
-        "ccl_moe_from_experts_grad": (st, [pp, pp, ctypes.POINTER(sz), pp, pp, ctypes.POINTER(sz), i32, i32, sz, i32,
-                                           pp, pp, vp]),
-        "ccl_moe_product": (st, [pp, pp, pp, ctypes.POINTER(sz), i32, i32, sz, sz, pp, vp]),
-        "ccl_moe_product_grad_input": (st, [pp, pp, pp, ctypes.POINTER(sz), i32, i32, sz, sz, pp, vp]),
-        "ccl_moe_product_grad_weight": (st, [pp, pp, pp, ctypes.POINTER(sz), i32, i32, sz, sz, i32, pp, vp]),
+        # arrays of addresses and sizes come as packed bytes (_pointers, _sizes)
+        "ccl_moe_sort": (st, [vp, vp, i32, i32, i32, vp, vp, vp, vp]),
+        "ccl_moe_to_experts": (st, [vp, vp, vp, i32, i32, sz, i32, vp, vp, vp]),
+        "ccl_moe_from_experts": (st, [vp, vp, vp, vp, vp, i32, i32, sz, i32, vp, vp]),
+        "ccl_moe_from_experts_grad": (st, [vp, vp, vp, vp, vp, vp, i32, i32, sz, i32, vp, vp, vp]),
+        "ccl_moe_product": (st, [vp, vp, vp, vp, i32, i32, sz, sz, vp, vp]),
+        "ccl_moe_product_grad_input": (st, [vp, vp, vp, vp, i32, i32, sz, sz, vp, vp]),
+        "ccl_moe_product_grad_weight": (st, [vp, vp, vp, vp, i32, i32, sz, sz, i32, vp, vp]),
         "ccl_adamw_step": (st, [ctypes.POINTER(AdamWTensor), sz, i32, i32, i32, ctypes.POINTER(AdamWHyper), vp]),
         "ccl_plan_buckets": (st, [ctypes.POINTER(sz), sz, sz, sz, ctypes.POINTER(ctypes.c_uint32),
                                   ctypes.POINTER(sz), ctypes.POINTER(sz), ctypes.POINTER(sz)]),
@@ -661,52 +662,91 @@ def ccl_moe_combine(y, expert_ids, weights, counts, slots, num_experts: int, out
 
 
 # --------------------------------------------------- MoE: a rank's own experts
-def _sizes(values):
-    return (ctypes.c_size_t * len(values))(*values)
+# These calls run once per layer and token step, on tens of microseconds of GPU
+# work, so their marshalling is kept short: one pass over each list with the
+# cheap tensor attributes, addresses packed with struct (an eighth of the time
+# that a ctypes array takes), and _tensors' full checks, with their messages,
+# only where the pass finds something.
+@functools.lru_cache(maxsize=None)
+def _packer(code: str, count: int):
+    return struct.Struct(f"{count}{code}").pack
 
 
-def _pointers(ts):
-    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+def _pointers(ts) -> bytes:
+    return _packer("P", len(ts))(*[t.data_ptr() for t in ts])
 
 
-def _ranks(ts, name: str, p: int, dtype, rows=None, width=None) -> list[torch.Tensor]:
-    """The p rank buffers of an argument, of one dtype; where given, rank r has
-    rows[r] rows of `width` elements."""
-    ts = _tensors(ts, name)
-    if len(ts) != p:
+def _sizes(values) -> bytes:
+    return _packer("N", len(values))(*values)
+
+
+def _buffers(ts, name: str, dtype=None, p: int | None = None):
+    """The rank buffers of an argument: contiguous, on one device, of one dtype."""
+    if type(ts) is not list:
+        ts = list(ts)
+    if p is not None and len(ts) != p:
         raise ValueError(f"{name} must hold {p} rank buffers, got {len(ts)}")
-    if ts[0].dtype != dtype:
+    if ts:
+        first = ts[0]
+        if isinstance(first, torch.Tensor) and len(ts) <= CCL_MAX_RANKS:
+            want, device = dtype or first.dtype, first.get_device()
+            if device >= 0:
+                for t in ts:
+                    if not isinstance(t, torch.Tensor) or t.dtype is not want or t.get_device() != device or not t.is_contiguous():
+                        break
+                else:
+                    return ts
+    ts = _tensors(ts, name)
+    if dtype is not None and ts[0].dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {ts[0].dtype}")
-    if rows is not None:
-        for r, t in enumerate(ts):
-            if t.numel() != rows[r] * width:
-                raise ValueError(f"{name}[{r}] has {t.numel()} elements, expected {rows[r]} x {width}")
     return ts
+
+
+def _ranks(ts, name: str, p: int, dtype, rows, width: int) -> bytes:
+    """Addresses of the p rank buffers, rank r of rows[r] rows of `width` elements."""
+    ts = _buffers(ts, name, dtype, p)
+    for r, t in enumerate(ts):
+        if t.numel() != rows[r] * width:
+            raise ValueError(f"{name}[{r}] has {t.numel()} elements, expected {rows[r]} x {width}")
+    return _pointers(ts)
 
 
 def _choices(rows, name: str = "rows"):
     """(buffers, tokens of each rank, k) of a list of (tokens, k) int32 tensors."""
-    rows = _tensors(rows, name)
-    if rows[0].dtype != torch.int32:
-        raise ValueError(f"{name} must be int32, got {rows[0].dtype}")
-    k = rows[0].shape[1] if rows[0].dim() == 2 else 1
+    rows = _buffers(rows, name, torch.int32)
+    k, tokens = None, []
     for r, t in enumerate(rows):
-        if t.dim() > 2 or (t.shape[1] if t.dim() == 2 else 1) != k:
+        shape = t.shape
+        this = shape[1] if len(shape) == 2 else 1
+        if k is None:
+            k = this
+        if this != k or not 1 <= len(shape) <= 2:
             raise ValueError(f"{name}[{r}] must be (tokens, {k})")
-    return rows, [t.shape[0] for t in rows], k
+        tokens.append(shape[0])
+    return rows, tokens, k
 
 
-def _row_buffers(ts, name: str, p: int, dtype=None):
+def _row_buffers(ts, name: str, p: int | None = None, dtype=None):
     """(buffers, rows of each rank, width) of a list of (rows, width) tensors."""
-    ts = _tensors(ts, name)
-    if len(ts) != p:
-        raise ValueError(f"{name} must hold {p} rank buffers, got {len(ts)}")
-    if dtype is not None and ts[0].dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {ts[0].dtype}")
+    ts = _buffers(ts, name, dtype, p)
+    width, rows = None, []
     for r, t in enumerate(ts):
-        if t.dim() != 2 or t.shape[1] != ts[0].shape[1]:
-            raise ValueError(f"{name}[{r}] must be (rows, {ts[0].shape[-1]})")
-    return ts, [t.shape[0] for t in ts], ts[0].shape[1]
+        shape = t.shape
+        if len(shape) != 2 or (width is not None and shape[1] != width):
+            raise ValueError(f"{name}[{r}] must be (rows, {'width' if width is None else width})")
+        width = shape[1]
+        rows.append(shape[0])
+    return ts, rows, width
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, t: torch.Tensor) -> int:
+    """The given stream, or torch's current one on the tensor's device."""
+    if stream is None and _raw_stream is not None and t.is_cuda:
+        return _raw_stream(t.get_device())
+    return _stream(stream, t.device)
 
 
 def ccl_moe_sort(expert_ids, num_experts: int, offsets, rows, first_expert=None, stream=None) -> None:
@@ -721,9 +761,9 @@ def ccl_moe_sort(expert_ids, num_experts: int, offsets, rows, first_expert=None,
     if first_expert is not None:
         if len(first_expert) != p:
             raise ValueError(f"first_expert must hold {p} numbers")
-        first = (ctypes.c_int32 * p)(*first_expert)
-    _check(LIB.ccl_moe_sort(_pointers(ids), _sizes(tokens), p, k, num_experts, first, _pointers(offsets),
-                            _pointers(rows), _stream(stream, ids[0].device)), "ccl_moe_sort")
+        first = _packer("i", p)(*first_expert)
+    _check(LIB.ccl_moe_sort(_pointers(ids), _sizes(tokens), p, k, num_experts, first, offsets, rows,
+                            _stream_of(stream, ids[0])), "ccl_moe_sort")
 
 
 def ccl_moe_to_experts(x, rows, sorted, stream=None) -> None:
@@ -732,9 +772,8 @@ def ccl_moe_to_experts(x, rows, sorted, stream=None) -> None:
     p = len(rows)
     sorted, cap, hidden = _row_buffers(sorted, "sorted", p)
     x = _ranks(x, "x", p, sorted[0].dtype, tokens, hidden)
-    _check(LIB.ccl_moe_to_experts(_pointers(x), _pointers(rows), _sizes(tokens), p, k, hidden, _dtype_code(x[0]),
-                                  _pointers(sorted), _sizes(cap), _stream(stream, rows[0].device)),
-           "ccl_moe_to_experts")
+    _check(LIB.ccl_moe_to_experts(x, _pointers(rows), _sizes(tokens), p, k, hidden, _dtype_code(sorted[0]),
+                                  _pointers(sorted), _sizes(cap), _stream_of(stream, rows[0])), "ccl_moe_to_experts")
 
 
 def ccl_moe_from_experts(y, rows, weights, out, stream=None) -> None:
@@ -746,10 +785,9 @@ def ccl_moe_from_experts(y, rows, weights, out, stream=None) -> None:
     y, cap, hidden = _row_buffers(y, "y", p)
     out = _ranks(out, "out", p, y[0].dtype, tokens, hidden)
     if weights is not None:
-        weights = _pointers(_ranks(weights, "weights", p, torch.float32, tokens, k))
+        weights = _ranks(weights, "weights", p, torch.float32, tokens, k)
     _check(LIB.ccl_moe_from_experts(_pointers(y), _sizes(cap), _pointers(rows), weights, _sizes(tokens), p, k, hidden,
-                                    _dtype_code(y[0]), _pointers(out), _stream(stream, rows[0].device)),
-           "ccl_moe_from_experts")
+                                    _dtype_code(y[0]), out, _stream_of(stream, rows[0])), "ccl_moe_from_experts")
 
 
 def ccl_moe_from_experts_grad(dout, y, rows, weights, dy=None, dweights=None, stream=None) -> None:
@@ -767,73 +805,68 @@ def ccl_moe_from_experts_grad(dout, y, rows, weights, dy=None, dweights=None, st
     dtype = expert_rows[0].dtype
     dout = _ranks(dout, "dout", p, dtype, tokens, hidden)
     if y is not None:
-        y = expert_rows
+        y = _pointers(expert_rows)
     if dy is not None:
         dy = _ranks(dy, "dy", p, dtype, cap, hidden)
     if weights is not None:
-        weights = _pointers(_ranks(weights, "weights", p, torch.float32, tokens, k))
+        weights = _ranks(weights, "weights", p, torch.float32, tokens, k)
     if dweights is not None:
-        dweights = _pointers(_ranks(dweights, "dweights", p, torch.float32, tokens, k))
-    _check(LIB.ccl_moe_from_experts_grad(_pointers(dout), None if y is None else _pointers(y), _sizes(cap),
-                                         _pointers(rows), weights, _sizes(tokens), p, k, hidden,
-                                         _dtype_code(dout[0]), None if dy is None else _pointers(dy), dweights,
-                                         _stream(stream, rows[0].device)), "ccl_moe_from_experts_grad")
+        dweights = _ranks(dweights, "dweights", p, torch.float32, tokens, k)
+    _check(LIB.ccl_moe_from_experts_grad(dout, y, _sizes(cap), _pointers(rows), weights, _sizes(tokens), p, k, hidden,
+                                         _dtype_code(expert_rows[0]), dy, dweights, _stream_of(stream, rows[0])),
+           "ccl_moe_from_experts_grad")
 
 
 def _weights(ts, name: str, p: int, dtype=torch.bfloat16):
     """(buffers, experts, n, contract) of a list of (experts, n, contract) tensors."""
-    ts = _tensors(ts, name)
-    if len(ts) != p:
-        raise ValueError(f"{name} must hold {p} rank buffers, got {len(ts)}")
-    if dtype is not None and ts[0].dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {ts[0].dtype}")
+    ts = _buffers(ts, name, dtype, p)
+    shape = ts[0].shape
     for r, t in enumerate(ts):
-        if t.dim() != 3 or t.shape != ts[0].shape:
+        if t.dim() != 3 or (r and t.shape != shape):
             raise ValueError(f"{name}[{r}] must be (experts, n, contract), alike on every rank")
-    return ts, *ts[0].shape
+    return ts, *shape
 
 
 def ccl_moe_product(x, offsets, w, y, stream=None) -> None:
     """y[rows of e] = x[rows of e] @ w[e].T for every expert e: x[r] (rows, contract),
     w[r] (experts, n, contract), y[r] (rows, n), bf16; offsets[r] from ccl_moe_sort."""
-    x, rows, contract = _row_buffers(x, "x", len(x), torch.bfloat16)
+    x, rows, contract = _row_buffers(x, "x", None, torch.bfloat16)
     p = len(x)
     w, experts, n, depth = _weights(w, "w", p)
     if depth != contract:
         raise ValueError(f"w has {depth} columns, x {contract}")
     y = _ranks(y, "y", p, torch.bfloat16, rows, n)
     offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
-    _check(LIB.ccl_moe_product(_pointers(x), _pointers(offsets), _pointers(w), _sizes(rows), p, experts, n, contract,
-                               _pointers(y), _stream(stream, x[0].device)), "ccl_moe_product")
+    _check(LIB.ccl_moe_product(_pointers(x), offsets, _pointers(w), _sizes(rows), p, experts, n, contract, y,
+                               _stream_of(stream, x[0])), "ccl_moe_product")
 
 
 def ccl_moe_product_grad_input(dy, offsets, w, dx, stream=None) -> None:
     """dx[rows of e] = dy[rows of e] @ w[e]: the gradient of ccl_moe_product for x."""
-    dy, rows, n = _row_buffers(dy, "dy", len(dy), torch.bfloat16)
+    dy, rows, n = _row_buffers(dy, "dy", None, torch.bfloat16)
     p = len(dy)
     w, experts, height, contract = _weights(w, "w", p)
     if height != n:
         raise ValueError(f"w has {height} rows, dy {n} columns")
     dx = _ranks(dx, "dx", p, torch.bfloat16, rows, contract)
     offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
-    _check(LIB.ccl_moe_product_grad_input(_pointers(dy), _pointers(offsets), _pointers(w), _sizes(rows), p, experts, n,
-                                          contract, _pointers(dx), _stream(stream, dy[0].device)),
-           "ccl_moe_product_grad_input")
+    _check(LIB.ccl_moe_product_grad_input(_pointers(dy), offsets, _pointers(w), _sizes(rows), p, experts, n, contract,
+                                          dx, _stream_of(stream, dy[0])), "ccl_moe_product_grad_input")
 
 
 def ccl_moe_product_grad_weight(dy, x, offsets, dw, stream=None) -> None:
     """dw[e] = dy[rows of e].T @ x[rows of e], fp32 or bf16 (zeros for an expert
     without rows): the gradient of ccl_moe_product for w."""
-    dy, rows, n = _row_buffers(dy, "dy", len(dy), torch.bfloat16)
+    dy, rows, n = _row_buffers(dy, "dy", None, torch.bfloat16)
     p = len(dy)
     dw, experts, height, contract = _weights(dw, "dw", p, None)
     if height != n:
         raise ValueError(f"dw has {height} rows, dy {n} columns")
     x = _ranks(x, "x", p, torch.bfloat16, rows, contract)
     offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
-    _check(LIB.ccl_moe_product_grad_weight(_pointers(dy), _pointers(x), _pointers(offsets), _sizes(rows), p, experts,
-                                           n, contract, _dtype_code(dw[0]), _pointers(dw),
-                                           _stream(stream, dy[0].device)), "ccl_moe_product_grad_weight")
+    _check(LIB.ccl_moe_product_grad_weight(_pointers(dy), x, offsets, _sizes(rows), p, experts, n, contract,
+                                           _dtype_code(dw[0]), _pointers(dw), _stream_of(stream, dy[0])),
+           "ccl_moe_product_grad_weight")
 
 
 # ------------------------------------------------------------------------ AdamW
@@ -904,7 +937,7 @@ def ccl_adamw_step(table: AdamWTable, step: int, lr: float, betas=(0.9, 0.999), 
     hyper = AdamWHyper(lr, betas[0], betas[1], eps, weight_decay, step,
                        None if grad_scale is None else grad_scale.data_ptr())
     _check(LIB.ccl_adamw_step(table.array, table.count, table.param_code, table.grad_code, table.state_bits,
-                              ctypes.byref(hyper), _stream(stream, table.device)), "ccl_adamw_step")
+                              ctypes.byref(hyper), _stream_of(stream, table.tensors["param"][0])), "ccl_adamw_step")
 
 
 # ------------------------------------------------ Ulysses head <-> sequence
