@@ -287,8 +287,9 @@ struct AdamwArgsT {
   AdamwTensor t[CAP];
   uint32_t chunk0[CAP + 1];  // first chunk of each tensor; chunk0[count] = the launch's chunks
   int count;
-  float beta1, one_minus_beta1, beta2, one_minus_beta2, decay, step_size, root_scale, eps;
+  float beta1, one_minus_beta1, beta2, one_minus_beta2, decay, step_size, root_scale, eps, one;  // one = 1
   uint32_t dither;           // step * 2654435769 mod 2^32
+  int any_range;             // the factors leave the range of the fast square root and quotient
   const float* grad_scale;
 };
 using AdamwSmall = AdamwArgsT<56>;

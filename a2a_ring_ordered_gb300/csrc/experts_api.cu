@@ -419,8 +419,11 @@ ccl_status_t adamw_run(const ccl_adamw_tensor_t* tensors, size_t count, int pdt,
   a.step_size = static_cast<float>(h.lr / (1.0 - pow(h.beta1, t)));
   a.root_scale = static_cast<float>(1.0 / sqrt(1.0 - pow(h.beta2, t)));
   a.eps = static_cast<float>(h.eps);
+  a.one = 1.0f;
   a.dither = static_cast<uint32_t>(h.step * 2654435769ull);
   a.grad_scale = h.grad_scale;
+  // with sqrt(v) 0 or in 2^-48 .. 2^20 the denominator stays in 2^-48 .. 2^30
+  a.any_range = !(a.eps >= ldexpf(1.0f, -48) && a.eps <= ldexpf(1.0f, 28) && a.root_scale <= ldexpf(1.0f, 9));
   return adamw_launches(a, tensors, count, pdt, gdt, bits, copy, stream);
 }
 

@@ -213,3 +213,41 @@ def test_refusals(optim):
     with pytest.raises(ccl().CclError, match="lr"):
         opt.step()
     assert opt.steps == 0
+
+
+def test_square_roots_of_every_mantissa(optim):
+    """The kernel's square root and quotient are worked out from approximations:
+    every mantissa of v at an even and an odd exponent, with random m, gives
+    the bits of numpy's correctly rounded ones."""
+    v = ((np.uint32(127) << 23) + np.arange(1 << 24, dtype=np.uint32)).view(np.float32)  # 1 .. 4
+    m = np.random.default_rng(8).standard_normal(v.size).astype(np.float32)
+    z = np.zeros(v.size, np.float32)
+    h = dict(lr=0.5, betas=(0.5, 0.5), eps=1e-8, weight_decay=0.0)
+    p = torch.zeros(v.size, device="cuda")
+    opt = optim.AdamW([p], [torch.zeros_like(p)], **h,
+                      states={"exp_avg": [torch.from_numpy(m).cuda()], "exp_avg_sq": [torch.from_numpy(v).cuda()]})
+    opt.step()
+    np.testing.assert_array_equal(p.cpu().numpy(), adamw.step32(z, z, m, v, 1, **h)[0])
+
+
+@pytest.mark.parametrize("eps", [1e-8, 0.0, 1e-20])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_ends_of_the_exponent_range(optim, bits, eps):
+    """Gradients from subnormal to huge, side by side: numbers outside the fast
+    square root's and quotient's range take the exact operations."""
+    rng = np.random.default_rng(9)
+    g = np.exp2(rng.uniform(-148, 62, 4096)).astype(np.float32) * np.where(rng.random(4096) < 0.5, -1, 1).astype(np.float32)
+    g[::7] = 0
+    z = np.zeros_like(g)
+    h = {**H, "eps": eps}
+    p = torch.zeros(g.size, device="cuda")
+    opt = optim.AdamW([p], [torch.from_numpy(g).cuda()], **h, state_bits=bits)
+    opt.step()
+    want, m, v, root = adamw.step32(z, g, z, z, 1, **h)
+    np.testing.assert_array_equal(p.cpu().numpy(), want)
+    if bits == 8:
+        np.testing.assert_array_equal(opt.table.tensors["exp_avg"][0].view(torch.uint8).cpu().numpy(), adamw.encode_m(m)[0])
+        np.testing.assert_array_equal(opt.table.tensors["exp_avg_sq"][0].view(torch.uint8).cpu().numpy(), adamw.encode_root(root, v, 1)[0])
+    else:
+        np.testing.assert_array_equal(opt.moments(0)[0].cpu().numpy(), m)
+        np.testing.assert_array_equal(opt.moments(0)[1].cpu().numpy(), v)
