@@ -231,9 +231,10 @@ cudaError_t read_device_error(unsigned int* flag, bool clear) {
     const unsigned int zero = 0;
     err = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
   }
-  unsigned int product = 0;
+  unsigned int product = 0, adamw = 0;
   if (err == cudaSuccess) err = read_product_error(&product, clear);
-  *flag |= product;
+  if (err == cudaSuccess) err = read_adamw_error(&adamw, clear);
+  *flag |= product | adamw;
   return err;
 }
 

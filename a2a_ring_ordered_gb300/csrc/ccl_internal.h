@@ -281,21 +281,32 @@ struct AdamwTensor {
   void* copy;
   uint64_t n;
 };
+// A factor twice over, as the paired instructions take it.
+struct alignas(8) AdamwPair {
+  uint64_t v;
+};
+struct AdamwPairs {
+  AdamwPair beta1, one_minus_beta1, beta2, one_minus_beta2, decay, minus_step, root_scale, eps;
+  AdamwPair one, minus_one, half, minus_half, tiny;  // tiny = 2^-120
+};
 template <int CAP>
 struct AdamwArgsT {
   static constexpr int kCap = CAP;
   AdamwTensor t[CAP];
   uint32_t chunk0[CAP + 1];  // first chunk of each tensor; chunk0[count] = the launch's chunks
   int count;
-  float beta1, one_minus_beta1, beta2, one_minus_beta2, decay, step_size, root_scale, eps, one;  // one = 1
+  AdamwPairs k;
+  float root_scale, eps;
   uint32_t dither;           // step * 2654435769 mod 2^32
   int any_range;             // the factors leave the range of the fast square root and quotient
   const float* grad_scale;
 };
-using AdamwSmall = AdamwArgsT<56>;
+using AdamwSmall = AdamwArgsT<54>;
 using AdamwLarge = AdamwArgsT<440>;
 static_assert(sizeof(AdamwSmall) <= 4096, "AdamW parameters exceed 4 KB");
 static_assert(sizeof(AdamwLarge) <= 32764, "AdamW parameters exceed 32,764 bytes");
+// AdamW's device error word, as read_device_error's.
+cudaError_t read_adamw_error(unsigned int* flag, bool clear);
 cudaError_t launch_adamw(int param_dt, int grad_dt, int bits, bool copy, const AdamwSmall& a, cudaStream_t s);
 cudaError_t launch_adamw(int param_dt, int grad_dt, int bits, bool copy, const AdamwLarge& a, cudaStream_t s);
 

@@ -406,20 +406,23 @@ ccl_status_t adamw_launches(Args& a, const ccl_adamw_tensor_t* tensors, size_t c
   return CCL_OK;
 }
 
+AdamwPair twice(double x) {
+  const float f = static_cast<float>(x);
+  uint32_t bits;
+  memcpy(&bits, &f, sizeof(bits));
+  return {static_cast<uint64_t>(bits) << 32 | bits};
+}
+
 template <typename Args>
 ccl_status_t adamw_run(const ccl_adamw_tensor_t* tensors, size_t count, int pdt, int gdt, int bits, bool copy,
                        const ccl_adamw_hyper_t& h, void* stream) {
   Args a;  // entries past the launch's tensors are never read
-  a.beta1 = static_cast<float>(h.beta1);
-  a.one_minus_beta1 = static_cast<float>(1.0 - h.beta1);
-  a.beta2 = static_cast<float>(h.beta2);
-  a.one_minus_beta2 = static_cast<float>(1.0 - h.beta2);
-  a.decay = static_cast<float>(1.0 - h.lr * h.weight_decay);
   const double t = static_cast<double>(h.step);
-  a.step_size = static_cast<float>(h.lr / (1.0 - pow(h.beta1, t)));
   a.root_scale = static_cast<float>(1.0 / sqrt(1.0 - pow(h.beta2, t)));
   a.eps = static_cast<float>(h.eps);
-  a.one = 1.0f;
+  a.k = {twice(h.beta1), twice(1.0 - h.beta1), twice(h.beta2), twice(1.0 - h.beta2), twice(1.0 - h.lr * h.weight_decay),
+         twice(-(h.lr / (1.0 - pow(h.beta1, t)))), twice(a.root_scale), twice(a.eps),
+         twice(1.0), twice(-1.0), twice(0.5), twice(-0.5), twice(ldexp(1.0, -120))};
   a.dither = static_cast<uint32_t>(h.step * 2654435769ull);
   a.grad_scale = h.grad_scale;
   // with sqrt(v) 0 or in 2^-48 .. 2^20 the denominator stays in 2^-48 .. 2^30
