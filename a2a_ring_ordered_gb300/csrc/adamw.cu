@@ -400,9 +400,12 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 // ---------------------------------------------- 8-bit states: a copied stage
 // With 8-bit states a block takes half the bytes and twice the arithmetic of
 // one with fp32 states: loads into registers then hold a warp up for as long
-// as its arithmetic does (157 M elements 622 us).  So a persistent CTA has the
-// next chunk's arrays copied into shared memory while it works on one; the
-// copies are whole 16-byte granules, which fits every alignment.
+// as its arithmetic does (157 M elements 622 us).  So a ninth warp of a
+// persistent CTA has the next chunk's arrays copied into shared memory while
+// the others work on one; the copies are whole 16-byte granules, which fits
+// every alignment.  The warps wait for the copies and give the stage back each
+// by itself (with barriers of the whole CTA in their place, and every warp
+// looking the tensor up: 553 us).
 constexpr int kStreamStages = 2;
 constexpr int kCtasPerSm = 3;
 constexpr long long kWaitCycles = 1ll << 32;  // two seconds
@@ -419,8 +422,12 @@ struct alignas(16) Stage {
 template <int PDT, int GDT>
 struct StreamShared {
   Stage<PDT, GDT> stage[kStreamStages];
-  uint64_t full[kStreamStages];
+  AdamwTensor tensor[kStreamStages];  // of the chunk in the stage
+  uint64_t c0[kStreamStages];         // and its first element
+  uint64_t full[kStreamStages], empty[kStreamStages];
+  uint32_t dead;  // a wait ran out
 };
+constexpr int kStreamThreads = kThreads + 32;
 
 __device__ __forceinline__ uint32_t shared_address(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -442,10 +449,8 @@ __device__ __forceinline__ const char* staged(const char* stage, const void* src
   return stage + (reinterpret_cast<uintptr_t>(src) & 15);
 }
 
-template <int PDT, int GDT, typename Args>
-__device__ __forceinline__ void copy_chunk(const Args& a, uint32_t chunk, Stage<PDT, GDT>& s, uint32_t bar, int at) {
-  const AdamwTensor& t = a.t[at];
-  const uint64_t c0 = static_cast<uint64_t>(chunk - a.chunk0[at]) * kAdamwChunk;
+template <int PDT, int GDT>
+__device__ __forceinline__ void copy_chunk(const AdamwTensor& t, uint64_t c0, Stage<PDT, GDT>& s, uint32_t bar) {
   const uint32_t n = static_cast<uint32_t>(min(t.n - c0, static_cast<uint64_t>(kAdamwChunk)));
   const uint32_t scales = (n + kAdamwBlock - 1) / kAdamwBlock * 4;
   const char* p = static_cast<const char*>(t.param) + c0 * Elem<PDT>::kBytes;
@@ -527,61 +532,79 @@ __device__ __forceinline__ void staged_chunk(const Args& a, const AdamwTensor& t
   }
 }
 
+// Waits for a barrier's phase; false once this or another wait of the CTA ran out.
+__device__ __forceinline__ bool stream_wait(uint64_t* barrier, uint32_t parity, volatile uint32_t* dead) {
+  const uint32_t bar = shared_address(barrier);
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    if (done) return true;
+    if (*dead) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *dead = 1;
+      atomicExch(&g_adamw_error, 1u);
+      return false;
+    }
+  }
+}
+
 template <int PDT, int GDT, bool COPY, typename Args>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) adamw_stream_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm) adamw_stream_kernel(const __grid_constant__ Args a) {
   extern __shared__ char raw[];
   StreamShared<PDT, GDT>& s = *reinterpret_cast<StreamShared<PDT, GDT>*>(raw);
   const uint32_t chunks = a.chunk0[a.count];
+  const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStreamStages; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_address(&s.full[i])) : "memory");
+    for (int i = 0; i < kStreamStages; ++i) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_address(&s.full[i])) : "memory");
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_address(&s.empty[i])), "r"(kThreads / 32) : "memory");
+    }
+    s.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
   pdl_enter();
-  const float grad_scale = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
-  // the first warp looks the tensors up, one lane of it copies
-  if (threadIdx.x < 32) {
-    for (int i = 0; i < kStreamStages; ++i) {
-      const uint32_t chunk = blockIdx.x + i * gridDim.x;
-      if (chunk >= chunks) break;
+  uint32_t st = 0, phase = 0;
+  if (threadIdx.x >= kThreads) {  // the copying warp
+    bool ok = true;
+    for (uint32_t chunk = blockIdx.x; ok && chunk < chunks; chunk += gridDim.x) {
       const int at = tensor_of(a, chunk);
-      if (threadIdx.x == 0) copy_chunk<PDT, GDT>(a, chunk, s.stage[i], shared_address(&s.full[i]), at);
+      if (lane == 0) {
+        ok = stream_wait(&s.empty[st], phase ^ 1, &s.dead);
+        if (ok) {
+          const AdamwTensor& t = a.t[at];
+          const uint64_t c0 = static_cast<uint64_t>(chunk - a.chunk0[at]) * kAdamwChunk;
+          s.tensor[st] = t;
+          s.c0[st] = c0;
+          copy_chunk<PDT, GDT>(t, c0, s.stage[st], shared_address(&s.full[st]));
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (++st == kStreamStages) st = 0, phase ^= 1;
     }
-  }
-  uint32_t st = 0, parity = 0;
-  for (uint32_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-    const uint32_t bar = shared_address(&s.full[st]);
-    bool here = false;
-    const long long t0 = clock64();
-    do {
-      uint32_t done;
-      asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-                   : "=r"(done)
-                   : "r"(bar), "r"(parity)
-                   : "memory");
-      here = done != 0;
-    } while (!here && clock64() - t0 < kWaitCycles);
-    if (__syncthreads_or(!here)) {  // one answer for the CTA
-      if (threadIdx.x == 0) atomicExch(&g_adamw_error, 1u);
-      const long long t1 = clock64();  // copies in flight still write this CTA's shared memory
+    if (!ok) {  // copies in flight still write this CTA's shared memory
+      const long long t1 = clock64();
       while (clock64() - t1 < (1ll << 22)) {
       }
-      return;
     }
-    const int at = tensor_of(a, chunk);
-    const AdamwTensor& t = a.t[at];
-    const uint64_t c0 = static_cast<uint64_t>(chunk - a.chunk0[at]) * kAdamwChunk;
+    return;
+  }
+  const float grad_scale = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
+  for (uint32_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+    if (!__all_sync(0xFFFFFFFFu, stream_wait(&s.full[st], phase, &s.dead))) return;
+    const AdamwTensor t = s.tensor[st];
+    const uint64_t c0 = s.c0[st];
     const bool whole = c0 + kAdamwChunk <= t.n;
     if (whole && on_vectors<PDT, GDT, 8>(t)) staged_chunk<PDT, GDT, COPY, true, true>(a, t, c0, s.stage[st], grad_scale);
     else if (whole) staged_chunk<PDT, GDT, COPY, false, true>(a, t, c0, s.stage[st], grad_scale);
     else staged_chunk<PDT, GDT, COPY, false, false>(a, t, c0, s.stage[st], grad_scale);
-    __syncthreads();  // the stage has been read
-    const uint32_t next = chunk + kStreamStages * gridDim.x;
-    if (threadIdx.x < 32 && next < chunks) {
-      const int later = tensor_of(a, next);
-      if (threadIdx.x == 0) copy_chunk<PDT, GDT>(a, next, s.stage[st], bar, later);
-    }
-    if (++st == kStreamStages) st = 0, parity ^= 1;
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_address(&s.empty[st])) : "memory");
+    if (++st == kStreamStages) st = 0, phase ^= 1;
   }
 }
 
@@ -597,7 +620,7 @@ cudaError_t launch_one(const Args& a, cudaStream_t s) {
     const uint32_t resident = static_cast<uint32_t>(current_sm_count()) * kCtasPerSm;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.chunk0[a.count] < resident || resident == 0 ? a.chunk0[a.count] : resident);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kStreamThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
