@@ -247,8 +247,8 @@ struct MoeRowsArgs {  // to_experts, from_experts and its gradient
 static_assert(sizeof(MoeSortArgs) <= 4096, "MoE sort parameters exceed 4 KB");
 static_assert(sizeof(MoeRowsArgs) <= 4096, "MoE row parameters exceed 4 KB");
 cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s);
-// `align`: the largest of 16, 4 and 2 that divides every row address
-cudaError_t launch_moe_to_experts(int dt, int align, const MoeRowsArgs& a, cudaStream_t s);
+// `vec`: every row starts on 16 bytes
+cudaError_t launch_moe_to_experts(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s);
 cudaError_t launch_moe_from_experts(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s);
 cudaError_t launch_moe_from_experts_grad(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s);
 

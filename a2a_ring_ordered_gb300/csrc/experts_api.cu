@@ -85,8 +85,8 @@ bool any_tokens(const size_t* tokens, int p) {
   return false;
 }
 
-// Largest of 16, 4 and 2 that divides `bits` (addresses and row bytes or-ed together).
-int alignment(uintptr_t bits) { return (bits & 15) == 0 ? 16 : (bits & 3) == 0 ? 4 : 2; }
+// Whether all rows start on 16 bytes; `bits`: addresses and row bytes or-ed together.
+bool on_grid(uintptr_t bits) { return (bits & 15) == 0; }
 
 ccl_status_t launched(cudaError_t err, const char* what) {
   if (err == cudaSuccess) return CCL_OK;
@@ -163,7 +163,7 @@ extern "C" ccl_status_t ccl_moe_to_experts(const void* const* x, const int32_t* 
   a.hidden = hidden;
   a.p = p;
   a.k = k;
-  return launched(launch_moe_to_experts(dt, alignment(bits), a, on(stream)), "MoE to-experts kernel");
+  return launched(launch_moe_to_experts(dt, on_grid(bits), a, on(stream)), "MoE to-experts kernel");
 }
 
 extern "C" ccl_status_t ccl_moe_from_experts(const void* const* y, const size_t* y_rows, const int32_t* const* rows,
@@ -206,7 +206,7 @@ extern "C" ccl_status_t ccl_moe_from_experts(const void* const* y, const size_t*
   a.hidden = hidden;
   a.p = p;
   a.k = k;
-  return launched(launch_moe_from_experts(dt, alignment(bits) == 16, a, on(stream)), "MoE from-experts kernel");
+  return launched(launch_moe_from_experts(dt, on_grid(bits), a, on(stream)), "MoE from-experts kernel");
 }
 
 extern "C" ccl_status_t ccl_moe_from_experts_grad(const void* const* dout, const void* const* y, const size_t* y_rows,
@@ -262,7 +262,7 @@ extern "C" ccl_status_t ccl_moe_from_experts_grad(const void* const* dout, const
   a.hidden = hidden;
   a.p = p;
   a.k = k;
-  return launched(launch_moe_from_experts_grad(dt, alignment(bits) == 16, a, on(stream)), "MoE from-experts gradient kernel");
+  return launched(launch_moe_from_experts_grad(dt, on_grid(bits), a, on(stream)), "MoE from-experts gradient kernel");
 }
 
 // ---------------------------------------------------------------- products

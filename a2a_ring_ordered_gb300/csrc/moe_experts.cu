@@ -10,6 +10,7 @@
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
+#include "realign.cuh"
 
 namespace ccl {
 namespace {
@@ -143,28 +144,6 @@ __global__ void moe_sort_kernel(const __grid_constant__ MoeSortArgs a) {
 }
 
 // ------------------------------------------------------------------ rows
-// Raw copies of B bytes (16, 4 or 2).
-template <int B>
-struct Raw {
-  using T = uint32_t;
-};
-template <>
-struct Raw<16> {
-  using T = uint4;
-};
-template <int B>
-__device__ __forceinline__ typename Raw<B>::T ld_raw(const char* p) {
-  if constexpr (B == 16) return ld_once16(p);
-  else if constexpr (B == 4) return ld_once4(p);
-  else return ld_once2(p);
-}
-template <int B>
-__device__ __forceinline__ void st_raw(char* p, typename Raw<B>::T v) {
-  if constexpr (B == 16) st_stream16(p, v);
-  else if constexpr (B == 4) st_stream4(p, v);
-  else st_stream2(p, v);
-}
-
 // The row of a choice, or -1 where it has none in the buffer.
 __device__ __forceinline__ int64_t row_of(const int32_t* rows, uint64_t item, uint32_t cap) {
   const int32_t row = __ldg(rows + item);
@@ -173,19 +152,20 @@ __device__ __forceinline__ int64_t row_of(const int32_t* rows, uint64_t item, ui
 
 // A rank's (token, vector) pairs are one flat range (grid y = rank); each
 // vector is read once and written to the token's k rows.
-template <int B, int U>
+constexpr int kCopyVectors = 4;  // per thread, loaded together
 __global__ void __launch_bounds__(kThreads) moe_to_experts_kernel(const __grid_constant__ MoeRowsArgs a, uint32_t nv) {
+  constexpr int U = kCopyVectors;
   pdl_enter();
   const int r = blockIdx.y, k = a.k;
   const uint64_t total = static_cast<uint64_t>(a.tokens[r]) * nv;
-  const uint64_t row_bytes = static_cast<uint64_t>(nv) * B;
+  const uint64_t row_bytes = static_cast<uint64_t>(nv) * 16;
   const uint64_t f0 = (static_cast<uint64_t>(blockIdx.x) * U) * kThreads + threadIdx.x;
   if (f0 >= total) return;
   const char* x = static_cast<const char*>(a.x[r]);
-  typename Raw<B>::T w[U];
+  uint4 w[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (f0 + u * kThreads < total) w[u] = ld_raw<B>(x + (f0 + u * kThreads) * B);
+    if (f0 + u * kThreads < total) w[u] = ld_once16(x + (f0 + u * kThreads) * 16);
   char* out = static_cast<char*>(a.out[r]);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -194,11 +174,219 @@ __global__ void __launch_bounds__(kThreads) moe_to_experts_kernel(const __grid_c
     const uint64_t t = f / nv, v = f - t * nv;
     for (int j = 0; j < k; ++j) {
       const int64_t row = row_of(a.rows[r], t * k + j, a.cap[r]);
-      if (row >= 0) st_raw<B>(out + row * row_bytes + v * B, w[u]);
+      if (row >= 0) st_stream16(out + row * row_bytes + v * 16, w[u]);
     }
   }
 }
 
+// ------------------------------------------------------------ off the grid
+// Rows that do not all start on 16 bytes (odd widths, views): the written row
+// is walked in its own aligned granules.  A whole granule is stored at once,
+// from source bytes that two aligned loads hold, whatever their phase; the
+// granules that the row shares with its neighbours, its first and its last,
+// go element by element.
+struct Granule {
+  char* at;       // aligned
+  bool any;       // it holds bytes of the row
+  bool whole;     // and no others
+  uint32_t lo, hi;  // the row's bytes in it
+};
+__device__ __forceinline__ Granule granule_of(char* row, uint64_t row_bytes, uint64_t u) {
+  const uintptr_t first = reinterpret_cast<uintptr_t>(row), end = first + row_bytes;
+  const uintptr_t at = (first & ~static_cast<uintptr_t>(15)) + 16 * u;
+  Granule g;
+  g.at = reinterpret_cast<char*>(at);
+  g.any = at < end;
+  g.lo = at < first ? static_cast<uint32_t>(first - at) : 0u;
+  g.hi = at + 16 > end ? static_cast<uint32_t>(end - at) : 16u;
+  g.whole = g.any && g.lo == 0 && g.hi == 16;
+  return g;
+}
+// Granules that a row of so many bytes can touch.
+__host__ __device__ constexpr uint64_t granules(uint64_t row_bytes) { return (row_bytes + 30) / 16; }
+
+template <int B>
+__device__ __forceinline__ uint32_t ld_element(const char* p) {
+  if constexpr (B == 4) return ld_once4(p);
+  else return ld_once2(p);
+}
+template <int B>
+__device__ __forceinline__ void st_element(char* p, uint32_t v) {
+  if constexpr (B == 4) st_stream4(p, v);
+  else st_stream2(p, v);
+}
+
+// One flat range of (token, choice, granule of the choice's row) per rank.
+template <int B>
+__global__ void __launch_bounds__(kThreads) moe_to_experts_off_kernel(const __grid_constant__ MoeRowsArgs a, uint64_t row_bytes) {
+  pdl_enter();
+  const int r = blockIdx.y;
+  const uint64_t ng = granules(row_bytes);
+  const uint64_t f = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const uint64_t item = f / ng, u = f - item * ng;
+  if (item >= static_cast<uint64_t>(a.tokens[r]) * a.k) return;
+  const int64_t row = row_of(a.rows[r], item, a.cap[r]);
+  if (row < 0) return;
+  char* to = static_cast<char*>(a.out[r]) + row * row_bytes;
+  const Granule g = granule_of(to, row_bytes, u);
+  if (!g.any) return;
+  const char* from = static_cast<const char*>(a.x[r]) + item / a.k * row_bytes + (g.at - to);  // of the granule's first byte
+  if (g.whole) {
+    st_stream16(g.at, load16_anywhere(from));
+  } else {
+    for (uint32_t b = g.lo; b < g.hi; b += B) st_element<B>(g.at + b, ld_element<B>(from + b));
+  }
+}
+
+// One flat range of (token, granule of its output row) per rank; the choices'
+// loads are issued (4 at a time) before any is added.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) moe_from_experts_off_kernel(const __grid_constant__ MoeRowsArgs a, uint64_t row_bytes) {
+  constexpr int B = Elem<DT>::kBytes, N = 16 / B;
+  pdl_enter();
+  const int r = blockIdx.y, k = a.k;
+  const uint64_t ng = granules(row_bytes);
+  const uint64_t f = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const uint64_t t = f / ng, u = f - t * ng;
+  if (t >= a.tokens[r]) return;
+  char* to = static_cast<char*>(a.out[r]) + t * row_bytes;
+  const Granule g = granule_of(to, row_bytes, u);
+  if (!g.any) return;
+  const int64_t into = g.at - to;  // of the granule's first byte, from the row's
+  const char* y = static_cast<const char*>(a.y[r]);
+  const float* weights = a.weights[r];
+  float acc[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+  bool have = false;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    uint4 raw[4];
+    int64_t row[4];
+    float wt[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      row[b] = j0 + b < k ? row_of(a.rows[r], t * k + j0 + b, a.cap[r]) : -1;
+      wt[b] = (weights != nullptr && j0 + b < k) ? __ldg(weights + t * k + j0 + b) : 1.0f;
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (row[b] < 0) continue;
+      const char* p = y + row[b] * row_bytes + into;
+      if (g.whole) {
+        raw[b] = load16_anywhere(p);
+      } else {
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const uint32_t at = e * B;
+          const uint32_t v = at >= g.lo && at < g.hi ? ld_element<B>(p + at) : 0u;
+          w[at / 4] |= v << (8 * (at & 3));
+        }
+        raw[b] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (row[b] < 0) continue;
+      const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float prod = __fmul_rn(wt[b], widen<DT>(w, e));
+        acc[e] = have ? __fadd_rn(acc[e], prod) : prod;
+      }
+      have = true;
+    }
+  }
+  uint32_t w[4];
+  pack_out<DT, N>(acc, w);
+  if (g.whole) {
+    st_stream16(g.at, make_uint4(w[0], w[1], w[2], w[3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e * B >= g.lo && e * B < g.hi) store_one<DT>(g.at, e, w, e);
+  }
+}
+
+// As moe_from_experts_grad_kernel, a choice after the other: its rows are
+// walked in the granules of dy's row (y's where only the gates are wanted).
+template <int DT>
+__global__ void __launch_bounds__(kThreads) moe_from_experts_grad_off_kernel(const __grid_constant__ MoeRowsArgs a,
+                                                                            uint64_t row_bytes, int tpt) {
+  constexpr int B = Elem<DT>::kBytes, N = 16 / B;
+  __shared__ float part[kThreads / 32];
+  pdl_enter();
+  const int r = blockIdx.y, k = a.k;
+  const int group = threadIdx.x / tpt, in = threadIdx.x - group * tpt, lane = threadIdx.x & 31;
+  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * (kThreads / tpt) + group;
+  if (static_cast<uint64_t>(blockIdx.x) * (kThreads / tpt) >= a.tokens[r]) return;
+  const bool live = t < a.tokens[r];
+  const char* dout = static_cast<const char*>(a.x[r]) + t * row_bytes;
+  char* dy = static_cast<char*>(a.out[r]);
+  const char* y = static_cast<const char*>(a.y[r]);
+  float* dw = a.dweights[r];
+  const uint64_t ng = granules(row_bytes);
+  for (int j = 0; j < k; ++j) {
+    const int64_t row = live ? row_of(a.rows[r], t * k + j, a.cap[r]) : -1;
+    const float wt = (live && a.weights[r] != nullptr) ? __ldg(a.weights[r] + t * k + j) : 1.0f;
+    float dot = 0.0f;
+    if (row >= 0) {
+      char* walked = (dy != nullptr ? dy : const_cast<char*>(y)) + row * row_bytes;
+      for (uint64_t u = in; u < ng; u += tpt) {
+        const Granule g = granule_of(walked, row_bytes, u);
+        if (!g.any) break;
+        const int64_t into = g.at - walked;
+        uint32_t d[4] = {}, v[4] = {};
+        if (g.whole) {
+          const uint4 dq = load16_anywhere(dout + into);
+          d[0] = dq.x, d[1] = dq.y, d[2] = dq.z, d[3] = dq.w;
+          if (dw != nullptr) {
+            const uint4 vq = load16_anywhere(y + row * row_bytes + into);
+            v[0] = vq.x, v[1] = vq.y, v[2] = vq.z, v[3] = vq.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const uint32_t at = e * B;
+            if (at < g.lo || at >= g.hi) continue;
+            d[at / 4] |= ld_element<B>(dout + into + at) << (8 * (at & 3));
+            if (dw != nullptr) v[at / 4] |= ld_element<B>(y + row * row_bytes + into + at) << (8 * (at & 3));
+          }
+        }
+        float o[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float de = widen<DT>(d, e);
+          o[e] = __fmul_rn(wt, de);
+          if (dw != nullptr) dot = fmaf(widen<DT>(v, e), de, dot);
+        }
+        if (dy == nullptr) continue;
+        uint32_t w[4];
+        pack_out<DT, N>(o, w);
+        if (g.whole) {
+          st_stream16(g.at, make_uint4(w[0], w[1], w[2], w[3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (e * B >= g.lo && e * B < g.hi) store_one<DT>(g.at, e, w, e);
+        }
+      }
+    }
+    if (dw == nullptr) continue;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+    if (lane == 0) part[threadIdx.x >> 5] = dot;
+    __syncthreads();
+    if (live && in == 0) {
+      float sum = 0.0f;
+      for (int w = 0; w < tpt / 32; ++w) sum += part[group * (tpt / 32) + w];
+      dw[t * k + j] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+// -------------------------------------------------------------- on the grid
 // The same flat range; the k rows' loads are issued (8 at a time) before any
 // is added.
 template <int DT, int VEC>
@@ -338,12 +526,32 @@ cudaError_t launch_rows(void (*kernel)(Params...), uint64_t ctas, int p, cudaStr
   return err;
 }
 
-template <int B>
 cudaError_t launch_copy(int elem, const MoeRowsArgs& a, cudaStream_t s) {
-  constexpr int U = 4;
-  const uint32_t nv = static_cast<uint32_t>(a.hidden * elem / B);
-  const uint64_t total = static_cast<uint64_t>(most_tokens(a)) * nv;
-  return launch_rows(moe_to_experts_kernel<B, U>, (total + kThreads * U - 1) / (kThreads * U), a.p, s, a, nv);
+  const uint32_t nv = static_cast<uint32_t>(a.hidden * elem / 16);
+  const uint64_t total = static_cast<uint64_t>(most_tokens(a)) * nv, per = kThreads * kCopyVectors;
+  return launch_rows(moe_to_experts_kernel, (total + per - 1) / per, a.p, s, a, nv);
+}
+
+uint64_t ctas_for(uint64_t threads) { return (threads + kThreads - 1) / kThreads; }
+
+template <int DT>
+cudaError_t launch_back_off(const MoeRowsArgs& a, cudaStream_t s) {
+  const uint64_t row_bytes = a.hidden * Elem<DT>::kBytes;
+  return launch_rows(moe_from_experts_off_kernel<DT>, ctas_for(most_tokens(a) * granules(row_bytes)), a.p, s, a, row_bytes);
+}
+
+int threads_per_token(uint64_t units) {
+  int tpt = 32;
+  while (tpt < kThreads && static_cast<uint64_t>(tpt) < units) tpt *= 2;
+  return tpt;
+}
+
+template <int DT>
+cudaError_t launch_back_grad_off(const MoeRowsArgs& a, cudaStream_t s) {
+  const uint64_t row_bytes = a.hidden * Elem<DT>::kBytes;
+  const int tpt = threads_per_token(granules(row_bytes));
+  const uint64_t per = kThreads / tpt;
+  return launch_rows(moe_from_experts_grad_off_kernel<DT>, (most_tokens(a) + per - 1) / per, a.p, s, a, row_bytes, tpt);
 }
 
 template <int DT, int VEC>
@@ -356,8 +564,7 @@ cudaError_t launch_back(const MoeRowsArgs& a, cudaStream_t s) {
 template <int DT, int VEC>
 cudaError_t launch_back_grad(const MoeRowsArgs& a, cudaStream_t s) {
   const uint32_t nv = static_cast<uint32_t>(a.hidden / VEC);
-  int tpt = 32;
-  while (tpt < kThreads && static_cast<uint32_t>(tpt) < nv) tpt *= 2;
+  const int tpt = threads_per_token(nv);
   const uint64_t per = kThreads / tpt;
   return launch_rows(moe_from_experts_grad_kernel<DT, VEC>, (most_tokens(a) + per - 1) / per, a.p, s, a, nv, tpt);
 }
@@ -396,19 +603,22 @@ cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
   return err;
 }
 
-cudaError_t launch_moe_to_experts(int dt, int align, const MoeRowsArgs& a, cudaStream_t s) {
+cudaError_t launch_moe_to_experts(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s) {
   const int elem = dt == kF32 ? 4 : 2;
-  return align == 16 ? launch_copy<16>(elem, a, s) : align == 4 ? launch_copy<4>(elem, a, s) : launch_copy<2>(elem, a, s);
+  if (vec) return launch_copy(elem, a, s);
+  const uint64_t row_bytes = a.hidden * elem, ctas = ctas_for(static_cast<uint64_t>(most_tokens(a)) * a.k * granules(row_bytes));
+  return elem == 4 ? launch_rows(moe_to_experts_off_kernel<4>, ctas, a.p, s, a, row_bytes)
+                   : launch_rows(moe_to_experts_off_kernel<2>, ctas, a.p, s, a, row_bytes);
 }
 
 cudaError_t launch_moe_from_experts(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s) {
-  if (dt == kF32) return vec ? launch_back<kF32, 4>(a, s) : launch_back<kF32, 1>(a, s);
-  return vec ? launch_back<kBF16, 8>(a, s) : launch_back<kBF16, 1>(a, s);
+  if (dt == kF32) return vec ? launch_back<kF32, 4>(a, s) : launch_back_off<kF32>(a, s);
+  return vec ? launch_back<kBF16, 8>(a, s) : launch_back_off<kBF16>(a, s);
 }
 
 cudaError_t launch_moe_from_experts_grad(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s) {
-  if (dt == kF32) return vec ? launch_back_grad<kF32, 4>(a, s) : launch_back_grad<kF32, 1>(a, s);
-  return vec ? launch_back_grad<kBF16, 8>(a, s) : launch_back_grad<kBF16, 1>(a, s);
+  if (dt == kF32) return vec ? launch_back_grad<kF32, 4>(a, s) : launch_back_grad_off<kF32>(a, s);
+  return vec ? launch_back_grad<kBF16, 8>(a, s) : launch_back_grad_off<kBF16>(a, s);
 }
 
 }  // namespace ccl

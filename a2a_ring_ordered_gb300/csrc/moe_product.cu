@@ -26,6 +26,7 @@
 #include <cuda.h>  // CUtensorMap and its enums; nothing links the driver
 
 #include "device_common.cuh"
+#include "realign.cuh"
 
 namespace ccl {
 namespace {
@@ -250,24 +251,11 @@ __device__ __forceinline__ uint4 load16_if(uintptr_t p, bool take) {
   return v;
 }
 
-// Bytes [at % 16, at % 16 + 16) of the pair (lo, hi), of which the first
-// `valid` bf16 elements are kept and the others are zero.
-__device__ __forceinline__ uint4 shift_unit(const uint4 lo, const uint4 hi, uint32_t at, int valid) {
-  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  if (at & 8) {
+// `v` with the elements from `valid` on zero.
+__device__ __forceinline__ uint4 keep(const uint4 v, int valid) {
+  uint32_t o[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (at & 4) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[i] = __funnelshift_r(w[i], w[i + 1], (at & 2) * 8);
-    o[i] = 2 * i + 1 < valid ? o[i] : 2 * i < valid ? (o[i] & 0xFFFFu) : 0u;
-  }
+  for (int i = 0; i < 4; ++i) o[i] = 2 * i + 1 < valid ? o[i] : 2 * i < valid ? (o[i] & 0xFFFFu) : 0u;
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -308,7 +296,7 @@ __device__ __forceinline__ void fill_lines(char* dst, int lo, int hi, int tid, U
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int l = l0 + b * kApart;
-      if (l < hi) *reinterpret_cast<uint4*>(dst + l * 128 + ((u ^ (l & 7)) << 4)) = shift_unit(g0[b], g1[b], at[b], valid[b]);
+      if (l < hi) *reinterpret_cast<uint4*>(dst + l * 128 + ((u ^ (l & 7)) << 4)) = keep(shift16(g0[b], g1[b], at[b]), valid[b]);
     }
   }
 }

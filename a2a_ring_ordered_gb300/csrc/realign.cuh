@@ -37,6 +37,28 @@ __device__ __forceinline__ uint4 realign16(const uint4 lo, const uint4 hi, int d
   return o;
 }
 
+// Bytes [at % 16, at % 16 + 16) of the pair (lo, hi), without a branch: for
+// threads whose phases differ within a warp.
+__device__ __forceinline__ uint4 shift16(const uint4 lo, const uint4 hi, uint32_t at) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = (at & 8) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = (at & 4) ? w[i + 1] : w[i];
+  const uint32_t sh = (at & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh), __funnelshift_r(w[2], w[3], sh),
+                    __funnelshift_r(w[3], w[4], sh));
+}
+
+// The 16 bytes at p, wherever it is, by the aligned granules that hold them.
+// Both allocate in L1: a granule's other bytes are the neighbour thread's.
+__device__ __forceinline__ uint4 load16_anywhere(const char* p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p), base = at & ~static_cast<uintptr_t>(15);
+  const uint4 lo = ld_l1_16(reinterpret_cast<const void*>(base));
+  const uint4 hi = ld_l1_16(reinterpret_cast<const void*>((at + 15) & ~static_cast<uintptr_t>(15)));
+  return shift16(lo, hi, static_cast<uint32_t>(at - base));
+}
+
 // The next lane's granule (lane 31 gets `own_next`, which it loaded itself).
 __device__ __forceinline__ uint4 next_lane(const uint4 v, const uint4 own_next, int lane) {
   uint4 n;
