@@ -38,12 +38,31 @@ constexpr int kOperandBytes = 128 * kStep * 2;  // one CTA's share of A or B in 
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMaxGroups = 2048;   // (rank, expert) pairs per launch
 constexpr int kLaunchRanks = 8;    // keeps the parameter block under 4 KB
-constexpr int kLoaderThreads = 256;
 constexpr int kEpilogueWarps = 8;  // two per 32 TMEM lanes
 constexpr int kTmaWarp = kEpilogueWarps, kMmaWarp = kTmaWarp + 1, kLoaderWarp = kMmaWarp + 1;
-constexpr int kProductThreads = kLoaderWarp * 32 + kLoaderThreads;
+// REGS (fp32 weight gradients, see kMostSummed): the epilogue's threads hold
+// 128 running sums each, for which the other warps give registers up; TMA
+// reads both operands, so that two warps are enough to clear last rows.
+// The shares add up to what the block is launched with.
+template <bool REGS>
+struct Crew {
+  static constexpr int kLoaders = REGS ? 64 : 256;  // loader threads
+  static constexpr int kThreads = kLoaderWarp * 32 + kLoaders;
+  static constexpr int kLaunchRegs = 168, kEpilogueRegs = 216, kOtherRegs = 72;  // a thread
+  static_assert(!REGS || (kEpilogueWarps * 32 * kEpilogueRegs + (kThreads - kEpilogueWarps * 32) * kOtherRegs == kThreads * kLaunchRegs &&
+                          kThreads % 128 == 0 && kThreads * kLaunchRegs <= 65536),
+                "register shares");
+};
 constexpr int kSmallBox = 16;      // rows of B's small box
 constexpr uint32_t kTmemColumns = 512;
+// The tensor core cuts its fp32 sums at the last bit instead of rounding them,
+// towards zero, once per 16 contraction elements: 1e-6 of the result after
+// 1024 of them, 1.9e-5 after 16384, where rounded sums stay at 2e-7 to 4e-7.
+// bf16 outputs round to 4e-3 and hide that; an fp32 weight gradient is summed
+// in parts of at most so many rows (5e-7), which the epilogue adds up: in
+// registers, or, where loaders fill the stages and set the pace, in the output
+// (32 experts of 1024 rows by TMA: 948 us that way).
+constexpr int kMostSummed = 512;
 constexpr long long kWaitCycles = 1ll << 32;  // two seconds
 
 __device__ unsigned int g_product_error;  // nonzero: a bounded wait ran out
@@ -70,7 +89,7 @@ struct Shared {
   uint64_t tmem_empty[2];
   uint32_t tmem;
   uint32_t dead;
-  uint32_t scan[kProductThreads / 32];
+  uint32_t scan[Crew<false>::kThreads / 32];
   uint32_t first[kMaxGroups + 1];  // row tiles before each (rank, expert)
   int32_t lo[kMaxGroups];          // its first row
   int32_t count[kMaxGroups];       // and its rows
@@ -193,6 +212,7 @@ struct Tile {
   int rank, expert;
   int lo;       // first row of the expert
   int depth;    // contraction elements
+  int segment;  // of them per sum in tensor memory: a multiple of kStep, or depth
   int c0;       // first column: a row of the rank, or an n
   int cols;     // columns that are stored
   int width;    // columns that are computed: a multiple of 32
@@ -202,7 +222,8 @@ struct Tile {
 // The same value in every lane, and known to be.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
-template <int KIND>
+// SPLIT: sums longer than kMostSummed are made in parts.
+template <int KIND, bool SPLIT>
 __device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int groups, uint64_t index, uint32_t mt) {
   const uint32_t rt = static_cast<uint32_t>(index / mt);
   Tile t;
@@ -237,6 +258,11 @@ __device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int 
   t.cols = uniform(t.cols);
   t.depth = uniform(t.depth);
   t.width = (t.cols + 31) & ~31;
+  t.segment = t.depth;
+  if (SPLIT && t.depth > kMostSummed) {
+    const int parts = (t.depth + kMostSummed - 1) / kMostSummed;
+    t.segment = ((t.depth + parts - 1) / parts + kStep - 1) / kStep * kStep;
+  }
   return t;
 }
 
@@ -260,13 +286,14 @@ __device__ __forceinline__ uint4 keep(const uint4 v, int valid) {
 }
 
 // A barrier among the loaders, and whether any of them says so.
+template <int THREADS>
 __device__ __forceinline__ bool any_loader(bool x) {
   uint32_t r;
   __syncwarp();
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x)), "n"(kLoaderThreads)
+      : "r"(static_cast<uint32_t>(x)), "n"(THREADS)
       : "memory");
   return r != 0;
 }
@@ -275,9 +302,9 @@ __device__ __forceinline__ bool any_loader(bool x) {
 // unit(l, u, p) says how many elements of a unit there are and points p at
 // them.  They come as the whole 16-byte granules that hold at least one of
 // them, kBatch units' loads issued before any is stored.
-template <typename Unit>
+template <int THREADS, typename Unit>
 __device__ __forceinline__ void fill_lines(char* dst, int lo, int hi, int tid, Unit unit) {
-  constexpr int kBatch = 4, kApart = kLoaderThreads / 8;
+  constexpr int kBatch = 4, kApart = THREADS / 8;
   const int u = tid & 7;
   for (int l0 = lo + (tid >> 3); l0 < hi; l0 += kBatch * kApart) {
     uint4 g0[kBatch], g1[kBatch];
@@ -302,8 +329,8 @@ __device__ __forceinline__ void fill_lines(char* dst, int lo, int hi, int tid, U
 }
 
 // Zeros in the lines of contraction rows from `left` on: line l holds row l mod 64.
-__device__ __forceinline__ void clear_lines(char* dst, int lines, int left, int tid) {
-  for (int i = tid; i < lines * 8; i += kLoaderThreads)
+__device__ __forceinline__ void clear_lines(char* dst, int lines, int left, int tid, int threads) {
+  for (int i = tid; i < lines * 8; i += threads)
     if (((i >> 3) & 63) >= left) *reinterpret_cast<uint4*>(dst + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
@@ -343,12 +370,22 @@ __device__ __forceinline__ void store_columns(char* p, uint64_t ld, const uint32
   else store_rows<OUT, false>(p, ld, v, count, live, even);
 }
 
+// As store_rows<kF32>, added to what the thread itself has stored there.
+__device__ __forceinline__ void add_rows(char* p, uint64_t ld, const uint32_t* v, int count, bool live) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (live && j < count) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p + j * ld), "f"(__uint_as_float(v[j])) : "memory");
+}
+
 // ------------------------------------------------------------------- kernel
-template <int KIND, int OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+template <int KIND, int OUT, bool REGS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads, 1)
     product_kernel(const __grid_constant__ PairArgs a) {
   constexpr bool kAColumns = KIND != kProductForward;     // A's contiguous axis is m
   constexpr bool kBColumns = KIND == kProductGradWeight;  // B's contiguous axis is c
+  constexpr bool kSplit = kBColumns && OUT == kF32;
+  using CREW = Crew<REGS>;
+  static_assert(!REGS || kSplit, "only sums in parts are held in registers");
   extern __shared__ char dynamic[];
   char* stages = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
   Shared& s = *reinterpret_cast<Shared*>(stages + static_cast<size_t>(kStages) * kStageBytes);
@@ -385,7 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
   // rows of every (rank, expert), cut to what the buffer holds, and a running
   // count of their row tiles: each thread counts a run of groups, then a scan
   {
-    const int per = (groups + kProductThreads - 1) / kProductThreads;
+    const int per = (groups + CREW::kThreads - 1) / CREW::kThreads;
     const int g0 = min(tid * per, groups), g1 = min(g0 + per, groups);
     uint32_t mine = 0;
     for (int g = g0; g < g1; ++g) {
@@ -412,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
       s.first[g] = run;
       run += (s.count[g] + kTile - 1) / kTile;
     }
-    if (tid == kProductThreads - 1) s.first[groups] = run;
+    if (tid == CREW::kThreads - 1) s.first[groups] = run;
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -423,6 +460,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                                                      : static_cast<uint64_t>(s.first[groups])) * mt;
   volatile uint32_t* dead = &s.dead;
 
+  if (warp >= kEpilogueWarps) {
+  if constexpr (REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CREW::kOtherRegs));
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------------ TMA
     // The whole warp walks the stages, so that addresses and coordinates are
@@ -433,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     const uint32_t own = smem_addr(s.full), empty = smem_addr(s.empty), data = smem_addr(stages);
     bool ok = true;
     for (uint64_t i = pair; ok && i < tiles; i += pairs) {
-      const Tile t = tile_at<KIND>(a, s, groups, i, mt);
+      const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
       const int half = t.width >> 1;
       const int c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
       const int boxes = kBColumns ? (half + 63) / 64 : half > 64 ? 1 : (half + kSmallBox - 1) / kSmallBox;
@@ -514,38 +553,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
       const uint64_t b0 = descriptor(smem_addr(stages) + kOperandBytes, kBColumns ? kStep * 128 : 16);
       constexpr uint64_t kNextA = (kAColumns ? 2048 : 32) >> 4, kNextB = (kBColumns ? 2048 : 32) >> 4;
       bool ok = true;
-      for (uint64_t i = pair; ok && i < tiles; i += pairs, ++n) {
-        const Tile t = tile_at<KIND>(a, s, groups, i, mt);
-        const uint32_t buf = n & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_empty[buf]), ((n >> 1) & 1) ^ 1, dead))) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t d = tmem + buf * kTile;
+      for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+        const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAColumns ? 1u << 15 : 0u) | (kBColumns ? 1u << 16 : 0u) |
                                (static_cast<uint32_t>(t.width >> 3) << 17) | (16u << 24);
-        for (int k = 0; k < t.depth; k += kStep) {
-          const bool loaded = !a.tma_a || !a.tma_b || (kBColumns && k + kStep > t.depth);
-          const uint32_t bar = full + 8 * ring.stage;
-          if (!__all_sync(0xFFFFFFFFu, loaded ? mbar_wait<true>(bar, ring.phase, dead) : mbar_wait(bar, ring.phase, dead))) {
+        int k0 = 0;
+        do {  // a segment, also of an expert without rows
+          const uint32_t buf = n & 1;
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_empty[buf]), ((n >> 1) & 1) ^ 1, dead))) {
             ok = false;
             break;
           }
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (issuer) {
-            const uint64_t da = a0 + ring.stage * (kStageBytes >> 4), db = b0 + ring.stage * (kStageBytes >> 4);
-            const int left = t.depth - k;  // contraction elements from here
-            mma(d, da, db, idesc, k != 0);
-            if (left > 16) mma(d, da + kNextA, db + kNextB, idesc, 1);
-            if (left > 32) mma(d, da + 2 * kNextA, db + 2 * kNextB, idesc, 1);
-            if (left > 48) mma(d, da + 3 * kNextA, db + 3 * kNextB, idesc, 1);
-            commit_pair(empty + 8 * ring.stage);
+          const uint32_t d = tmem + buf * kTile;
+          const int k1 = min(k0 + t.segment, t.depth);
+          for (int k = k0; k < k1; k += kStep) {
+            const bool loaded = !a.tma_a || !a.tma_b || (kBColumns && k + kStep > t.depth);
+            const uint32_t bar = full + 8 * ring.stage;
+            if (!__all_sync(0xFFFFFFFFu, loaded ? mbar_wait<true>(bar, ring.phase, dead) : mbar_wait(bar, ring.phase, dead))) {
+              ok = false;
+              break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (issuer) {
+              const uint64_t da = a0 + ring.stage * (kStageBytes >> 4), db = b0 + ring.stage * (kStageBytes >> 4);
+              const int left = k1 - k;  // contraction elements from here
+              mma(d, da, db, idesc, k != k0);
+              if (left > 16) mma(d, da + kNextA, db + kNextB, idesc, 1);
+              if (left > 32) mma(d, da + 2 * kNextA, db + 2 * kNextB, idesc, 1);
+              if (left > 48) mma(d, da + 3 * kNextA, db + 3 * kNextB, idesc, 1);
+              commit_pair(empty + 8 * ring.stage);
+            }
+            ring.next();
           }
-          ring.next();
-        }
-        if (ok && issuer) commit_pair(smem_addr(&s.tmem_full[buf]));
-        __syncwarp();
+          if (ok && issuer) commit_pair(smem_addr(&s.tmem_full[buf]));
+          __syncwarp();
+          k0 += t.segment;
+          ++n;
+        } while (ok && k0 < t.depth);
       }
     }
-  } else if (warp >= kLoaderWarp) {
+  } else {
     // -------------------------------------------------------------- loaders
     if (loaders) {
       const int ltid = tid - kLoaderWarp * 32;
@@ -556,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
       uint32_t parity = 0;
       bool ok = true;
       for (uint64_t i = pair; ok && i < tiles; i += pairs) {
-        const Tile t = tile_at<KIND>(a, s, groups, i, mt);
+        const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
         const int half = t.width >> 1;
         const int64_t c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
         const int64_t N = a.n, K = a.contract, rows = a.rows[t.rank];
@@ -599,14 +647,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             return max(min(valid, 64) - u * 8, 0);
           };
           if (here) {
-            fill_lines(sa, l_lo, l_hi, ltid, unit);
+            if constexpr (!REGS) fill_lines<CREW::kLoaders>(sa, l_lo, l_hi, ltid, unit);
             if (tail) {  // rows behind the expert's last: the next expert's, or nobody's
-              if (a.tma_a) clear_lines(sa, 128, left, ltid);
-              if (a.tma_b) clear_lines(sb, lines_b, left, ltid);
+              if (a.tma_a) clear_lines(sa, 128, left, ltid, CREW::kLoaders);
+              if (a.tma_b) clear_lines(sb, lines_b, left, ltid, CREW::kLoaders);
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (any_loader(!here)) {  // one answer for all of them
+          if (any_loader<CREW::kLoaders>(!here)) {  // one answer for all of them
             ok = false;
             break;
           }
@@ -614,37 +662,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
       }
     }
+  }
   } else {
     // ------------------------------------------------------------- epilogue
+    if constexpr (REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CREW::kEpilogueRegs));
     uint32_t n = 0;
-    for (uint64_t i = pair; i < tiles; i += pairs, ++n) {
-      const Tile t = tile_at<KIND>(a, s, groups, i, mt);
-      const uint32_t buf = n & 1;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_full[buf]), (n >> 1) & 1, dead))) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t quarter = warp & 3;  // the 32 lanes that this warp can read
+    bool ok = true;
+    const uint32_t quarter = warp & 3;  // the 32 lanes that this warp can read
+    constexpr int kBytes = Elem<OUT>::kBytes;
+    for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+      const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
       const uint32_t m = t.m0 + cta * 128 + quarter * 32 + lane;
       const uint64_t at = (KIND == kProductGradWeight ? static_cast<uint64_t>(t.expert) * a.n + t.c0 : static_cast<uint64_t>(t.c0)) * M + m;
-      constexpr int kBytes = Elem<OUT>::kBytes;
       // bf16 outputs two by two: where every row starts on four bytes
       const bool even = OUT == kBF16 && (M & 1) == 0 && (reinterpret_cast<uintptr_t>(a.out[t.rank]) & 3) == 0;
       char* out = static_cast<char*>(a.out[t.rank]) + at * kBytes;
-      const uint32_t from = tmem + buf * kTile + (quarter << 21);  // lane 32 * quarter
-      for (int c = (warp >> 2) * 32; c < t.width; c += kEpilogueWarps / 4 * 32) {
-        uint32_t v[32];
-        if (t.depth > 0) {
-          tmem_load32(from + c, v);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        } else {
+      const uint64_t ld = static_cast<uint64_t>(M) * kBytes;
+      const int c0 = (warp >> 2) * 32;  // every other 32 columns are this warp's
+      float sum[REGS ? kTile / 64 : 1][32];  // this thread's columns
+      if constexpr (REGS) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0;
-        }
-        store_columns<OUT>(out + static_cast<uint64_t>(c) * M * kBytes, static_cast<uint64_t>(M) * kBytes, v, t.cols - c, m < M, even);
-        __syncwarp();
+        for (int q = 0; q < kTile / 64; ++q)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[q][j] = 0.0f;
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(in_cta(smem_addr(&s.tmem_empty[buf]), 0));
+      int k0 = 0;
+      do {  // a segment
+        const uint32_t buf = n & 1;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_full[buf]), (n >> 1) & 1, dead))) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t from = tmem + buf * kTile + (quarter << 21);  // lane 32 * quarter
+        if constexpr (REGS) {
+          if (t.depth > 0) {
+#pragma unroll
+            for (int q = 0; q < kTile / 64; ++q) {
+              if (c0 + q * 64 < t.width) {
+                uint32_t v[32];
+                tmem_load32(from + c0 + q * 64, v);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[q][j] += __uint_as_float(v[j]);
+              }
+            }
+          }
+        } else {
+          for (int c = c0; c < t.width; c += 64) {
+            uint32_t v[32];
+            if (t.depth > 0) {
+              tmem_load32(from + c, v);
+              asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0;
+            }
+            char* p = out + static_cast<uint64_t>(c) * ld;
+            if (kSplit && k0 > 0) add_rows(p, ld, v, t.cols - c, m < M);
+            else store_columns<OUT>(p, ld, v, t.cols - c, m < M, even);
+            __syncwarp();
+          }
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(in_cta(smem_addr(&s.tmem_empty[buf]), 0));
+        k0 += t.segment;
+        ++n;
+      } while (k0 < t.depth);
+      if constexpr (REGS) {
+#pragma unroll
+        for (int q = 0; q < kTile / 64; ++q) {
+          const int c = c0 + q * 64;
+          if (ok && c < t.cols)
+            store_columns<OUT>(out + static_cast<uint64_t>(c) * ld, ld, reinterpret_cast<const uint32_t*>(sum[q]), t.cols - c, m < M, even);
+        }
+      }
     }
   }
   __syncwarp();
@@ -694,16 +787,23 @@ bool encode(CUtensorMap* map, const void* p, uint64_t width, uint64_t height, ui
 // Whether TMA can read rows of `width` bf16 elements at p.
 bool on_grid(const void* p, uint64_t width) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && width % 8 == 0; }
 
-template <int KIND, int OUT>
+template <int KIND, int OUT, bool REGS = false>
 cudaError_t launch_pairs(const PairArgs& a, uint64_t most_tiles, cudaStream_t s) {
+  const auto kernel = product_kernel<KIND, OUT, REGS>;
   // per host thread and device: the attribute belongs to the context
   static thread_local int ready_dev = -1;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev != ready_dev) {
-    err = cudaFuncSetAttribute(product_kernel<KIND, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (err != cudaSuccess) return err;
+    if (REGS) {  // a block launched with fewer registers would wait for its shares for ever
+      cudaFuncAttributes attr;
+      err = cudaFuncGetAttributes(&attr, kernel);
+      if (err != cudaSuccess) return err;
+      if (attr.numRegs < Crew<REGS>::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    }
     ready_dev = dev;
   }
   uint64_t pairs = static_cast<uint64_t>(current_sm_count() / 2);
@@ -711,7 +811,7 @@ cudaError_t launch_pairs(const PairArgs& a, uint64_t most_tiles, cudaStream_t s)
   if (pairs == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-  cfg.blockDim = dim3(kProductThreads);
+  cfg.blockDim = dim3(Crew<REGS>::kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -719,7 +819,7 @@ cudaError_t launch_pairs(const PairArgs& a, uint64_t most_tiles, cudaStream_t s)
   attr[0].val.programmaticStreamSerializationAllowed = CCL_PDL ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, product_kernel<KIND, OUT>, a);
+  err = cudaLaunchKernelEx(&cfg, kernel, a);
   if (err == cudaSuccess) note_launch();
   return err;
 }
@@ -783,8 +883,9 @@ cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& args, cu
     const uint64_t most_tiles = (kind == kProductGradWeight ? static_cast<uint64_t>(a.p) * E * ((n + kTile - 1) / kTile) : rows) * mt;
     const cudaError_t err = kind == kProductForward     ? launch_pairs<kProductForward, kBF16>(a, most_tiles, s)
                             : kind == kProductGradInput ? launch_pairs<kProductGradInput, kBF16>(a, most_tiles, s)
-                            : out_dt == kF32            ? launch_pairs<kProductGradWeight, kF32>(a, most_tiles, s)
-                                                        : launch_pairs<kProductGradWeight, kBF16>(a, most_tiles, s);
+                            : out_dt == kBF16           ? launch_pairs<kProductGradWeight, kBF16>(a, most_tiles, s)
+                            : a.tma_a && a.tma_b        ? launch_pairs<kProductGradWeight, kF32, true>(a, most_tiles, s)
+                                                        : launch_pairs<kProductGradWeight, kF32>(a, most_tiles, s);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;

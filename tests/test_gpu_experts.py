@@ -416,3 +416,18 @@ def test_rows_past_32_bit_offsets(lib):
     out = [torch.empty_like(x)]
     lib.ccl_moe_from_experts(ordered, rows, None, out)
     assert torch.equal(out[0], x * 2)
+
+
+def test_long_sums_keep_fp32_precision(lib):
+    """An fp32 weight gradient over 20,000 rows.  The tensor core cuts its sums
+    towards zero once per 16 rows, by half a unit in the last place (2^-24) on
+    average; in parts of 512 rows that is at most 32 * 2^-24 of the result,
+    where one sum would be off by 1250 * 2^-24.  Odd widths take the loaders."""
+    rng = np.random.default_rng(10)
+    for n, k in ((128, 256), (99, 131)):
+        x, dy = bf16_exact(rng, (20000, k)), bf16_exact(rng, (20000, n))
+        dw = [torch.empty(1, n, k, device="cuda")]
+        lib.ccl_moe_product_grad_weight([dev(dy, torch.bfloat16)], [dev(x, torch.bfloat16)],
+                                        [torch.tensor([0, 20000], dtype=torch.int32, device="cuda")], dw)
+        want = dy.astype(np.float64).T @ x.astype(np.float64)
+        assert np.linalg.norm(host(dw[0])[0] - want) <= 32 * 2.0 ** -24 * np.linalg.norm(want)
