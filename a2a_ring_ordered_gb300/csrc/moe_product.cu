@@ -790,21 +790,17 @@ bool on_grid(const void* p, uint64_t width) { return (reinterpret_cast<uintptr_t
 template <int KIND, int OUT, bool REGS = false>
 cudaError_t launch_pairs(const PairArgs& a, uint64_t most_tiles, cudaStream_t s) {
   const auto kernel = product_kernel<KIND, OUT, REGS>;
-  // per host thread and device: the attribute belongs to the context
-  static thread_local int ready_dev = -1;
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (err != cudaSuccess) return err;
-  if (dev != ready_dev) {
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (err != cudaSuccess) return err;
-    if (REGS) {  // a block launched with fewer registers would wait for its shares for ever
+  if (REGS) {  // a block launched with fewer registers would wait for its shares for ever
+    static thread_local int regs = 0;
+    if (regs == 0) {
       cudaFuncAttributes attr;
       err = cudaFuncGetAttributes(&attr, kernel);
       if (err != cudaSuccess) return err;
-      if (attr.numRegs < Crew<REGS>::kLaunchRegs) return cudaErrorInvalidConfiguration;
+      regs = attr.numRegs;
     }
-    ready_dev = dev;
+    if (regs < Crew<REGS>::kLaunchRegs) return cudaErrorInvalidConfiguration;
   }
   uint64_t pairs = static_cast<uint64_t>(current_sm_count() / 2);
   if (most_tiles < pairs) pairs = most_tiles;
