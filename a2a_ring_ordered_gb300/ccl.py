@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import struct
 from typing import Sequence
@@ -95,7 +96,7 @@ def _load() -> ctypes.CDLL:
         "ccl_moe_dispatch": (st, [pp, pp, vp, pp, i32, sz, i32, i32, sz, i32, pp, ctypes.POINTER(sz),
                                   pp, pp, vp]),
         "ccl_moe_combine": (st, [pp, ctypes.POINTER(sz), pp, pp, vp, pp, i32, sz, i32, i32, sz, pp, vp]),
-        # arrays of addresses and sizes come as packed bytes (_pointers, _sizes)
+        # arrays of addresses and sizes come as packed bytes (_ranks, _shaped, _sizes)
         "ccl_moe_sort": (st, [vp, vp, i32, i32, i32, vp, vp, vp, vp]),
         "ccl_moe_to_experts": (st, [vp, vp, vp, i32, i32, sz, i32, vp, vp, vp]),
         "ccl_moe_from_experts": (st, [vp, vp, vp, vp, vp, i32, i32, sz, i32, vp, vp]),
@@ -662,41 +663,29 @@ def ccl_moe_combine(y, expert_ids, weights, counts, slots, num_experts: int, out
 
 
 # --------------------------------------------------- MoE: a rank's own experts
-# These calls run once per layer and token step, on tens of microseconds of GPU
-# work, so their marshalling is kept short: one pass over each list with the
-# cheap tensor attributes, addresses packed with struct (an eighth of the time
-# that a ctypes array takes), and _tensors' full checks, with their messages,
-# only where the pass finds something.
-@functools.lru_cache(maxsize=None)
-def _packer(code: str, count: int):
-    return struct.Struct(f"{count}{code}").pack
-
-
-def _pointers(ts) -> bytes:
-    return _packer("P", len(ts))(*[t.data_ptr() for t in ts])
+# These calls run once per layer and token step, on microseconds of GPU work,
+# so their marshalling is kept short: one pass over each list with the cheap
+# tensor attributes, addresses packed with struct (an eighth of the time that a
+# ctypes array takes), and _tensors' full checks, with their messages, only
+# where the pass finds something amiss.
+_PACK_POINTERS = [struct.Struct(f"{n}P").pack for n in range(CCL_MAX_RANKS + 1)]
+_PACK_SIZES = [struct.Struct(f"{n}N").pack for n in range(CCL_MAX_RANKS + 1)]
 
 
 def _sizes(values) -> bytes:
-    return _packer("N", len(values))(*values)
+    return _PACK_SIZES[len(values)](*values)
 
 
-def _buffers(ts, name: str, dtype=None, p: int | None = None):
-    """The rank buffers of an argument: contiguous, on one device, of one dtype."""
-    if type(ts) is not list:
-        ts = list(ts)
+def _explain(ts, name: str, p=None, dtype=None):
+    """The rank buffers by the slow road: raises where one of them is not a
+    contiguous tensor of the dtype on the first one's device."""
+    ts = list(ts)
+    for i, t in enumerate(ts):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name}[{i}] must be a CUDA tensor or a pinned host tensor")
+    ts = _tensors(ts, name)
     if p is not None and len(ts) != p:
         raise ValueError(f"{name} must hold {p} rank buffers, got {len(ts)}")
-    if ts:
-        first = ts[0]
-        if isinstance(first, torch.Tensor) and len(ts) <= CCL_MAX_RANKS:
-            want, device = dtype or first.dtype, first.get_device()
-            if device >= 0:
-                for t in ts:
-                    if not isinstance(t, torch.Tensor) or t.dtype is not want or t.get_device() != device or not t.is_contiguous():
-                        break
-                else:
-                    return ts
-    ts = _tensors(ts, name)
     if dtype is not None and ts[0].dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {ts[0].dtype}")
     return ts
@@ -704,39 +693,58 @@ def _buffers(ts, name: str, dtype=None, p: int | None = None):
 
 def _ranks(ts, name: str, p: int, dtype, rows, width: int) -> bytes:
     """Addresses of the p rank buffers, rank r of rows[r] rows of `width` elements."""
-    ts = _buffers(ts, name, dtype, p)
+    try:
+        device, pointers = ts[0].get_device(), []
+        if device >= 0 and len(ts) == p:
+            for t, n in zip(ts, rows):
+                if t.dtype is not dtype or t.get_device() != device or t.numel() != n * width or not t.is_contiguous():
+                    break
+                pointers.append(t.data_ptr())
+            else:
+                return _PACK_POINTERS[p](*pointers)
+    except (AttributeError, TypeError, IndexError):
+        pass
+    ts = _explain(ts, name, p, dtype)
     for r, t in enumerate(ts):
         if t.numel() != rows[r] * width:
             raise ValueError(f"{name}[{r}] has {t.numel()} elements, expected {rows[r]} x {width}")
-    return _pointers(ts)
+    return _PACK_POINTERS[p](*[t.data_ptr() for t in ts])
+
+
+def _shaped(ts, name: str, dims: int, p=None, dtype=None):
+    """(addresses, first tensor, first dimension of each rank, the others) of
+    rank buffers of `dims` dimensions that are alike but for the first."""
+    try:
+        first = ts[0]
+        rest = tuple(first.shape)[1:]
+        device, want, per = first.get_device(), dtype or first.dtype, math.prod(rest)
+        if device >= 0 and (p is None or len(ts) == p) and 1 + len(rest) == dims:
+            pointers, sizes = [], []
+            for t in ts:
+                n = t.shape[0]  # of two dimensions, the count of elements says the second
+                if (t.dtype is not want or t.get_device() != device or not t.is_contiguous() or t.dim() != dims
+                        or t.numel() != n * per or (dims > 2 and t.shape[1:] != rest)):
+                    break
+                pointers.append(t.data_ptr())
+                sizes.append(n)
+            else:
+                return _PACK_POINTERS[len(ts)](*pointers), first, sizes, rest
+    except (AttributeError, TypeError, IndexError):
+        pass
+    ts = _explain(ts, name, p, dtype)
+    rest = tuple(ts[0].shape)[1:]
+    for r, t in enumerate(ts):
+        if t.dim() != dims or tuple(t.shape)[1:] != rest:
+            raise ValueError(f"{name}[{r}] must have {dims} dimensions, all but the first as the other ranks'")
+    return _PACK_POINTERS[len(ts)](*[t.data_ptr() for t in ts]), ts[0], [t.shape[0] for t in ts], rest
 
 
 def _choices(rows, name: str = "rows"):
-    """(buffers, tokens of each rank, k) of a list of (tokens, k) int32 tensors."""
-    rows = _buffers(rows, name, torch.int32)
-    k, tokens = None, []
-    for r, t in enumerate(rows):
-        shape = t.shape
-        this = shape[1] if len(shape) == 2 else 1
-        if k is None:
-            k = this
-        if this != k or not 1 <= len(shape) <= 2:
-            raise ValueError(f"{name}[{r}] must be (tokens, {k})")
-        tokens.append(shape[0])
-    return rows, tokens, k
-
-
-def _row_buffers(ts, name: str, p: int | None = None, dtype=None):
-    """(buffers, rows of each rank, width) of a list of (rows, width) tensors."""
-    ts = _buffers(ts, name, dtype, p)
-    width, rows = None, []
-    for r, t in enumerate(ts):
-        shape = t.shape
-        if len(shape) != 2 or (width is not None and shape[1] != width):
-            raise ValueError(f"{name}[{r}] must be (rows, {'width' if width is None else width})")
-        width = shape[1]
-        rows.append(shape[0])
-    return ts, rows, width
+    """(addresses, first tensor, tokens of each rank, k) of a list of (tokens, k)
+    int32 tensors; of one dimension, k is 1."""
+    flat = len(rows) > 0 and isinstance(rows[0], torch.Tensor) and rows[0].dim() == 1
+    pointers, first, tokens, rest = _shaped(rows, name, 1 if flat else 2, None, torch.int32)
+    return pointers, first, tokens, 1 if flat else rest[0]
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -753,120 +761,115 @@ def ccl_moe_sort(expert_ids, num_experts: int, offsets, rows, first_expert=None,
     """expert_ids[r] ((tokens, k) int32) -> offsets[r] (num_experts + 1 int32) and
     rows[r] ((tokens, k) int32: the row of each choice in expert order, -1 for
     an id outside [first_expert[r], first_expert[r] + num_experts))."""
-    ids, tokens, k = _choices(expert_ids, "expert_ids")
-    p = len(ids)
+    ids, one, tokens, k = _choices(expert_ids, "expert_ids")
+    p = len(tokens)
     offsets = _ranks(offsets, "offsets", p, torch.int32, [num_experts + 1] * p, 1)
     rows = _ranks(rows, "rows", p, torch.int32, tokens, k)
     first = None
     if first_expert is not None:
         if len(first_expert) != p:
             raise ValueError(f"first_expert must hold {p} numbers")
-        first = _packer("i", p)(*first_expert)
-    _check(LIB.ccl_moe_sort(_pointers(ids), _sizes(tokens), p, k, num_experts, first, offsets, rows,
-                            _stream_of(stream, ids[0])), "ccl_moe_sort")
+        first = struct.pack(f"{p}i", *first_expert)
+    _check(LIB.ccl_moe_sort(ids, _sizes(tokens), p, k, num_experts, first, offsets, rows, _stream_of(stream, one)),
+           "ccl_moe_sort")
 
 
 def ccl_moe_to_experts(x, rows, sorted, stream=None) -> None:
     """sorted[r][rows[r][t, j]] = x[r][t]: the tokens' rows in expert order."""
-    rows, tokens, k = _choices(rows)
-    p = len(rows)
-    sorted, cap, hidden = _row_buffers(sorted, "sorted", p)
-    x = _ranks(x, "x", p, sorted[0].dtype, tokens, hidden)
-    _check(LIB.ccl_moe_to_experts(x, _pointers(rows), _sizes(tokens), p, k, hidden, _dtype_code(sorted[0]),
-                                  _pointers(sorted), _sizes(cap), _stream_of(stream, rows[0])), "ccl_moe_to_experts")
+    rows, _, tokens, k = _choices(rows)
+    p = len(tokens)
+    sorted, one, cap, (hidden,) = _shaped(sorted, "sorted", 2, p)
+    x = _ranks(x, "x", p, one.dtype, tokens, hidden)
+    _check(LIB.ccl_moe_to_experts(x, rows, _sizes(tokens), p, k, hidden, _dtype_code(one), sorted, _sizes(cap),
+                                  _stream_of(stream, one)), "ccl_moe_to_experts")
 
 
 def ccl_moe_from_experts(y, rows, weights, out, stream=None) -> None:
     """out[r][t] = sum_j weights[r][t, j] * y[r][rows[r][t, j]] in fp32, rounded
     once; weights None adds the rows as they are (the gradient of
     ccl_moe_to_experts)."""
-    rows, tokens, k = _choices(rows)
-    p = len(rows)
-    y, cap, hidden = _row_buffers(y, "y", p)
-    out = _ranks(out, "out", p, y[0].dtype, tokens, hidden)
+    rows, _, tokens, k = _choices(rows)
+    p = len(tokens)
+    y, one, cap, (hidden,) = _shaped(y, "y", 2, p)
+    out = _ranks(out, "out", p, one.dtype, tokens, hidden)
     if weights is not None:
         weights = _ranks(weights, "weights", p, torch.float32, tokens, k)
-    _check(LIB.ccl_moe_from_experts(_pointers(y), _sizes(cap), _pointers(rows), weights, _sizes(tokens), p, k, hidden,
-                                    _dtype_code(y[0]), out, _stream_of(stream, rows[0])), "ccl_moe_from_experts")
+    _check(LIB.ccl_moe_from_experts(y, _sizes(cap), rows, weights, _sizes(tokens), p, k, hidden, _dtype_code(one), out,
+                                    _stream_of(stream, one)), "ccl_moe_from_experts")
 
 
 def ccl_moe_from_experts_grad(dout, y, rows, weights, dy=None, dweights=None, stream=None) -> None:
     """The gradient of ccl_moe_from_experts: dy[r][row] = weights * dout[r][t]
     and dweights[r][t, j] = <y[r][row], dout[r][t]>; either may be None (y too,
     when dweights is)."""
-    rows, tokens, k = _choices(rows)
-    p = len(rows)
+    rows, _, tokens, k = _choices(rows)
+    p = len(tokens)
     if dy is None and dweights is None:
         raise ValueError("dy or dweights must be given")
     if dweights is not None and y is None:
         raise ValueError("dweights needs y")
-    expert_rows = y if y is not None else dy
-    expert_rows, cap, hidden = _row_buffers(expert_rows, "y" if y is not None else "dy", p)
-    dtype = expert_rows[0].dtype
-    dout = _ranks(dout, "dout", p, dtype, tokens, hidden)
-    if y is not None:
-        y = _pointers(expert_rows)
-    if dy is not None:
-        dy = _ranks(dy, "dy", p, dtype, cap, hidden)
+    held, one, cap, (hidden,) = _shaped(y if y is not None else dy, "y" if y is not None else "dy", 2, p)
+    dout = _ranks(dout, "dout", p, one.dtype, tokens, hidden)
+    if dy is not None and y is not None:
+        dy = _ranks(dy, "dy", p, one.dtype, cap, hidden)
+    elif dy is not None:
+        dy, held = held, None
     if weights is not None:
         weights = _ranks(weights, "weights", p, torch.float32, tokens, k)
     if dweights is not None:
         dweights = _ranks(dweights, "dweights", p, torch.float32, tokens, k)
-    _check(LIB.ccl_moe_from_experts_grad(dout, y, _sizes(cap), _pointers(rows), weights, _sizes(tokens), p, k, hidden,
-                                         _dtype_code(expert_rows[0]), dy, dweights, _stream_of(stream, rows[0])),
+    _check(LIB.ccl_moe_from_experts_grad(dout, held, _sizes(cap), rows, weights, _sizes(tokens), p, k, hidden,
+                                         _dtype_code(one), dy, dweights, _stream_of(stream, one)),
            "ccl_moe_from_experts_grad")
 
 
 def _weights(ts, name: str, p: int, dtype=torch.bfloat16):
-    """(buffers, experts, n, contract) of a list of (experts, n, contract) tensors."""
-    ts = _buffers(ts, name, dtype, p)
-    shape = ts[0].shape
-    for r, t in enumerate(ts):
-        if t.dim() != 3 or (r and t.shape != shape):
-            raise ValueError(f"{name}[{r}] must be (experts, n, contract), alike on every rank")
-    return ts, *shape
+    """(addresses, first tensor, experts, n, contract) of a list of (experts, n, contract) tensors."""
+    pointers, one, experts, (n, contract) = _shaped(ts, name, 3, p, dtype)
+    if experts.count(experts[0]) != p:
+        raise ValueError(f"{name} must hold as many experts on every rank")
+    return pointers, one, experts[0], n, contract
 
 
 def ccl_moe_product(x, offsets, w, y, stream=None) -> None:
     """y[rows of e] = x[rows of e] @ w[e].T for every expert e: x[r] (rows, contract),
     w[r] (experts, n, contract), y[r] (rows, n), bf16; offsets[r] from ccl_moe_sort."""
-    x, rows, contract = _row_buffers(x, "x", None, torch.bfloat16)
-    p = len(x)
-    w, experts, n, depth = _weights(w, "w", p)
+    x, one, rows, (contract,) = _shaped(x, "x", 2, None, torch.bfloat16)
+    p = len(rows)
+    w, _, experts, n, depth = _weights(w, "w", p)
     if depth != contract:
         raise ValueError(f"w has {depth} columns, x {contract}")
     y = _ranks(y, "y", p, torch.bfloat16, rows, n)
     offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
-    _check(LIB.ccl_moe_product(_pointers(x), offsets, _pointers(w), _sizes(rows), p, experts, n, contract, y,
-                               _stream_of(stream, x[0])), "ccl_moe_product")
+    _check(LIB.ccl_moe_product(x, offsets, w, _sizes(rows), p, experts, n, contract, y, _stream_of(stream, one)),
+           "ccl_moe_product")
 
 
 def ccl_moe_product_grad_input(dy, offsets, w, dx, stream=None) -> None:
     """dx[rows of e] = dy[rows of e] @ w[e]: the gradient of ccl_moe_product for x."""
-    dy, rows, n = _row_buffers(dy, "dy", None, torch.bfloat16)
-    p = len(dy)
-    w, experts, height, contract = _weights(w, "w", p)
+    dy, one, rows, (n,) = _shaped(dy, "dy", 2, None, torch.bfloat16)
+    p = len(rows)
+    w, _, experts, height, contract = _weights(w, "w", p)
     if height != n:
         raise ValueError(f"w has {height} rows, dy {n} columns")
     dx = _ranks(dx, "dx", p, torch.bfloat16, rows, contract)
     offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
-    _check(LIB.ccl_moe_product_grad_input(_pointers(dy), offsets, _pointers(w), _sizes(rows), p, experts, n, contract,
-                                          dx, _stream_of(stream, dy[0])), "ccl_moe_product_grad_input")
+    _check(LIB.ccl_moe_product_grad_input(dy, offsets, w, _sizes(rows), p, experts, n, contract, dx,
+                                          _stream_of(stream, one)), "ccl_moe_product_grad_input")
 
 
 def ccl_moe_product_grad_weight(dy, x, offsets, dw, stream=None) -> None:
     """dw[e] = dy[rows of e].T @ x[rows of e], fp32 or bf16 (zeros for an expert
     without rows): the gradient of ccl_moe_product for w."""
-    dy, rows, n = _row_buffers(dy, "dy", None, torch.bfloat16)
-    p = len(dy)
-    dw, experts, height, contract = _weights(dw, "dw", p, None)
+    dy, one, rows, (n,) = _shaped(dy, "dy", 2, None, torch.bfloat16)
+    p = len(rows)
+    dw, held, experts, height, contract = _weights(dw, "dw", p, None)
     if height != n:
         raise ValueError(f"dw has {height} rows, dy {n} columns")
     x = _ranks(x, "x", p, torch.bfloat16, rows, contract)
     offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
-    _check(LIB.ccl_moe_product_grad_weight(_pointers(dy), x, offsets, _sizes(rows), p, experts, n, contract,
-                                           _dtype_code(dw[0]), _pointers(dw), _stream_of(stream, dy[0])),
-           "ccl_moe_product_grad_weight")
+    _check(LIB.ccl_moe_product_grad_weight(dy, x, offsets, _sizes(rows), p, experts, n, contract, _dtype_code(held), dw,
+                                           _stream_of(stream, one)), "ccl_moe_product_grad_weight")
 
 
 # ------------------------------------------------------------------------ AdamW

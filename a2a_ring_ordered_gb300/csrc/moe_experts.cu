@@ -144,6 +144,23 @@ __global__ void moe_sort_kernel(const __grid_constant__ MoeSortArgs a) {
 }
 
 // ------------------------------------------------------------------ rows
+// f / n and f % n; a 32-bit division wherever it serves.
+struct Split {
+  uint64_t q;
+  uint32_t r;
+};
+__device__ __forceinline__ Split split(uint64_t f, uint32_t n) {
+  Split s;
+  if ((f >> 32) == 0) {
+    s.q = static_cast<uint32_t>(f) / n;
+    s.r = static_cast<uint32_t>(f) - static_cast<uint32_t>(s.q) * n;
+  } else {
+    s.q = f / n;
+    s.r = static_cast<uint32_t>(f - s.q * n);
+  }
+  return s;
+}
+
 // The row of a choice, or -1 where it has none in the buffer.
 __device__ __forceinline__ int64_t row_of(const int32_t* rows, uint64_t item, uint32_t cap) {
   const int32_t row = __ldg(rows + item);
@@ -171,7 +188,8 @@ __global__ void __launch_bounds__(kThreads) moe_to_experts_kernel(const __grid_c
   for (int u = 0; u < U; ++u) {
     const uint64_t f = f0 + u * kThreads;
     if (f >= total) continue;
-    const uint64_t t = f / nv, v = f - t * nv;
+    const Split at = split(f, nv);
+    const uint64_t t = at.q, v = at.r;
     for (int j = 0; j < k; ++j) {
       const int64_t row = row_of(a.rows[r], t * k + j, a.cap[r]);
       if (row >= 0) st_stream16(out + row * row_bytes + v * 16, w[u]);
@@ -221,16 +239,15 @@ template <int B>
 __global__ void __launch_bounds__(kThreads) moe_to_experts_off_kernel(const __grid_constant__ MoeRowsArgs a, uint64_t row_bytes) {
   pdl_enter();
   const int r = blockIdx.y;
-  const uint64_t ng = granules(row_bytes);
-  const uint64_t f = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint64_t item = f / ng, u = f - item * ng;
+  const Split at = split(static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x, static_cast<uint32_t>(granules(row_bytes)));
+  const uint64_t item = at.q, u = at.r;
   if (item >= static_cast<uint64_t>(a.tokens[r]) * a.k) return;
   const int64_t row = row_of(a.rows[r], item, a.cap[r]);
   if (row < 0) return;
   char* to = static_cast<char*>(a.out[r]) + row * row_bytes;
   const Granule g = granule_of(to, row_bytes, u);
   if (!g.any) return;
-  const char* from = static_cast<const char*>(a.x[r]) + item / a.k * row_bytes + (g.at - to);  // of the granule's first byte
+  const char* from = static_cast<const char*>(a.x[r]) + static_cast<uint32_t>(item) / static_cast<uint32_t>(a.k) * row_bytes + (g.at - to);  // of the granule's first byte
   if (g.whole) {
     st_stream16(g.at, load16_anywhere(from));
   } else {
@@ -245,9 +262,8 @@ __global__ void __launch_bounds__(kThreads) moe_from_experts_off_kernel(const __
   constexpr int B = Elem<DT>::kBytes, N = 16 / B;
   pdl_enter();
   const int r = blockIdx.y, k = a.k;
-  const uint64_t ng = granules(row_bytes);
-  const uint64_t f = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint64_t t = f / ng, u = f - t * ng;
+  const Split at = split(static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x, static_cast<uint32_t>(granules(row_bytes)));
+  const uint64_t t = at.q, u = at.r;
   if (t >= a.tokens[r]) return;
   char* to = static_cast<char*>(a.out[r]) + t * row_bytes;
   const Granule g = granule_of(to, row_bytes, u);
@@ -397,7 +413,8 @@ __global__ void __launch_bounds__(kThreads) moe_from_experts_kernel(const __grid
   const uint64_t total = static_cast<uint64_t>(a.tokens[r]) * nv;
   const uint64_t f = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
   if (f >= total) return;
-  const uint64_t t = f / nv, v = f - t * nv;
+  const Split at = split(f, nv);
+  const uint64_t t = at.q, v = at.r;
   const float* weights = a.weights[r];
   float acc[VEC];
 #pragma unroll

@@ -431,3 +431,31 @@ def test_long_sums_keep_fp32_precision(lib):
                                         [torch.tensor([0, 20000], dtype=torch.int32, device="cuda")], dw)
         want = dy.astype(np.float64).T @ x.astype(np.float64)
         assert np.linalg.norm(host(dw[0])[0] - want) <= 32 * 2.0 ** -24 * np.linalg.norm(want)
+
+
+def test_refusals_of_the_binding(lib):
+    """What the binding says of wrong tensors: lists, places, types, shapes, strides."""
+    rows = [torch.zeros(4, 2, dtype=torch.int32, device="cuda")]
+    y, out = [torch.zeros(8, 16, device="cuda")], [torch.zeros(4, 16, device="cuda")]
+    w = [torch.ones(4, 2, device="cuda")]
+    lib.ccl_moe_from_experts(y, rows, w, out)
+    for args, said in [((y, [rows[0].long()], w, out), "int32"), ((y, [rows[0].cpu()], w, out), "CUDA"),
+                       ((y * 2, rows, w, out), "1 rank buffers"), ((y, rows, w, [out[0][:3]]), "elements"),
+                       ((y, rows, w, [out[0].bfloat16()]), "float32"), ((y, rows, [w[0].double()], out), "float32"),
+                       (([torch.zeros(16, 8, device="cuda").T], rows, w, out), "contiguous"),
+                       (([torch.zeros(8, 16, 1, device="cuda")], rows, w, out), "dimensions"),
+                       (([3], rows, w, out), "must be a CUDA tensor"), (([], rows, w, out), "rank buffers"),
+                       ((y, rows + [rows[0][:, :1].contiguous()], w, out), "dimensions"),
+                       (([torch.zeros(8, 16, dtype=torch.float64, device="cuda")], rows, w, out), "float64")]:
+        with pytest.raises(ValueError, match=said):
+            lib.ccl_moe_from_experts(*args)
+    with pytest.raises(lib.CclError, match="overlaps"):
+        lib.ccl_moe_from_experts(y, rows, w, [y[0][:4]])
+    with pytest.raises(lib.CclError, match="bf16"):
+        lib.ccl_moe_to_experts([torch.zeros(4, 16, dtype=torch.int32, device="cuda")], rows,
+                               [torch.zeros(8, 16, dtype=torch.int32, device="cuda")])
+    with pytest.raises(ValueError, match="columns"):
+        lib.ccl_moe_product([torch.zeros(4, 8, device="cuda").bfloat16()], rows, [torch.zeros(2, 8, 9, device="cuda").bfloat16()],
+                            [torch.zeros(4, 8, device="cuda").bfloat16()])
+    with pytest.raises(ValueError, match="dweights needs y"):
+        lib.ccl_moe_from_experts_grad(out, None, rows, w, None, w)
