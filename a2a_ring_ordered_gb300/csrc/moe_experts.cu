@@ -204,259 +204,264 @@ __global__ void __launch_bounds__(kThreads) moe_to_experts_kernel(const __grid_c
 // granules that the row shares with its neighbours, its first and its last,
 // go element by element.
 struct Granule {
-  char* at;       // aligned
-  bool any;       // it holds bytes of the row
-  bool whole;     // and no others
-  uint32_t lo, hi;  // the row's bytes in it
+  char* at;         // aligned
+  uint32_t lo, hi;  // the row's bytes in it; none where lo == hi
+  __device__ __forceinline__ bool any() const { return lo < hi; }
+  __device__ __forceinline__ bool whole() const { return hi - lo == 16; }
 };
 __device__ __forceinline__ Granule granule_of(char* row, uint64_t row_bytes, uint64_t u) {
   const uintptr_t first = reinterpret_cast<uintptr_t>(row), end = first + row_bytes;
   const uintptr_t at = (first & ~static_cast<uintptr_t>(15)) + 16 * u;
   Granule g;
   g.at = reinterpret_cast<char*>(at);
-  g.any = at < end;
   g.lo = at < first ? static_cast<uint32_t>(first - at) : 0u;
-  g.hi = at + 16 > end ? static_cast<uint32_t>(end - at) : 16u;
-  g.whole = g.any && g.lo == 0 && g.hi == 16;
+  g.hi = at >= end ? g.lo : at + 16 > end ? static_cast<uint32_t>(end - at) : 16u;
   return g;
+}
+// Stores the row's bytes of a granule.
+template <int B>
+__device__ __forceinline__ void store_granule(const Granule& g, const uint4 v) {
+  if (g.whole()) {
+    st_stream16(g.at, v);
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 16 / B; ++e) {
+    const uint32_t at = e * B;
+    if (at < g.lo || at >= g.hi) continue;
+    if constexpr (B == 4) st_stream4(g.at + at, w[e]);
+    else st_stream2(g.at + at, (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
+  }
+}
+// Zeros in place of the bytes that are not the row's.
+template <int B>
+__device__ __forceinline__ uint4 only_row(const Granule& g, const uint4 v) {
+  if (g.whole()) return v;
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 16 / B; ++e) {
+    const uint32_t at = e * B;
+    if (at >= g.lo && at < g.hi) continue;
+    w[at / 4] &= B == 4 ? 0u : (e & 1) ? 0xFFFFu : 0xFFFF0000u;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // Granules that a row of so many bytes can touch.
 __host__ __device__ constexpr uint64_t granules(uint64_t row_bytes) { return (row_bytes + 30) / 16; }
 
-template <int B>
-__device__ __forceinline__ uint32_t ld_element(const char* p) {
-  if constexpr (B == 4) return ld_once4(p);
-  else return ld_once2(p);
-}
-template <int B>
-__device__ __forceinline__ void st_element(char* p, uint32_t v) {
-  if constexpr (B == 4) st_stream4(p, v);
-  else st_stream2(p, v);
-}
-
-// One flat range of (token, choice, granule of the choice's row) per rank.
+// One flat range of (token, choice, granule of the choice's row) per rank,
+// kOffUnits of them per thread with their loads on the way together.
+constexpr int kOffUnits = 2;
 template <int B>
 __global__ void __launch_bounds__(kThreads) moe_to_experts_off_kernel(const __grid_constant__ MoeRowsArgs a, uint64_t row_bytes) {
+  constexpr int U = kOffUnits;
   pdl_enter();
   const int r = blockIdx.y;
-  const Split at = split(static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x, static_cast<uint32_t>(granules(row_bytes)));
-  const uint64_t item = at.q, u = at.r;
-  if (item >= static_cast<uint64_t>(a.tokens[r]) * a.k) return;
-  const int64_t row = row_of(a.rows[r], item, a.cap[r]);
-  if (row < 0) return;
-  char* to = static_cast<char*>(a.out[r]) + row * row_bytes;
-  const Granule g = granule_of(to, row_bytes, u);
-  if (!g.any) return;
-  const char* from = static_cast<const char*>(a.x[r]) + static_cast<uint32_t>(item) / static_cast<uint32_t>(a.k) * row_bytes + (g.at - to);  // of the granule's first byte
-  if (g.whole) {
-    st_stream16(g.at, load16_anywhere(from));
-  } else {
-    for (uint32_t b = g.lo; b < g.hi; b += B) st_element<B>(g.at + b, ld_element<B>(from + b));
+  const uint32_t ng = static_cast<uint32_t>(granules(row_bytes));
+  const uint64_t items = static_cast<uint64_t>(a.tokens[r]) * a.k;
+  const uint64_t f0 = static_cast<uint64_t>(blockIdx.x) * U * kThreads + threadIdx.x;
+  Granule g[U];
+  const char* from[U];
+  uint4 w[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Split at = split(f0 + u * kThreads, ng);
+    const int64_t row = at.q < items ? row_of(a.rows[r], at.q, a.cap[r]) : -1;
+    char* to = static_cast<char*>(a.out[r]) + row * row_bytes;
+    g[u].at = to;
+    g[u].lo = g[u].hi = 0;
+    if (row >= 0) g[u] = granule_of(to, row_bytes, at.r);
+    // of the granule's first byte
+    from[u] = static_cast<const char*>(a.x[r]) + static_cast<uint32_t>(at.q) / static_cast<uint32_t>(a.k) * row_bytes + (g[u].at - to);
   }
+#pragma unroll
+  for (int u = 0; u < U; ++u) w[u] = load16_part(from[u], g[u].lo, g[u].hi);
+#pragma unroll
+  for (int u = 0; u < U; ++u) store_granule<B>(g[u], w[u]);
 }
 
-// One flat range of (token, granule of its output row) per rank; the choices'
-// loads are issued (4 at a time) before any is added.
-template <int DT>
+// One flat range of (token, granule of its output row) per rank; the rows of
+// KB choices (all of them, or 8 at a time) are looked up together, then loaded
+// together, before any is added.
+template <int DT, int KB>
 __global__ void __launch_bounds__(kThreads) moe_from_experts_off_kernel(const __grid_constant__ MoeRowsArgs a, uint64_t row_bytes) {
   constexpr int B = Elem<DT>::kBytes, N = 16 / B;
   pdl_enter();
   const int r = blockIdx.y, k = a.k;
   const Split at = split(static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x, static_cast<uint32_t>(granules(row_bytes)));
-  const uint64_t t = at.q, u = at.r;
+  const uint64_t t = at.q;
   if (t >= a.tokens[r]) return;
   char* to = static_cast<char*>(a.out[r]) + t * row_bytes;
-  const Granule g = granule_of(to, row_bytes, u);
-  if (!g.any) return;
-  const int64_t into = g.at - to;  // of the granule's first byte, from the row's
-  const char* y = static_cast<const char*>(a.y[r]);
+  const Granule g = granule_of(to, row_bytes, at.r);
+  if (!g.any()) return;
+  const char* y = static_cast<const char*>(a.y[r]) + (g.at - to);  // of the granule's first byte, in row 0
   const float* weights = a.weights[r];
   float acc[N];
 #pragma unroll
-  for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+  for (int e = 0; e < N; ++e) acc[e] = -0.0f;  // -0 + x is x, to the bit
   bool have = false;
-  for (int j0 = 0; j0 < k; j0 += 4) {
-    uint4 raw[4];
-    int64_t row[4];
-    float wt[4];
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    uint4 raw[KB];
+    int64_t row[KB];
+    float wt[KB];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < KB; ++b) {
       row[b] = j0 + b < k ? row_of(a.rows[r], t * k + j0 + b, a.cap[r]) : -1;
       wt[b] = (weights != nullptr && j0 + b < k) ? __ldg(weights + t * k + j0 + b) : 1.0f;
     }
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      if (row[b] < 0) continue;
-      const char* p = y + row[b] * row_bytes + into;
-      if (g.whole) {
-        raw[b] = load16_anywhere(p);
-      } else {
-        uint32_t w[4] = {};
+    for (int b = 0; b < KB; ++b) raw[b] = load16_part(y + row[b] * static_cast<int64_t>(row_bytes), g.lo, row[b] >= 0 ? g.hi : g.lo);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const uint32_t at = e * B;
-          const uint32_t v = at >= g.lo && at < g.hi ? ld_element<B>(p + at) : 0u;
-          w[at / 4] |= v << (8 * (at & 3));
-        }
-        raw[b] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < KB; ++b) {
       if (row[b] < 0) continue;
       const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float prod = __fmul_rn(wt[b], widen<DT>(w, e));
-        acc[e] = have ? __fadd_rn(acc[e], prod) : prod;
-      }
+      for (int e = 0; e < N; ++e) acc[e] = __fadd_rn(acc[e], __fmul_rn(wt[b], widen<DT>(w, e)));
       have = true;
     }
   }
+  if (!have) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+  }
   uint32_t w[4];
   pack_out<DT, N>(acc, w);
-  if (g.whole) {
-    st_stream16(g.at, make_uint4(w[0], w[1], w[2], w[3]));
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (e * B >= g.lo && e * B < g.hi) store_one<DT>(g.at, e, w, e);
-  }
+  store_granule<B>(g, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// As moe_from_experts_grad_kernel, a choice after the other: its rows are
-// walked in the granules of dy's row (y's where only the gates are wanted).
+// `tpi` lanes (a power of two, up to a warp) per (token, choice): its row is
+// walked in the granules of dy's row (y's where only the gates are wanted), and
+// the lanes' dot products are added in a fixed tree.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) moe_from_experts_grad_off_kernel(const __grid_constant__ MoeRowsArgs a,
-                                                                            uint64_t row_bytes, int tpt) {
-  constexpr int B = Elem<DT>::kBytes, N = 16 / B;
-  __shared__ float part[kThreads / 32];
+                                                                            uint64_t row_bytes, int tpi) {
+  constexpr int B = Elem<DT>::kBytes, N = 16 / B, U = 2;
   pdl_enter();
-  const int r = blockIdx.y, k = a.k;
-  const int group = threadIdx.x / tpt, in = threadIdx.x - group * tpt, lane = threadIdx.x & 31;
-  const uint64_t t = static_cast<uint64_t>(blockIdx.x) * (kThreads / tpt) + group;
-  if (static_cast<uint64_t>(blockIdx.x) * (kThreads / tpt) >= a.tokens[r]) return;
-  const bool live = t < a.tokens[r];
+  const int r = blockIdx.y;
+  const uint32_t slot = threadIdx.x / tpi, in = threadIdx.x - slot * tpi;
+  const uint64_t item = static_cast<uint64_t>(blockIdx.x) * (kThreads / tpi) + slot;
+  const bool live = item < static_cast<uint64_t>(a.tokens[r]) * a.k;
+  const int64_t row = live ? row_of(a.rows[r], item, a.cap[r]) : -1;
+  const float wt = (live && a.weights[r] != nullptr) ? __ldg(a.weights[r] + item) : 1.0f;
+  const uint64_t t = live ? static_cast<uint32_t>(item) / static_cast<uint32_t>(a.k) : 0;
   const char* dout = static_cast<const char*>(a.x[r]) + t * row_bytes;
   char* dy = static_cast<char*>(a.out[r]);
-  const char* y = static_cast<const char*>(a.y[r]);
   float* dw = a.dweights[r];
-  const uint64_t ng = granules(row_bytes);
-  for (int j = 0; j < k; ++j) {
-    const int64_t row = live ? row_of(a.rows[r], t * k + j, a.cap[r]) : -1;
-    const float wt = (live && a.weights[r] != nullptr) ? __ldg(a.weights[r] + t * k + j) : 1.0f;
-    float dot = 0.0f;
-    if (row >= 0) {
-      char* walked = (dy != nullptr ? dy : const_cast<char*>(y)) + row * row_bytes;
-      for (uint64_t u = in; u < ng; u += tpt) {
-        const Granule g = granule_of(walked, row_bytes, u);
-        if (!g.any) break;
-        const int64_t into = g.at - walked;
-        uint32_t d[4] = {}, v[4] = {};
-        if (g.whole) {
-          const uint4 dq = load16_anywhere(dout + into);
-          d[0] = dq.x, d[1] = dq.y, d[2] = dq.z, d[3] = dq.w;
-          if (dw != nullptr) {
-            const uint4 vq = load16_anywhere(y + row * row_bytes + into);
-            v[0] = vq.x, v[1] = vq.y, v[2] = vq.z, v[3] = vq.w;
-          }
-        } else {
+  float dot = 0.0f;
+  if (row >= 0) {
+    const char* y = static_cast<const char*>(a.y[r]) + row * row_bytes;
+    char* walked = dy != nullptr ? dy + row * row_bytes : const_cast<char*>(y);
+    const uint32_t ng = static_cast<uint32_t>(granules(row_bytes));
+    for (uint32_t u0 = in; u0 < ng; u0 += tpi * U) {
+      Granule g[U];
+      uint4 d[U], v[U];
 #pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const uint32_t at = e * B;
-            if (at < g.lo || at >= g.hi) continue;
-            d[at / 4] |= ld_element<B>(dout + into + at) << (8 * (at & 3));
-            if (dw != nullptr) v[at / 4] |= ld_element<B>(y + row * row_bytes + into + at) << (8 * (at & 3));
-          }
-        }
+      for (int u = 0; u < U; ++u) {
+        g[u] = granule_of(walked, row_bytes, u0 + u * tpi);
+        const int64_t into = g[u].at - walked;
+        d[u] = load16_part(dout + into, g[u].lo, g[u].hi);
+        v[u] = load16_part(y + into, g[u].lo, dw != nullptr ? g[u].hi : g[u].lo);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!g[u].any()) continue;
+        const uint4 dc = only_row<B>(g[u], d[u]), vc = only_row<B>(g[u], v[u]);
+        const uint32_t dq[4] = {dc.x, dc.y, dc.z, dc.w}, vq[4] = {vc.x, vc.y, vc.z, vc.w};
         float o[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          const float de = widen<DT>(d, e);
+          const float de = widen<DT>(dq, e);
           o[e] = __fmul_rn(wt, de);
-          if (dw != nullptr) dot = fmaf(widen<DT>(v, e), de, dot);
+          if (dw != nullptr) dot = fmaf(widen<DT>(vq, e), de, dot);
         }
         if (dy == nullptr) continue;
         uint32_t w[4];
         pack_out<DT, N>(o, w);
-        if (g.whole) {
-          st_stream16(g.at, make_uint4(w[0], w[1], w[2], w[3]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < N; ++e)
-            if (e * B >= g.lo && e * B < g.hi) store_one<DT>(g.at, e, w, e);
-        }
+        store_granule<B>(g[u], make_uint4(w[0], w[1], w[2], w[3]));
       }
     }
-    if (dw == nullptr) continue;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
-    if (lane == 0) part[threadIdx.x >> 5] = dot;
-    __syncthreads();
-    if (live && in == 0) {
-      float sum = 0.0f;
-      for (int w = 0; w < tpt / 32; ++w) sum += part[group * (tpt / 32) + w];
-      dw[t * k + j] = sum;
-    }
-    __syncthreads();
   }
+  for (int o = tpi / 2; o >= 1; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+  if (dw != nullptr && live && in == 0) dw[item] = dot;
 }
 
 // -------------------------------------------------------------- on the grid
-// The same flat range; the k rows' loads are issued (8 at a time) before any
-// is added.
-template <int DT, int VEC>
+// The same flat range, U vectors per thread: the rows of KB choices (all of
+// them, or 8 at a time) of its vectors are looked up together, then loaded
+// together, before any is added.  One choice of 32000 fp32 rows of 1000 took
+// 146 us with registers for eight choices, 95 with one choice and 8 vectors
+// per thread, 51 with 4 and 48 with 2: the lookups' latency needs warps.
+template <int DT, int VEC, int KB, int U>
 __global__ void __launch_bounds__(kThreads) moe_from_experts_kernel(const __grid_constant__ MoeRowsArgs a, uint32_t nv) {
   constexpr int W = (VEC * Elem<DT>::kBytes + 3) / 4;
   pdl_enter();
   const int r = blockIdx.y, k = a.k;
   const uint64_t total = static_cast<uint64_t>(a.tokens[r]) * nv;
-  const uint64_t f = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (f >= total) return;
-  const Split at = split(f, nv);
-  const uint64_t t = at.q, v = at.r;
+  const uint64_t f0 = static_cast<uint64_t>(blockIdx.x) * U * kThreads + threadIdx.x;
+  if (f0 >= total) return;
   const float* weights = a.weights[r];
-  float acc[VEC];
+  Split at[U];
+  float acc[U][VEC];
+  bool have[U];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
-  bool have = false;
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    uint32_t raw[8][W];
-    int64_t row[8];
-    float wt[8];
+  for (int u = 0; u < U; ++u) {
+    at[u] = split(f0 + u * kThreads, nv);
+    have[u] = false;
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      row[b] = j0 + b < k ? row_of(a.rows[r], t * k + j0 + b, a.cap[r]) : -1;
-      wt[b] = (weights != nullptr && j0 + b < k) ? __ldg(weights + t * k + j0 + b) : 1.0f;
-    }
-#pragma unroll
-    for (int b = 0; b < 8; ++b)
-      if (row[b] >= 0) load_raw<DT, VEC>(a.y[r], row[b] * a.hidden + v * VEC, raw[b]);
-#pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      if (row[b] < 0) continue;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float prod = __fmul_rn(wt[b], widen<DT>(raw[b], e));
-        acc[e] = have ? __fadd_rn(acc[e], prod) : prod;
-      }
-      have = true;
-    }
+    for (int e = 0; e < VEC; ++e) acc[u][e] = -0.0f;  // -0 + x is x, to the bit
   }
-  uint32_t w[W];
-  pack_out<DT, VEC>(acc, w);
-  store_raw<DT, VEC>(a.out[r], t * a.hidden + v * VEC, w);
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    uint32_t raw[U][KB][W];
+    int64_t row[U][KB];
+    float wt[U][KB];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        const bool there = f0 + u * kThreads < total && j0 + b < k;
+        row[u][b] = there ? row_of(a.rows[r], at[u].q * k + j0 + b, a.cap[r]) : -1;
+        wt[u][b] = (there && weights != nullptr) ? __ldg(weights + at[u].q * k + j0 + b) : 1.0f;
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+        if (row[u][b] >= 0) load_raw<DT, VEC>(a.y[r], row[u][b] * a.hidden + static_cast<uint64_t>(at[u].r) * VEC, raw[u][b]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        if (row[u][b] < 0) continue;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          acc[u][e] = __fadd_rn(acc[u][e], __fmul_rn(wt[u][b], widen<DT>(raw[u][b], e)));
+        }
+        have[u] = true;
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (f0 + u * kThreads >= total) continue;
+    if (!have[u]) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[u][e] = 0.0f;
+    }
+    uint32_t w[W];
+    pack_out<DT, VEC>(acc[u], w);
+    store_raw<DT, VEC>(a.out[r], at[u].q * a.hidden + static_cast<uint64_t>(at[u].r) * VEC, w);
+  }
 }
 
-// `tpt` threads (a power of two, 32..128) per token walk its vectors: dout is
-// read once for 8 choices, each y vector once, each dy vector written once.
-// The dot products are added per thread, then in a warp's fixed shuffle tree,
-// then warp by warp.
-template <int DT, int VEC>
+// `tpt` threads (a power of two, 1..128) per token walk its vectors, U of them
+// at a time: dout is read once for KB choices (all of them, or 8 at a time),
+// each y vector once, each dy vector written once.  The dot products are added
+// per thread, then in a fixed shuffle tree, then warp by warp.
+template <int DT, int VEC, int KB, int U>
 __global__ void __launch_bounds__(kThreads) moe_from_experts_grad_kernel(const __grid_constant__ MoeRowsArgs a,
                                                                         uint32_t nv, int tpt) {
   constexpr int W = (VEC * Elem<DT>::kBytes + 3) / 4;
-  __shared__ float part[kThreads / 32][8];
+  __shared__ float part[kThreads / 32][KB];
   pdl_enter();
   const int r = blockIdx.y, k = a.k;
   const int group = threadIdx.x / tpt, in = threadIdx.x - group * tpt, lane = threadIdx.x & 31;
@@ -466,52 +471,66 @@ __global__ void __launch_bounds__(kThreads) moe_from_experts_grad_kernel(const _
   const float* weights = a.weights[r];
   void* dy = a.out[r];
   float* dw = a.dweights[r];
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    int64_t row[8];
-    float wt[8], dot[8];
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    int64_t row[KB];
+    float wt[KB], dot[KB];
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
+    for (int b = 0; b < KB; ++b) {
       row[b] = (live && j0 + b < k) ? row_of(a.rows[r], t * k + j0 + b, a.cap[r]) : -1;
       wt[b] = (live && weights != nullptr && j0 + b < k) ? __ldg(weights + t * k + j0 + b) : 1.0f;
       dot[b] = 0.0f;
     }
-    for (uint32_t v = in; live && v < nv; v += tpt) {
-      uint32_t d[W], y[8][W];
-      load_raw<DT, VEC>(a.x[r], t * a.hidden + static_cast<uint64_t>(v) * VEC, d);
-      if (dw != nullptr) {
+    for (uint32_t v0 = in; live && v0 < nv; v0 += tpt * U) {
+      uint32_t d[U][W], y[U][KB][W];
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
-          if (row[b] >= 0) load_raw<DT, VEC>(a.y[r], row[b] * a.hidden + static_cast<uint64_t>(v) * VEC, y[b]);
+      for (int u = 0; u < U; ++u) {
+        const uint32_t v = v0 + u * tpt;
+        if (v >= nv) continue;
+        load_raw<DT, VEC>(a.x[r], t * a.hidden + static_cast<uint64_t>(v) * VEC, d[u]);
+        if (dw == nullptr) continue;
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+          if (row[b] >= 0) load_raw<DT, VEC>(a.y[r], row[b] * a.hidden + static_cast<uint64_t>(v) * VEC, y[u][b]);
       }
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        if (row[b] < 0) continue;
-        float o[VEC];
+      for (int u = 0; u < U; ++u) {
+        const uint32_t v = v0 + u * tpt;
+        if (v >= nv) continue;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float de = widen<DT>(d, e);
-          o[e] = __fmul_rn(wt[b], de);
-          if (dw != nullptr) dot[b] = fmaf(widen<DT>(y[b], e), de, dot[b]);
-        }
-        if (dy != nullptr) {
-          uint32_t w[W];
-          pack_out<DT, VEC>(o, w);
-          store_raw<DT, VEC>(dy, row[b] * a.hidden + static_cast<uint64_t>(v) * VEC, w);
+        for (int b = 0; b < KB; ++b) {
+          if (row[b] < 0) continue;
+          float o[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float de = widen<DT>(d[u], e);
+            o[e] = __fmul_rn(wt[b], de);
+            if (dw != nullptr) dot[b] = fmaf(widen<DT>(y[u][b], e), de, dot[b]);
+          }
+          if (dy != nullptr) {
+            uint32_t w[W];
+            pack_out<DT, VEC>(o, w);
+            store_raw<DT, VEC>(dy, row[b] * a.hidden + static_cast<uint64_t>(v) * VEC, w);
+          }
         }
       }
     }
     if (dw == nullptr) continue;
+    for (int o = (tpt < 32 ? tpt : 32) / 2; o >= 1; o >>= 1) {
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
+      for (int b = 0; b < KB; ++b) dot[b] += __shfl_xor_sync(kAll, dot[b], o);
+    }
+    if (tpt <= 32) {
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) dot[b] += __shfl_xor_sync(kAll, dot[b], o);
+      for (int b = 0; b < KB; ++b)
+        if (live && in == 0 && j0 + b < k) dw[t * k + j0 + b] = dot[b];
+      continue;
     }
     if (lane == 0) {
 #pragma unroll
-      for (int b = 0; b < 8; ++b) part[threadIdx.x >> 5][b] = dot[b];
+      for (int b = 0; b < KB; ++b) part[threadIdx.x >> 5][b] = dot[b];
     }
     __syncthreads();
-    if (live && in < 8 && j0 + in < k) {
+    if (live && in < KB && j0 + in < k) {
       float sum = 0.0f;
       for (int w = 0; w < tpt / 32; ++w) sum += part[group * (tpt / 32) + w][in];
       dw[t * k + j0 + in] = sum;
@@ -551,41 +570,63 @@ cudaError_t launch_copy(int elem, const MoeRowsArgs& a, cudaStream_t s) {
 
 uint64_t ctas_for(uint64_t threads) { return (threads + kThreads - 1) / kThreads; }
 
-template <int DT>
-cudaError_t launch_back_off(const MoeRowsArgs& a, cudaStream_t s) {
-  const uint64_t row_bytes = a.hidden * Elem<DT>::kBytes;
-  return launch_rows(moe_from_experts_off_kernel<DT>, ctas_for(most_tokens(a) * granules(row_bytes)), a.p, s, a, row_bytes);
-}
-
-// At most 128: 8 ranks x 2048 tokens x 7168 bf16 of 8 choices took 631 us with
-// 256 threads per token, 597 with 128 or 64, 601 with 32.
-int threads_per_token(uint64_t units) {
-  int tpt = 32;
-  while (tpt < 128 && static_cast<uint64_t>(tpt) < units) tpt *= 2;
-  return tpt;
+// The power of two of threads that walk `units` units, between lo and hi.
+int walkers(uint64_t units, int lo, int hi) {
+  int n = lo;
+  while (n < hi && static_cast<uint64_t>(n) < units) n *= 2;
+  return n;
 }
 
 template <int DT>
 cudaError_t launch_back_grad_off(const MoeRowsArgs& a, cudaStream_t s) {
   const uint64_t row_bytes = a.hidden * Elem<DT>::kBytes;
-  const int tpt = threads_per_token(granules(row_bytes));
-  const uint64_t per = kThreads / tpt;
-  return launch_rows(moe_from_experts_grad_off_kernel<DT>, (most_tokens(a) + per - 1) / per, a.p, s, a, row_bytes, tpt);
+  const int tpi = walkers(granules(row_bytes), 1, 32);
+  const uint64_t per = kThreads / tpi, items = static_cast<uint64_t>(most_tokens(a)) * a.k;
+  return launch_rows(moe_from_experts_grad_off_kernel<DT>, (items + per - 1) / per, a.p, s, a, row_bytes, tpi);
+}
+
+// Calls f(KB, U) with the choices that are loaded together and the vectors per
+// thread.
+template <typename F>
+cudaError_t by_choices(int k, F f) {
+  if (k == 1) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
+  if (k == 2) return f(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
+  if (k <= 4) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+  return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+}
+
+template <int DT>
+cudaError_t launch_back_off(const MoeRowsArgs& a, cudaStream_t s) {
+  const uint64_t row_bytes = a.hidden * Elem<DT>::kBytes, ctas = ctas_for(most_tokens(a) * granules(row_bytes));
+  return by_choices(a.k, [&](auto kb, auto) {
+    return launch_rows(moe_from_experts_off_kernel<DT, decltype(kb)::value>, ctas, a.p, s, a, row_bytes);
+  });
 }
 
 template <int DT, int VEC>
 cudaError_t launch_back(const MoeRowsArgs& a, cudaStream_t s) {
   const uint32_t nv = static_cast<uint32_t>(a.hidden / VEC);
   const uint64_t total = static_cast<uint64_t>(most_tokens(a)) * nv;
-  return launch_rows(moe_from_experts_kernel<DT, VEC>, (total + kThreads - 1) / kThreads, a.p, s, a, nv);
+  // few vectors: one per thread, so that more SMs have some
+  const bool few = total <= static_cast<uint64_t>(kThreads) * 4 * 152;
+  return by_choices(a.k, [&](auto kb, auto u) {
+    constexpr int KB = decltype(kb)::value, U = decltype(u)::value;
+    if (few) return launch_rows(moe_from_experts_kernel<DT, VEC, KB, 1>, ctas_for(total), a.p, s, a, nv);
+    return launch_rows(moe_from_experts_kernel<DT, VEC, KB, U>, ctas_for((total + U - 1) / U), a.p, s, a, nv);
+  });
 }
 
+// At most 128 threads a token: 8 ranks x 2048 tokens x 7168 bf16 of 8 choices
+// took 631 us with 256, 597 with 128 or 64, 601 with 32.
 template <int DT, int VEC>
 cudaError_t launch_back_grad(const MoeRowsArgs& a, cudaStream_t s) {
   const uint32_t nv = static_cast<uint32_t>(a.hidden / VEC);
-  const int tpt = threads_per_token(nv);
-  const uint64_t per = kThreads / tpt;
-  return launch_rows(moe_from_experts_grad_kernel<DT, VEC>, (most_tokens(a) + per - 1) / per, a.p, s, a, nv, tpt);
+  return by_choices(a.k, [&](auto kb, auto u) {
+    constexpr int KB = decltype(kb)::value, U = KB == 1 ? 4 : decltype(u)::value;
+    const int tpt = walkers((nv + U - 1) / U, 1, 128);
+    const uint64_t per = kThreads / tpt;
+    return launch_rows(moe_from_experts_grad_kernel<DT, VEC, KB, U>, (most_tokens(a) + per - 1) / per, a.p, s, a, nv, tpt);
+  });
 }
 
 }  // namespace
@@ -625,7 +666,7 @@ cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
 cudaError_t launch_moe_to_experts(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s) {
   const int elem = dt == kF32 ? 4 : 2;
   if (vec) return launch_copy(elem, a, s);
-  const uint64_t row_bytes = a.hidden * elem, ctas = ctas_for(static_cast<uint64_t>(most_tokens(a)) * a.k * granules(row_bytes));
+  const uint64_t row_bytes = a.hidden * elem, ctas = ctas_for((static_cast<uint64_t>(most_tokens(a)) * a.k * granules(row_bytes) + kOffUnits - 1) / kOffUnits);
   return elem == 4 ? launch_rows(moe_to_experts_off_kernel<4>, ctas, a.p, s, a, row_bytes)
                    : launch_rows(moe_to_experts_off_kernel<2>, ctas, a.p, s, a, row_bytes);
 }

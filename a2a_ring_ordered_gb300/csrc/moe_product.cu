@@ -267,16 +267,6 @@ __device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int 
 }
 
 // ------------------------------------------------------------------ loaders
-// The 16 bytes at p, or zeros.
-__device__ __forceinline__ uint4 load16_if(uintptr_t p, bool take) {
-  uint4 v;
-  asm("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
-      " @p ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "r"(static_cast<uint32_t>(take)));
-  return v;
-}
-
 // `v` with the elements from `valid` on zero.
 __device__ __forceinline__ uint4 keep(const uint4 v, int valid) {
   uint32_t o[4] = {v.x, v.y, v.z, v.w};

@@ -50,13 +50,24 @@ __device__ __forceinline__ uint4 shift16(const uint4 lo, const uint4 hi, uint32_
                     __funnelshift_r(w[3], w[4], sh));
 }
 
-// The 16 bytes at p, wherever it is, by the aligned granules that hold them.
-// Both allocate in L1: a granule's other bytes are the neighbour thread's.
-__device__ __forceinline__ uint4 load16_anywhere(const char* p) {
+// The aligned 16 bytes at p, or zeros; allocates in L1.
+__device__ __forceinline__ uint4 load16_if(uintptr_t p, bool take) {
+  uint4 v;
+  asm("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
+      " @p ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(static_cast<uint32_t>(take)));
+  return v;
+}
+
+// The 16 bytes at p, wherever it is, of which bytes [lo, hi) exist (the others
+// come out as anything): by the aligned granules that hold some of them, and
+// no granule else is touched.
+__device__ __forceinline__ uint4 load16_part(const char* p, uint32_t lo, uint32_t hi) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(p), base = at & ~static_cast<uintptr_t>(15);
-  const uint4 lo = ld_l1_16(reinterpret_cast<const void*>(base));
-  const uint4 hi = ld_l1_16(reinterpret_cast<const void*>((at + 15) & ~static_cast<uintptr_t>(15)));
-  return shift16(lo, hi, static_cast<uint32_t>(at - base));
+  const uint4 a = load16_if(base, lo < hi && base + 16 > at + lo);
+  const uint4 b = load16_if(base + 16, lo < hi && base + 16 < at + hi);
+  return shift16(a, b, static_cast<uint32_t>(at - base));
 }
 
 // The next lane's granule (lane 31 gets `own_next`, which it loaded itself).
