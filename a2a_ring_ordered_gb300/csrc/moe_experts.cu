@@ -15,7 +15,7 @@
 namespace ccl {
 namespace {
 
-constexpr int kSortMaxCluster = 8;       // portable cluster size
+constexpr int kSortMaxCluster = 16;
 constexpr int kSortUnroll = 4;           // id loads in flight per lane
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
@@ -26,12 +26,24 @@ __device__ __forceinline__ int sort_expert(const int32_t* ids, uint32_t i, uint3
   return (e >= 0 && e < experts) ? static_cast<int>(e) : -1;
 }
 
+// The lanes whose value has the same low `bits` bits as this lane's, by one
+// vote per bit.
+__device__ __forceinline__ unsigned lanes_alike(int value, int bits) {
+  unsigned alike = kAll;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (value >> b) & 1;
+    const unsigned ones = __ballot_sync(kAll, one);
+    alike &= one ? ones : ~ones;
+  }
+  return alike;
+}
+
 // One cluster of CTAs per rank (grid x = CTA in the cluster, grid y = rank).
 // CTA c owns a contiguous range of the rank's items and warp w of it a
 // contiguous part of that, so walking parts in order keeps the sort stable.
 //  1. Each warp counts its part's items per expert in its own row of
-//     hist (lanes of equal expert found by __match_any_sync, the first of
-//     them adds the group), so nothing is atomic.
+//     hist (the first of the lanes of one expert adds the group), so nothing
+//     is atomic.
 //  2. A column of hist becomes the running count of the warps before; the
 //     CTAs' totals are exchanged through distributed shared memory; a scan
 //     over the experts gives every expert its first row.
@@ -41,6 +53,7 @@ __global__ void moe_sort_kernel(const __grid_constant__ MoeSortArgs a) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t smem[];
   const int E = a.num_experts;
+  const int bits = 33 - __clz(E);  // of 0 .. E - 1, and one that -1 alone has
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   uint32_t* hist = smem;             // [warps][E]
   uint32_t* total = hist + warps * E;  // [E]: this CTA's items of each expert
@@ -69,7 +82,7 @@ __global__ void moe_sort_kernel(const __grid_constant__ MoeSortArgs a) {
     for (int u = 0; u < kSortUnroll; ++u) e[u] = sort_expert(ids, b + 32 * u + lane, hi, first, E);
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) {
-      const unsigned same = __match_any_sync(kAll, e[u]);
+      const unsigned same = lanes_alike(e[u], bits);
       if (e[u] >= 0 && lane == __ffs(same) - 1) mine[e[u]] += __popc(same);
       __syncwarp();
     }
@@ -131,7 +144,7 @@ __global__ void moe_sort_kernel(const __grid_constant__ MoeSortArgs a) {
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) {
       const uint32_t i = b + 32 * u + lane;
-      const unsigned same = __match_any_sync(kAll, e[u]);
+      const unsigned same = lanes_alike(e[u], bits);
       const uint32_t before = __popc(same & ((1u << lane) - 1u));
       const uint32_t at = e[u] >= 0 ? mine[e[u]] : 0;
       __syncwarp();
@@ -642,7 +655,8 @@ cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
   warps = warps < 8 ? 8 : warps > 32 ? 32 : warps;
   const size_t smem = (static_cast<size_t>(warps) + 2) * a.num_experts * sizeof(uint32_t);
   cudaError_t err = cudaSuccess;
-  if (smem > 48 * 1024) err = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (ctas > 8) err = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (err == cudaSuccess && smem > 48 * 1024) err = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, static_cast<unsigned>(a.p));
