@@ -112,6 +112,13 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+// Behind a proxy fence and a barrier of the writers: what they wrote lies in
+// their own SM's shared memory, which is where the tensor core reads it.  (A
+// release at cluster scope waits for all of the thread's memory operations, a
+// microsecond a stage.)
+__device__ __forceinline__ void mbar_arrive_loaded(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -558,9 +565,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
           const uint32_t d = tmem + buf * kTile;
           const int k1 = min(k0 + t.segment, t.depth);
           for (int k = k0; k < k1; k += kStep) {
-            const bool loaded = !a.tma_a || !a.tma_b || (kBColumns && k + kStep > t.depth);
             const uint32_t bar = full + 8 * ring.stage;
-            if (!__all_sync(0xFFFFFFFFu, loaded ? mbar_wait<true>(bar, ring.phase, dead) : mbar_wait(bar, ring.phase, dead))) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar, ring.phase, dead))) {
               ok = false;
               break;
             }
@@ -648,7 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
             ok = false;
             break;
           }
-          if (ltid == 0) mbar_arrive(in_cta(smem_addr(&s.full[st]), 0));
+          if (ltid == 0) mbar_arrive_loaded(in_cta(smem_addr(&s.full[st]), 0));
         }
       }
     }
