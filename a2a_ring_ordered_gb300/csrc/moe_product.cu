@@ -19,7 +19,7 @@
 //        columns) against the next tile's products
 //   8    TMA: one thread issues the stage's bulk tensor copies
 //   9    MMA: one thread of the even CTA issues for the pair
-//   10-17 loaders: what TMA cannot do -- operands that do not sit on 16 bytes,
+//   10-25 loaders: what TMA cannot do -- operands that do not sit on 16 bytes,
 //        and grad_weight's last rows, which must read as zero where the next
 //        expert begins -- by whole 16-byte loads, shifted and masked
 // Every wait is bounded: one that runs out sets the device error word.
@@ -46,7 +46,7 @@ constexpr int kTmaWarp = kEpilogueWarps, kMmaWarp = kTmaWarp + 1, kLoaderWarp = 
 // The shares add up to what the block is launched with.
 template <bool REGS>
 struct Crew {
-  static constexpr int kLoaders = REGS ? 64 : 256;  // loader threads
+  static constexpr int kLoaders = REGS ? 64 : 512;  // loader threads
   static constexpr int kThreads = kLoaderWarp * 32 + kLoaders;
   static constexpr int kLaunchRegs = 168, kEpilogueRegs = 216, kOtherRegs = 72;  // a thread
   static_assert(!REGS || (kEpilogueWarps * 32 * kEpilogueRegs + (kThreads - kEpilogueWarps * 32) * kOtherRegs == kThreads * kLaunchRegs &&
@@ -295,33 +295,40 @@ __device__ __forceinline__ bool any_loader(bool x) {
   return r != 0;
 }
 
-// Fills lines [lo, hi) of a stage, 8 swizzled units of 8 elements each;
-// unit(l, u, p) says how many elements of a unit there are and points p at
-// them.  They come as the whole 16-byte granules that hold at least one of
-// them, kBatch units' loads issued before any is stored.
-template <int THREADS, typename Unit>
-__device__ __forceinline__ void fill_lines(char* dst, int lo, int hi, int tid, Unit unit) {
-  constexpr int kBatch = 4, kApart = THREADS / 8;
-  const int u = tid & 7;
-  for (int l0 = lo + (tid >> 3); l0 < hi; l0 += kBatch * kApart) {
-    uint4 g0[kBatch], g1[kBatch];
-    uint32_t at[kBatch];
-    int valid[kBatch];
+// What a loader thread fetches of an operand's share of a stage: unit u (8
+// elements) of lines l0 and l0 + 64, of 64 elements each.  COLUMNS: line l is
+// contraction row l mod 64 of 64-element chunk l / 64.
+template <bool COLUMNS>
+struct Fetch {
+  const __nv_bfloat16* p;  // unit u of line l0 in the tile's first stage
+  int64_t apart;           // elements from there to line l0 + 64
+  int extent;              // COLUMNS: elements of the row from the unit on; else lines from l0 on
+};
+// 16-byte granules in flight: the lower and the upper one of each unit.
+struct Units {
+  uint4 lo[2], hi[2];
+  int phase[2], valid[2];  // bytes of the lower one before the unit; elements
+};
+template <bool COLUMNS>
+__device__ __forceinline__ void fetch_units(const Fetch<COLUMNS>& f, const __nv_bfloat16* p, int left, int l0, int u, Units& v) {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const __nv_bfloat16* p;
-      valid[b] = unit(l0 + b * kApart, u, p);
-      if (l0 + b * kApart >= hi) valid[b] = 0;
-      const uintptr_t from = reinterpret_cast<uintptr_t>(p), base = from & ~static_cast<uintptr_t>(15);
-      at[b] = static_cast<uint32_t>(from - base);
-      g0[b] = load16_if(base, valid[b] > 0);
-      g1[b] = load16_if(base + 16, valid[b] > 0 && at[b] + 2 * valid[b] > 16);
-    }
+  for (int j = 0; j < 2; ++j) {
+    const int n = COLUMNS ? (l0 < left ? f.extent - 64 * j : 0) : 64 * j < f.extent ? left - 8 * u : 0;
+    v.valid[j] = min(max(n, 0), 8);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p + j * f.apart), base = at & ~static_cast<uintptr_t>(15);
+    v.phase[j] = static_cast<int>(at - base);
+    v.lo[j] = load16_if(base, v.valid[j] > 0);
+    v.hi[j] = load16_if(base + 16, v.valid[j] > 0 && v.phase[j] + 2 * v.valid[j] > 16);
+  }
+}
+__device__ __forceinline__ void put_units(char* dst, int lines, int l0, int u, const Units& v) {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int l = l0 + b * kApart;
-      if (l < hi) *reinterpret_cast<uint4*>(dst + l * 128 + ((u ^ (l & 7)) << 4)) = keep(shift16(g0[b], g1[b], at[b]), valid[b]);
-    }
+  for (int j = 0; j < 2; ++j) {
+    const int l = l0 + 64 * j;
+    if (l >= lines) continue;
+    uint4 x = shift16(v.lo[j], v.hi[j], v.phase[j]);
+    if (v.valid[j] < 8) x = keep(x, v.valid[j]);
+    *reinterpret_cast<uint4*>(dst + l * 128 + ((u ^ (l & 7)) << 4)) = x;
   }
 }
 
@@ -604,46 +611,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
         const int half = t.width >> 1;
         const int64_t c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
         const int64_t N = a.n, K = a.contract, rows = a.rows[t.rank];
-        const __nv_bfloat16* pa = static_cast<const __nv_bfloat16*>(a.pa[t.rank]);
-        const __nv_bfloat16* pb = static_cast<const __nv_bfloat16*>(a.pb[t.rank]);
+        const int lines_b = kBColumns ? (half + 63) & ~63 : half;
+        const int l0 = ltid >> 3, u = ltid & 7;
+        Fetch<kAColumns> fa;
+        Fetch<kBColumns> fb;
+        const int64_t ld_a = K, ld_b = KIND == kProductForward ? K : N;
+        if constexpr (!REGS) {
+          const __nv_bfloat16* pa = static_cast<const __nv_bfloat16*>(a.pa[t.rank]);
+          const __nv_bfloat16* pb = static_cast<const __nv_bfloat16*>(a.pb[t.rank]);
+          fa.apart = kAColumns ? 64 : 64 * ld_a;
+          fb.apart = kBColumns ? 64 : 64 * ld_b;
+          if constexpr (KIND == kProductForward) {
+            fa.p = pa + (static_cast<int64_t>(t.expert) * N + m + l0) * K + 8 * u;
+            fa.extent = static_cast<int>(N - m) - l0;
+          } else {
+            fa.p = pa + ((KIND == kProductGradInput ? static_cast<int64_t>(t.expert) * N : t.lo) + l0) * K + m + 8 * u;
+            fa.extent = static_cast<int>(K - m) - 8 * u;
+          }
+          if constexpr (kBColumns) {
+            fb.p = pb + (static_cast<int64_t>(t.lo) + l0) * N + c + 8 * u;
+            fb.extent = static_cast<int>(N - c) - 8 * u;
+          } else {
+            fb.p = pb + (c + l0) * ld_b + 8 * u;
+            fb.extent = static_cast<int>(rows - c) - l0;
+          }
+        }
         for (int k = 0; k < t.depth; k += kStep, ring.next()) {
           const uint32_t st = ring.stage;
           const bool tail = kBColumns && k + kStep > t.depth;
           if (a.tma_a && a.tma_b && !tail) continue;
+          const int left = t.depth - k;  // contraction elements from here
+          // the loads do not wait for the stage to be free
+          Units va, vb;
+          if constexpr (!REGS) {
+            if (!a.tma_a) fetch_units<kAColumns>(fa, fa.p + (kAColumns ? k * ld_a : k), left, l0, u, va);
+            if (!a.tma_b) fetch_units<kBColumns>(fb, fb.p + (kBColumns ? k * ld_b : k), left, l0, u, vb);
+          }
           const bool here = mbar_wait(smem_addr(&s.go[st]), (parity >> st) & 1, dead);
           parity ^= 1u << st;
-          const int left = t.depth - k;  // contraction elements from here
           char* sa = stages + static_cast<size_t>(st) * kStageBytes;
           char* sb = sa + kOperandBytes;
-          // lines of the stage: A's 128, then B's; each is 64 elements, `valid` of which are in the product
-          const int lines_b = kBColumns ? (half + 63) & ~63 : half;
-          const int l_lo = a.tma_a ? 128 : 0, l_hi = a.tma_b ? 128 : 128 + lines_b;
-          const auto unit = [&](int l, int u, const __nv_bfloat16*& p) {  // elements of unit u of line l, and where
-            int valid;
-            if (l < 128) {
-              if constexpr (KIND == kProductForward) {
-                p = pa + (static_cast<int64_t>(t.expert) * N + m + l) * K + k;
-                valid = m + l < N ? left : 0;
-              } else {
-                const int64_t row = KIND == kProductGradInput ? static_cast<int64_t>(t.expert) * N + k : static_cast<int64_t>(t.lo) + k;
-                p = pa + (row + (l & 63)) * K + m + (l & 64);
-                valid = (l & 63) < left ? static_cast<int>(min(K - m - (l & 64), int64_t{64})) : 0;
-              }
-            } else {
-              l -= 128;
-              if constexpr (kBColumns) {
-                p = pb + (static_cast<int64_t>(t.lo) + k + (l & 63)) * N + c + (l & 64);
-                valid = (l & 63) < left ? static_cast<int>(min(N - c - (l & 64), int64_t{64})) : 0;
-              } else {
-                p = pb + (c + l) * (KIND == kProductForward ? K : N) + k;
-                valid = c + l < rows ? left : 0;
-              }
-            }
-            p += u * 8;
-            return max(min(valid, 64) - u * 8, 0);
-          };
           if (here) {
-            if constexpr (!REGS) fill_lines<CREW::kLoaders>(sa, l_lo, l_hi, ltid, unit);
+            if constexpr (!REGS) {
+              if (!a.tma_a) put_units(sa, 128, l0, u, va);
+              if (!a.tma_b) put_units(sb, lines_b, l0, u, vb);
+            }
             if (tail) {  // rows behind the expert's last: the next expert's, or nobody's
               if (a.tma_a) clear_lines(sa, 128, left, ltid, CREW::kLoaders);
               if (a.tma_b) clear_lines(sb, lines_b, left, ltid, CREW::kLoaders);
