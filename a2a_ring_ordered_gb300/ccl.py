@@ -676,13 +676,13 @@ def _sizes(values) -> bytes:
     return _PACK_SIZES[len(values)](*values)
 
 
-def _explain(ts, name: str, p=None, dtype=None):
+def _explain(ts, name: str, p=None, dtype=None, cuda=False):
     """The rank buffers by the slow road: raises where one of them is not a
-    contiguous tensor of the dtype on the first one's device."""
+    contiguous tensor of the dtype on the first one's device (`cuda`: on a GPU)."""
     ts = list(ts)
     for i, t in enumerate(ts):
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name}[{i}] must be a CUDA tensor or a pinned host tensor")
+        if not isinstance(t, torch.Tensor) or (cuda and not t.is_cuda):
+            raise ValueError(f"{name}[{i}] must be a CUDA tensor" + ("" if cuda else " or a pinned host tensor"))
     ts = _tensors(ts, name)
     if p is not None and len(ts) != p:
         raise ValueError(f"{name} must hold {p} rank buffers, got {len(ts)}")
@@ -691,7 +691,7 @@ def _explain(ts, name: str, p=None, dtype=None):
     return ts
 
 
-def _ranks(ts, name: str, p: int, dtype, rows, width: int) -> bytes:
+def _ranks(ts, name: str, p: int, dtype, rows, width: int, cuda=False) -> bytes:
     """Addresses of the p rank buffers, rank r of rows[r] rows of `width` elements."""
     try:
         device, pointers = ts[0].get_device(), []
@@ -704,14 +704,14 @@ def _ranks(ts, name: str, p: int, dtype, rows, width: int) -> bytes:
                 return _PACK_POINTERS[p](*pointers)
     except (AttributeError, TypeError, IndexError):
         pass
-    ts = _explain(ts, name, p, dtype)
+    ts = _explain(ts, name, p, dtype, cuda)
     for r, t in enumerate(ts):
         if t.numel() != rows[r] * width:
             raise ValueError(f"{name}[{r}] has {t.numel()} elements, expected {rows[r]} x {width}")
     return _PACK_POINTERS[p](*[t.data_ptr() for t in ts])
 
 
-def _shaped(ts, name: str, dims: int, p=None, dtype=None):
+def _shaped(ts, name: str, dims: int, p=None, dtype=None, cuda=False):
     """(addresses, first tensor, first dimension of each rank, the others) of
     rank buffers of `dims` dimensions that are alike but for the first."""
     try:
@@ -731,7 +731,7 @@ def _shaped(ts, name: str, dims: int, p=None, dtype=None):
                 return _PACK_POINTERS[len(ts)](*pointers), first, sizes, rest
     except (AttributeError, TypeError, IndexError):
         pass
-    ts = _explain(ts, name, p, dtype)
+    ts = _explain(ts, name, p, dtype, cuda)
     rest = tuple(ts[0].shape)[1:]
     for r, t in enumerate(ts):
         if t.dim() != dims or tuple(t.shape)[1:] != rest:
@@ -825,7 +825,7 @@ def ccl_moe_from_experts_grad(dout, y, rows, weights, dy=None, dweights=None, st
 
 def _weights(ts, name: str, p: int, dtype=torch.bfloat16):
     """(addresses, first tensor, experts, n, contract) of a list of (experts, n, contract) tensors."""
-    pointers, one, experts, (n, contract) = _shaped(ts, name, 3, p, dtype)
+    pointers, one, experts, (n, contract) = _shaped(ts, name, 3, p, dtype, cuda=True)
     if experts.count(experts[0]) != p:
         raise ValueError(f"{name} must hold as many experts on every rank")
     return pointers, one, experts[0], n, contract
@@ -834,26 +834,26 @@ def _weights(ts, name: str, p: int, dtype=torch.bfloat16):
 def ccl_moe_product(x, offsets, w, y, stream=None) -> None:
     """y[rows of e] = x[rows of e] @ w[e].T for every expert e: x[r] (rows, contract),
     w[r] (experts, n, contract), y[r] (rows, n), bf16; offsets[r] from ccl_moe_sort."""
-    x, one, rows, (contract,) = _shaped(x, "x", 2, None, torch.bfloat16)
+    x, one, rows, (contract,) = _shaped(x, "x", 2, None, torch.bfloat16, cuda=True)
     p = len(rows)
     w, _, experts, n, depth = _weights(w, "w", p)
     if depth != contract:
         raise ValueError(f"w has {depth} columns, x {contract}")
-    y = _ranks(y, "y", p, torch.bfloat16, rows, n)
-    offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
+    y = _ranks(y, "y", p, torch.bfloat16, rows, n, True)
+    offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1, True)
     _check(LIB.ccl_moe_product(x, offsets, w, _sizes(rows), p, experts, n, contract, y, _stream_of(stream, one)),
            "ccl_moe_product")
 
 
 def ccl_moe_product_grad_input(dy, offsets, w, dx, stream=None) -> None:
     """dx[rows of e] = dy[rows of e] @ w[e]: the gradient of ccl_moe_product for x."""
-    dy, one, rows, (n,) = _shaped(dy, "dy", 2, None, torch.bfloat16)
+    dy, one, rows, (n,) = _shaped(dy, "dy", 2, None, torch.bfloat16, cuda=True)
     p = len(rows)
     w, _, experts, height, contract = _weights(w, "w", p)
     if height != n:
         raise ValueError(f"w has {height} rows, dy {n} columns")
-    dx = _ranks(dx, "dx", p, torch.bfloat16, rows, contract)
-    offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
+    dx = _ranks(dx, "dx", p, torch.bfloat16, rows, contract, True)
+    offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1, True)
     _check(LIB.ccl_moe_product_grad_input(dy, offsets, w, _sizes(rows), p, experts, n, contract, dx,
                                           _stream_of(stream, one)), "ccl_moe_product_grad_input")
 
@@ -861,13 +861,13 @@ def ccl_moe_product_grad_input(dy, offsets, w, dx, stream=None) -> None:
 def ccl_moe_product_grad_weight(dy, x, offsets, dw, stream=None) -> None:
     """dw[e] = dy[rows of e].T @ x[rows of e], fp32 or bf16 (zeros for an expert
     without rows): the gradient of ccl_moe_product for w."""
-    dy, one, rows, (n,) = _shaped(dy, "dy", 2, None, torch.bfloat16)
+    dy, one, rows, (n,) = _shaped(dy, "dy", 2, None, torch.bfloat16, cuda=True)
     p = len(rows)
     dw, held, experts, height, contract = _weights(dw, "dw", p, None)
     if height != n:
         raise ValueError(f"dw has {height} rows, dy {n} columns")
-    x = _ranks(x, "x", p, torch.bfloat16, rows, contract)
-    offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1)
+    x = _ranks(x, "x", p, torch.bfloat16, rows, contract, True)
+    offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1, True)
     _check(LIB.ccl_moe_product_grad_weight(dy, x, offsets, _sizes(rows), p, experts, n, contract, _dtype_code(held), dw,
                                            _stream_of(stream, one)), "ccl_moe_product_grad_weight")
 

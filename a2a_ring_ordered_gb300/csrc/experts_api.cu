@@ -286,7 +286,7 @@ ccl_status_t product(int kind, const void* const* first, const char* first_name,
   const bool weights_out = kind == kProductGradWeight;
   bool any = weights_out;
   for (int r = 0; r < p; ++r) {
-    if (rows[r] > 0x7FFFFFFFull) return report_error(CCL_ERR_INVALID_ARG, "rows[%d] must stay below 2^31", r);
+    if (rows[r] > 0x7FFFFF00ull) return report_error(CCL_ERR_INVALID_ARG, "rows[%d] must stay below 2^31 - 255", r);
     any = any || rows[r] != 0;
   }
   if (!any) return CCL_OK;

@@ -620,11 +620,8 @@ template <int DT, int VEC>
 cudaError_t launch_back(const MoeRowsArgs& a, cudaStream_t s) {
   const uint32_t nv = static_cast<uint32_t>(a.hidden / VEC);
   const uint64_t total = static_cast<uint64_t>(most_tokens(a)) * nv;
-  // few vectors: one per thread, so that more SMs have some
-  const bool few = total <= static_cast<uint64_t>(kThreads) * 4 * 152;
   return by_choices(a.k, [&](auto kb, auto u) {
     constexpr int KB = decltype(kb)::value, U = decltype(u)::value;
-    if (few) return launch_rows(moe_from_experts_kernel<DT, VEC, KB, 1>, ctas_for(total), a.p, s, a, nv);
     return launch_rows(moe_from_experts_kernel<DT, VEC, KB, U>, ctas_for((total + U - 1) / U), a.p, s, a, nv);
   });
 }

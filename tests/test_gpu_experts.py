@@ -457,5 +457,8 @@ def test_refusals_of_the_binding(lib):
     with pytest.raises(ValueError, match="columns"):
         lib.ccl_moe_product([torch.zeros(4, 8, device="cuda").bfloat16()], rows, [torch.zeros(2, 8, 9, device="cuda").bfloat16()],
                             [torch.zeros(4, 8, device="cuda").bfloat16()])
+    with pytest.raises(ValueError, match="must be a CUDA tensor$"):
+        lib.ccl_moe_product([torch.zeros(4, 8).bfloat16().pin_memory()], rows, [torch.zeros(1, 8, 8, device="cuda").bfloat16()],
+                            [torch.zeros(4, 8, device="cuda").bfloat16()])
     with pytest.raises(ValueError, match="dweights needs y"):
         lib.ccl_moe_from_experts_grad(out, None, rows, w, None, w)
