@@ -400,69 +400,80 @@ __global__ void __launch_bounds__(kThreads) moe_from_experts_grad_off_kernel(con
 }
 
 // -------------------------------------------------------------- on the grid
-// The same flat range, U vectors per thread: the rows of KB choices (all of
-// them, or 8 at a time) of its vectors are looked up together, then loaded
-// together, before any is added.  One choice of 32000 fp32 rows of 1000 took
-// 146 us with registers for eight choices, 95 with one choice and 8 vectors
-// per thread, 51 with 4 and 48 with 2: the lookups' latency needs warps.
+// The same flat range; a CTA takes `passes` runs of U vectors per thread.  The
+// rows and gates of its tokens, which lie together, are looked up once into
+// shared memory; in a pass a thread has the loads of KB choices (all of them,
+// or 8 at a time) on the way before any is added.
+constexpr uint32_t kLeastVectors = 8;    // per row, for the table to hold the tokens of one pass
+constexpr uint32_t kTableEntries = 1024;
 template <int DT, int VEC, int KB, int U>
-__global__ void __launch_bounds__(kThreads) moe_from_experts_kernel(const __grid_constant__ MoeRowsArgs a, uint32_t nv) {
+__global__ void __launch_bounds__(kThreads) moe_from_experts_kernel(const __grid_constant__ MoeRowsArgs a, uint32_t nv, uint32_t passes) {
   constexpr int W = (VEC * Elem<DT>::kBytes + 3) / 4;
+  static_assert((U * kThreads / kLeastVectors + 2) * (U > 1 ? KB : kMoeMaxK) <= kTableEntries, "the table holds a pass's choices");
+  __shared__ int64_t first[kTableEntries];  // element of the row, or -1
+  __shared__ float gate[kTableEntries];
   pdl_enter();
   const int r = blockIdx.y, k = a.k;
   const uint64_t total = static_cast<uint64_t>(a.tokens[r]) * nv;
-  const uint64_t f0 = static_cast<uint64_t>(blockIdx.x) * U * kThreads + threadIdx.x;
-  if (f0 >= total) return;
+  const uint64_t cta0 = static_cast<uint64_t>(blockIdx.x) * passes * (U * kThreads);
+  if (cta0 >= total) return;
+  const uint64_t cta1 = min(cta0 + static_cast<uint64_t>(passes) * (U * kThreads), total);
+  const uint64_t t0 = split(cta0, nv).q, t1 = split(cta1 - 1, nv).q;
+  const uint32_t entries = static_cast<uint32_t>(t1 - t0 + 1) * k;
   const float* weights = a.weights[r];
-  Split at[U];
-  float acc[U][VEC];
-  bool have[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    at[u] = split(f0 + u * kThreads, nv);
-    have[u] = false;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[u][e] = -0.0f;  // -0 + x is x, to the bit
+  for (uint32_t i = threadIdx.x; i < entries; i += kThreads) {
+    const int64_t row = row_of(a.rows[r], t0 * k + i, a.cap[r]);
+    first[i] = row >= 0 ? row * static_cast<int64_t>(a.hidden) : -1;
+    gate[i] = weights != nullptr ? __ldg(weights + t0 * k + i) : 1.0f;
   }
-  for (int j0 = 0; j0 < k; j0 += KB) {
-    uint32_t raw[U][KB][W];
-    int64_t row[U][KB];
-    float wt[U][KB];
+  __syncthreads();
+  // vectors from the first token's on: 32 bits serve
+  const uint32_t f1 = static_cast<uint32_t>(cta1 - t0 * nv);
+  for (uint32_t f0 = static_cast<uint32_t>(cta0 - t0 * nv) + threadIdx.x; f0 < f1; f0 += U * kThreads) {
+    uint32_t token[U], v[U];
+    float acc[U][VEC];
+    bool have[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      token[u] = (f0 + u * kThreads) / nv;
+      v[u] = (f0 + u * kThreads - token[u] * nv) * VEC;
+      have[u] = false;
 #pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        const bool there = f0 + u * kThreads < total && j0 + b < k;
-        row[u][b] = there ? row_of(a.rows[r], at[u].q * k + j0 + b, a.cap[r]) : -1;
-        wt[u][b] = (there && weights != nullptr) ? __ldg(weights + at[u].q * k + j0 + b) : 1.0f;
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int b = 0; b < KB; ++b)
-        if (row[u][b] >= 0) load_raw<DT, VEC>(a.y[r], row[u][b] * a.hidden + static_cast<uint64_t>(at[u].r) * VEC, raw[u][b]);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        if (row[u][b] < 0) continue;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          acc[u][e] = __fadd_rn(acc[u][e], __fmul_rn(wt[u][b], widen<DT>(raw[u][b], e)));
-        }
-        have[u] = true;
-      }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (f0 + u * kThreads >= total) continue;
-    if (!have[u]) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[u][e] = 0.0f;
+      for (int e = 0; e < VEC; ++e) acc[u][e] = -0.0f;  // -0 + x is x, to the bit
     }
-    uint32_t w[W];
-    pack_out<DT, VEC>(acc[u], w);
-    store_raw<DT, VEC>(a.out[r], at[u].q * a.hidden + static_cast<uint64_t>(at[u].r) * VEC, w);
+    for (int j0 = 0; j0 < k; j0 += KB) {
+      uint32_t raw[U][KB][W];
+      bool there[U][KB];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          const int64_t at = f0 + u * kThreads < f1 && j0 + b < k ? first[token[u] * k + j0 + b] : -1;
+          there[u][b] = at >= 0;
+          if (there[u][b]) load_raw<DT, VEC>(a.y[r], at + v[u], raw[u][b]);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          if (!there[u][b]) continue;
+          const float wt = gate[token[u] * k + j0 + b];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) acc[u][e] = __fadd_rn(acc[u][e], __fmul_rn(wt, widen<DT>(raw[u][b], e)));
+          have[u] = true;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (f0 + u * kThreads >= f1) continue;
+      if (!have[u]) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[u][e] = 0.0f;
+      }
+      uint32_t w[W];
+      pack_out<DT, VEC>(acc[u], w);
+      store_raw<DT, VEC>(a.out[r], (t0 + token[u]) * a.hidden + v[u], w);
+    }
   }
 }
 
@@ -616,13 +627,24 @@ cudaError_t launch_back_off(const MoeRowsArgs& a, cudaStream_t s) {
   });
 }
 
+constexpr uint64_t kPassCtas = 4 * 152 * 4;
+
 template <int DT, int VEC>
 cudaError_t launch_back(const MoeRowsArgs& a, cudaStream_t s) {
   const uint32_t nv = static_cast<uint32_t>(a.hidden / VEC);
   const uint64_t total = static_cast<uint64_t>(most_tokens(a)) * nv;
   return by_choices(a.k, [&](auto kb, auto u) {
     constexpr int KB = decltype(kb)::value, U = decltype(u)::value;
-    return launch_rows(moe_from_experts_kernel<DT, VEC, KB, U>, ctas_for((total + U - 1) / U), a.p, s, a, nv);
+    // as many passes as leave four waves of CTAs (eight at most), and no more
+    // than the table has room for
+    const uint64_t pass = static_cast<uint64_t>(U) * kThreads;
+    uint64_t passes = total * a.p / (pass * kPassCtas);
+    const uint64_t room = (kTableEntries / a.k - 2) * nv / pass;
+    passes = passes > 8 ? 8 : passes;
+    passes = passes > room ? room : passes;
+    if (passes == 0) passes = 1;
+    return launch_rows(moe_from_experts_kernel<DT, VEC, KB, U>, (total + pass * passes - 1) / (pass * passes), a.p, s, a, nv,
+                       static_cast<uint32_t>(passes));
   });
 }
 
@@ -683,8 +705,9 @@ cudaError_t launch_moe_to_experts(int dt, bool vec, const MoeRowsArgs& a, cudaSt
 }
 
 cudaError_t launch_moe_from_experts(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s) {
-  if (dt == kF32) return vec ? launch_back<kF32, 4>(a, s) : launch_back_off<kF32>(a, s);
-  return vec ? launch_back<kBF16, 8>(a, s) : launch_back_off<kBF16>(a, s);
+  // rows of fewer vectors than the table allows go by granules too
+  if (dt == kF32) return vec && a.hidden >= 4 * kLeastVectors ? launch_back<kF32, 4>(a, s) : launch_back_off<kF32>(a, s);
+  return vec && a.hidden >= 8 * kLeastVectors ? launch_back<kBF16, 8>(a, s) : launch_back_off<kBF16>(a, s);
 }
 
 cudaError_t launch_moe_from_experts_grad(int dt, bool vec, const MoeRowsArgs& a, cudaStream_t s) {
