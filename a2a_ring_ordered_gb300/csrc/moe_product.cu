@@ -19,10 +19,23 @@
 //        columns) against the next tile's products
 //   8    TMA: one thread issues the stage's bulk tensor copies
 //   9    MMA: one thread of the even CTA issues for the pair
-//   10-25 loaders: what TMA cannot do -- operands that do not sit on 16 bytes,
-//        and grad_weight's last rows, which must read as zero where the next
-//        expert begins -- by whole 16-byte loads, shifted and masked
+//   10-  loaders: what TMA cannot do -- operands that do not sit on 16 bytes
+//        (16 warps), by whole 16-byte loads, shifted and masked; and
+//        grad_weight's last rows, which must read as zero where the next
+//        expert begins (2 warps of them clear those where TMA reads the rest)
 // Every wait is bounded: one that runs out sets the device error word.
+//
+// Measured on bf16 operands (one GB300; 1944 TFLOP/s is the library's rate on
+// one large product in a burst, 6.78 TB/s a copy's):
+//   32 experts x 1024 rows, 2048 <- 7168: forward 523 us (1.84 PFLOP/s), input
+//     gradient 530, fp32 weight gradient 655.  The tensor pipe bounds the first
+//     two (92 % of cycles); the last reads both operands and writes its 1.9 GB
+//     through the same path from L2 to the SMs, 62 of its 64 bytes a clock.
+//   32 experts x 7..8 rows, the weights' stream: 155 us, 6.1 TB/s.
+//   operands off the grid (2047 x 7167): 3.4 ms forward, 2.6 ms backward; the
+//     loaders' instructions bound them.
+//   1 expert of 66 columns by 5376 contraction elements: 25 us, 84 stages one
+//     behind the other in a single pair.
 #include <cuda.h>  // CUtensorMap and its enums; nothing links the driver
 
 #include "device_common.cuh"
@@ -125,30 +138,19 @@ __device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive_own(uint32_t bar, uint32_t count = 1) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t done;
-  if constexpr (CLUSTER)
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(done)
+               : "r"(bar), "r"(parity)
+               : "memory");
   return done != 0;
 }
-// False once this or another wait of the CTA ran out.  CLUSTER: what the other
-// CTA's threads wrote before they arrived is seen behind it.
-template <bool CLUSTER = false>
+// False once this or another wait of the CTA ran out.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
-  if (mbar_try<CLUSTER>(bar, parity)) return true;
+  if (mbar_try(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try<CLUSTER>(bar, parity)) {
+  while (!mbar_try(bar, parity)) {
     if (*dead) return false;
     if (clock64() - t0 > kWaitCycles) {
       *dead = 1;
@@ -465,212 +467,212 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
   volatile uint32_t* dead = &s.dead;
 
   if (warp >= kEpilogueWarps) {
-  if constexpr (REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CREW::kOtherRegs));
-  if (warp == kTmaWarp) {
-    // ------------------------------------------------------------------ TMA
-    // The whole warp walks the stages, so that addresses and coordinates are
-    // uniform; one lane issues.
-    const bool issuer = elect_one();
-    Ring ring;
-    const uint32_t even = in_cta(smem_addr(s.full), 0);
-    const uint32_t own = smem_addr(s.full), empty = smem_addr(s.empty), data = smem_addr(stages);
-    bool ok = true;
-    for (uint64_t i = pair; ok && i < tiles; i += pairs) {
-      const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
-      const int half = t.width >> 1;
-      const int c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
-      const int boxes = kBColumns ? (half + 63) / 64 : half > 64 ? 1 : (half + kSmallBox - 1) / kSmallBox;
-      const uint32_t box_bytes = kBColumns ? kStep * 128 : half > 64 ? kOperandBytes : kSmallBox * 128;
-      const CUtensorMap* map_a = &a.a[t.rank];
-      const CUtensorMap* map_b = !kBColumns && half <= 64 ? &a.b_small[t.rank] : &a.b[t.rank];
-      const CUtensorMap* map_small = &a.b_small[t.rank];
-      const int z = KIND == kProductGradWeight ? 0 : t.expert;
-      for (int k = 0; k < t.depth; k += kStep) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead))) {
-          ok = false;
-          break;
-        }
-        if (issuer) {
-          // the even CTA's barrier counts both CTAs' copies; its own TMA
-          // thread alone arrives, for the bytes of both
-          uint32_t bar = even + 8 * ring.stage;
-          const bool tail = kBColumns && k + kStep > t.depth;
-          const bool do_a = a.tma_a, do_b = a.tma_b;
-          const uint32_t bytes = (do_a ? kOperandBytes : 0) + (do_b ? boxes * box_bytes : 0);
-          const bool loaded = tail || !do_a || !do_b;  // the loaders have a part in the stage
-          const uint32_t go = smem_addr(&s.go[ring.stage]);
-          if (loaded) mbar_arrive_tx(go, tail ? bytes : 0);
-          if (cta == 0) {
-            if (loaders && !loaded) mbar_arrive_own(own + 8 * ring.stage, 2);  // in the loaders' place
-            mbar_arrive_tx(own + 8 * ring.stage, tail ? 0 : 2 * bytes);
-          }
-          if (tail) bar = go;  // the loaders clear what lies behind the last row
-          const uint32_t sa = data + ring.stage * kStageBytes, sb = sa + kOperandBytes;
-          if (do_a) {
-            if constexpr (!kAColumns) {
-              tma(sa, map_a, k, m, 0, z, bar);
-            } else {
-              const int line = KIND == kProductGradInput ? k : t.lo + k;
-              if (a.whole_a) {
-                tma(sa, map_a, 0, line, m >> 6, z, bar);
-              } else {
-                tma(sa, map_a, m, line, 0, z, bar);
-                tma(sa + kStep * 128, map_a, m + 64, line, 0, z, bar);
-              }
-            }
-          }
-          if (do_b) {
-            if constexpr (kBColumns) {
-              if (a.whole_b && boxes > 1) {
-                tma(sb, map_b, 0, t.lo + k, c >> 6, 0, bar);
-              } else {
-                tma(sb, map_small, c, t.lo + k, 0, 0, bar);
-                if (boxes > 1) tma(sb + kStep * 128, map_small, c + 64, t.lo + k, 0, 0, bar);
-              }
-            } else {
-              tma(sb, map_b, k, c, 0, 0, bar);
-              for (int q = 1; q < boxes; ++q) tma(sb + q * kSmallBox * 128, map_b, k, c + q * kSmallBox, 0, 0, bar);
-            }
-          }
-        }
-        ring.next();
-      }
-    }
-    // every stage given back: no signal of the tensor core is on its way to a
-    // CTA that has left
-    for (int j = 0; ok && j < kStages; ++j, ring.next())
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead));
-    if (!ok) {  // copies in flight still write this CTA's shared memory
-      const long long t0 = clock64();
-      while (clock64() - t0 < (1ll << 22)) {
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ MMA
-    if (cta == 0) {
+    if constexpr (REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CREW::kOtherRegs));
+    if (warp == kTmaWarp) {
+      // ------------------------------------------------------------------ TMA
+      // The whole warp walks the stages, so that addresses and coordinates are
+      // uniform; one lane issues.
       const bool issuer = elect_one();
       Ring ring;
-      uint32_t n = 0;
-      const uint32_t full = smem_addr(s.full), empty = smem_addr(s.empty);
-      // descriptors of stage 0; a stage, and 16 contraction elements, further on
-      const uint64_t a0 = descriptor(smem_addr(stages), kAColumns ? kStep * 128 : 16);
-      const uint64_t b0 = descriptor(smem_addr(stages) + kOperandBytes, kBColumns ? kStep * 128 : 16);
-      constexpr uint64_t kNextA = (kAColumns ? 2048 : 32) >> 4, kNextB = (kBColumns ? 2048 : 32) >> 4;
-      bool ok = true;
-      for (uint64_t i = pair; ok && i < tiles; i += pairs) {
-        const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
-        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAColumns ? 1u << 15 : 0u) | (kBColumns ? 1u << 16 : 0u) |
-                               (static_cast<uint32_t>(t.width >> 3) << 17) | (16u << 24);
-        int k0 = 0;
-        do {  // a segment, also of an expert without rows
-          const uint32_t buf = n & 1;
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_empty[buf]), ((n >> 1) & 1) ^ 1, dead))) {
-            ok = false;
-            break;
-          }
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t d = tmem + buf * kTile;
-          const int k1 = min(k0 + t.segment, t.depth);
-          for (int k = k0; k < k1; k += kStep) {
-            const uint32_t bar = full + 8 * ring.stage;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar, ring.phase, dead))) {
-              ok = false;
-              break;
-            }
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            if (issuer) {
-              const uint64_t da = a0 + ring.stage * (kStageBytes >> 4), db = b0 + ring.stage * (kStageBytes >> 4);
-              const int left = k1 - k;  // contraction elements from here
-              mma(d, da, db, idesc, k != k0);
-              if (left > 16) mma(d, da + kNextA, db + kNextB, idesc, 1);
-              if (left > 32) mma(d, da + 2 * kNextA, db + 2 * kNextB, idesc, 1);
-              if (left > 48) mma(d, da + 3 * kNextA, db + 3 * kNextB, idesc, 1);
-              commit_pair(empty + 8 * ring.stage);
-            }
-            ring.next();
-          }
-          if (ok && issuer) commit_pair(smem_addr(&s.tmem_full[buf]));
-          __syncwarp();
-          k0 += t.segment;
-          ++n;
-        } while (ok && k0 < t.depth);
-      }
-    }
-  } else {
-    // -------------------------------------------------------------- loaders
-    if (loaders) {
-      const int ltid = tid - kLoaderWarp * 32;
-      Ring ring;
-      // parity of each stage's next `go`.  The loaders skip stages, so they
-      // could not follow `empty` by its parity: several of its phases may pass
-      // between two of theirs, while `go` moves on only once they have filled.
-      uint32_t parity = 0;
+      const uint32_t even = in_cta(smem_addr(s.full), 0);
+      const uint32_t own = smem_addr(s.full), empty = smem_addr(s.empty), data = smem_addr(stages);
       bool ok = true;
       for (uint64_t i = pair; ok && i < tiles; i += pairs) {
         const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
         const int half = t.width >> 1;
-        const int64_t c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
-        const int64_t N = a.n, K = a.contract, rows = a.rows[t.rank];
-        const int lines_b = kBColumns ? (half + 63) & ~63 : half;
-        const int l0 = ltid >> 3, u = ltid & 7;
-        Fetch<kAColumns> fa;
-        Fetch<kBColumns> fb;
-        const int64_t ld_a = K, ld_b = KIND == kProductForward ? K : N;
-        if constexpr (!REGS) {
-          const __nv_bfloat16* pa = static_cast<const __nv_bfloat16*>(a.pa[t.rank]);
-          const __nv_bfloat16* pb = static_cast<const __nv_bfloat16*>(a.pb[t.rank]);
-          fa.apart = kAColumns ? 64 : 64 * ld_a;
-          fb.apart = kBColumns ? 64 : 64 * ld_b;
-          if constexpr (KIND == kProductForward) {
-            fa.p = pa + (static_cast<int64_t>(t.expert) * N + m + l0) * K + 8 * u;
-            fa.extent = static_cast<int>(N - m) - l0;
-          } else {
-            fa.p = pa + ((KIND == kProductGradInput ? static_cast<int64_t>(t.expert) * N : t.lo) + l0) * K + m + 8 * u;
-            fa.extent = static_cast<int>(K - m) - 8 * u;
-          }
-          if constexpr (kBColumns) {
-            fb.p = pb + (static_cast<int64_t>(t.lo) + l0) * N + c + 8 * u;
-            fb.extent = static_cast<int>(N - c) - 8 * u;
-          } else {
-            fb.p = pb + (c + l0) * ld_b + 8 * u;
-            fb.extent = static_cast<int>(rows - c) - l0;
-          }
-        }
-        for (int k = 0; k < t.depth; k += kStep, ring.next()) {
-          const uint32_t st = ring.stage;
-          const bool tail = kBColumns && k + kStep > t.depth;
-          if (a.tma_a && a.tma_b && !tail) continue;
-          const int left = t.depth - k;  // contraction elements from here
-          // the loads do not wait for the stage to be free
-          Units va, vb;
-          if constexpr (!REGS) {
-            if (!a.tma_a) fetch_units<kAColumns>(fa, fa.p + (kAColumns ? k * ld_a : k), left, l0, u, va);
-            if (!a.tma_b) fetch_units<kBColumns>(fb, fb.p + (kBColumns ? k * ld_b : k), left, l0, u, vb);
-          }
-          const bool here = mbar_wait(smem_addr(&s.go[st]), (parity >> st) & 1, dead);
-          parity ^= 1u << st;
-          char* sa = stages + static_cast<size_t>(st) * kStageBytes;
-          char* sb = sa + kOperandBytes;
-          if (here) {
-            if constexpr (!REGS) {
-              if (!a.tma_a) put_units(sa, 128, l0, u, va);
-              if (!a.tma_b) put_units(sb, lines_b, l0, u, vb);
-            }
-            if (tail) {  // rows behind the expert's last: the next expert's, or nobody's
-              if (a.tma_a) clear_lines(sa, 128, left, ltid, CREW::kLoaders);
-              if (a.tma_b) clear_lines(sb, lines_b, left, ltid, CREW::kLoaders);
-            }
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (any_loader<CREW::kLoaders>(!here)) {  // one answer for all of them
+        const int c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
+        const int boxes = kBColumns ? (half + 63) / 64 : half > 64 ? 1 : (half + kSmallBox - 1) / kSmallBox;
+        const uint32_t box_bytes = kBColumns ? kStep * 128 : half > 64 ? kOperandBytes : kSmallBox * 128;
+        const CUtensorMap* map_a = &a.a[t.rank];
+        const CUtensorMap* map_b = !kBColumns && half <= 64 ? &a.b_small[t.rank] : &a.b[t.rank];
+        const CUtensorMap* map_small = &a.b_small[t.rank];
+        const int z = KIND == kProductGradWeight ? 0 : t.expert;
+        for (int k = 0; k < t.depth; k += kStep) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead))) {
             ok = false;
             break;
           }
-          if (ltid == 0) mbar_arrive_loaded(in_cta(smem_addr(&s.full[st]), 0));
+          if (issuer) {
+            // the even CTA's barrier counts both CTAs' copies; its own TMA
+            // thread alone arrives, for the bytes of both
+            uint32_t bar = even + 8 * ring.stage;
+            const bool tail = kBColumns && k + kStep > t.depth;
+            const bool do_a = a.tma_a, do_b = a.tma_b;
+            const uint32_t bytes = (do_a ? kOperandBytes : 0) + (do_b ? boxes * box_bytes : 0);
+            const bool loaded = tail || !do_a || !do_b;  // the loaders have a part in the stage
+            const uint32_t go = smem_addr(&s.go[ring.stage]);
+            if (loaded) mbar_arrive_tx(go, tail ? bytes : 0);
+            if (cta == 0) {
+              if (loaders && !loaded) mbar_arrive_own(own + 8 * ring.stage, 2);  // in the loaders' place
+              mbar_arrive_tx(own + 8 * ring.stage, tail ? 0 : 2 * bytes);
+            }
+            if (tail) bar = go;  // the loaders clear what lies behind the last row
+            const uint32_t sa = data + ring.stage * kStageBytes, sb = sa + kOperandBytes;
+            if (do_a) {
+              if constexpr (!kAColumns) {
+                tma(sa, map_a, k, m, 0, z, bar);
+              } else {
+                const int line = KIND == kProductGradInput ? k : t.lo + k;
+                if (a.whole_a) {
+                  tma(sa, map_a, 0, line, m >> 6, z, bar);
+                } else {
+                  tma(sa, map_a, m, line, 0, z, bar);
+                  tma(sa + kStep * 128, map_a, m + 64, line, 0, z, bar);
+                }
+              }
+            }
+            if (do_b) {
+              if constexpr (kBColumns) {
+                if (a.whole_b && boxes > 1) {
+                  tma(sb, map_b, 0, t.lo + k, c >> 6, 0, bar);
+                } else {
+                  tma(sb, map_small, c, t.lo + k, 0, 0, bar);
+                  if (boxes > 1) tma(sb + kStep * 128, map_small, c + 64, t.lo + k, 0, 0, bar);
+                }
+              } else {
+                tma(sb, map_b, k, c, 0, 0, bar);
+                for (int q = 1; q < boxes; ++q) tma(sb + q * kSmallBox * 128, map_b, k, c + q * kSmallBox, 0, 0, bar);
+              }
+            }
+          }
+          ring.next();
+        }
+      }
+      // every stage given back: no signal of the tensor core is on its way to a
+      // CTA that has left
+      for (int j = 0; ok && j < kStages; ++j, ring.next())
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead));
+      if (!ok) {  // copies in flight still write this CTA's shared memory
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1ll << 22)) {
+        }
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------------ MMA
+      if (cta == 0) {
+        const bool issuer = elect_one();
+        Ring ring;
+        uint32_t n = 0;
+        const uint32_t full = smem_addr(s.full), empty = smem_addr(s.empty);
+        // descriptors of stage 0; a stage, and 16 contraction elements, further on
+        const uint64_t a0 = descriptor(smem_addr(stages), kAColumns ? kStep * 128 : 16);
+        const uint64_t b0 = descriptor(smem_addr(stages) + kOperandBytes, kBColumns ? kStep * 128 : 16);
+        constexpr uint64_t kNextA = (kAColumns ? 2048 : 32) >> 4, kNextB = (kBColumns ? 2048 : 32) >> 4;
+        bool ok = true;
+        for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+          const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
+          const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAColumns ? 1u << 15 : 0u) | (kBColumns ? 1u << 16 : 0u) |
+                                 (static_cast<uint32_t>(t.width >> 3) << 17) | (16u << 24);
+          int k0 = 0;
+          do {  // a segment, also of an expert without rows
+            const uint32_t buf = n & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_empty[buf]), ((n >> 1) & 1) ^ 1, dead))) {
+              ok = false;
+              break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t d = tmem + buf * kTile;
+            const int k1 = min(k0 + t.segment, t.depth);
+            for (int k = k0; k < k1; k += kStep) {
+              const uint32_t bar = full + 8 * ring.stage;
+              if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar, ring.phase, dead))) {
+                ok = false;
+                break;
+              }
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+              if (issuer) {
+                const uint64_t da = a0 + ring.stage * (kStageBytes >> 4), db = b0 + ring.stage * (kStageBytes >> 4);
+                const int left = k1 - k;  // contraction elements from here
+                mma(d, da, db, idesc, k != k0);
+                if (left > 16) mma(d, da + kNextA, db + kNextB, idesc, 1);
+                if (left > 32) mma(d, da + 2 * kNextA, db + 2 * kNextB, idesc, 1);
+                if (left > 48) mma(d, da + 3 * kNextA, db + 3 * kNextB, idesc, 1);
+                commit_pair(empty + 8 * ring.stage);
+              }
+              ring.next();
+            }
+            if (ok && issuer) commit_pair(smem_addr(&s.tmem_full[buf]));
+            __syncwarp();
+            k0 += t.segment;
+            ++n;
+          } while (ok && k0 < t.depth);
+        }
+      }
+    } else {
+      // -------------------------------------------------------------- loaders
+      if (loaders) {
+        const int ltid = tid - kLoaderWarp * 32;
+        Ring ring;
+        // parity of each stage's next `go`.  The loaders skip stages, so they
+        // could not follow `empty` by its parity: several of its phases may pass
+        // between two of theirs, while `go` moves on only once they have filled.
+        uint32_t parity = 0;
+        bool ok = true;
+        for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+          const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
+          const int half = t.width >> 1;
+          const int64_t c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
+          const int64_t N = a.n, K = a.contract, rows = a.rows[t.rank];
+          const int lines_b = kBColumns ? (half + 63) & ~63 : half;
+          const int l0 = ltid >> 3, u = ltid & 7;
+          Fetch<kAColumns> fa;
+          Fetch<kBColumns> fb;
+          const int64_t ld_a = K, ld_b = KIND == kProductForward ? K : N;
+          if constexpr (!REGS) {
+            const __nv_bfloat16* pa = static_cast<const __nv_bfloat16*>(a.pa[t.rank]);
+            const __nv_bfloat16* pb = static_cast<const __nv_bfloat16*>(a.pb[t.rank]);
+            fa.apart = kAColumns ? 64 : 64 * ld_a;
+            fb.apart = kBColumns ? 64 : 64 * ld_b;
+            if constexpr (KIND == kProductForward) {
+              fa.p = pa + (static_cast<int64_t>(t.expert) * N + m + l0) * K + 8 * u;
+              fa.extent = static_cast<int>(N - m) - l0;
+            } else {
+              fa.p = pa + ((KIND == kProductGradInput ? static_cast<int64_t>(t.expert) * N : t.lo) + l0) * K + m + 8 * u;
+              fa.extent = static_cast<int>(K - m) - 8 * u;
+            }
+            if constexpr (kBColumns) {
+              fb.p = pb + (static_cast<int64_t>(t.lo) + l0) * N + c + 8 * u;
+              fb.extent = static_cast<int>(N - c) - 8 * u;
+            } else {
+              fb.p = pb + (c + l0) * ld_b + 8 * u;
+              fb.extent = static_cast<int>(rows - c) - l0;
+            }
+          }
+          for (int k = 0; k < t.depth; k += kStep, ring.next()) {
+            const uint32_t st = ring.stage;
+            const bool tail = kBColumns && k + kStep > t.depth;
+            if (a.tma_a && a.tma_b && !tail) continue;
+            const int left = t.depth - k;  // contraction elements from here
+            // the loads do not wait for the stage to be free
+            Units va, vb;
+            if constexpr (!REGS) {
+              if (!a.tma_a) fetch_units<kAColumns>(fa, fa.p + (kAColumns ? k * ld_a : k), left, l0, u, va);
+              if (!a.tma_b) fetch_units<kBColumns>(fb, fb.p + (kBColumns ? k * ld_b : k), left, l0, u, vb);
+            }
+            const bool here = mbar_wait(smem_addr(&s.go[st]), (parity >> st) & 1, dead);
+            parity ^= 1u << st;
+            char* sa = stages + static_cast<size_t>(st) * kStageBytes;
+            char* sb = sa + kOperandBytes;
+            if (here) {
+              if constexpr (!REGS) {
+                if (!a.tma_a) put_units(sa, 128, l0, u, va);
+                if (!a.tma_b) put_units(sb, lines_b, l0, u, vb);
+              }
+              if (tail) {  // rows behind the expert's last: the next expert's, or nobody's
+                if (a.tma_a) clear_lines(sa, 128, left, ltid, CREW::kLoaders);
+                if (a.tma_b) clear_lines(sb, lines_b, left, ltid, CREW::kLoaders);
+              }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (any_loader<CREW::kLoaders>(!here)) {  // one answer for all of them
+              ok = false;
+              break;
+            }
+            if (ltid == 0) mbar_arrive_loaded(in_cta(smem_addr(&s.full[st]), 0));
+          }
         }
       }
     }
-  }
   } else {
     // ------------------------------------------------------------- epilogue
     if constexpr (REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CREW::kEpilogueRegs));
