@@ -122,14 +122,14 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+// On a barrier of either CTA of the pair.  A release at cluster scope would wait
+// for all of the thread's memory operations, which nothing here needs: the
+// loaders' writes, behind a proxy fence and a barrier of the writers, lie in
+// their own SM's shared memory, where the tensor core reads them (a release
+// there took a microsecond a stage); the epilogue has read tensor memory, which
+// its fence orders, and its stores are nobody's concern (with one, the fp32
+// weight gradients of 32 experts of 512 rows took 489 us instead of 437).
 __device__ __forceinline__ void mbar_arrive(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-// Behind a proxy fence and a barrier of the writers: what they wrote lies in
-// their own SM's shared memory, which is where the tensor core reads it.  (A
-// release at cluster scope waits for all of the thread's memory operations, a
-// microsecond a stage.)
-__device__ __forceinline__ void mbar_arrive_loaded(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
@@ -233,17 +233,18 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, 
 
 // SPLIT: sums longer than kMostSummed are made in parts.
 template <int KIND, bool SPLIT>
-__device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int groups, uint64_t index, uint32_t mt) {
-  const uint32_t rt = static_cast<uint32_t>(index / mt);
+__device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int groups, uint32_t index, uint32_t mt) {
+  const uint32_t rt = index / mt;
   Tile t;
-  t.m0 = static_cast<int>(index - static_cast<uint64_t>(rt) * mt) * kTile;
+  t.m0 = static_cast<int>(index - rt * mt) * kTile;
   int g;
   if constexpr (KIND == kProductGradWeight) {
     const uint32_t nt = (a.n + kTile - 1) / kTile;
     g = static_cast<int>(rt / nt);
+    t.lo = uniform(s.lo[g]);
     t.c0 = static_cast<int>(rt - g * nt) * kTile;
     t.cols = min(kTile, static_cast<int>(a.n) - t.c0);
-    t.depth = s.count[g];
+    t.depth = uniform(s.count[g]);
   } else {
     int lo = 0, hi = groups - 1;  // the last group that begins at or before rt
     while (lo < hi) {
@@ -251,21 +252,17 @@ __device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int 
       if (s.first[mid] <= rt) lo = mid;
       else hi = mid - 1;
     }
-    g = lo;
-    const int rows = s.count[g], tiles = (rows + kTile - 1) / kTile;
+    g = uniform(lo);
+    t.lo = uniform(s.lo[g]);
+    const int rows = uniform(s.count[g]), tiles = (rows + kTile - 1) / kTile;
     const int each = ((rows + tiles - 1) / tiles + 31) & ~31;
-    const int at = static_cast<int>(rt - s.first[g]) * each;
-    t.c0 = s.lo[g] + at;
+    const int at = static_cast<int>(rt - uniform(s.first[g])) * each;
+    t.c0 = t.lo + at;
     t.cols = min(each, rows - at);
     t.depth = static_cast<int>(KIND == kProductForward ? a.contract : a.n);
   }
-  t.lo = uniform(s.lo[g]);
-  t.rank = uniform(g / a.num_experts);
-  t.expert = uniform(g - t.rank * a.num_experts);
-  t.m0 = uniform(t.m0);
-  t.c0 = uniform(t.c0);
-  t.cols = uniform(t.cols);
-  t.depth = uniform(t.depth);
+  t.rank = g / a.num_experts;
+  t.expert = g - t.rank * a.num_experts;
   t.width = (t.cols + 31) & ~31;
   t.segment = t.depth;
   if (SPLIT && t.depth > kMostSummed) {
@@ -350,7 +347,7 @@ __device__ __forceinline__ void store_rows(char* p, uint64_t ld, const uint32_t*
   if constexpr (OUT == kF32) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (live && (ALL || j < count)) *reinterpret_cast<uint32_t*>(p + j * ld) = v[j];
+      if (live && (ALL || j < count)) st_stream4(p + j * ld, v[j]);
   } else {
     const int odd = threadIdx.x & 1;
     if (even) {
@@ -462,8 +459,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s.tmem;
-  const uint64_t tiles = (KIND == kProductGradWeight ? static_cast<uint64_t>(groups) * ((a.n + kTile - 1) / kTile)
-                                                     : static_cast<uint64_t>(s.first[groups])) * mt;
+  // 32 bits serve: 2^32 tiles of full size are 2^49 bytes of output, and at most
+  // groups * 2^14 + rows / 256 are not
+  const uint32_t tiles = (KIND == kProductGradWeight ? groups * ((a.n + kTile - 1) / kTile) : s.first[groups]) * mt;
   volatile uint32_t* dead = &s.dead;
 
   if (warp >= kEpilogueWarps) {
@@ -477,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
       const uint32_t even = in_cta(smem_addr(s.full), 0);
       const uint32_t own = smem_addr(s.full), empty = smem_addr(s.empty), data = smem_addr(stages);
       bool ok = true;
-      for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+      for (uint32_t i = pair; ok && i < tiles; i += pairs) {
         const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
         const int half = t.width >> 1;
         const int c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
@@ -559,7 +557,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
         const uint64_t b0 = descriptor(smem_addr(stages) + kOperandBytes, kBColumns ? kStep * 128 : 16);
         constexpr uint64_t kNextA = (kAColumns ? 2048 : 32) >> 4, kNextB = (kBColumns ? 2048 : 32) >> 4;
         bool ok = true;
-        for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+        for (uint32_t i = pair; ok && i < tiles; i += pairs) {
           const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
           const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAColumns ? 1u << 15 : 0u) | (kBColumns ? 1u << 16 : 0u) |
                                  (static_cast<uint32_t>(t.width >> 3) << 17) | (16u << 24);
@@ -608,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
         // between two of theirs, while `go` moves on only once they have filled.
         uint32_t parity = 0;
         bool ok = true;
-        for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+        for (uint32_t i = pair; ok && i < tiles; i += pairs) {
           const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
           const int half = t.width >> 1;
           const int64_t c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
@@ -668,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
               ok = false;
               break;
             }
-            if (ltid == 0) mbar_arrive_loaded(in_cta(smem_addr(&s.full[st]), 0));
+            if (ltid == 0) mbar_arrive(in_cta(smem_addr(&s.full[st]), 0));
           }
         }
       }
@@ -680,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
     bool ok = true;
     const uint32_t quarter = warp & 3;  // the 32 lanes that this warp can read
     constexpr int kBytes = Elem<OUT>::kBytes;
-    for (uint64_t i = pair; ok && i < tiles; i += pairs) {
+    for (uint32_t i = pair; ok && i < tiles; i += pairs) {
       const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
       const uint32_t m = t.m0 + cta * 128 + quarter * 32 + lane;
       const uint64_t at = (KIND == kProductGradWeight ? static_cast<uint64_t>(t.expert) * a.n + t.c0 : static_cast<uint64_t>(t.c0)) * M + m;
