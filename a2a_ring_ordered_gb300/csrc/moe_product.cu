@@ -27,10 +27,13 @@
 //
 // Measured on bf16 operands (one GB300; 1944 TFLOP/s is the library's rate on
 // one large product in a burst, 6.78 TB/s a copy's):
-//   32 experts x 1024 rows, 2048 <- 7168: forward 523 us (1.84 PFLOP/s), input
-//     gradient 530, fp32 weight gradient 655.  The tensor pipe bounds the first
-//     two (92 % of cycles); the last reads both operands and writes its 1.9 GB
-//     through the same path from L2 to the SMs, 62 of its 64 bytes a clock.
+//   32 experts x 1024 rows, 2048 <- 7168: forward 525 us (1.83 PFLOP/s), input
+//     gradient 530, fp32 weight gradient 650.  The tensor pipe bounds the first
+//     two (92 % of cycles).  The last takes 532 without its 1.9 GB of stores,
+//     which delay the loads; a quarter fewer loads gained 4 %, and tiles of two
+//     or four experts under way at a time lost 5 %.
+//   32 experts x 512 rows: weight gradient 415 us; without rows, 1.9 GB of
+//     zeros, 287 us (6.5 TB/s).
 //   32 experts x 7..8 rows, the weights' stream: 155 us, 6.1 TB/s.
 //   operands off the grid (2047 x 7167): 3.4 ms forward, 2.6 ms backward; the
 //     loaders' instructions bound them.
@@ -74,7 +77,7 @@ constexpr uint32_t kTmemColumns = 512;
 // bf16 outputs round to 4e-3 and hide that; an fp32 weight gradient is summed
 // in parts of at most so many rows (5e-7), which the epilogue adds up: in
 // registers, or, where loaders fill the stages and set the pace, in the output
-// (32 experts of 1024 rows by TMA: 948 us that way).
+// (32 experts of 1024 rows by TMA took 948 us that way, 650 in registers).
 constexpr int kMostSummed = 512;
 constexpr long long kWaitCycles = 1ll << 32;  // two seconds
 
