@@ -7,8 +7,10 @@
 // fp32 parameters and states and bf16 gradients, 14.125 with 8-bit states (and
 // 2 for a bf16 copy).  Measured with the copy, 157 M elements: fp32 states 629
 // us (7.0 TB/s); 8-bit states 429 us (5.9 TB/s) with every array on the
-// vectors' grid, 480 with gradients off it, where issue slots (0.71 a cycle)
-// and HBM are both two thirds full.
+// vectors' grid, where issue slots (0.71 a cycle) and HBM are both two thirds
+// full; 480 with parameters, gradients and copies off it: a tenth more
+// instructions, for which the stage's vectors cannot serve, since stores of
+// neighbours per lane would ask for every sector four times.
 //
 // An 8-bit state is e4m3 codes with one fp32 scale per 128 elements.  A warp
 // holds such a block with four elements per lane, so its amax is one
