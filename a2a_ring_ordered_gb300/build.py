@@ -1,4 +1,5 @@
-"""Build ``lib/libccl.so`` in-tree with nvcc for sm_103a (GB300).
+"""Build ``lib/libccl.so`` in-tree with nvcc for sm_103a (GB300), and the
+binding's ``lib/_tensors.so`` with g++ against the installed torch.
 
 Each translation unit compiles in parallel, then one link step produces the
 shared library (CUDA runtime linked statically, so the library needs only the
@@ -10,10 +11,12 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libccl.so")
+TENSORS = os.path.join(LIBDIR, "_tensors.so")
+TENSORS_SRC = os.path.join(CSRC, "tensors.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [
@@ -47,11 +52,42 @@ def _deps() -> list[str]:
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(product: str, deps: list[str]) -> bool:
+    if not os.path.exists(product):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    t = os.path.getmtime(product)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def _torch() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch is required to build _tensors.so")
+    return list(spec.submodule_search_locations)[0]
+
+
+def build_tensors(force: bool = False, verbose: bool = False) -> str:
+    """Compile the binding's helper if needed; returns its path."""
+    torch = _torch()
+    if not force and _newer(TENSORS, [TENSORS_SRC, os.path.abspath(__file__), os.path.join(torch, "version.py")]):
+        return TENSORS
+    os.makedirs(LIBDIR, exist_ok=True)
+    include = os.path.join(torch, "include")
+    tmp = TENSORS + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-o", tmp, TENSORS_SRC,
+           "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on tensors.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TENSORS)
+    return TENSORS
 
 
 def _compile(src: str, verbose: bool, ptxas_v: bool) -> str:
@@ -70,7 +106,16 @@ def _compile(src: str, verbose: bool, ptxas_v: bool) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
-    """Compile and link the library if needed; returns its path."""
+    """Compile and link the library, and the binding's helper, if needed;
+    returns the library's path."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        helper = ex.submit(build_tensors, force, verbose)
+        lib = _build_library(force, verbose, ptxas_v)
+        helper.result()
+    return lib
+
+
+def _build_library(force: bool, verbose: bool, ptxas_v: bool) -> str:
     if not force and not ptxas_v and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -13,7 +13,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import math
+import importlib.machinery
+import importlib.util
 import os
 import struct
 from typing import Sequence
@@ -121,6 +122,22 @@ def _load() -> ctypes.CDLL:
 
 
 LIB = _load()
+
+
+def _load_tensors():
+    """csrc/tensors.cpp: addresses and sizes of a list of tensors."""
+    path = os.path.join(_PKG, "lib", "_tensors.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python -m a2a_ring_ordered_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_tensors", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_tensors", path, loader=loader))
+    loader.exec_module(module)
+    if torch.__version__.split("+")[0] != module.TORCH_VERSION.split("+")[0]:
+        raise ImportError(f"{path} was built for torch {module.TORCH_VERSION}: build it again")
+    return module
+
+
+_TENSORS = _load_tensors()
 
 
 class CclError(RuntimeError):
@@ -693,17 +710,9 @@ def _explain(ts, name: str, p=None, dtype=None, cuda=False):
 
 def _ranks(ts, name: str, p: int, dtype, rows, width: int, cuda=False) -> bytes:
     """Addresses of the p rank buffers, rank r of rows[r] rows of `width` elements."""
-    try:
-        device, pointers = ts[0].get_device(), []
-        if device >= 0 and len(ts) == p:
-            for t, n in zip(ts, rows):
-                if t.dtype is not dtype or t.get_device() != device or t.numel() != n * width or not t.is_contiguous():
-                    break
-                pointers.append(t.data_ptr())
-            else:
-                return _PACK_POINTERS[p](*pointers)
-    except (AttributeError, TypeError, IndexError):
-        pass
+    packed = _TENSORS.ranks(ts, p, dtype, rows, width)
+    if packed is not None:
+        return packed
     ts = _explain(ts, name, p, dtype, cuda)
     for r, t in enumerate(ts):
         if t.numel() != rows[r] * width:
@@ -714,23 +723,10 @@ def _ranks(ts, name: str, p: int, dtype, rows, width: int, cuda=False) -> bytes:
 def _shaped(ts, name: str, dims: int, p=None, dtype=None, cuda=False):
     """(addresses, first tensor, first dimension of each rank, the others) of
     rank buffers of `dims` dimensions that are alike but for the first."""
-    try:
-        first = ts[0]
-        rest = tuple(first.shape)[1:]
-        device, want, per = first.get_device(), dtype or first.dtype, math.prod(rest)
-        if device >= 0 and (p is None or len(ts) == p) and 1 + len(rest) == dims:
-            pointers, sizes = [], []
-            for t in ts:
-                n = t.shape[0]  # of two dimensions, the count of elements says the second
-                if (t.dtype is not want or t.get_device() != device or not t.is_contiguous() or t.dim() != dims
-                        or t.numel() != n * per or (dims > 2 and t.shape[1:] != rest)):
-                    break
-                pointers.append(t.data_ptr())
-                sizes.append(n)
-            else:
-                return _PACK_POINTERS[len(ts)](*pointers), first, sizes, rest
-    except (AttributeError, TypeError, IndexError):
-        pass
+    packed = _TENSORS.shaped(ts, dims, p, dtype)
+    if packed is not None:
+        pointers, sizes, rest = packed
+        return pointers, ts[0], sizes, rest
     ts = _explain(ts, name, p, dtype, cuda)
     rest = tuple(ts[0].shape)[1:]
     for r, t in enumerate(ts):
