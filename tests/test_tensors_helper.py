@@ -6,11 +6,19 @@ import struct
 import pytest
 import torch
 
-from gpu_util import ccl
+
+@pytest.fixture(scope="module")
+def helper():
+    from a2a_ring_ordered_gb300 import build
+
+    build.build()
+    from a2a_ring_ordered_gb300 import ccl as lib
+
+    return lib._TENSORS
 
 
-def test_what_is_not_a_list_of_gpu_buffers_is_left_to_the_caller():
-    t = ccl()._TENSORS
+def test_what_is_not_a_list_of_gpu_buffers_is_left_to_the_caller(helper):
+    t = helper
     host = torch.zeros(2, 3)
     for ts in ([host], (host,), [], [1], [None], "x", None, 7, iter([host]), [host] * 129):
         assert t.ranks(ts, 1, torch.float32, [2], 3) is None
@@ -24,8 +32,8 @@ def test_what_is_not_a_list_of_gpu_buffers_is_left_to_the_caller():
 
 
 @pytest.mark.gpu
-def test_addresses_and_sizes_of_gpu_buffers():
-    t = ccl()._TENSORS
+def test_addresses_and_sizes_of_gpu_buffers(helper):
+    t = helper
     bf = torch.bfloat16
     ts = [torch.zeros(n, 3, 5, dtype=bf, device="cuda") for n in (4, 0, 7)]
     packed = struct.pack("3P", *[x.data_ptr() for x in ts])
