@@ -7,8 +7,8 @@
 // out[t] = sum_j w[t][j] y[row(t, j)] (from_experts), and the gradient of the
 // latter, dy[row(t, j)] = w[t][j] dout[t], dw[t][j] = <y[row(t, j)], dout[t]>.
 // The sort is bound by latency, the others move rows and are bound by HBM.
-// Measured, 8 choices of 256 experts, rows of 7168 bf16: the sort of 32,768
-// items 10 us; 8 ranks x 2048 tokens: sort and to_experts 325 us (6.5 TB/s),
+// Measured, 8 choices of 256 experts, rows of 7168 bf16: the sort
+// of 4096 items 3.3 us, of 1,048,576 77 us; 8 ranks x 2048 tokens: sort and to_experts 325 us (6.5 TB/s),
 // the gradient 614 us (6.5 TB/s); 8 ranks x 4096: from_experts 636 us (6.65
 // TB/s).
 #include <cooperative_groups.h>
@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kSortMaxCluster = 16;
 constexpr int kSortUnroll = 4;           // id loads in flight per lane
+constexpr uint32_t kPerTurn = 32 * kSortUnroll;  // items that a warp takes at a time
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // The expert of an item among the rank's own, or -1.
@@ -30,17 +31,26 @@ __device__ __forceinline__ int sort_expert(const int32_t* ids, uint32_t i, uint3
   return (e >= 0 && e < experts) ? static_cast<int>(e) : -1;
 }
 
-// The lanes whose value has the same low `bits` bits as this lane's, by one
-// vote per bit.
-__device__ __forceinline__ unsigned lanes_alike(int value, int bits) {
-  unsigned alike = kAll;
-  for (int b = 0; b < bits; ++b) {
-    const bool one = (value >> b) & 1;
-    const unsigned ones = __ballot_sync(kAll, one);
-    alike &= one ? ones : ~ones;
+// kSortUnroll groups of 32 items of one warp: each lane's experts, and the lanes
+// that hold the same one (with the same low `bits` bits), by one vote per bit.
+struct SortItems {
+  int e[kSortUnroll];
+  unsigned same[kSortUnroll];
+  __device__ __forceinline__ SortItems(const int32_t* ids, uint32_t b, uint32_t hi, int first, int experts, int bits) {
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+    for (int u = 0; u < kSortUnroll; ++u) {
+      e[u] = sort_expert(ids, b + 32 * u + lane, hi, first, experts);
+      same[u] = kAll;
+    }
+    for (int i = 31; i > 31 - bits; --i)
+#pragma unroll
+      for (int u = 0; u < kSortUnroll; ++u) {
+        const int one = e[u] << i >> 31;  // the bit, in all places
+        same[u] &= ~(__ballot_sync(kAll, one < 0) ^ static_cast<unsigned>(one));
+      }
   }
-  return alike;
-}
+};
 
 // One cluster of CTAs per rank (grid x = CTA in the cluster, grid y = rank).
 // CTA c owns a contiguous range of the rank's items and warp w of it a
@@ -51,8 +61,9 @@ __device__ __forceinline__ unsigned lanes_alike(int value, int bits) {
 //  2. A column of hist becomes the running count of the warps before; the
 //     CTAs' totals are exchanged through distributed shared memory; a scan
 //     over the experts gives every expert its first row.
-//  3. The warp walks its part again: row = hist entry + rank among the lanes
-//     of the same expert, and the entry moves on by the group.
+//  3. The warp walks its part again (its first turn's items are still in
+//     registers: most parts are no longer): row = hist entry + rank among the
+//     lanes of the same expert, and the entry moves on by the group.
 __global__ void moe_sort_kernel(const __grid_constant__ MoeSortArgs a) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t smem[];
@@ -80,24 +91,28 @@ __global__ void moe_sort_kernel(const __grid_constant__ MoeSortArgs a) {
   uint32_t* mine = hist + warp * E;
   __syncthreads();
 
-  for (uint32_t b = lo; b < hi; b += 32 * kSortUnroll) {
-    int e[kSortUnroll];
-#pragma unroll
-    for (int u = 0; u < kSortUnroll; ++u) e[u] = sort_expert(ids, b + 32 * u + lane, hi, first, E);
+  const auto count = [&](const SortItems& x) {
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) {
-      const unsigned same = lanes_alike(e[u], bits);
-      if (e[u] >= 0 && lane == __ffs(same) - 1) mine[e[u]] += __popc(same);
+      if (x.e[u] >= 0 && lane == __ffs(x.same[u]) - 1) mine[x.e[u]] += __popc(x.same[u]);
       __syncwarp();
     }
-  }
+  };
+  const SortItems held(ids, lo, hi, first, E, bits);  // all that most warps have
+  count(held);
+  for (uint32_t b = lo + kPerTurn; b < hi; b += kPerTurn) count(SortItems(ids, b, hi, first, E, bits));
   __syncthreads();
   for (int e = tid; e < E; e += blockDim.x) {
     uint32_t run = 0;
-    for (int w = 0; w < warps; ++w) {
-      const uint32_t v = hist[w * E + e];
-      hist[w * E + e] = run;
-      run += v;
+    for (int w0 = 0; w0 < warps; w0 += 8) {  // warps is a multiple of 8
+      uint32_t v[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v[w] = hist[(w0 + w) * E + e];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        hist[(w0 + w) * E + e] = run;
+        run += v[w];
+      }
     }
     total[e] = run;
   }
@@ -141,22 +156,20 @@ __global__ void moe_sort_kernel(const __grid_constant__ MoeSortArgs a) {
   cluster.barrier_arrive();  // the other CTAs may still read this one's totals
 
   int32_t* rows = a.rows[r];
-  for (uint32_t b = lo; b < hi; b += 32 * kSortUnroll) {
-    int e[kSortUnroll];
-#pragma unroll
-    for (int u = 0; u < kSortUnroll; ++u) e[u] = sort_expert(ids, b + 32 * u + lane, hi, first, E);
+  const auto place = [&](const SortItems& x, uint32_t b) {
 #pragma unroll
     for (int u = 0; u < kSortUnroll; ++u) {
       const uint32_t i = b + 32 * u + lane;
-      const unsigned same = lanes_alike(e[u], bits);
-      const uint32_t before = __popc(same & ((1u << lane) - 1u));
-      const uint32_t at = e[u] >= 0 ? mine[e[u]] : 0;
+      const uint32_t before = __popc(x.same[u] & ((1u << lane) - 1u));
+      const uint32_t at = x.e[u] >= 0 ? mine[x.e[u]] : 0;
       __syncwarp();
-      if (e[u] >= 0 && before == 0) mine[e[u]] = at + __popc(same);
+      if (x.e[u] >= 0 && before == 0) mine[x.e[u]] = at + __popc(x.same[u]);
       __syncwarp();
-      if (i < hi) rows[i] = e[u] >= 0 ? static_cast<int32_t>(base[e[u]] + at + before) : -1;
+      if (i < hi) rows[i] = x.e[u] >= 0 ? static_cast<int32_t>(base[x.e[u]] + at + before) : -1;
     }
-  }
+  };
+  place(held, lo);
+  for (uint32_t b = lo + kPerTurn; b < hi; b += kPerTurn) place(SortItems(ids, b, hi, first, E, bits), b);
   cluster.barrier_wait();
 }
 
@@ -670,11 +683,13 @@ cudaError_t launch_back_grad(const MoeRowsArgs& a, cudaStream_t s) {
 cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
   uint32_t most = 0;
   for (int r = 0; r < a.p; ++r) most = a.items[r] > most ? a.items[r] : most;
-  // a warp's part is at least 32 lanes x kSortUnroll items while that leaves
-  // no CTA of 32 warps without work; then more CTAs
-  constexpr uint32_t kPerWarp = 32 * kSortUnroll, kPerCta = kPerWarp * 32;
-  const uint32_t ctas = most <= kPerCta ? 1 : (most + kPerCta - 1) / kPerCta >= kSortMaxCluster ? kSortMaxCluster : (most + kPerCta - 1) / kPerCta;
-  uint32_t warps = (most + kPerWarp - 1) / kPerWarp;
+  // CTAs of few warps before warps: the votes fill a SM's issue slots (4096
+  // items of 256 experts 3.3 us in 4 CTAs of 8 warps, 4.3 in 2 of 16, 6.8 in one
+  // of 32), and columns of few warps are short.  Once the cluster has 16 CTAs,
+  // up to 32 warps each.
+  constexpr uint32_t kLeastWarps = 8, kPerCta = kPerTurn * kLeastWarps;
+  const uint32_t wanted = (most + kPerCta - 1) / kPerCta, ctas = wanted < 1 ? 1 : wanted > kSortMaxCluster ? kSortMaxCluster : wanted;
+  uint32_t warps = ((most + ctas * kPerTurn - 1) / (ctas * kPerTurn) + 7) / 8 * 8;
   warps = warps < 8 ? 8 : warps > 32 ? 32 : warps;
   const size_t smem = (static_cast<size_t>(warps) + 2) * a.num_experts * sizeof(uint32_t);
   cudaError_t err = cudaSuccess;
