@@ -7,10 +7,10 @@
 // out[t] = sum_j w[t][j] y[row(t, j)] (from_experts), and the gradient of the
 // latter, dy[row(t, j)] = w[t][j] dout[t], dw[t][j] = <y[row(t, j)], dout[t]>.
 // The sort is bound by latency, the others move rows and are bound by HBM.
-// Measured, 8 choices of 256 experts, rows of 7168 bf16: the sort
-// of 4096 items 3.3 us, of 1,048,576 77 us; 8 ranks x 2048 tokens: sort and to_experts 325 us (6.5 TB/s),
-// the gradient 614 us (6.5 TB/s); 8 ranks x 4096: from_experts 636 us (6.65
-// TB/s).
+// Measured, 8 choices of 256 experts, rows of 7168 bf16: the sort of 4096 items
+// 3.3 us, of 1,048,576 77 us; 8 ranks x 2048 tokens: sort and to_experts 324 us
+// (6.5 TB/s), the gradient 614 us (6.5 TB/s); 8 ranks x 4096: from_experts 636
+// us (6.65 TB/s).
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
