@@ -524,7 +524,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
             }
             if (do_b) {
               if constexpr (kBColumns) {
-                if (a.whole_b && boxes > 1) {
+                // of 192 columns, the odd CTA's half begins inside a chunk
+                if (a.whole_b && boxes > 1 && (c & 63) == 0) {
                   tma(sb, map_b, 0, t.lo + k, c >> 6, 0, bar);
                 } else {
                   tma(sb, map_small, c, t.lo + k, 0, 0, bar);
