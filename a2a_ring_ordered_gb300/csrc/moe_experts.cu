@@ -20,6 +20,7 @@ namespace ccl {
 namespace {
 
 constexpr int kSortMaxCluster = 16;
+constexpr uint32_t kSortMaxWarps = 32;
 constexpr int kSortUnroll = 4;           // id loads in flight per lane
 constexpr uint32_t kPerTurn = 32 * kSortUnroll;  // items that a warp takes at a time
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -690,11 +691,15 @@ cudaError_t launch_moe_sort(const MoeSortArgs& a, cudaStream_t s) {
   constexpr uint32_t kLeastWarps = 8, kPerCta = kPerTurn * kLeastWarps;
   const uint32_t wanted = (most + kPerCta - 1) / kPerCta, ctas = wanted < 1 ? 1 : wanted > kSortMaxCluster ? kSortMaxCluster : wanted;
   uint32_t warps = ((most + ctas * kPerTurn - 1) / (ctas * kPerTurn) + 7) / 8 * 8;
-  warps = warps < 8 ? 8 : warps > 32 ? 32 : warps;
+  warps = warps < 8 ? 8 : warps > kSortMaxWarps ? kSortMaxWarps : warps;
   const size_t smem = (static_cast<size_t>(warps) + 2) * a.num_experts * sizeof(uint32_t);
+  // The limits belong to the function, not to the call: always the most that a
+  // call may need, so that host threads cannot lower each other's between the
+  // setting and the launch.
+  constexpr int kMostSmem = (kSortMaxWarps + 2) * kSortMaxExperts * sizeof(uint32_t);
   cudaError_t err = cudaSuccess;
   if (ctas > 8) err = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (err == cudaSuccess && smem > 48 * 1024) err = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err == cudaSuccess && smem > 48 * 1024) err = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, static_cast<unsigned>(a.p));
