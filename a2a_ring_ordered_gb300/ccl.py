@@ -870,8 +870,9 @@ def ccl_moe_product_grad_weight(dy, x, offsets, dw, stream=None) -> None:
 
 # ------------------------------------------------------------------------ AdamW
 class AdamWTable:
-    """The tensors of an AdamW step, checked and packed once; it holds them, so
-    their addresses stay good for as long as the table is used.
+    """The tensors of an AdamW step, checked and packed once, and again when one
+    of them is found in another place (``p.data = ...``, ``set_``, a resized
+    storage): every step compares, and works on what the tensors are then.
 
     params fp32 or bf16; grads fp32 or bf16; exp_avg and exp_avg_sq fp32, or
     8-bit codes (float8_e4m3fn or uint8) with exp_avg_scale and
@@ -881,8 +882,18 @@ class AdamWTable:
     def __init__(self, params, grads, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None, copies=None):
         fields = {"param": params, "grad": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
                   "exp_avg_scale": exp_avg_scale, "exp_avg_sq_scale": exp_avg_sq_scale, "copy": copies}
-        fields = {k: list(v) for k, v in fields.items() if v is not None}
-        self.tensors = fields
+        self.tensors = {k: tuple(v) for k, v in fields.items() if v is not None}
+        self.all = tuple(self.tensors.values())
+        self._pack()
+
+    def follow(self) -> None:
+        """Packs anew where a tensor has moved or changed since the last time."""
+        if not _TENSORS.in_place(self.all, self.places):
+            self._pack()
+
+    def _pack(self) -> None:
+        fields = self.tensors
+        self.places = b""  # of a table that was refused
         count = len(fields["param"])
         if count == 0:
             raise ValueError("no tensors")
@@ -912,6 +923,8 @@ class AdamWTable:
                     raise ValueError(f"{name}[{i}] has dtype {t.dtype}")
                 if t.numel() != want:
                     raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {want}")
+                if (t.storage_offset() + want) * t.element_size() > t.untyped_storage().nbytes():
+                    raise ValueError(f"{name}[{i}] has lost its storage")
                 if want:
                     spans.append((t.data_ptr(), t.data_ptr() + want * t.element_size(), f"{name}[{i}]"))
         spans.sort()
@@ -925,6 +938,7 @@ class AdamWTable:
             for name, ts in fields.items():
                 setattr(entry, name, ts[i].data_ptr())
             entry.n = fields["param"][i].numel()
+        self.places = _TENSORS.places(self.all)
 
 
 def ccl_adamw_step(table: AdamWTable, step: int, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -933,6 +947,7 @@ def ccl_adamw_step(table: AdamWTable, step: int, lr: float, betas=(0.9, 0.999), 
     is a one-element fp32 CUDA tensor that multiplies every gradient."""
     if grad_scale is not None and (not grad_scale.is_cuda or grad_scale.dtype != torch.float32 or grad_scale.numel() != 1):
         raise ValueError("grad_scale must be one fp32 number on the GPU")
+    table.follow()
     hyper = AdamWHyper(lr, betas[0], betas[1], eps, weight_decay, step,
                        None if grad_scale is None else grad_scale.data_ptr())
     _check(LIB.ccl_adamw_step(table.array, table.count, table.param_code, table.grad_code, table.state_bits,
