@@ -83,10 +83,15 @@ class AdamW:
         mine = {n: ts for n, ts in self.table.tensors.items() if n.startswith("exp_avg")}
         if set(state["states"]) != set(mine):
             raise ValueError(f"states hold {sorted(state['states'])}, expected {sorted(mine)}")
+        # all of it is looked at before any of it is taken
+        codes = (torch.float8_e4m3fn, torch.uint8)
         for name, ts in mine.items():
             if [t.numel() for t in ts] != [t.numel() for t in state["states"][name]]:
                 raise ValueError(f"{name}: other sizes")
+            for i, (to, got) in enumerate(zip(ts, state["states"][name])):
+                if got.dtype != to.dtype and not (got.dtype in codes and to.dtype in codes):
+                    raise ValueError(f"{name}[{i}] is {got.dtype}, expected {to.dtype}")
         for name, ts in mine.items():
             for to, got in zip(ts, state["states"][name]):
-                to.copy_(got.view(to.dtype) if got.dtype != to.dtype else got)
+                to.copy_(got.view(to.dtype).reshape(to.shape))
         self.steps = state["step"]
