@@ -17,6 +17,7 @@ import importlib.machinery
 import importlib.util
 import os
 import struct
+import warnings
 from typing import Sequence
 
 import torch
@@ -124,20 +125,49 @@ def _load() -> ctypes.CDLL:
 LIB = _load()
 
 
-def _load_tensors():
-    """csrc/tensors.cpp: addresses and sizes of a list of tensors."""
-    path = os.path.join(_PKG, "lib", "_tensors.so")
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it with `python -m a2a_ring_ordered_gb300.build`")
-    loader = importlib.machinery.ExtensionFileLoader("_tensors", path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_tensors", path, loader=loader))
-    loader.exec_module(module)
-    if torch.__version__.split("+")[0] != module.TORCH_VERSION.split("+")[0]:
-        raise ImportError(f"{path} was built for torch {module.TORCH_VERSION}: build it again")
-    return module
+class _PlainTensors:
+    """csrc/tensors.cpp's functions where it is not built (for this torch): the
+    calls ask each tensor by the slow road, which costs about half a microsecond
+    a tensor."""
+
+    @staticmethod
+    def ranks(ts, p, dtype, rows, width):
+        return None
+
+    @staticmethod
+    def shaped(ts, dims, p, dtype):
+        return None
+
+    @staticmethod
+    def places(tuples):
+        return [(t.data_ptr(), t.storage_offset(), t.untyped_storage().nbytes(), t.dtype, t.shape, t.stride())
+                for ts in tuples for t in ts]
+
+    @staticmethod
+    def in_place(tuples, places):
+        return _PlainTensors.places(tuples) == places
 
 
-_TENSORS = _load_tensors()
+def _load_tensors(path: str):
+    """csrc/tensors.cpp: addresses and sizes of a list of tensors.  Only marshalling:
+    without it every call does the same, more slowly."""
+    why = "it is missing"
+    if os.path.exists(path):
+        try:
+            loader = importlib.machinery.ExtensionFileLoader("_tensors", path)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_tensors", path, loader=loader))
+            loader.exec_module(module)
+            if torch.__version__.split("+")[0] == module.TORCH_VERSION.split("+")[0]:
+                return module
+            why = f"it was built for torch {module.TORCH_VERSION}"
+        except ImportError as e:
+            why = str(e)
+    warnings.warn(f"{path} is not used ({why}): calls take some microseconds longer until "
+                  "`python -m a2a_ring_ordered_gb300.build` has built it", RuntimeWarning, stacklevel=2)
+    return _PlainTensors
+
+
+_TENSORS = _load_tensors(os.path.join(_PKG, "lib", "_tensors.so"))
 
 
 class CclError(RuntimeError):
