@@ -17,6 +17,8 @@
 // warp-wide integer maximum of the magnitudes' bits.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "device_common.cuh"
 
 namespace ccl {
@@ -417,6 +419,7 @@ constexpr int kCtasPerSm = 3;
 constexpr long long kWaitCycles = 1ll << 32;  // two seconds
 
 __device__ unsigned int g_adamw_error;  // nonzero: a bounded wait ran out
+std::atomic<bool> g_streamed{false};    // whether a kernel that waits was launched; never taken back
 
 template <int PDT, int GDT>
 struct alignas(16) Stage {
@@ -634,6 +637,7 @@ cudaError_t launch_one(const Args& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = CCL_PDL ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    g_streamed.store(true, std::memory_order_relaxed);
     return cudaLaunchKernelEx(&cfg, kernel, a);
   }
 }
@@ -658,6 +662,8 @@ cudaError_t launch_any(int pdt, int gdt, int bits, bool copy, const Args& a, cud
 }  // namespace
 
 cudaError_t read_adamw_error(unsigned int* flag, bool clear) {
+  *flag = 0;
+  if (!g_streamed.load(std::memory_order_relaxed)) return cudaSuccess;
   cudaError_t err = cudaMemcpyFromSymbol(flag, g_adamw_error, sizeof(unsigned int));
   if (err == cudaSuccess && clear && *flag != 0) {
     const unsigned int zero = 0;

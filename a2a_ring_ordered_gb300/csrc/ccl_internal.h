@@ -264,7 +264,8 @@ struct ProductArgs {
   uint64_t n, contract;
   int p, num_experts;
 };
-// The products' device error word, as read_device_error's.
+// The products' device error word, as read_device_error's; 0 without a copy
+// until the process has launched one.
 cudaError_t read_product_error(unsigned int* flag, bool clear);
 cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& a, cudaStream_t s);
 
@@ -305,7 +306,7 @@ using AdamwSmall = AdamwArgsT<54>;
 using AdamwLarge = AdamwArgsT<440>;
 static_assert(sizeof(AdamwSmall) <= 4096, "AdamW parameters exceed 4 KB");
 static_assert(sizeof(AdamwLarge) <= 32764, "AdamW parameters exceed 32,764 bytes");
-// AdamW's device error word, as read_device_error's.
+// AdamW's device error word, likewise (the kernels with 8-bit states wait).
 cudaError_t read_adamw_error(unsigned int* flag, bool clear);
 cudaError_t launch_adamw(int param_dt, int grad_dt, int bits, bool copy, const AdamwSmall& a, cudaStream_t s);
 cudaError_t launch_adamw(int param_dt, int grad_dt, int bits, bool copy, const AdamwLarge& a, cudaStream_t s);

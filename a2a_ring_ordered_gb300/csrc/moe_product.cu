@@ -41,6 +41,8 @@
 //     behind the other in a single pair.
 #include <cuda.h>  // CUtensorMap and its enums; nothing links the driver
 
+#include <atomic>
+
 #include "device_common.cuh"
 #include "realign.cuh"
 
@@ -82,6 +84,7 @@ constexpr int kMostSummed = 512;
 constexpr long long kWaitCycles = 1ll << 32;  // two seconds
 
 __device__ unsigned int g_product_error;  // nonzero: a bounded wait ran out
+std::atomic<bool> g_launched{false};      // in this process; never taken back, since a captured graph may run at any time
 
 struct PairArgs {
   CUtensorMap a[kLaunchRanks], b[kLaunchRanks], b_small[kLaunchRanks];
@@ -827,6 +830,7 @@ cudaError_t launch_pairs(const PairArgs& a, uint64_t most_tiles, cudaStream_t s)
   attr[0].val.programmaticStreamSerializationAllowed = CCL_PDL ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  g_launched.store(true, std::memory_order_relaxed);
   err = cudaLaunchKernelEx(&cfg, kernel, a);
   if (err == cudaSuccess) note_launch();
   return err;
@@ -835,6 +839,8 @@ cudaError_t launch_pairs(const PairArgs& a, uint64_t most_tiles, cudaStream_t s)
 }  // namespace
 
 cudaError_t read_product_error(unsigned int* flag, bool clear) {
+  *flag = 0;
+  if (!g_launched.load(std::memory_order_relaxed)) return cudaSuccess;
   cudaError_t err = cudaMemcpyFromSymbol(flag, g_product_error, sizeof(unsigned int));
   if (err == cudaSuccess && clear && *flag != 0) {
     const unsigned int zero = 0;
