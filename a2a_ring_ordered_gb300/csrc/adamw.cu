@@ -42,6 +42,29 @@ __device__ __forceinline__ int element(int lane, int q) {
   return VEC ? lane * kPer + q : lane + 32 * q;
 }
 
+// Parameters and moments are written by this kernel: no read-only path, and
+// in the program's order before the stores.
+__device__ __forceinline__ uint4 ld_own16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_own8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_own4(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_own2(const void* p) {
+  unsigned short v;
+  asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+
 template <int DT>
 struct Raw4 {
   uint32_t w[kPer];  // VEC: as loaded; else element q in the low bits of w[q]
@@ -51,16 +74,16 @@ template <int DT, bool VEC, bool WHOLE>
 __device__ __forceinline__ void load4(const void* base, uint64_t i0, int lane, int count, Raw4<DT>& r) {
   const char* p = static_cast<const char*>(base) + i0 * Elem<DT>::kBytes;
   if constexpr (VEC && DT == kF32) {
-    const uint4 v = ld_once16(p + lane * 16);
+    const uint4 v = ld_own16(p + lane * 16);
     r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
   } else if constexpr (VEC) {
-    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p + lane * 8));
+    const uint2 v = ld_own8(p + lane * 8);
     r.w[0] = v.x, r.w[1] = v.y;
   } else {
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const int i = element<VEC>(lane, q);
-      r.w[q] = !WHOLE && i >= count ? 0u : DT == kF32 ? ld_once4(p + i * 4) : ld_once2(p + i * 2);
+      r.w[q] = !WHOLE && i >= count ? 0u : DT == kF32 ? ld_own4(p + i * 4) : ld_own2(p + i * 2);
     }
   }
 }
