@@ -115,12 +115,12 @@ __device__ __forceinline__ void store_codes(void* base, uint64_t i0, int lane, i
   uint8_t* p = static_cast<uint8_t*>(base) + i0;
   if constexpr (VEC) {
     st_stream4(p + lane * kPer, w);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const int i = element<VEC>(lane, q);
-    if (WHOLE || i < count) __stcs(p + i, static_cast<uint8_t>(w >> (8 * q)));
+    for (int q = 0; q < kPer; ++q) {
+      const int i = element<VEC>(lane, q);
+      if (WHOLE || i < count) __stcs(p + i, static_cast<uint8_t>(w >> (8 * q)));
+    }
   }
 }
 
@@ -438,7 +438,6 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 // by itself (with barriers of the whole CTA in their place, and every warp
 // looking the tensor up: 553 us).
 constexpr int kStreamStages = 2;
-constexpr int kCtasPerSm = 3;
 constexpr long long kWaitCycles = 1ll << 32;  // two seconds
 
 __device__ unsigned int g_adamw_error;  // nonzero: a bounded wait ran out
@@ -460,6 +459,11 @@ struct StreamShared {
   uint32_t dead;  // a wait ran out
 };
 constexpr int kStreamThreads = kThreads + 32;
+// CTAs that an SM's 228 KB hold, 1 KB of each the system's, three at most: two
+// where parameters and gradients are fp32 (82 KB a CTA).  Chunks are dealt out by
+// the grid, so it may not have more CTAs than run together.
+template <int PDT, int GDT>
+constexpr int kCtasPerSm = (228 << 10) / (sizeof(StreamShared<PDT, GDT>) + 1024) < 3 ? (228 << 10) / (sizeof(StreamShared<PDT, GDT>) + 1024) : 3;
 
 __device__ __forceinline__ uint32_t shared_address(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -585,7 +589,7 @@ __device__ __forceinline__ bool stream_wait(uint64_t* barrier, uint32_t parity, 
 }
 
 template <int PDT, int GDT, bool COPY, typename Args>
-__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm) adamw_stream_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<PDT, GDT>) adamw_stream_kernel(const __grid_constant__ Args a) {
   extern __shared__ char raw[];
   StreamShared<PDT, GDT>& s = *reinterpret_cast<StreamShared<PDT, GDT>*>(raw);
   const uint32_t chunks = a.chunk0[a.count];
@@ -646,10 +650,11 @@ cudaError_t launch_one(const Args& a, cudaStream_t s) {
     return launch_kernel(adamw_kernel<PDT, GDT, COPY, Args>, dim3(a.chunk0[a.count]), dim3(kThreads), s, a);
   } else {
     constexpr size_t smem = sizeof(StreamShared<PDT, GDT>);
+    static_assert(kCtasPerSm<PDT, GDT> >= 1 && kCtasPerSm<PDT, GDT> * (smem + 1024) <= 228 << 10, "every CTA of the grid runs at once");
     const auto kernel = adamw_stream_kernel<PDT, GDT, COPY, Args>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
-    const uint32_t resident = static_cast<uint32_t>(current_sm_count()) * kCtasPerSm;
+    const uint32_t resident = static_cast<uint32_t>(current_sm_count()) * kCtasPerSm<PDT, GDT>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.chunk0[a.count] < resident || resident == 0 ? a.chunk0[a.count] : resident);
     cfg.blockDim = dim3(kStreamThreads);
