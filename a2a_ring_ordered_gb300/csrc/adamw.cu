@@ -622,6 +622,13 @@ __global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<PDT, GDT>) adamw_st
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if (++st == kStreamStages) st = 0, phase ^= 1;
     }
+    // every stage given back: no copy is on its way to a CTA that has left, not
+    // even where the others' wait for it ran out
+    for (int j = 0; ok && j < kStreamStages; ++j) {
+      if (lane == 0) ok = stream_wait(&s.empty[st], phase ^ 1, &s.dead);
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (++st == kStreamStages) st = 0, phase ^= 1;
+    }
     if (!ok) {  // copies in flight still write this CTA's shared memory
       const long long t1 = clock64();
       while (clock64() - t1 < (1ll << 22)) {
