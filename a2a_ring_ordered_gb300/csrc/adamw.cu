@@ -569,7 +569,7 @@ __device__ __forceinline__ void staged_chunk(const Args& a, const AdamwTensor& t
 }
 
 // Waits for a barrier's phase; false once this or another wait of the CTA ran out.
-__device__ __forceinline__ bool stream_wait(uint64_t* barrier, uint32_t parity, volatile uint32_t* dead) {
+__device__ __forceinline__ bool stream_wait(uint64_t* barrier, uint32_t parity, volatile uint32_t* dead, long long cycles = kWaitCycles) {
   const uint32_t bar = shared_address(barrier);
   const long long t0 = clock64();
   for (;;) {
@@ -580,9 +580,9 @@ __device__ __forceinline__ bool stream_wait(uint64_t* barrier, uint32_t parity, 
                  : "memory");
     if (done) return true;
     if (*dead) return false;
-    if (clock64() - t0 > kWaitCycles) {
+    if (clock64() - t0 > cycles) {
       *dead = 1;
-      atomicExch(&g_adamw_error, 1u);
+      atomicExch(&g_adamw_error, kAdamwError);
       return false;
     }
   }
@@ -651,6 +651,17 @@ __global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<PDT, GDT>) adamw_st
   }
 }
 
+// Self-test of the bounded wait: a barrier that nothing completes.
+__global__ void __launch_bounds__(32) adamw_wait_probe_kernel(long long cycles) {
+  __shared__ alignas(8) uint64_t bar;
+  __shared__ uint32_t dead;
+  if (threadIdx.x != 0) return;
+  dead = 0;
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_address(&bar)) : "memory");
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  stream_wait(&bar, 0, &dead, cycles);
+}
+
 template <int PDT, int GDT, int BITS, bool COPY, typename Args>
 cudaError_t launch_one(const Args& a, cudaStream_t s) {
   if constexpr (BITS == 32) {
@@ -695,6 +706,14 @@ cudaError_t launch_any(int pdt, int gdt, int bits, bool copy, const Args& a, cud
 }
 
 }  // namespace
+
+cudaError_t launch_adamw_wait_probe(cudaStream_t s) {
+  g_streamed.store(true, std::memory_order_relaxed);
+  adamw_wait_probe_kernel<<<1, 32, 0, s>>>(1ll << 14);
+  const cudaError_t err = cudaGetLastError();
+  if (err == cudaSuccess) note_launch();
+  return err;
+}
 
 cudaError_t read_adamw_error(unsigned int* flag, bool clear) {
   *flag = 0;

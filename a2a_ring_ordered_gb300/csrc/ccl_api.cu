@@ -263,6 +263,8 @@ extern "C" ccl_status_t ccl_selftest_bounded_wait(void* stream) {
   CCL_TRACE();
   clear_error();
   cudaError_t err = launch_bounded_wait_probe(as_stream(stream));
+  if (err == cudaSuccess) err = launch_product_wait_probe(as_stream(stream));
+  if (err == cudaSuccess) err = launch_adamw_wait_probe(as_stream(stream));
   if (err != cudaSuccess) return cuda_fail(err, "bounded-wait probe launch");
   return CCL_OK;
 }

@@ -93,6 +93,11 @@ cudaError_t launch_fanout(FanoutArgs a, cudaStream_t s);
 cudaError_t read_device_error(unsigned int* flag, bool clear);
 // One-thread kernel whose mbarrier wait runs out by construction (self-test).
 cudaError_t launch_bounded_wait_probe(cudaStream_t s);
+// Bits of the error word that the products' and AdamW's waits set (the
+// fan-out's and its probe's are 1 and 2).
+constexpr unsigned int kProductError = 4, kAdamwError = 8;
+cudaError_t launch_product_wait_probe(cudaStream_t s);
+cudaError_t launch_adamw_wait_probe(cudaStream_t s);
 // Broadcast: send[0] (n elements) copied to recv[0..p-1]; `vec`: all 16-byte aligned.
 cudaError_t launch_broadcast(int dt, bool vec, const GatherArgs& a, uint64_t n, cudaStream_t s);
 

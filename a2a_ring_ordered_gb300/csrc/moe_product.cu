@@ -81,7 +81,11 @@ constexpr uint32_t kTmemColumns = 512;
 // registers, or, where loaders fill the stages and set the pace, in the output
 // (32 experts of 1024 rows by TMA took 948 us that way, 650 in registers).
 constexpr int kMostSummed = 512;
-constexpr long long kWaitCycles = 1ll << 32;  // two seconds
+// Two seconds without a stage: a wait for a whole tile, or for the next stage
+// that the loaders have a part in, may take any number of stages (10^9 rows of
+// one expert are 16 million: five seconds), so it runs out only where no stage
+// was issued for so long.
+constexpr long long kWaitCycles = 1ll << 32;
 
 __device__ unsigned int g_product_error;  // nonzero: a bounded wait ran out
 std::atomic<bool> g_launched{false};      // in this process; never taken back, since a captured graph may run at any time
@@ -100,6 +104,11 @@ struct PairArgs {
 };
 static_assert(sizeof(PairArgs) <= 4096, "product parameters exceed 4 KB");
 
+// What a waiting warp looks at.
+struct Watch {
+  uint32_t dead;      // a wait of the CTA ran out
+  uint32_t progress;  // stages that its TMA warp has issued
+};
 struct Shared {
   alignas(8) uint64_t full[kStages];
   uint64_t empty[kStages];
@@ -107,7 +116,7 @@ struct Shared {
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
   uint32_t tmem;
-  uint32_t dead;
+  Watch watch;
   uint32_t scan[Crew<false>::kThreads / 32];
   uint32_t first[kMaxGroups + 1];  // row tiles before each (rank, expert)
   int32_t lo[kMaxGroups];          // its first row
@@ -153,16 +162,21 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 // False once this or another wait of the CTA ran out.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile Watch* watch, long long cycles = kWaitCycles) {
   if (mbar_try(bar, parity)) return true;
-  const long long t0 = clock64();
+  long long t0 = clock64();
+  uint32_t seen = watch->progress;
   while (!mbar_try(bar, parity)) {
-    if (*dead) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *dead = 1;
-      atomicExch(&g_product_error, 1u);
+    if (watch->dead) return false;
+    if (clock64() - t0 <= cycles) continue;
+    const uint32_t now = watch->progress;
+    if (now == seen) {
+      watch->dead = 1;
+      atomicExch(&g_product_error, kProductError);
       return false;
     }
+    seen = now;
+    t0 = clock64();
   }
   return true;
 }
@@ -417,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
       mbar_init(smem_addr(&s.tmem_full[i]), 1);
       mbar_init(smem_addr(&s.tmem_empty[i]), 2 * kEpilogueWarps);  // the epilogue's warps of both CTAs
     }
-    s.dead = 0;
+    s.watch.dead = s.watch.progress = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -468,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
   // 32 bits serve: 2^32 tiles of full size are 2^49 bytes of output, and at most
   // groups * 2^14 + rows / 256 are not
   const uint32_t tiles = (KIND == kProductGradWeight ? groups * ((a.n + kTile - 1) / kTile) : s.first[groups]) * mt;
-  volatile uint32_t* dead = &s.dead;
+  volatile Watch* watch = &s.watch;
 
   if (warp >= kEpilogueWarps) {
     if constexpr (REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CREW::kOtherRegs));
@@ -480,6 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
       Ring ring;
       const uint32_t even = in_cta(smem_addr(s.full), 0);
       const uint32_t own = smem_addr(s.full), empty = smem_addr(s.empty), data = smem_addr(stages);
+      uint32_t issued = 0;
       bool ok = true;
       for (uint32_t i = pair; ok && i < tiles; i += pairs) {
         const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
@@ -492,11 +507,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
         const CUtensorMap* map_small = &a.b_small[t.rank];
         const int z = KIND == kProductGradWeight ? 0 : t.expert;
         for (int k = 0; k < t.depth; k += kStep) {
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead))) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, watch))) {
             ok = false;
             break;
           }
+          ++issued;
           if (issuer) {
+            watch->progress = issued;
             // the even CTA's barrier counts both CTAs' copies; its own TMA
             // thread alone arrives, for the bytes of both
             uint32_t bar = even + 8 * ring.stage;
@@ -546,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
       // every stage given back: no signal of the tensor core is on its way to a
       // CTA that has left
       for (int j = 0; ok && j < kStages; ++j, ring.next())
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty + 8 * ring.stage, ring.phase ^ 1, watch));
       if (!ok) {  // copies in flight still write this CTA's shared memory
         const long long t0 = clock64();
         while (clock64() - t0 < (1ll << 22)) {
@@ -571,7 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
           int k0 = 0;
           do {  // a segment, also of an expert without rows
             const uint32_t buf = n & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_empty[buf]), ((n >> 1) & 1) ^ 1, dead))) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_empty[buf]), ((n >> 1) & 1) ^ 1, watch))) {
               ok = false;
               break;
             }
@@ -580,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
             const int k1 = min(k0 + t.segment, t.depth);
             for (int k = k0; k < k1; k += kStep) {
               const uint32_t bar = full + 8 * ring.stage;
-              if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar, ring.phase, dead))) {
+              if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar, ring.phase, watch))) {
                 ok = false;
                 break;
               }
@@ -654,7 +671,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
               if (!a.tma_a) fetch_units<kAColumns>(fa, fa.p + (kAColumns ? k * ld_a : k), left, l0, u, va);
               if (!a.tma_b) fetch_units<kBColumns>(fb, fb.p + (kBColumns ? k * ld_b : k), left, l0, u, vb);
             }
-            const bool here = mbar_wait(smem_addr(&s.go[st]), (parity >> st) & 1, dead);
+            const bool here = mbar_wait(smem_addr(&s.go[st]), (parity >> st) & 1, watch);
             parity ^= 1u << st;
             char* sa = stages + static_cast<size_t>(st) * kStageBytes;
             char* sb = sa + kOperandBytes;
@@ -704,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
       int k0 = 0;
       do {  // a segment
         const uint32_t buf = n & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_full[buf]), (n >> 1) & 1, dead))) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_full[buf]), (n >> 1) & 1, watch))) {
           ok = false;
           break;
         }
@@ -764,6 +781,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns));
   }
+}
+
+// Self-test of the bounded wait: a barrier that nothing completes, stages that
+// nobody issues.
+__global__ void __launch_bounds__(32) product_wait_probe_kernel(long long cycles) {
+  __shared__ alignas(8) uint64_t bar;
+  __shared__ Watch watch;
+  if (threadIdx.x != 0) return;
+  watch.dead = watch.progress = 0;
+  mbar_init(smem_addr(&bar), 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  mbar_wait(smem_addr(&bar), 0, &watch, cycles);
 }
 
 // ---------------------------------------------------------------- host side
@@ -837,6 +866,14 @@ cudaError_t launch_pairs(const PairArgs& a, uint64_t most_tiles, cudaStream_t s)
 }
 
 }  // namespace
+
+cudaError_t launch_product_wait_probe(cudaStream_t s) {
+  g_launched.store(true, std::memory_order_relaxed);
+  product_wait_probe_kernel<<<1, 32, 0, s>>>(1ll << 14);
+  const cudaError_t err = cudaGetLastError();
+  if (err == cudaSuccess) note_launch();
+  return err;
+}
 
 cudaError_t read_product_error(unsigned int* flag, bool clear) {
   *flag = 0;

@@ -98,8 +98,9 @@ const char* ccl_last_error(void);
 uint64_t ccl_kernel_launch_count(void);
 
 /* The device error word: nonzero once a bounded device-side wait ran out (the
- * bulk-copy fan-out of ccl_all_gather / ccl_broadcast waits on its own copies
- * with a bound; no wait of this library depends on another launch or rank).
+ * bulk-copy fan-out of ccl_all_gather / ccl_broadcast, the experts' products and
+ * the AdamW step with 8-bit states wait on their own copies and warps with a
+ * bound; no wait of this library depends on another launch or rank).
  * Synchronous (reads device memory); clear != 0 resets it to 0 afterwards.
  * Errors: flag NULL -> CCL_ERR_INVALID_ARG; a failed copy -> CCL_ERR_CUDA. */
 ccl_status_t ccl_device_error_flag(unsigned int* flag, int clear);
@@ -110,10 +111,10 @@ ccl_status_t ccl_device_error_flag(unsigned int* flag, int clear);
  * way.  A failed synchronization -> CCL_ERR_CUDA. */
 ccl_status_t ccl_stream_check(void* stream);
 
-/* Self-test of that path: enqueues a one-thread kernel whose mbarrier wait
- * can never complete, so it gives up after a short bound (well under a
- * millisecond) and sets the error word; no copy is in flight and nothing
- * faults.  The next ccl_stream_check on `stream` returns CCL_ERR_TIMEOUT. */
+/* Self-test of that path: for each of those three, enqueues a one-thread kernel
+ * whose mbarrier wait can never complete, so it gives up after a short bound
+ * (well under a millisecond) and sets a bit of the error word; no copy is in
+ * flight and nothing faults.  The next ccl_stream_check on `stream` returns CCL_ERR_TIMEOUT. */
 ccl_status_t ccl_selftest_bounded_wait(void* stream);
 
 /* Chunk c of an n-element buffer cut into p chunks (the rule under CHUNKS AND
