@@ -42,6 +42,7 @@
 #include <cuda.h>  // CUtensorMap and its enums; nothing links the driver
 
 #include <atomic>
+#include <climits>
 
 #include "device_common.cuh"
 #include "realign.cuh"
@@ -58,7 +59,7 @@ constexpr int kMaxGroups = 2048;   // (rank, expert) pairs per launch
 constexpr int kLaunchRanks = 8;    // keeps the parameter block under 4 KB
 constexpr int kEpilogueWarps = 8;  // two per 32 TMEM lanes
 constexpr int kTmaWarp = kEpilogueWarps, kMmaWarp = kTmaWarp + 1, kLoaderWarp = kMmaWarp + 1;
-// REGS (fp32 weight gradients, see kMostSummed): the epilogue's threads hold
+// REGS (fp32 weight gradients, see kMostF32): the epilogue's threads hold
 // 128 running sums each, for which the other warps give registers up; TMA
 // reads both operands, so that two warps are enough to clear last rows.
 // The shares add up to what the block is launched with.
@@ -75,12 +76,18 @@ constexpr int kSmallBox = 16;      // rows of B's small box
 constexpr uint32_t kTmemColumns = 512;
 // The tensor core cuts its fp32 sums at the last bit instead of rounding them,
 // towards zero, once per 16 contraction elements: 1e-6 of the result after
-// 1024 of them, 1.9e-5 after 16384, where rounded sums stay at 2e-7 to 4e-7.
-// bf16 outputs round to 4e-3 and hide that; an fp32 weight gradient is summed
-// in parts of at most so many rows (5e-7), which the epilogue adds up: in
-// registers, or, where loaders fill the stages and set the pace, in the output
-// (32 experts of 1024 rows by TMA took 948 us that way, 650 in registers).
-constexpr int kMostSummed = 512;
+// 1024 of them, 1.9e-5 after 16384, and so on, where rounded sums stay at 2e-7
+// to 4e-7.  So long sums are made in parts, which the epilogue adds up, rounded.
+// fp32 outputs, the weight gradients: parts of at most so many rows (5e-7), added
+// up in registers, or, where loaders fill the stages and set the pace, in the
+// output (32 experts of 1024 rows by TMA took 948 us that way, 650 in registers).
+constexpr int kMostF32 = 512;
+// bf16 outputs round to 4e-3 and hide 1.9e-5, but not what a million rows would
+// come to, always towards zero: parts of at most so many, added up in tensor
+// memory.  The first part stays in its buffer and the others take turns in the
+// other one, so that the tensor core waits while each of them is added (8 experts
+// of 1024 rows, 2048 <- 32768: 641 -> 647 us).
+constexpr int kMostBF16 = 16384;
 // Two seconds without a stage: a wait for a whole tile, or for the next stage
 // that the loaders have a part in, may take any number of stages (10^9 rows of
 // one expert are 16 million: five seconds), so it runs out only where no stage
@@ -210,6 +217,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
         "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(addr));
 }
+__device__ __forceinline__ void tmem_load8(uint32_t addr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void tma(uint32_t dst, const CUtensorMap* map, int x, int line, int chunk, int z, uint32_t cluster_bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
@@ -241,7 +258,7 @@ struct Tile {
   int rank, expert;
   int lo;       // first row of the expert
   int depth;    // contraction elements
-  int segment;  // of them per sum in tensor memory: a multiple of kStep, or depth
+  int segment;  // of them per part of the sum: a multiple of kStep, or depth
   int c0;       // first column: a row of the rank, or an n
   int cols;     // columns that are stored
   int width;    // columns that are computed: a multiple of 32
@@ -251,8 +268,8 @@ struct Tile {
 // The same value in every lane, and known to be.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
-// SPLIT: sums longer than kMostSummed are made in parts.
-template <int KIND, bool SPLIT>
+// Sums of more than MOST contraction elements are made in parts.
+template <int KIND, int MOST>
 __device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int groups, uint32_t index, uint32_t mt) {
   const uint32_t rt = index / mt;
   Tile t;
@@ -285,9 +302,9 @@ __device__ __forceinline__ Tile tile_at(const PairArgs& a, const Shared& s, int 
   t.expert = g - t.rank * a.num_experts;
   t.width = (t.cols + 31) & ~31;
   t.segment = t.depth;
-  if (SPLIT && t.depth > kMostSummed) {
-    const int parts = (t.depth + kMostSummed - 1) / kMostSummed;
-    t.segment = ((t.depth + parts - 1) / parts + kStep - 1) / kStep * kStep;
+  if (t.depth > MOST) {
+    const int parts = (t.depth - 1) / MOST + 1;
+    t.segment = ((t.depth - 1) / parts + kStep) / kStep * kStep;
   }
   return t;
 }
@@ -400,15 +417,37 @@ __device__ __forceinline__ void add_rows(char* p, uint64_t ld, const uint32_t* v
     if (live && j < count) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p + j * ld), "f"(__uint_as_float(v[j])) : "memory");
 }
 
+// Adds a part to the sum of those before it, both in tensor memory: this warp's columns.
+__device__ __forceinline__ void add_part(uint32_t sum, uint32_t part, int c0, int width) {
+  for (int c = c0; c < width; c += 64) {
+#pragma unroll
+    for (int h = 0; h < 32; h += 8) {
+      uint32_t u[8], v[8];
+      tmem_load8(sum + c + h, u);
+      tmem_load8(part + c + h, v);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(__fadd_rn(__uint_as_float(u[j]), __uint_as_float(v[j])));
+      tmem_store8(sum + c + h, u);
+    }
+  }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // ------------------------------------------------------------------- kernel
-template <int KIND, int OUT, bool REGS>
+// HELD: sums of a bf16 output may have several parts.  A variant of its own: in
+// one kernel with the others, the code for it cost short sums up to 4 % (32
+// experts of 512 rows, bf16 weight gradient: 358 -> 373 us).
+template <int KIND, int OUT, bool REGS, bool HELD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads, 1)
     product_kernel(const __grid_constant__ PairArgs a) {
   constexpr bool kAColumns = KIND != kProductForward;     // A's contiguous axis is m
   constexpr bool kBColumns = KIND == kProductGradWeight;  // B's contiguous axis is c
-  constexpr bool kSplit = kBColumns && OUT == kF32;
+  constexpr int kMost = OUT == kF32 ? kMostF32 : HELD ? kMostBF16 : INT_MAX;
   using CREW = Crew<REGS>;
-  static_assert(!REGS || kSplit, "only sums in parts are held in registers");
+  static_assert(OUT == kBF16 || kBColumns, "weight gradients alone are fp32");
+  static_assert(!REGS || OUT == kF32, "parts of fp32 outputs alone are added up in registers");
+  static_assert(!HELD || OUT == kBF16, "and parts of bf16 outputs in tensor memory");
   extern __shared__ char dynamic[];
   char* stages = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
   Shared& s = *reinterpret_cast<Shared*>(stages + static_cast<size_t>(kStages) * kStageBytes);
@@ -497,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
       uint32_t issued = 0;
       bool ok = true;
       for (uint32_t i = pair; ok && i < tiles; i += pairs) {
-        const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
+        const Tile t = tile_at<KIND, kMost>(a, s, groups, i, mt);
         const int half = t.width >> 1;
         const int c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
         const int boxes = kBColumns ? (half + 63) / 64 : half > 64 ? 1 : (half + kSmallBox - 1) / kSmallBox;
@@ -574,7 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
       if (cta == 0) {
         const bool issuer = elect_one();
         Ring ring;
-        uint32_t n = 0;
+        uint32_t buf = 0, uses = 0;  // the next part's buffer; a bit for each: whether it was used an odd number of times
         const uint32_t full = smem_addr(s.full), empty = smem_addr(s.empty);
         // descriptors of stage 0; a stage, and 16 contraction elements, further on
         const uint64_t a0 = descriptor(smem_addr(stages), kAColumns ? kStep * 128 : 16);
@@ -582,19 +621,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
         constexpr uint64_t kNextA = (kAColumns ? 2048 : 32) >> 4, kNextB = (kBColumns ? 2048 : 32) >> 4;
         bool ok = true;
         for (uint32_t i = pair; ok && i < tiles; i += pairs) {
-          const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
+          const Tile t = tile_at<KIND, kMost>(a, s, groups, i, mt);
           const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAColumns ? 1u << 15 : 0u) | (kBColumns ? 1u << 16 : 0u) |
                                  (static_cast<uint32_t>(t.width >> 3) << 17) | (16u << 24);
+          const bool held = HELD && t.segment < t.depth;
           int k0 = 0;
-          do {  // a segment, also of an expert without rows
-            const uint32_t buf = n & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_empty[buf]), ((n >> 1) & 1) ^ 1, watch))) {
+          do {  // a part, also of an expert without rows
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_empty[buf]), ((uses >> buf) & 1) ^ 1, watch))) {
               ok = false;
               break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t d = tmem + buf * kTile;
-            const int k1 = min(k0 + t.segment, t.depth);
+            const int k1 = t.depth - k0 > t.segment ? k0 + t.segment : t.depth;
             for (int k = k0; k < k1; k += kStep) {
               const uint32_t bar = full + 8 * ring.stage;
               if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar, ring.phase, watch))) {
@@ -615,8 +654,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
             }
             if (ok && issuer) commit_pair(smem_addr(&s.tmem_full[buf]));
             __syncwarp();
-            k0 += t.segment;
-            ++n;
+            uses ^= 1u << buf;
+            if (!held || k0 == 0) buf ^= 1;
+            k0 = k1;
           } while (ok && k0 < t.depth);
         }
       }
@@ -631,7 +671,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
         uint32_t parity = 0;
         bool ok = true;
         for (uint32_t i = pair; ok && i < tiles; i += pairs) {
-          const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
+          const Tile t = tile_at<KIND, kMost>(a, s, groups, i, mt);
           const int half = t.width >> 1;
           const int64_t c = t.c0 + static_cast<int>(cta) * half, m = t.m0 + static_cast<int>(cta) * 128;
           const int64_t N = a.n, K = a.contract, rows = a.rows[t.rank];
@@ -698,12 +738,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
   } else {
     // ------------------------------------------------------------- epilogue
     if constexpr (REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CREW::kEpilogueRegs));
-    uint32_t n = 0;
+    uint32_t buf = 0, uses = 0;  // as the tensor core's warp counts them
     bool ok = true;
     const uint32_t quarter = warp & 3;  // the 32 lanes that this warp can read
     constexpr int kBytes = Elem<OUT>::kBytes;
     for (uint32_t i = pair; ok && i < tiles; i += pairs) {
-      const Tile t = tile_at<KIND, kSplit>(a, s, groups, i, mt);
+      const Tile t = tile_at<KIND, kMost>(a, s, groups, i, mt);
       const uint32_t m = t.m0 + cta * 128 + quarter * 32 + lane;
       const uint64_t at = (KIND == kProductGradWeight ? static_cast<uint64_t>(t.expert) * a.n + t.c0 : static_cast<uint64_t>(t.c0)) * M + m;
       // bf16 outputs two by two: where every row starts on four bytes
@@ -718,15 +758,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
 #pragma unroll
           for (int j = 0; j < 32; ++j) sum[q][j] = 0.0f;
       }
+      const bool held = HELD && t.segment < t.depth;
       int k0 = 0;
-      do {  // a segment
-        const uint32_t buf = n & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_full[buf]), (n >> 1) & 1, watch))) {
+      do {  // a part
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&s.tmem_full[buf]), (uses >> buf) & 1, watch))) {
           ok = false;
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t from = tmem + buf * kTile + (quarter << 21);  // lane 32 * quarter
+        const uint32_t lanes = tmem + (quarter << 21);  // lane 32 * quarter
+        const uint32_t to = held && k0 > 0 ? buf ^ 1 : buf;  // where the parts are added up
+        const uint32_t from = lanes + to * kTile;
+        const bool last = t.depth - k0 <= t.segment;
         if constexpr (REGS) {
           if (t.depth > 0) {
 #pragma unroll
@@ -741,7 +784,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
             }
           }
         } else {
-          for (int c = c0; c < t.width; c += 64) {
+          if (held && k0 > 0) add_part(from, lanes + buf * kTile, c0, t.width);
+          for (int c = c0; c < t.width && (last || !held); c += 64) {
             uint32_t v[32];
             if (t.depth > 0) {
               tmem_load32(from + c, v);
@@ -751,16 +795,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Crew<REGS>::kThreads
               for (int j = 0; j < 32; ++j) v[j] = 0;
             }
             char* p = out + static_cast<uint64_t>(c) * ld;
-            if (kSplit && k0 > 0) add_rows(p, ld, v, t.cols - c, m < M);
+            if (OUT == kF32 && k0 > 0) add_rows(p, ld, v, t.cols - c, m < M);
             else store_columns<OUT>(p, ld, v, t.cols - c, m < M, even);
             __syncwarp();
           }
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(in_cta(smem_addr(&s.tmem_empty[buf]), 0));
-        k0 += t.segment;
-        ++n;
+        if (lane == 0) {
+          if (!held || k0 > 0) mbar_arrive(in_cta(smem_addr(&s.tmem_empty[buf]), 0));
+          if (held && last) mbar_arrive(in_cta(smem_addr(&s.tmem_empty[to]), 0));
+        }
+        uses ^= 1u << buf;
+        if (!held || k0 == 0) buf ^= 1;
+        k0 = last ? t.depth : k0 + t.segment;
       } while (k0 < t.depth);
       if constexpr (REGS) {
 #pragma unroll
@@ -831,9 +879,9 @@ bool encode(CUtensorMap* map, const void* p, uint64_t width, uint64_t height, ui
 // Whether TMA can read rows of `width` bf16 elements at p.
 bool on_grid(const void* p, uint64_t width) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && width % 8 == 0; }
 
-template <int KIND, int OUT, bool REGS = false>
+template <int KIND, int OUT, bool REGS = false, bool HELD = false>
 cudaError_t launch_pairs(const PairArgs& a, uint64_t most_tiles, cudaStream_t s) {
-  const auto kernel = product_kernel<KIND, OUT, REGS>;
+  const auto kernel = product_kernel<KIND, OUT, REGS, HELD>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (err != cudaSuccess) return err;
   if (REGS) {  // a block launched with fewer registers would wait for its shares for ever
@@ -901,6 +949,7 @@ cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& args, cu
     a.whole_a = a_width % 64 == 0 && a_width >= 128;
     a.whole_b = b_width % 64 == 0 && b_width >= 128;
     uint64_t rows = 0;
+    uint64_t most_depth = kind == kProductForward ? k : kind == kProductGradInput ? n : 0;  // that a sum may have
     for (int i = 0; i < a.p; ++i) {
       a.pa[i] = args.a[r0 + i];
       a.pb[i] = args.b[r0 + i];
@@ -908,6 +957,7 @@ cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& args, cu
       a.offsets[i] = args.offsets[r0 + i];
       a.rows[i] = args.rows[r0 + i];
       rows += (a.rows[i] + kTile - 1) / kTile + (a.rows[i] != 0 ? E : 0);
+      if (kind == kProductGradWeight && a.rows[i] > most_depth) most_depth = a.rows[i];
       if (a.rows[i] == 0) continue;
       a.tma_a = a.tma_a && on_grid(a.pa[i], a_width);
       a.tma_b = a.tma_b && on_grid(a.pb[i], b_width);
@@ -932,11 +982,18 @@ cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& args, cu
     }
     const uint64_t mt = ((kind == kProductForward ? n : k) + kTile - 1) / kTile;
     const uint64_t most_tiles = (kind == kProductGradWeight ? static_cast<uint64_t>(a.p) * E * ((n + kTile - 1) / kTile) : rows) * mt;
-    const cudaError_t err = kind == kProductForward     ? launch_pairs<kProductForward, kBF16>(a, most_tiles, s)
-                            : kind == kProductGradInput ? launch_pairs<kProductGradInput, kBF16>(a, most_tiles, s)
-                            : out_dt == kBF16           ? launch_pairs<kProductGradWeight, kBF16>(a, most_tiles, s)
-                            : a.tma_a && a.tma_b        ? launch_pairs<kProductGradWeight, kF32, true>(a, most_tiles, s)
-                                                        : launch_pairs<kProductGradWeight, kF32>(a, most_tiles, s);
+    cudaError_t err;
+    if (out_dt == kF32)
+      err = a.tma_a && a.tma_b ? launch_pairs<kProductGradWeight, kF32, true>(a, most_tiles, s)
+                               : launch_pairs<kProductGradWeight, kF32>(a, most_tiles, s);
+    else if (most_depth > kMostBF16)
+      err = kind == kProductForward     ? launch_pairs<kProductForward, kBF16, false, true>(a, most_tiles, s)
+            : kind == kProductGradInput ? launch_pairs<kProductGradInput, kBF16, false, true>(a, most_tiles, s)
+                                        : launch_pairs<kProductGradWeight, kBF16, false, true>(a, most_tiles, s);
+    else
+      err = kind == kProductForward     ? launch_pairs<kProductForward, kBF16>(a, most_tiles, s)
+            : kind == kProductGradInput ? launch_pairs<kProductGradInput, kBF16>(a, most_tiles, s)
+                                        : launch_pairs<kProductGradWeight, kBF16>(a, most_tiles, s);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;

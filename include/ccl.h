@@ -448,15 +448,19 @@ ccl_status_t ccl_moe_from_experts_grad(const void* const* dout, const void* cons
  * Everything is bf16, row-major and contiguous, except dw, which is dw_dt
  * (CCL_F32, as gradient buckets hold it, or CCL_BF16).  Products are summed
  * in fp32 in an order fixed by the sizes and rounded once.  The tensor cores
- * cut their running sums towards zero: 1e-6 of a result per 1024 contraction
- * elements, far below bf16's rounding; fp32 weight gradients are summed in
- * parts of at most 512 rows and stay within 5e-7.  Everything is device
- * memory; rows[r] < 2^31 - 255; n and contract <= 2^22.  Buffers on 16 bytes
- * whose rows are multiples of 16 bytes are read by TMA, others at about a
- * fifth of the rate.  A wait of the kernels that ran out would be reported by
- * ccl_stream_check.  Rows that no expert has (below offsets[0], from offsets[num_experts] on) are not written;
- * offsets beyond rows[r] are cut to it.  num_experts <= 1024.  The ranks may
- * share one w; no output may overlap an input or another output. */
+ * cut their running sums towards zero, so sums are made in parts, of at most
+ * 512 rows for an fp32 dw and 16384 contraction elements for bf16 outputs, which
+ * are added up rounded.  With S the sum of an output's terms' magnitudes and L
+ * its contraction length, an fp32 dw is within (64 + L / 512) * 2^-23 * S (5e-7
+ * of the 2-norm measured at L = 16384), and a bf16 output within (2048 + L /
+ * 16384) * 2^-23 * S before its rounding (1.9e-5 of the norm measured).
+ * Everything is device memory; rows[r] < 2^31 - 255; n and contract <= 2^22.
+ * Buffers on 16 bytes whose rows are multiples of 16 bytes are read by TMA,
+ * others at about a fifth of the rate.  A wait of the kernels that ran out would
+ * be reported by ccl_stream_check.  Rows that no expert has (below offsets[0],
+ * from offsets[num_experts] on) are not written; offsets beyond rows[r] are cut
+ * to it.  num_experts <= 1024.  The ranks may share one w; no output may overlap
+ * an input or another output. */
 ccl_status_t ccl_moe_product(const void* const* x, const int32_t* const* offsets, const void* const* w,
                              const size_t* rows, int p, int num_experts, size_t n, size_t contract,
                              void* const* y, void* stream);
