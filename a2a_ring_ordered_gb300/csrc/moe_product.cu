@@ -144,15 +144,16 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-// On a barrier of either CTA of the pair.  A release at cluster scope would wait
-// for all of the thread's memory operations, which nothing here needs: the
-// loaders' writes, behind a proxy fence and a barrier of the writers, lie in
-// their own SM's shared memory, where the tensor core reads them (a release
-// there took a microsecond a stage); the epilogue has read tensor memory, which
-// its fence orders, and its stores are nobody's concern (with one, the fp32
-// weight gradients of 32 experts of 512 rows took 489 us instead of 437).
+// On a barrier of either CTA of the pair.  Released to it is what lies in this
+// CTA's shared memory: what the loaders have written, behind a proxy fence of the
+// writers and a barrier among them; the epilogue has read tensor memory, which its
+// own fence orders.  Only that: a release at cluster scope of all of a thread's
+// memory takes 700 ns, a loader's with its loads on the way a microsecond, the
+// epilogue's with its stores longer (fp32 weight gradients of 32 experts of 512
+// rows 489 us instead of 437).
 __device__ __forceinline__ void mbar_arrive(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -162,7 +163,7 @@ __device__ __forceinline__ void mbar_arrive_own(uint32_t bar, uint32_t count = 1
 }
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t done;
-  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
                : "=r"(done)
                : "r"(bar), "r"(parity)
                : "memory");
