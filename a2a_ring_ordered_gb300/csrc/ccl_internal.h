@@ -241,7 +241,7 @@ struct MoeRowsArgs {  // to_experts, from_experts and its gradient
   const void* x[kMoeMaxRanks];         // token rows read (to_experts: x; the gradient: dout)
   const void* y[kMoeMaxRanks];         // expert rows read
   const int32_t* rows[kMoeMaxRanks];
-  const float* weights[kMoeMaxRanks];  // weights[0] NULL: ones
+  const float* weights[kMoeMaxRanks];  // NULL: ones
   void* out[kMoeMaxRanks];             // expert rows (to_experts, dy) or token rows (from_experts) written
   float* dweights[kMoeMaxRanks];
   uint32_t tokens[kMoeMaxRanks];

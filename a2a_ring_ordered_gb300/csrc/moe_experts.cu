@@ -69,7 +69,7 @@ __global__ void moe_sort_kernel(const __grid_constant__ MoeSortArgs a) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t smem[];
   const int E = a.num_experts;
-  const int bits = 33 - __clz(E);  // of 0 .. E - 1, and one that -1 alone has
+  const int bits = 33 - __clz(E);  // they tell 0 .. E - 1 and -1 apart, with one to spare
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   uint32_t* hist = smem;             // [warps][E]
   uint32_t* total = hist + warps * E;  // [E]: this CTA's items of each expert
@@ -645,7 +645,7 @@ cudaError_t launch_back_off(const MoeRowsArgs& a, cudaStream_t s) {
   });
 }
 
-constexpr uint64_t kPassCtas = 4 * 152 * 4;
+constexpr uint64_t kPassCtas = 4 * 152 * 4;  // waves, SMs, CTAs that an SM takes
 
 template <int DT, int VEC>
 cudaError_t launch_back(const MoeRowsArgs& a, cudaStream_t s) {
