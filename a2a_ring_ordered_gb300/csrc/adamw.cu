@@ -10,7 +10,9 @@
 // vectors' grid, where issue slots (0.71 a cycle) and HBM are both two thirds
 // full; 480 with parameters, gradients and copies off it: a tenth more
 // instructions, for which the stage's vectors cannot serve, since stores of
-// neighbours per lane would ask for every sector four times.
+// neighbours per lane would ask for every sector four times.  Without a copy:
+// fp32 gradients 412 us, off the grid 457; bf16 parameters and gradients 395 and
+// 459, bound by the same instructions for 10 bytes an element.
 //
 // An 8-bit state is e4m3 codes with one fp32 scale per 128 elements.  A warp
 // holds such a block with four elements per lane, so its amax is one

@@ -31,11 +31,11 @@
 //     gradient 530, fp32 weight gradient 650.  The tensor pipe bounds the first
 //     two (92 % of cycles).  The last takes 532 without its 1.9 GB of stores,
 //     which delay the loads; a quarter fewer loads gained 4 %, and tiles of two
-//     or four experts under way at a time lost 5 %.
-//   32 experts x 512 rows: weight gradient 415 us; without rows, 1.9 GB of
-//     zeros, 287 us (6.5 TB/s).
-//   32 experts x 7..8 rows, the weights' stream: 155 us, 6.1 TB/s.
-//   operands off the grid (2047 x 7167): 3.4 ms forward, 2.6 ms backward; the
+//     or four experts under way at a time lost 5 %.  bf16 weight gradient 590.
+//   32 experts x 512 rows: weight gradient 415 us, bf16 355; without rows, 1.9 GB
+//     of zeros, 287 us (6.5 TB/s).
+//   32 experts x 4 rows on average, the weights' stream: 153 us, 6.2 TB/s.
+//   operands off the grid (2047 x 7167): 3.3 ms forward, 2.5 ms backward; the
 //     loaders' instructions bound them.
 //   1 expert of 66 columns by 5376 contraction elements: 25 us, 84 stages one
 //     behind the other in a single pair.

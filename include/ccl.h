@@ -456,7 +456,7 @@ ccl_status_t ccl_moe_from_experts_grad(const void* const* dout, const void* cons
  * 16384) * 2^-23 * S before its rounding (1.9e-5 of the norm measured).
  * Everything is device memory; rows[r] < 2^31 - 255; n and contract <= 2^22.
  * Buffers on 16 bytes whose rows are multiples of 16 bytes are read by TMA,
- * others at about a fifth of the rate.  A wait of the kernels that ran out would
+ * others at a fifth to a sixth of the rate.  A wait of the kernels that ran out would
  * be reported by ccl_stream_check.  Rows that no expert has (below offsets[0],
  * from offsets[num_experts] on) are not written; offsets beyond rows[r] are cut
  * to it.  num_experts <= 1024.  The ranks may share one w; no output may overlap
