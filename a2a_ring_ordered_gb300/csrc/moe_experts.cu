@@ -589,6 +589,7 @@ uint32_t most_tokens(const MoeRowsArgs& a) {
 
 template <typename... Params>
 cudaError_t launch_rows(void (*kernel)(Params...), uint64_t ctas, int p, cudaStream_t s, Params... params) {
+  if (ctas == 0) return cudaSuccess;  // no rank has a row to write
   if (ctas > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(p));
