@@ -34,6 +34,7 @@ SCHEDULES = {"ring": 0, "recursive_doubling": 1, "rabenseifner": 2, "binomial_tr
 CCL_MAX_RANKS = 128
 
 _DTYPES = {torch.float32: CCL_F32, torch.bfloat16: CCL_BF16, torch.int32: CCL_I32}
+_SCORES = {"softmax": 0, "sigmoid": 1}
 _OPS = {"sum": CCL_SUM, "max": CCL_MAX, "min": CCL_MIN}
 
 
@@ -106,6 +107,14 @@ def _load() -> ctypes.CDLL:
         "ccl_moe_product": (st, [vp, vp, vp, vp, i32, i32, sz, sz, vp, vp]),
         "ccl_moe_product_grad_input": (st, [vp, vp, vp, vp, i32, i32, sz, sz, vp, vp]),
         "ccl_moe_product_grad_weight": (st, [vp, vp, vp, vp, i32, i32, sz, sz, i32, vp, vp]),
+        "ccl_moe_balance_workspace_bytes": (sz, [i32, i32]),
+        "ccl_moe_gate": (st, [vp, vp, i32, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, i32, vp, vp, vp, sz, vp]),
+        "ccl_moe_gate_grad": (st, [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp, ctypes.c_float, vp, vp]),
+        "ccl_moe_balance": (st, [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp]),
+        "ccl_moe_balance_grad": (st, [vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_float, vp, vp]),
+        "ccl_layer_norm": (st, [vp, vp, vp, vp, vp, i32, sz, ctypes.c_double, i32, i32, vp, vp, vp, vp, vp]),
+        "ccl_layer_norm_grad_workspace_bytes": (sz, [i32, sz]),
+        "ccl_layer_norm_grad": (st, [vp, vp, vp, vp, vp, vp, vp, i32, sz, i32, i32, vp, i32, vp, vp, vp, sz, vp]),
         "ccl_adamw_step": (st, [ctypes.POINTER(AdamWTensor), sz, i32, i32, i32, ctypes.POINTER(AdamWHyper), vp]),
         "ccl_plan_buckets": (st, [ctypes.POINTER(sz), sz, sz, sz, ctypes.POINTER(ctypes.c_uint32),
                                   ctypes.POINTER(sz), ctypes.POINTER(sz), ctypes.POINTER(sz)]),
@@ -896,6 +905,207 @@ def ccl_moe_product_grad_weight(dy, x, offsets, dw, stream=None) -> None:
     offsets = _ranks(offsets, "offsets", p, torch.int32, [experts + 1] * p, 1, True)
     _check(LIB.ccl_moe_product_grad_weight(dy, x, offsets, _sizes(rows), p, experts, n, contract, _dtype_code(held), dw,
                                            _stream_of(stream, one)), "ccl_moe_product_grad_weight")
+
+
+# ------------------------------------------------------ MoE: the router's choice
+def _one_device(first: torch.Tensor, *lists):
+    """Refuses lists on another GPU than the first tensor's (a list's own tensors are
+    alike, and tensors at all, by the checks that _ranks and _shaped make)."""
+    at = first.get_device()
+    for ts in lists:
+        if ts and isinstance(ts[0], torch.Tensor) and ts[0].get_device() != at:
+            raise ValueError(f"buffers on {ts[0].device} and {first.device} in one call")
+
+
+class _Scratch:
+    """The workspace of one call: the caller's, or one that torch allocates and
+    keeps until the call's work on `stream` is done."""
+
+    def __init__(self, given, need: int, first: torch.Tensor, stream):
+        if given is not None:
+            if not given.is_cuda or given.device != first.device or not given.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on {first.device}")
+            self.tensor = given
+        else:
+            self.tensor = torch.empty(need, dtype=torch.uint8, device=first.device)
+            if stream is not None:
+                self.tensor.record_stream(stream)
+        self.pointer, self.bytes = self.tensor.data_ptr(), self.tensor.numel() * self.tensor.element_size()
+
+
+class _On:
+    """Launches go to the tensors' GPU, whichever is current."""
+
+    def __init__(self, first: torch.Tensor):
+        self.guard = torch.cuda.device(first.device) if first.is_cuda and first.get_device() != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *error):
+        if self.guard is not None:
+            self.guard.__exit__(*error)
+
+
+def _score_code(score: str) -> int:
+    try:
+        return _SCORES[score]
+    except KeyError:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}") from None
+
+
+def ccl_moe_balance_workspace_bytes(p: int, num_experts: int) -> int:
+    """Bytes of workspace for ccl_moe_balance, and ccl_moe_gate with counts."""
+    return LIB.ccl_moe_balance_workspace_bytes(p, num_experts)
+
+
+def ccl_moe_gate(logits, ids, gates, score: str = "softmax", normalize: bool = True, scale: float = 1.0, counts=None,
+                 losses=None, together: bool = False, workspace=None, stream=None) -> None:
+    """The k experts of each token and their gates: logits[r] (tokens, experts) fp32
+    or bf16 -> ids[r] (tokens, k) int32 (-1 where fewer than k logits are above
+    -inf) and gates[r] (tokens, k) fp32.  With counts[r] (experts + 1 int32) and
+    losses[r] (1 fp32) also what ccl_moe_balance gives."""
+    logits, one, tokens, (experts,) = _shaped(logits, "logits", 2, None, None, True)
+    p = len(tokens)
+    packed, first, rows, k = _choices(ids, "ids")
+    if rows != tokens:
+        raise ValueError("ids must hold a row per token of logits")
+    held = _ranks(gates, "gates", p, torch.float32, tokens, k, True)
+    _one_device(one, ids, gates, counts, losses)
+    with_loss = counts is not None or losses is not None
+    if with_loss:
+        if counts is None or losses is None:
+            raise ValueError("counts and losses are given together")
+        counts = _ranks(counts, "counts", p, torch.int32, [experts + 1] * p, 1, True)
+        losses = _ranks(losses, "losses", p, torch.float32, [1] * p, 1, True)
+    code = _score_code(score)
+    with _On(one):
+        scratch = _Scratch(workspace, ccl_moe_balance_workspace_bytes(p, experts), one, stream) if with_loss else None
+        _check(LIB.ccl_moe_gate(logits, _sizes(tokens), p, k, experts, _dtype_code(one), code, 1 if normalize else 0, scale, packed,
+                                held, 1 if together else 0, counts, losses, scratch and scratch.pointer,
+                                scratch.bytes if scratch else 0, _stream_of(stream, one)), "ccl_moe_gate")
+
+
+def ccl_moe_gate_grad(logits, ids, dgates, dlogits, score: str = "softmax", normalize: bool = True, scale: float = 1.0,
+                      counts=None, dlosses=None, balance_scale: float = 1.0, stream=None) -> None:
+    """dlogits[r] = the gradient of sum dgates * gates, plus, with counts, that of
+    balance_scale * dlosses[r] * loss (dlosses None: ones)."""
+    logits, one, tokens, (experts,) = _shaped(logits, "logits", 2, None, None, True)
+    p = len(tokens)
+    packed, first, rows, k = _choices(ids, "ids")
+    if rows != tokens:
+        raise ValueError("ids must hold a row per token of logits")
+    held = _ranks(dgates, "dgates", p, torch.float32, tokens, k, True)
+    out = _ranks(dlogits, "dlogits", p, one.dtype, tokens, experts, True)
+    _one_device(one, ids, dgates, dlogits, counts, dlosses)
+    counts, dlosses = _balance_inputs(counts, dlosses, p, experts)
+    code = _score_code(score)
+    with _On(one):
+        _check(LIB.ccl_moe_gate_grad(logits, packed, held, _sizes(tokens), p, k, experts, _dtype_code(one), code,
+                                     1 if normalize else 0, scale, counts, dlosses, balance_scale, out, _stream_of(stream, one)),
+               "ccl_moe_gate_grad")
+
+
+def _balance_inputs(counts, dlosses, p: int, experts: int):
+    if counts is not None:
+        counts = _ranks(counts, "counts", p, torch.int32, [experts + 1] * p, 1, True)
+    if dlosses is not None:
+        dlosses = _ranks(dlosses, "dlosses", p, torch.float32, [1] * p, 1, True)
+    return counts, dlosses
+
+
+def ccl_moe_balance(logits, ids, counts, losses, score: str = "softmax", together: bool = False, workspace=None,
+                    stream=None) -> None:
+    """counts[r] (experts + 1 int32: choices of each expert, then the tokens with a
+    logit above -inf) and losses[r] (1 fp32) of given ids[r] (tokens, k)."""
+    logits, one, tokens, (experts,) = _shaped(logits, "logits", 2, None, None, True)
+    p = len(tokens)
+    packed, first, rows, k = _choices(ids, "ids")
+    if rows != tokens:
+        raise ValueError("ids must hold a row per token of logits")
+    _one_device(one, ids, counts, losses)
+    counts = _ranks(counts, "counts", p, torch.int32, [experts + 1] * p, 1, True)
+    losses = _ranks(losses, "losses", p, torch.float32, [1] * p, 1, True)
+    code = _score_code(score)
+    with _On(one):
+        scratch = _Scratch(workspace, ccl_moe_balance_workspace_bytes(p, experts), one, stream)
+        _check(LIB.ccl_moe_balance(logits, packed, _sizes(tokens), p, k, experts, _dtype_code(one), code, 1 if together else 0,
+                                   counts, losses, scratch.pointer, scratch.bytes, _stream_of(stream, one)), "ccl_moe_balance")
+
+
+def ccl_moe_balance_grad(logits, counts, dlogits, k: int, score: str = "softmax", dlosses=None, scale: float = 1.0,
+                         stream=None) -> None:
+    """dlogits[r] = the gradient of scale * dlosses[r] * loss (dlosses None: ones),
+    counts as ccl_moe_balance or ccl_moe_gate gave them for k choices a token."""
+    logits, one, tokens, (experts,) = _shaped(logits, "logits", 2, None, None, True)
+    p = len(tokens)
+    out = _ranks(dlogits, "dlogits", p, one.dtype, tokens, experts, True)
+    _one_device(one, counts, dlogits, dlosses)
+    counts, dlosses = _balance_inputs(counts, dlosses, p, experts)
+    code = _score_code(score)
+    with _On(one):
+        _check(LIB.ccl_moe_balance_grad(logits, counts, dlosses, _sizes(tokens), p, k, experts, _dtype_code(one), code, scale, out,
+                                        _stream_of(stream, one)), "ccl_moe_balance_grad")
+
+
+# ------------------------------------------------------------------ layer norm
+def _vectors(ts, name: str, p: int, cols: int, dtype=None):
+    """(addresses, first tensor) of a list of (cols,) tensors."""
+    pointers, one, sizes, _ = _shaped(ts, name, 1, p, dtype, True)
+    if sizes != [cols] * p:
+        raise ValueError(f"{name} must hold {cols} elements on every rank")
+    return pointers, one
+
+
+def ccl_layer_norm(x, weight, bias, y, residual=None, sum=None, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
+    """y[r] = (v - mean) * rstd * weight[r] + bias[r] over rows v of x[r] (rows, cols),
+    or of x[r] + residual[r], which sum[r] then receives; bias may be None, mean[r]
+    and rstd[r] (rows fp32, for the gradient) too."""
+    packed, one, rows, (cols,) = _shaped(x, "x", 2, None, None, True)
+    p, dt = len(rows), one.dtype
+    weight, first = _vectors(weight, "weight", p, cols)
+    _one_device(one, [first], bias, y, residual, sum, mean, rstd)
+    bias = _vectors(bias, "bias", p, cols, first.dtype)[0] if bias is not None else None
+    out = _ranks(y, "y", p, dt, rows, cols, True)
+    residual = _ranks(residual, "residual", p, dt, rows, cols, True) if residual is not None else None
+    sum = _ranks(sum, "sum", p, dt, rows, cols, True) if sum is not None else None
+    mean = _ranks(mean, "mean", p, torch.float32, rows, 1, True) if mean is not None else None
+    rstd = _ranks(rstd, "rstd", p, torch.float32, rows, 1, True) if rstd is not None else None
+    with _On(one):
+        _check(LIB.ccl_layer_norm(packed, residual, weight, bias, _sizes(rows), p, cols, eps, _dtype_code(one), _dtype_code(first), out,
+                                  sum, mean, rstd, _stream_of(stream, one)), "ccl_layer_norm")
+
+
+def ccl_layer_norm_grad_workspace_bytes(p: int, cols: int) -> int:
+    """Bytes of workspace for ccl_layer_norm_grad with dweight or dbias."""
+    return LIB.ccl_layer_norm_grad_workspace_bytes(p, cols)
+
+
+def ccl_layer_norm_grad(dy, x, weight, mean, rstd, dx, dsum=None, dweight=None, dbias=None, workspace=None, stream=None) -> None:
+    """The gradients of ccl_layer_norm: dx[r] (plus dsum[r], the gradient that reaches
+    the sum past the norm), dweight[r] and dbias[r] (cols, fp32 or bf16; either may
+    be None).  x is what was normed: sum where there was a residual."""
+    packed, one, rows, (cols,) = _shaped(x, "x", 2, None, None, True)
+    p, dt = len(rows), one.dtype
+    weight, first = _vectors(weight, "weight", p, cols)
+    _one_device(one, [first], dy, mean, rstd, dx, dsum, dweight, dbias)
+    grads = _ranks(dy, "dy", p, dt, rows, cols, True)
+    out = _ranks(dx, "dx", p, dt, rows, cols, True)
+    dsum = _ranks(dsum, "dsum", p, dt, rows, cols, True) if dsum is not None else None
+    mean = _ranks(mean, "mean", p, torch.float32, rows, 1, True)
+    rstd = _ranks(rstd, "rstd", p, torch.float32, rows, 1, True)
+    held = None
+    if dweight is not None:
+        dweight, held = _vectors(dweight, "dweight", p, cols)
+    if dbias is not None:
+        dbias, held = _vectors(dbias, "dbias", p, cols, None if held is None else held.dtype)
+    code = CCL_F32 if held is None else _dtype_code(held)
+    with _On(one):
+        scratch = None if held is None else _Scratch(workspace, ccl_layer_norm_grad_workspace_bytes(p, cols), one, stream)
+        _check(LIB.ccl_layer_norm_grad(grads, dsum, packed, weight, mean, rstd, _sizes(rows), p, cols, _dtype_code(one),
+                                       _dtype_code(first), out, code, dweight, dbias, scratch and scratch.pointer,
+                                       scratch.bytes if scratch else 0, _stream_of(stream, one)), "ccl_layer_norm_grad")
 
 
 # ------------------------------------------------------------------------ AdamW

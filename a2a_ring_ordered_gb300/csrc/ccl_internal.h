@@ -274,6 +274,84 @@ struct ProductArgs {
 cudaError_t read_product_error(unsigned int* flag, bool clear);
 cudaError_t launch_moe_product(int kind, int out_dt, const ProductArgs& a, cudaStream_t s);
 
+// ------------------------------------------------- rows in parts, per rank
+// The rows of all ranks are cut into parts, one per CTA: part i of the n that
+// rank r has holds its rows [rows * i / n, rows * (i + 1) / n).  A rank gets
+// parts by its share of all rows, so that ragged ranks take alike.
+struct RankParts {
+  uint32_t first[kMoeMaxRanks + 1];  // first part of each rank; first[p] = the launch's CTAs
+  uint32_t rows[kMoeMaxRanks];
+};
+// At most `most` + p parts, of at least `least` rows where there are as many;
+// `all`: a rank without rows gets one too.
+void cut_rows(RankParts* parts, const size_t* rows, int p, uint32_t most, uint32_t least, bool all);
+
+// ------------------------------------------------- MoE: the router's choice
+constexpr uint32_t kBalanceParts = 608;  // CTAs that a call with the balance loss has, beside one a rank
+struct GateArgs {
+  const void* logits[kMoeMaxRanks];
+  const int32_t* ids_in[kMoeMaxRanks];  // the gradient, and a loss of given ids
+  int32_t* ids[kMoeMaxRanks];
+  float* gates[kMoeMaxRanks];
+  const float* dgates[kMoeMaxRanks];
+  void* dlogits[kMoeMaxRanks];
+  const int32_t* counts[kMoeMaxRanks];  // the gradient of the loss
+  const float* dlosses[kMoeMaxRanks];   // NULL: ones
+  RankParts parts;
+  float* partial;                       // per part: num_experts sums of shares, then num_experts + 1 counts (int32)
+  float scale, balance_scale;
+  int p, k, num_experts, score, normalize;
+};
+struct BalanceJoinArgs {
+  int32_t* counts[kMoeMaxRanks];
+  float* losses[kMoeMaxRanks];
+  uint32_t first[kMoeMaxRanks + 1];
+  const float* partial;
+  int p, k, num_experts, together;
+};
+static_assert(sizeof(GateArgs) <= 32764, "router parameters exceed 32,764 bytes");
+static_assert(sizeof(BalanceJoinArgs) <= 4096, "balance parameters exceed 4 KB");
+// Words of a part in the workspace.
+__host__ __device__ constexpr size_t balance_part_words(int num_experts) { return 2 * static_cast<size_t>(num_experts) + 1; }
+// select: ids and gates; balance: partial sums for launch_balance_join.  `vec`: rows start on 16 bytes.
+cudaError_t launch_gate(int dt, bool vec, bool select, bool balance, const GateArgs& a, cudaStream_t s);
+cudaError_t launch_balance_join(const BalanceJoinArgs& a, cudaStream_t s);
+// gates: of dgates; balance: of the loss
+cudaError_t launch_gate_grad(int dt, bool vec, bool gates, bool balance, const GateArgs& a, cudaStream_t s);
+
+// -------------------------------------------------------------- layer norm
+constexpr size_t kNormMaxCols = 16384;
+constexpr uint32_t kNormParts = 304;  // CTAs of the gradient, beside one a rank: parts of the sums over rows
+struct NormArgs {
+  const void* x[kMoeMaxRanks];
+  const void* extra[kMoeMaxRanks];  // residual, or dsum
+  const void* dy[kMoeMaxRanks];
+  const void* weight[kMoeMaxRanks];
+  const void* bias[kMoeMaxRanks];
+  void* out[kMoeMaxRanks];          // y, or dx
+  void* sum[kMoeMaxRanks];
+  float* mean[kMoeMaxRanks];
+  float* rstd[kMoeMaxRanks];
+  RankParts parts;
+  float* partial;                   // per part: cols sums for the weight, then cols for the bias
+  double eps;
+  uint32_t cols;
+  int p;
+};
+struct NormJoinArgs {
+  void* dweight[kMoeMaxRanks];
+  void* dbias[kMoeMaxRanks];
+  uint32_t first[kMoeMaxRanks + 1];
+  const float* partial;
+  uint32_t cols;
+  int p, bias, weight;
+};
+static_assert(sizeof(NormArgs) <= 32764, "norm parameters exceed 32,764 bytes");
+static_assert(sizeof(NormJoinArgs) <= 4096, "norm parameters exceed 4 KB");
+cudaError_t launch_norm(int dt, int weight_dt, bool vec, const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_grad(int dt, int weight_dt, bool vec, bool weights, const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_join(int dw_dt, const NormJoinArgs& a, cudaStream_t s);
+
 // ------------------------------------------------------------------ AdamW
 constexpr int kAdamwBlock = 128;           // elements that share a scale in an 8-bit state
 constexpr uint32_t kAdamwChunk = 4096;     // elements of a tensor per CTA

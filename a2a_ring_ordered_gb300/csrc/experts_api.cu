@@ -4,8 +4,7 @@
 #include <math.h>
 #include <string.h>
 
-#include <algorithm>
-
+#include "api_checks.h"
 #include "device_common.cuh"
 
 using namespace ccl;
@@ -13,87 +12,15 @@ using namespace ccl;
 namespace {
 
 constexpr size_t kMaxWidth = size_t{1} << 28;  // elements of a row
-
-#define EXPERTS_TRY(call)                    \
-  do {                                       \
-    const ccl_status_t st_ = (call);         \
-    if (st_ != CCL_OK) return st_;           \
-  } while (0)
-
-ccl_status_t bad(const char* what) { return report_error(CCL_ERR_INVALID_ARG, "%s", what); }
-
-// The byte ranges of a call: an output may overlap nothing.  Fixed storage,
-// so that no entry point can throw.
-class Spans {
- public:
-  void add(const void* p, uint64_t bytes, bool out) {
-    if (bytes == 0 || p == nullptr) return;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    s_[n_++] = {lo, lo + bytes, out};
-  }
-  bool clash() {
-    std::sort(s_, s_ + n_, [](const Span& a, const Span& b) { return a.lo < b.lo; });
-    uintptr_t any = 0, out = 0;  // furthest end so far, of all and of outputs
-    for (int i = 0; i < n_; ++i) {
-      if (s_[i].lo < out || (s_[i].out && s_[i].lo < any)) return true;
-      any = std::max(any, s_[i].hi);
-      if (s_[i].out) out = std::max(out, s_[i].hi);
-    }
-    return false;
-  }
-
- private:
-  struct Span {
-    uintptr_t lo, hi;
-    bool out;
-  };
-  Span s_[kMoeMaxRanks * 6];
-  int n_ = 0;
-};
-
-ccl_status_t check_buffer(const char* name, int r, const void* p, size_t align) {
-  if (p == nullptr) return report_error(CCL_ERR_INVALID_ARG, "%s[%d] is NULL", name, r);
-  if (reinterpret_cast<uintptr_t>(p) % align)
-    return report_error(CCL_ERR_INVALID_ARG, "%s[%d] is not %zu-byte aligned", name, r, align);
-  return CCL_OK;
-}
-
-ccl_status_t check_tokens(const size_t* tokens, int p, int k) {
-  if (p < 1 || p > kMoeMaxRanks) return report_error(CCL_ERR_INVALID_ARG, "p=%d outside 1..%d", p, kMoeMaxRanks);
-  if (k < 1 || k > kMoeMaxK) return report_error(CCL_ERR_INVALID_ARG, "k=%d outside 1..%d", k, kMoeMaxK);
-  if (tokens == nullptr) return bad("tokens is NULL");
-  for (int r = 0; r < p; ++r)
-    if (tokens[r] > 0x7FFFFFFFull / static_cast<size_t>(k))
-      return report_error(CCL_ERR_INVALID_ARG, "tokens[%d] * k must stay below 2^31", r);
-  return CCL_OK;
-}
+using Spans = SpansOf<kMoeMaxRanks * 6>;
 
 ccl_status_t check_rows(const size_t* tokens, int p, int k, size_t hidden, ccl_dtype_t dt) {
   EXPERTS_TRY(check_tokens(tokens, p, k));
   if (hidden == 0 || hidden > kMaxWidth) return report_error(CCL_ERR_INVALID_ARG, "hidden=%zu outside 1..2^28", hidden);
-  if (dt != CCL_F32 && dt != CCL_BF16)
-    return dt == CCL_I32 ? report_error(CCL_ERR_UNSUPPORTED, "rows are fp32 or bf16")
-                         : report_error(CCL_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dt));
-  return CCL_OK;
+  return check_float_dtype(dt, "rows");
 }
 
 uint32_t capacity(size_t rows) { return static_cast<uint32_t>(std::min<size_t>(rows, 0x7FFFFFFFu)); }
-
-bool any_tokens(const size_t* tokens, int p) {
-  for (int r = 0; r < p; ++r)
-    if (tokens[r] != 0) return true;
-  return false;
-}
-
-// Whether all rows start on 16 bytes; `bits`: addresses and row bytes or-ed together.
-bool on_grid(uintptr_t bits) { return (bits & 15) == 0; }
-
-ccl_status_t launched(cudaError_t err, const char* what) {
-  if (err == cudaSuccess) return CCL_OK;
-  return report_error(CCL_ERR_CUDA, "%s launch: %s (%s)", what, cudaGetErrorString(err), cudaGetErrorName(err));
-}
-
-cudaStream_t on(void* stream) { return static_cast<cudaStream_t>(stream); }
 
 }  // namespace
 

@@ -474,6 +474,110 @@ ccl_status_t ccl_moe_product_grad_weight(const void* const* dy, const void* cons
                                          int num_experts, size_t n, size_t contract, ccl_dtype_t dw_dt,
                                          void* const* dw, void* stream);
 
+/* ------------------------------------------------ MoE: the router's choice
+ * logits[r] is tokens[r] x num_experts of dt (bf16 or fp32), row-major and
+ * contiguous.  p <= 64, 1 <= k <= min(16, num_experts), num_experts <= 1024,
+ * tokens[r] * k < 2^31.  With the score
+ *   u(l) = exp(l) (CCL_SCORE_SOFTMAX)   or   1 / (1 + exp(-l)) (CCL_SCORE_SIGMOID)
+ * and the shares p_e = u(l_e) / sum_i u(l_i) of a token:
+ *
+ * ccl_moe_gate: ids[r] (tokens[r] x k int32) are the experts of the k largest
+ *   logits, largest first, equal ones by the lower index (-0 equals 0, a NaN
+ *   comes before all numbers); -1 where fewer than k logits are above -inf.
+ *   gates[r] (fp32, likewise) are
+ *     scale * u(l_e) / sum over the chosen of u     with `normalize`,
+ *     scale * p_e (softmax), scale * u(l_e) (sigmoid)  without;
+ *   0 beside an id of -1.  A row of -inf alone (padding) chooses nothing.
+ *   ids and gates are what ccl_moe_sort and ccl_moe_from_experts take.
+ * ccl_moe_balance: the balance loss of ids that are given (any, ids outside
+ *   [0, num_experts) count nowhere).  counts[r] (num_experts + 1 int32): the
+ *   (token, choice) pairs of each expert, then T, the tokens that have a logit
+ *   above -inf.  losses[r] (one fp32):
+ *     L = num_experts / (k * T^2) * sum_e counts_e * sum_t p_te
+ *   (1 where all experts get alike; 0 where T is 0).  `together`: the ranks'
+ *   tokens are one batch, counts and loss are over all of them and every rank
+ *   gets the same (as an all-reduce would give them).
+ *   ccl_moe_gate makes both in its own pass where counts and losses are given
+ *   (both NULL: neither is made).
+ * ccl_moe_gate_grad: dlogits[r] (of dt, rounded once) = the gradient of
+ *   sum dgates * gates, for the ids that are given (outside [0, num_experts):
+ *   nothing; an expert that a token has twice counts twice) plus, where counts
+ *   is given, that of balance_scale * dlosses[r] * L, counts held constant (L is
+ *   linear in the shares, as its definition has it; dlosses NULL: ones).  With
+ *   `together` counts each rank gets its own tokens' part of the one loss.
+ * ccl_moe_balance_grad: dlogits[r] = the gradient of scale * dlosses[r] * L alone.
+ *
+ * A masked logit (-inf) gets gradient 0.  Scores, sums and gradients are fp32;
+ * column sums over tokens are added in a fixed order, joined in 64 bits.
+ * workspace (device, 16-byte aligned, ccl_moe_balance_workspace_bytes) is
+ * scratch of one call at a time; it may hold anything.  No output may overlap
+ * an input or another output of its rank. */
+typedef enum { CCL_SCORE_SOFTMAX = 0, CCL_SCORE_SIGMOID = 1 } ccl_score_t;
+
+/* Bytes of workspace that ccl_moe_balance, and ccl_moe_gate with counts, take
+ * on any number of tokens; 0 for invalid arguments. */
+size_t ccl_moe_balance_workspace_bytes(int p, int num_experts);
+
+ccl_status_t ccl_moe_gate(const void* const* logits, const size_t* tokens, int p, int k, int num_experts,
+                          ccl_dtype_t dt, ccl_score_t score, int normalize, float scale, int32_t* const* ids,
+                          float* const* gates, int together, int32_t* const* counts, float* const* losses,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+ccl_status_t ccl_moe_gate_grad(const void* const* logits, const int32_t* const* ids, const float* const* dgates,
+                               const size_t* tokens, int p, int k, int num_experts, ccl_dtype_t dt,
+                               ccl_score_t score, int normalize, float scale, const int32_t* const* counts,
+                               const float* const* dlosses, float balance_scale, void* const* dlogits,
+                               void* stream);
+
+ccl_status_t ccl_moe_balance(const void* const* logits, const int32_t* const* ids, const size_t* tokens, int p,
+                             int k, int num_experts, ccl_dtype_t dt, ccl_score_t score, int together,
+                             int32_t* const* counts, float* const* losses, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+ccl_status_t ccl_moe_balance_grad(const void* const* logits, const int32_t* const* counts,
+                                  const float* const* dlosses, const size_t* tokens, int p, int k,
+                                  int num_experts, ccl_dtype_t dt, ccl_score_t score, float scale,
+                                  void* const* dlogits, void* stream);
+
+/* -------------------------------------------------------------- layer norm
+ * Rows of `cols` elements of dt (bf16 or fp32), row-major and contiguous, at
+ * any alignment; 1 <= cols <= 16384; p <= 64; rows[r] < 2^31; weight[r] and
+ * bias[r] hold cols elements of weight_dt (bf16 or fp32; the ranks may share
+ * them), bias may be NULL.
+ *
+ * ccl_layer_norm: with v = x[r], or x[r] + residual[r] rounded once to dt,
+ *   mean = sum(v) / cols,  rstd = (sum((v - mean)^2) / cols + eps)^-1/2,
+ *   y[r] = (v - mean) * rstd * weight + bias, in fp32, rounded once.
+ *   sum[r] receives v where residual is given (needed then, else NULL); mean[r]
+ *   and rstd[r] (fp32, one per row) may be NULL together.
+ * ccl_layer_norm_grad: with x what was normed (sum[r] where there was a
+ *   residual), g = dy * weight, z = (x - mean) * rstd:
+ *   dx[r] = rstd * (g - sum(g) / cols - z * sum(g * z) / cols) + dsum[r]
+ *     (dsum: the gradient that reaches the sum past the norm; may be NULL),
+ *     which is the gradient for x and for residual alike;
+ *   dweight[r] = sum over the rank's rows of dy * z, dbias[r] of dy, in dw_dt
+ *     (CCL_F32, as gradient buckets hold them, or CCL_BF16); either may be
+ *     NULL; zeros for a rank without rows.  Each rank's are its own, also where
+ *     the ranks share a weight.
+ *   Sums over rows are fp32 and made in an order that the sizes fix.
+ *   workspace (device, 16-byte aligned, ccl_layer_norm_grad_workspace_bytes; not
+ *   needed where dweight and dbias are NULL) is scratch of one call at a time;
+ *   it may hold anything.
+ * No output may overlap an input or another output. */
+ccl_status_t ccl_layer_norm(const void* const* x, const void* const* residual, const void* const* weight,
+                            const void* const* bias, const size_t* rows, int p, size_t cols, double eps,
+                            ccl_dtype_t dt, ccl_dtype_t weight_dt, void* const* y, void* const* sum,
+                            float* const* mean, float* const* rstd, void* stream);
+
+/* Bytes of workspace on any number of rows; 0 for invalid arguments. */
+size_t ccl_layer_norm_grad_workspace_bytes(int p, size_t cols);
+
+ccl_status_t ccl_layer_norm_grad(const void* const* dy, const void* const* dsum, const void* const* x,
+                                 const void* const* weight, const float* const* mean, const float* const* rstd,
+                                 const size_t* rows, int p, size_t cols, ccl_dtype_t dt, ccl_dtype_t weight_dt,
+                                 void* const* dx, ccl_dtype_t dw_dt, void* const* dweight, void* const* dbias,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------ AdamW
  * One AdamW step over many tensors, behind the gradient buckets
  * (ccl_bucket_allreduce_scale_cast's bf16 averages are its gradients).  For
