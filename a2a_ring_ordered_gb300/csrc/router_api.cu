@@ -410,7 +410,7 @@ extern "C" ccl_status_t ccl_layer_norm_grad(const void* const* dy, const void* c
   a.cols = static_cast<uint32_t>(cols);
   a.p = p;
   cut_rows(&a.parts, rows, p, kNormParts, 1, false);
-  if (any) EXPERTS_TRY(launched(launch_norm_grad(dt, weight_dt, on_grid(bits), weights, a, on(stream)), "layer norm gradient kernel"));
+  if (any) EXPERTS_TRY(launched(launch_norm_grad(dt, weight_dt, on_grid(bits), &a, on(stream)), "layer norm gradient kernel"));
   if (!weights) return CCL_OK;
   memcpy(j.first, a.parts.first, sizeof(j.first));
   j.partial = a.partial;
