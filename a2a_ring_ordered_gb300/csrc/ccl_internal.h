@@ -287,7 +287,7 @@ struct RankParts {
 void cut_rows(RankParts* parts, const size_t* rows, int p, uint32_t most, uint32_t least, bool all);
 
 // ------------------------------------------------- MoE: the router's choice
-constexpr uint32_t kBalanceParts = 608;  // CTAs that a call with the balance loss has, beside one a rank
+constexpr uint32_t kBalanceParts = 304;  // CTAs that a call with the balance loss has, beside one a rank
 struct GateArgs {
   const void* logits[kMoeMaxRanks];
   const int32_t* ids_in[kMoeMaxRanks];  // the gradient, and a loss of given ids
@@ -301,6 +301,7 @@ struct GateArgs {
   float* partial;                       // per part: num_experts sums of shares, then num_experts + 1 counts (int32)
   float scale, balance_scale;
   int p, k, num_experts, score, normalize;
+  int vec;                              // rows start on 16 bytes
 };
 struct BalanceJoinArgs {
   int32_t* counts[kMoeMaxRanks];
@@ -313,11 +314,13 @@ static_assert(sizeof(GateArgs) <= 32764, "router parameters exceed 32,764 bytes"
 static_assert(sizeof(BalanceJoinArgs) <= 4096, "balance parameters exceed 4 KB");
 // Words of a part in the workspace.
 __host__ __device__ constexpr size_t balance_part_words(int num_experts) { return 2 * static_cast<size_t>(num_experts) + 1; }
-// select: ids and gates; balance: partial sums for launch_balance_join.  `vec`: rows start on 16 bytes.
-cudaError_t launch_gate(int dt, bool vec, bool select, bool balance, const GateArgs& a, cudaStream_t s);
+// The launchers cut the rows (of which a->parts holds the numbers) into the parts
+// that they leave there.  select: ids and gates; balance: the partial sums for
+// launch_balance_join, of ids_in where nothing is selected.
+cudaError_t launch_gate(int dt, bool select, bool balance, GateArgs* a, cudaStream_t s);
 cudaError_t launch_balance_join(const BalanceJoinArgs& a, cudaStream_t s);
 // gates: of dgates; balance: of the loss
-cudaError_t launch_gate_grad(int dt, bool vec, bool gates, bool balance, const GateArgs& a, cudaStream_t s);
+cudaError_t launch_gate_grad(int dt, bool gates, bool balance, GateArgs* a, cudaStream_t s);
 
 // -------------------------------------------------------------- layer norm
 constexpr size_t kNormMaxCols = 16384;

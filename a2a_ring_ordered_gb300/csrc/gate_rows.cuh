@@ -1,0 +1,174 @@
+// gate_rows.cuh -- a token's logits in the registers of a few lanes, shared by
+// the router's kernels.
+//
+// L lanes (a power of two) have a row, NV columns each: eight consecutive ones at
+// lane * 8, and where a row has more than 256 columns again at 256, 512, ... of
+// them.  So a lane's columns come by 16-byte loads, and of equal logits the
+// lowest lane has the lowest column.  Columns behind the row are -inf.
+#pragma once
+
+#include "row_parts.cuh"
+
+namespace ccl {
+
+constexpr unsigned kAllLanes = 0xFFFFFFFFu;
+
+template <int L>
+__device__ __forceinline__ int gate_column(int lane, int i) {
+  return (i / 8) * (8 * L) + lane * 8 + i % 8;
+}
+
+template <int DT, int NV>
+struct GateRow {
+  static constexpr int kWords = NV * Elem<DT>::kBytes / 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ float value(int i) const { return widen<DT>(w, i); }
+
+  // `there`: the row exists; `vec`: rows start on 16 bytes.
+  template <int L>
+  __device__ __forceinline__ void load(const void* logits, uint64_t row, int experts, int lane, bool there, bool vec) {
+    constexpr uint32_t kNone = DT == kF32 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+    constexpr int kPer = 16 / Elem<DT>::kBytes;
+    const char* base = static_cast<const char*>(logits) + row * experts * Elem<DT>::kBytes;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = kNone;
+    if (!there) return;
+    if (vec) {
+#pragma unroll
+      for (int q = 0; q < NV / kPer; ++q) {
+        const int c = gate_column<L>(lane, q * kPer);
+        if (c >= experts) continue;
+        const uint4 v = ld_l1_16(base + c * Elem<DT>::kBytes);
+        w[4 * q] = v.x;
+        w[4 * q + 1] = v.y;
+        w[4 * q + 2] = v.z;
+        w[4 * q + 3] = v.w;
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = gate_column<L>(lane, i);
+      if (c >= experts) continue;
+      if constexpr (DT == kF32) {
+        w[i] = __ldg(reinterpret_cast<const uint32_t*>(base) + c);
+      } else {
+        const uint32_t h = __ldg(reinterpret_cast<const unsigned short*>(base) + c);
+        w[i / 2] = (i & 1) ? (w[i / 2] & 0xFFFFu) | h << 16 : (w[i / 2] & 0xFFFF0000u) | h;
+      }
+    }
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ float gate_logit(const void* logits, uint64_t row, int experts, int e) {
+  const uint64_t at = row * experts + e;
+  if constexpr (DT == kF32) return __ldg(static_cast<const float*>(logits) + at);
+  else return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const unsigned short*>(logits) + at)) << 16);
+}
+
+// ------------------------------------------------------------ among L lanes
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAllLanes, v, o);
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAllLanes, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (L == 32) return __reduce_max_sync(kAllLanes, v);
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAllLanes, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
+  if constexpr (L == 32) return __reduce_min_sync(kAllLanes, v);
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(kAllLanes, v, o));
+  return v;
+}
+
+// ------------------------------------------------------------------- scores
+// exp(x), x <= 0: the hardware's power of two of the rounded x log2(e): off by
+// |x| 2^-24 from the product's rounding and two units more, which gates and
+// shares, of fp32, carry on.
+__device__ __forceinline__ float exp_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float reciprocal_of(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Scores are kept over exp(base), base max(row) for softmax and min(max(row), 0)
+// for sigmoid, so that the row's largest stays away from 0; 0 for a row of -inf.
+__device__ __forceinline__ float base_of(float top, bool sigmoid) {
+  if (top == -INFINITY) return 0.f;
+  return sigmoid ? fminf(top, 0.f) : top;
+}
+__device__ __forceinline__ float score_of(float l, float base, bool sigmoid) {
+  if (!sigmoid) return exp_of(l - base);
+  const float t = exp_of(-fabsf(l));
+  // base is 0 for nearly every row
+  const float up = base == 0.f ? (l >= 0.f ? 1.f : t) : exp_of(fminf(l, 0.f) - base);
+  return up * reciprocal_of(1.f + t);
+}
+// 1 - sigmoid(l)
+__device__ __forceinline__ float away_of(float l) {
+  const float t = exp_of(-fabsf(l));
+  return (l > 0.f ? t : 1.f) * reciprocal_of(1.f + t);
+}
+
+// Lanes of a row that can hold the choices and, eight columns each, the row.
+inline int gate_lanes(int experts, int k) {
+  int lanes = 1;
+  while (lanes < 32 && (lanes * 8 < experts || lanes < k)) lanes *= 2;
+  return lanes;
+}
+
+// Calls f(DT, L, NV).
+template <typename F>
+cudaError_t by_row(int dt, int experts, int k, F f) {
+  const auto with = [&](auto d) {
+    constexpr std::integral_constant<int, 8> eight{};
+    if (experts > 512) return f(d, std::integral_constant<int, 32>{}, std::integral_constant<int, 32>{});
+    if (experts > 256) return f(d, std::integral_constant<int, 32>{}, std::integral_constant<int, 16>{});
+    switch (gate_lanes(experts, k)) {
+      case 1: return f(d, std::integral_constant<int, 1>{}, eight);
+      case 2: return f(d, std::integral_constant<int, 2>{}, eight);
+      case 4: return f(d, std::integral_constant<int, 4>{}, eight);
+      case 8: return f(d, std::integral_constant<int, 8>{}, eight);
+      case 16: return f(d, std::integral_constant<int, 16>{}, eight);
+      default: return f(d, std::integral_constant<int, 32>{}, eight);
+    }
+  };
+  return dt == kF32 ? with(std::integral_constant<int, kF32>{}) : with(std::integral_constant<int, kBF16>{});
+}
+
+inline cudaError_t launch_gate_parts(void (*kernel)(GateArgs), const GateArgs& a, int threads, size_t smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.parts.first[a.p]);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = CCL_PDL ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (err == cudaSuccess) note_launch();
+  return err;
+}
+
+}  // namespace ccl

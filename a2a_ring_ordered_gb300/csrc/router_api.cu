@@ -33,6 +33,10 @@ void cut_rows(RankParts* parts, const size_t* rows, int p, uint32_t most, uint32
 
 namespace {
 
+void take_rows(RankParts* parts, const size_t* rows, int p) {
+  for (int r = 0; r < p; ++r) parts->rows[r] = static_cast<uint32_t>(rows[r]);
+}
+
 // ------------------------------------------------------------------ router
 using GateSpans = SpansOf<kMoeMaxRanks * 7 + 1>;
 
@@ -136,8 +140,9 @@ extern "C" ccl_status_t ccl_moe_gate(const void* const* logits, const size_t* to
   a.num_experts = num_experts;
   a.score = score;
   a.normalize = normalize != 0;
-  cut_rows(&a.parts, tokens, p, kBalanceParts, 8, balance);
-  EXPERTS_TRY(launched(launch_gate(dt, on_grid(bits), true, balance, a, on(stream)), "MoE gate kernel"));
+  take_rows(&a.parts, tokens, p);
+  a.vec = on_grid(bits);
+  EXPERTS_TRY(launched(launch_gate(dt, true, balance, &a, on(stream)), "MoE gate kernel"));
   return balance ? run_balance(a, &j, stream) : CCL_OK;
 }
 
@@ -170,8 +175,9 @@ extern "C" ccl_status_t ccl_moe_balance(const void* const* logits, const int32_t
   a.k = k;
   a.num_experts = num_experts;
   a.score = score;
-  cut_rows(&a.parts, tokens, p, kBalanceParts, 8, true);
-  EXPERTS_TRY(launched(launch_gate(dt, on_grid(bits), false, true, a, on(stream)), "MoE balance kernel"));
+  take_rows(&a.parts, tokens, p);
+  a.vec = on_grid(bits);
+  EXPERTS_TRY(launched(launch_gate(dt, false, true, &a, on(stream)), "MoE balance kernel"));
   return run_balance(a, &j, stream);
 }
 
@@ -228,8 +234,9 @@ ccl_status_t router_grad(const void* const* logits, const int32_t* const* ids, c
   a.num_experts = num_experts;
   a.score = score;
   a.normalize = normalize != 0;
-  cut_rows(&a.parts, tokens, p, kBalanceParts, 8, false);
-  return launched(launch_gate_grad(dt, on_grid(bits), gates, balance, a, on(stream)), what);
+  take_rows(&a.parts, tokens, p);
+  a.vec = on_grid(bits);
+  return launched(launch_gate_grad(dt, gates, balance, &a, on(stream)), what);
 }
 
 }  // namespace
@@ -329,7 +336,7 @@ extern "C" ccl_status_t ccl_layer_norm(const void* const* x, const void* const* 
   a.eps = eps;
   a.cols = static_cast<uint32_t>(cols);
   a.p = p;
-  cut_rows(&a.parts, rows, p, kNormParts, 1, false);
+  take_rows(&a.parts, rows, p);
   return launched(launch_norm(dt, weight_dt, on_grid(bits), a, on(stream)), "layer norm kernel");
 }
 
@@ -409,7 +416,7 @@ extern "C" ccl_status_t ccl_layer_norm_grad(const void* const* dy, const void* c
   a.partial = static_cast<float*>(workspace);
   a.cols = static_cast<uint32_t>(cols);
   a.p = p;
-  cut_rows(&a.parts, rows, p, kNormParts, 1, false);
+  take_rows(&a.parts, rows, p);
   if (any) EXPERTS_TRY(launched(launch_norm_grad(dt, weight_dt, on_grid(bits), &a, on(stream)), "layer norm gradient kernel"));
   if (!weights) return CCL_OK;
   memcpy(j.first, a.parts.first, sizeof(j.first));

@@ -177,6 +177,34 @@ def test_gradients(tokens, experts, k, dtype, score):
             assert (np.abs(got - want) <= 2 * share_tolerance(v) * size + step * np.abs(want) + 1e-38).all()
 
 
+@pytest.mark.parametrize("experts,k", [(8, 3), (60, 6), (256, 8), (256, 16), (300, 8), (1024, 16)])
+def test_choice_by_the_last_bit(experts, k):
+    """fp32 logits that differ in their last bits alone, around 0 too."""
+    c = ccl()
+    rng = np.random.default_rng(experts + k)
+    v = (1.0 + rng.integers(-300, 300, size=(90, experts)) * 2.0 ** -23).astype(np.float32)
+    v[30:60] = (rng.integers(-5, 5, size=(30, experts)) * 2.0 ** -149).astype(np.float32)
+    v[60:, ::2] *= -1
+    ids, gates = [torch.empty(90, k, dtype=torch.int32, device="cuda")], [torch.empty(90, k, device="cuda")]
+    c.ccl_moe_gate([torch.from_numpy(v).cuda()], ids, gates)
+    np.testing.assert_array_equal(ids[0].cpu().numpy(), router.choose(v, k))
+
+
+def test_gates_of_chosen_experts_far_below_the_row():
+    """Given ids whose logits are far below the row's largest still share their gates."""
+    c = ccl()
+    l = torch.zeros(5, 16, device="cuda")
+    l[:, 0] = 300.0
+    ids, d = [torch.tensor([[1, 2]] * 5, dtype=torch.int32, device="cuda")], [torch.tensor([[1.0, -1.0]] * 5, device="cuda")]
+    for score in ("softmax", "sigmoid"):
+        out = [torch.empty_like(l)]
+        c.ccl_moe_gate_grad([l], ids, d, out, score=score)
+        want = router.gate_grad(l.double().cpu().numpy(), ids[0].cpu().numpy(), d[0].cpu().numpy(), score, True, 1.0)
+        if score == "softmax":  # the 64-bit definition keeps the row's largest: exp(-300) is a number there
+            assert want[0, 1] == 0.5
+        np.testing.assert_allclose(out[0].cpu().numpy(), want, rtol=64 * ONE, atol=0)
+
+
 def test_without_dlosses_they_are_ones():
     c = ccl()
     l = [torch.randn(50, 16, device="cuda")]
