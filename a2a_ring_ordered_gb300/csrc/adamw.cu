@@ -22,6 +22,7 @@
 #include <atomic>
 
 #include "device_common.cuh"
+#include "pairs.cuh"
 
 namespace ccl {
 namespace {
@@ -126,34 +127,8 @@ __device__ __forceinline__ void store_codes(void* base, uint64_t i0, int lane, i
   }
 }
 
-// ------------------------------------------------------- pairs of fp32 numbers
-// One instruction, two operations, each rounded to nearest as the single ones
-// are.
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 pair(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ F2 both(float a) { return pair(a, a); }
+using ccl::both;  // beside the one below
 __device__ __forceinline__ F2 both(const AdamwPair& c) { return F2{c.v}; }
-__device__ __forceinline__ float2 parts(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
 // a + b, where a is a product that was rounded by itself.  `one` is 1, but the
 // assembler must not know: it joined paired products with paired sums behind
 // them, for all that both name their rounding, and the product's was lost.

@@ -8,6 +8,8 @@
 // Rows move once in each direction, so HBM bounds all of it.  A group of one or
 // more warps has a row; a thread has the same columns of every row that its
 // group takes, so that the sums over rows stay in its registers.
+#include "pairs.cuh"
+#include "realign.cuh"
 #include "row_parts.cuh"
 
 namespace ccl {
@@ -15,42 +17,93 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
-// N consecutive elements at `base` + i as floats: by one load where they are 16
-// bytes, by 16-byte loads where they are more.
-template <int DT, int N>
-__device__ __forceinline__ void widen_raw(const uint32_t* w, float* f) {
+// ------------------------------------------------------------------- units
+// A row goes in units of 16 bytes from its start, thread t of a group having units
+// t, t + threads, ...: the same columns in every row.  GRID: all rows start on 16
+// bytes and are whole units.  Off the grid a unit is cut out of the two aligned
+// granules that hold it, the last unit may be part of one, and aligned granules
+// are put together from neighbouring lanes' units for the stores.
+template <int DT, bool GRID>
+struct Units {
+  static constexpr int kBytes = Elem<DT>::kBytes, kPer = 16 / kBytes;
+  uint32_t row_bytes, count;
+  __device__ __forceinline__ explicit Units(uint32_t cols) : row_bytes(cols * kBytes), count((row_bytes + 15) / 16) {}
+  // The unit's bytes that are the row's.
+  __device__ __forceinline__ uint32_t bytes(uint32_t u) const {
+    if (GRID) return u < count ? 16 : 0;
+    return u < count ? min(16u, row_bytes - 16 * u) : 0;
+  }
+  // The unit, zeros where it is not the row's.
+  __device__ __forceinline__ uint4 load(const char* row, uint32_t u) const {
+    if constexpr (GRID) return u < count ? ld_once16(row + 16 * u) : make_uint4(0, 0, 0, 0);
+    const uint32_t n = bytes(u);
+    const uint4 v = load16_part(row + 16 * u, 0, n);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int e = 0; e < N; ++e) f[e] = widen<DT>(w, e);
-}
-
-// The weights of N columns.  They are read again for every row and stay in L1.
-// `grid`: on 16 bytes, as N columns' bytes are.
-template <int WT, int N>
-__device__ __forceinline__ void load_weights(const void* base, uint32_t c, bool grid, float* f) {
-  constexpr int B = Elem<WT>::kBytes;
-  const char* p = static_cast<const char*>(base) + static_cast<size_t>(c) * B;
-  if (N * B >= 16 && grid) {
-    uint32_t w[N * B >= 16 ? N * B / 4 : 4];
-#pragma unroll
-    for (int k = 0; k < N * B / 16; ++k) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[k];
-      w[4 * k] = v.x;
-      w[4 * k + 1] = v.y;
-      w[4 * k + 2] = v.z;
-      w[4 * k + 3] = v.w;
+    for (uint32_t k = 0; k < 4; ++k) w[k] = n >= 4 * k + 4 ? w[k] : n == 4 * k + 2 ? w[k] & 0xFFFFu : 0;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // All lanes of a warp together.
+  __device__ __forceinline__ void store(char* row, uint32_t u, const uint32_t* w) const {
+    const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+    const uint32_t n = bytes(u), phase = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15;
+    char* to = row + 16 * u;
+    if constexpr (GRID) {
+      if (n) st_stream16(to, v);
+      return;
     }
-    widen_raw<WT, N>(w, f);
-  } else if (N * B == 8 && grid) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    const uint32_t w[2] = {v.x, v.y};
-    widen_raw<WT, N>(w, f);
-  } else {
+    // `first` bytes of the unit lie in its first granule; the second one takes the rest and the next lane's first
+    const int lane = threadIdx.x & 31;
+    const uint32_t first = 16 - phase;
+    const uint4 next = next_lane(v, make_uint4(0, 0, 0, 0), lane);
+    const uint32_t next_n = __shfl_down_sync(kAll, n, 1);
+    const bool whole = n == 16 && (phase == 0 || (lane < 31 && next_n >= first));
+    if (whole) st_stream16(phase == 0 ? to : to + first, phase == 0 ? v : shift16(v, next, first));
+    // what no lane's granule holds
+    const bool head = phase != 0 && (lane == 0 || n < first);
+    if (!head && whole) return;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      if constexpr (WT == kF32) f[e] = reinterpret_cast<const float*>(p)[e];
-      else f[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[e]);
+    for (uint32_t e = 0; e < kPer; ++e) {
+      const uint32_t at = e * kBytes;
+      if (at < n && (phase != 0 && at < first ? head : !whole)) store_one<DT>(to, e, w, e);
     }
   }
+};
+
+// The weights of the N columns from c on, zeros from cols on; they are read again
+// for every row and stay in L1.  `grid`: their columns start on 16 bytes.
+template <int WT, int N>
+__device__ __forceinline__ void load_weights(const void* base, uint32_t c, uint32_t cols, bool grid, F2* f) {
+  constexpr int B = Elem<WT>::kBytes, kWords = N * B / 4;
+  const char* p = static_cast<const char*>(base) + static_cast<size_t>(c) * B;
+  uint32_t w[kWords];
+  if (grid && c + N <= cols) {
+    if constexpr (kWords >= 4) {
+#pragma unroll
+      for (int k = 0; k < kWords / 4; ++k) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[k];
+        w[4 * k] = v.x;
+        w[4 * k + 1] = v.y;
+        w[4 * k + 2] = v.z;
+        w[4 * k + 3] = v.w;
+      }
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (c + e >= cols) continue;
+      if constexpr (WT == kF32) w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+      else w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(p)[e]) << (16 * (e & 1));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) f[i] = widen2<WT>(w, i);
 }
 
 // ------------------------------------------------------------ groups of warps
@@ -97,82 +150,99 @@ struct Group {
 
 // -------------------------------------------------------------------- forward
 // The row stays in registers between its three walks (mean, variance, output).
-// VEC elements are 16 bytes on the grid, one element off it; a thread has U
-// such units.
-template <int DT, int WT, int VEC, int U, bool SUM>
-__global__ void __launch_bounds__(512) norm_kernel(const __grid_constant__ NormArgs a, int group_threads, uint32_t weights_on_grid) {
-  constexpr int WORDS = VEC * Elem<DT>::kBytes >= 4 ? VEC * Elem<DT>::kBytes / 4 : 1;
+template <int DT, int WT, int U, bool SUM, bool GRID>
+__global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const __grid_constant__ NormArgs a, int group_threads, uint32_t weights_on_grid) {
+  constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2;
   __shared__ float4 slots[2 * kMostWarps];
   pdl_enter();
   Group group(slots, group_threads);
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
   const int r = part.r, groups = blockDim.x / group_threads, t = threadIdx.x - group.id * group_threads;
-  const uint32_t cols = a.cols, units = cols / VEC;
+  const uint32_t cols = a.cols;
+  const Units<DT, GRID> units(cols);
   const float n = static_cast<float>(cols), eps = static_cast<float>(a.eps);
+  const char *x = static_cast<const char*>(a.x[r]), *extra = static_cast<const char*>(a.extra[r]);
   for (uint32_t row = part.lo + group.id; row < part.hi; row += groups) {
-    const uint64_t at = static_cast<uint64_t>(row) * cols;
-    uint32_t w[U][WORDS];
+    const uint64_t at = static_cast<uint64_t>(row) * units.row_bytes;
+    F2 f[U][P];
+    {
+      uint4 v[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const uint32_t u = t + i * group_threads;
+      for (int i = 0; i < U; ++i) v[i] = units.load(x + at, t + i * group_threads);
+      if constexpr (SUM) {
+        uint4 q[U];
 #pragma unroll
-      for (int k = 0; k < WORDS; ++k) w[i][k] = 0;
-      if (u < units) load_raw<DT, VEC>(a.x[r], at + u * VEC, w[i]);
-    }
-    if constexpr (SUM) {
-      uint32_t q[U][WORDS];
+        for (int i = 0; i < U; ++i) q[i] = units.load(extra + at, t + i * group_threads);
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const uint32_t u = t + i * group_threads;
+        for (int i = 0; i < U; ++i) {
+          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, o[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+          if constexpr (DT == kBF16) {
 #pragma unroll
-        for (int k = 0; k < WORDS; ++k) q[i][k] = 0;
-        if (u < units) load_raw<DT, VEC>(a.extra[r], at + u * VEC, q[i]);
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 h = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&w[k]), *reinterpret_cast<__nv_bfloat162*>(&o[k]));
+              w[k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) + __uint_as_float(o[k]));
+          }
+          units.store(static_cast<char*>(a.sum[r]) + at, t + i * group_threads, w);
+          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const uint32_t u = t + i * group_threads;
-        float f[VEC];
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) f[e] = widen<DT>(w[i], e) + widen<DT>(q[i], e);
-        pack_out<DT, VEC>(f, w[i]);
-        if (u < units) store_raw<DT, VEC>(a.sum[r], at + u * VEC, w[i]);
+        for (int k = 0; k < P; ++k) f[i][k] = widen2<DT>(w, k);
       }
     }
-    float total[1] = {0.f};
+    F2 sum = both(0.f);
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) total[0] += widen<DT>(w[i], e);
+      for (int k = 0; k < P; ++k) sum = add2(sum, f[i][k]);
+    float total[1] = {total2(sum)};
     group.sum<1>(total);
     const float mean = total[0] / n;
-    float square[1] = {0.f};
+    const F2 less = both(-mean);
+    sum = both(0.f);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const uint32_t u = t + i * group_threads;
-      if (u >= units) continue;
+      const uint32_t left = units.bytes(t + i * group_threads) / Elem<DT>::kBytes;  // elements of the unit
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = widen<DT>(w[i], e) - mean;
-        square[0] = fmaf(d, d, square[0]);
+      for (int k = 0; k < P; ++k) {
+        f[i][k] = add2(f[i][k], less);
+        if (GRID) {
+          if (left == 0) f[i][k] = both(0.f);
+        } else {
+          const float2 d = parts(f[i][k]);
+          f[i][k] = pair(left > 2 * k ? d.x : 0.f, left > 2 * k + 1 ? d.y : 0.f);
+        }
+        sum = fma2(f[i][k], f[i][k], sum);
       }
     }
+    float square[1] = {total2(sum)};
     group.sum<1>(square);
     const float rstd = 1.f / sqrtf(square[0] / n + eps);
+    const F2 scale = both(rstd);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t u = t + i * group_threads;
-      if (u >= units) continue;
-      float scale[VEC], shift[VEC], f[VEC];
-      load_weights<WT, VEC>(a.weight[r], u * VEC, weights_on_grid, scale);
-      if (a.bias[r] != nullptr) load_weights<WT, VEC>(a.bias[r], u * VEC, weights_on_grid, shift);
+      if (GRID && u >= units.count) break;
+      F2 w[P], b[P];
+      load_weights<WT, VEC>(a.weight[r], u * VEC, cols, weights_on_grid, w);
+      if (a.bias[r] != nullptr) {
+        load_weights<WT, VEC>(a.bias[r], u * VEC, cols, weights_on_grid, b);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (a.bias[r] == nullptr) shift[e] = 0.f;
-        f[e] = fmaf((widen<DT>(w[i], e) - mean) * rstd, scale[e], shift[e]);
+        for (int k = 0; k < P; ++k) f[i][k] = fma2(mul2(f[i][k], scale), w[k], b[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < P; ++k) f[i][k] = mul2(mul2(f[i][k], scale), w[k]);
       }
-      uint32_t o[WORDS];
-      pack_out<DT, VEC>(f, o);
-      store_raw<DT, VEC>(a.out[r], at + u * VEC, o);
+      uint32_t o[4];
+      pack2<DT, P>(f[i], o);
+      units.store(static_cast<char*>(a.out[r]) + at, u, o);
     }
     if (t == 0 && a.mean[r] != nullptr) {
       a.mean[r][row] = mean;
@@ -182,10 +252,38 @@ __global__ void __launch_bounds__(512) norm_kernel(const __grid_constant__ NormA
 }
 
 // ------------------------------------------------------------------- backward
+// What a unit of x and dy adds to a row's two sums and to the sums over rows.
+template <int DT, int P>
+__device__ __forceinline__ void add_unit(const uint4& xv, const uint4& dv, const F2* weight, F2 rstd, F2 shift, F2& sg, F2& sgz, F2* dw, F2* db) {
+  const uint32_t x[4] = {xv.x, xv.y, xv.z, xv.w}, dy[4] = {dv.x, dv.y, dv.z, dv.w};
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    const F2 z = fma2(widen2<DT>(x, k), rstd, shift), d = widen2<DT>(dy, k), g = mul2(d, weight[k]);
+    sg = add2(sg, g);
+    sgz = fma2(g, z, sgz);
+    dw[k] = fma2(d, z, dw[k]);
+    db[k] = add2(db[k], d);
+  }
+}
+// dx of a unit; means: -mean(g) and -mean(g z).
+template <int DT, int P, bool EXTRA>
+__device__ __forceinline__ void grad_unit(const uint4& xv, const uint4& dv, const uint4& ev, const F2* weight, F2 rstd, F2 shift, F2 mean_g, F2 mean_gz,
+                                          uint32_t* o) {
+  const uint32_t x[4] = {xv.x, xv.y, xv.z, xv.w}, dy[4] = {dv.x, dv.y, dv.z, dv.w}, more[4] = {ev.x, ev.y, ev.z, ev.w};
+  F2 f[P];
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    const F2 z = fma2(widen2<DT>(x, k), rstd, shift);
+    f[k] = fma2(z, mean_gz, fma2(widen2<DT>(dy, k), weight[k], mean_g));
+    f[k] = EXTRA ? fma2(f[k], rstd, widen2<DT>(more, k)) : mul2(f[k], rstd);
+  }
+  pack2<DT, P>(f, o);
+}
+
 // The sums over rows of a CTA's groups, group after group, to its part.
 template <int VEC, int U>
 __device__ __forceinline__ void write_part(const NormArgs& a, const Group& group, int groups, int group_threads, float* shared,
-                                           const float (&dw)[U][VEC], const float (&db)[U][VEC]) {
+                                           const F2 (&dw)[U][VEC / 2], const F2 (&db)[U][VEC / 2]) {
   if (a.partial == nullptr) return;
   const uint32_t cols = a.cols;
   const int t = threadIdx.x - group.id * group_threads;
@@ -196,15 +294,16 @@ __device__ __forceinline__ void write_part(const NormArgs& a, const Group& group
     if (g != group.id) continue;
     float* to = g == groups - 1 ? out : shared;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const uint32_t c = (t + i * group_threads) * VEC;
-      if (c >= cols) continue;
+    for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        to[c + e] = g == 0 ? dw[i][e] : shared[c + e] + dw[i][e];
-        to[cols + c + e] = g == 0 ? db[i][e] : shared[cols + c + e] + db[i][e];
+        const uint32_t c = (t + i * group_threads) * VEC + e;
+        if (c >= cols) break;
+        const float2 w = parts(dw[i][e / 2]), b = parts(db[i][e / 2]);
+        const float vw = e & 1 ? w.y : w.x, vb = e & 1 ? b.y : b.x;
+        to[c] = g == 0 ? vw : shared[c] + vw;
+        to[cols + c] = g == 0 ? vb : shared[cols + c] + vb;
       }
-    }
   }
 }
 
@@ -218,7 +317,7 @@ __device__ __forceinline__ void copy16_async(uint32_t to, const void* from) {
 // row (sums, then output) read it there.
 template <int DT, int WT, int U, int R, bool EXTRA>
 __global__ void __launch_bounds__(512) norm_grad_kernel(const __grid_constant__ NormArgs a, int group_threads, int depth, uint32_t weights_on_grid) {
-  constexpr int VEC = 16 / Elem<DT>::kBytes, ARRAYS = EXTRA ? 3 : 2, PER_STAGE = R * ARRAYS * U;
+  constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2, ARRAYS = EXTRA ? 3 : 2, PER_STAGE = R * ARRAYS * U;
   extern __shared__ uint4 ring[];  // [depth][R][ARRAYS][U][threads]
   __shared__ float4 slots[2 * kMostWarps];
   pdl_enter();
@@ -226,29 +325,32 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(const __grid_constant__ 
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
   const int r = part.r, groups = blockDim.x / group_threads, t = threadIdx.x - group.id * group_threads;
   const uint32_t cols = a.cols, units = cols / VEC;
+  const uint64_t row_bytes = static_cast<uint64_t>(cols) * Elem<DT>::kBytes;
   const float inv = 1.f / static_cast<float>(cols);
   const uint4* mine = ring + threadIdx.x;
   const uint32_t mine_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine)), step = blockDim.x * 16;
-  float dw[U][VEC], db[U][VEC];
+  F2 dw[U][P], db[U][P];
 #pragma unroll
   for (int i = 0; i < U; ++i)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = 0.f;
+    for (int k = 0; k < P; ++k) dw[i][k] = db[i][k] = both(0.f);
 
+  const char *x = static_cast<const char*>(a.x[r]) + t * 16, *dy = static_cast<const char*>(a.dy[r]) + t * 16;
+  const char* extra = static_cast<const char*>(a.extra[r]) + t * 16;
+  char* out = static_cast<char*>(a.out[r]) + t * 16;
+  const uint32_t hop = group_threads * 16;
   const auto fetch = [&](uint64_t row0, int stage) {
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       if (row0 + j >= part.hi) break;
-      const uint64_t at = (row0 + j) * cols;
+      const uint64_t at = (row0 + j) * row_bytes;
+      const uint32_t to = mine_at + (stage * PER_STAGE + j * ARRAYS * U) * step;
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const uint32_t u = t + i * group_threads;
-        if (u >= units) break;
-        const uint64_t byte = (at + u * VEC) * Elem<DT>::kBytes;
-        const uint32_t to = mine_at + (stage * PER_STAGE + j * ARRAYS * U + i) * step;
-        copy16_async(to, static_cast<const char*>(a.x[r]) + byte);
-        copy16_async(to + U * step, static_cast<const char*>(a.dy[r]) + byte);
-        if constexpr (EXTRA) copy16_async(to + 2 * U * step, static_cast<const char*>(a.extra[r]) + byte);
+        if (t + i * group_threads >= units) break;
+        copy16_async(to + i * step, x + at + i * hop);
+        copy16_async(to + (U + i) * step, dy + at + i * hop);
+        if constexpr (EXTRA) copy16_async(to + (2 * U + i) * step, extra + at + i * hop);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -265,7 +367,7 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(const __grid_constant__ 
   }
   for (int stage = 0; row0 < part.hi; row0 += stride) {
     {
-      int next = stage + depth - 1;
+      const int next = stage + depth - 1;
       fetch(ahead, next >= depth ? next - depth : next);
       ahead += stride;
     }
@@ -280,56 +382,44 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(const __grid_constant__ 
     else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
     else asm volatile("cp.async.wait_group 1;" ::: "memory");
     const uint4* here = mine + stage * PER_STAGE * blockDim.x;
-    float sums[2 * R];
+    F2 sg[R], sgz[R];
 #pragma unroll
-    for (int j = 0; j < 2 * R; ++j) sums[j] = 0.f;
+    for (int j = 0; j < R; ++j) sg[j] = sgz[j] = both(0.f);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t u = t + i * group_threads;
       if (u >= units) break;
-      float weight[VEC];
-      load_weights<WT, VEC>(a.weight[r], u * VEC, weights_on_grid, weight);
+      F2 weight[P];
+      load_weights<WT, VEC>(a.weight[r], u * VEC, cols, weights_on_grid, weight);
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         if (row0 + j >= part.hi) break;
-        const uint4 xv = here[(j * ARRAYS * U + i) * blockDim.x], dv = here[(j * ARRAYS * U + U + i) * blockDim.x];
-        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, dyw[4] = {dv.x, dv.y, dv.z, dv.w};
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float z = (widen<DT>(xw, e) - mean[j]) * rstd[j], d = widen<DT>(dyw, e), g = d * weight[e];
-          sums[2 * j] += g;
-          sums[2 * j + 1] = fmaf(g, z, sums[2 * j + 1]);
-          dw[i][e] = fmaf(d, z, dw[i][e]);
-          db[i][e] += d;
-        }
+        add_unit<DT, P>(here[(j * ARRAYS * U + i) * blockDim.x], here[(j * ARRAYS * U + U + i) * blockDim.x], weight, both(rstd[j]),
+                        both(-mean[j] * rstd[j]), sg[j], sgz[j], dw[i], db[i]);
       }
+    }
+    float sums[2 * R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      sums[2 * j] = total2(sg[j]);
+      sums[2 * j + 1] = total2(sgz[j]);
     }
     group.sum<2 * R>(sums);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t u = t + i * group_threads;
       if (u >= units) break;
-      float weight[VEC];
-      load_weights<WT, VEC>(a.weight[r], u * VEC, weights_on_grid, weight);
+      F2 weight[P];
+      load_weights<WT, VEC>(a.weight[r], u * VEC, cols, weights_on_grid, weight);
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         if (row0 + j >= part.hi) break;
-        const uint4 xv = here[(j * ARRAYS * U + i) * blockDim.x], dv = here[(j * ARRAYS * U + U + i) * blockDim.x];
-        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, dyw[4] = {dv.x, dv.y, dv.z, dv.w};
-        uint4 ev = make_uint4(0, 0, 0, 0);
-        if constexpr (EXTRA) ev = here[(j * ARRAYS * U + 2 * U + i) * blockDim.x];
-        const uint32_t ew[4] = {ev.x, ev.y, ev.z, ev.w};
-        const float mg = sums[2 * j] * inv, mgz = sums[2 * j + 1] * inv;
-        float f[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float z = (widen<DT>(xw, e) - mean[j]) * rstd[j];
-          f[e] = (fmaf(widen<DT>(dyw, e), weight[e], -mg) - z * mgz) * rstd[j];
-          if constexpr (EXTRA) f[e] += widen<DT>(ew, e);
-        }
+        uint4 more = make_uint4(0, 0, 0, 0);
+        if constexpr (EXTRA) more = here[(j * ARRAYS * U + 2 * U + i) * blockDim.x];
         uint32_t o[4];
-        pack_out<DT, VEC>(f, o);
-        store_raw<DT, VEC>(a.out[r], (row0 + j) * cols + u * VEC, o);
+        grad_unit<DT, P, EXTRA>(here[(j * ARRAYS * U + i) * blockDim.x], here[(j * ARRAYS * U + U + i) * blockDim.x], more, weight, both(rstd[j]),
+                                both(-mean[j] * rstd[j]), both(-sums[2 * j] * inv), both(-sums[2 * j + 1] * inv), o);
+        st_stream16(out + (row0 + j) * row_bytes + i * hop, make_uint4(o[0], o[1], o[2], o[3]));
       }
     }
 #pragma unroll
@@ -343,10 +433,11 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(const __grid_constant__ 
   write_part<VEC, U>(a, group, groups, group_threads, reinterpret_cast<float*>(ring), dw, db);
 }
 
-// Rows off the grid, or too long for a ring: element by element; the second walk
-// finds the row in L1 or L2.
-template <int DT, int WT, int U>
-__global__ void __launch_bounds__(512) norm_grad_off_kernel(const __grid_constant__ NormArgs a, int group_threads) {
+// Rows off the grid, or too long for a ring: a row waits in registers, the next one
+// is on its way there.
+template <int DT, int WT, int U, bool EXTRA>
+__global__ void __launch_bounds__(512) norm_grad_off_kernel(const __grid_constant__ NormArgs a, int group_threads, uint32_t weights_on_grid) {
+  constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2;
   extern __shared__ uint4 ring[];
   __shared__ float4 slots[2 * kMostWarps];
   pdl_enter();
@@ -354,47 +445,66 @@ __global__ void __launch_bounds__(512) norm_grad_off_kernel(const __grid_constan
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
   const int r = part.r, groups = blockDim.x / group_threads, t = threadIdx.x - group.id * group_threads;
   const uint32_t cols = a.cols;
+  const Units<DT, false> units(cols);
   const float inv = 1.f / static_cast<float>(cols);
-  float dw[U][1], db[U][1];
+  const char *x = static_cast<const char*>(a.x[r]), *dy = static_cast<const char*>(a.dy[r]), *extra = static_cast<const char*>(a.extra[r]);
+  F2 dw[U][P], db[U][P];
 #pragma unroll
-  for (int i = 0; i < U; ++i) dw[i][0] = db[i][0] = 0.f;
-  const auto one = [](const void* base, uint64_t i) {
-    if constexpr (DT == kF32) return static_cast<const float*>(base)[i];
-    else return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
-  };
-  for (uint64_t row = part.lo + static_cast<uint64_t>(group.id); row < part.hi; row += groups) {
-    const uint64_t at = row * cols;
-    const float mean = a.mean[r][row], rstd = a.rstd[r][row];
-    float sums[2] = {0.f, 0.f};
+  for (int i = 0; i < U; ++i)
+#pragma unroll
+    for (int k = 0; k < P; ++k) dw[i][k] = db[i][k] = both(0.f);
+  uint64_t row = part.lo + static_cast<uint64_t>(group.id);
+  uint4 next_x[U], next_dy[U];
+  float next_mean = 0.f, next_rstd = 0.f;
+  const auto fetch = [&](uint64_t row) {
+    if (row >= part.hi) return;
+    const uint64_t at = row * units.row_bytes;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const uint32_t c = t + i * group_threads;
-      if (c >= cols) break;
-      float weight;
-      load_weights<WT, 1>(a.weight[r], c, false, &weight);
-      const float z = (one(a.x[r], at + c) - mean) * rstd, d = one(a.dy[r], at + c), g = d * weight;
-      sums[0] += g;
-      sums[1] = fmaf(g, z, sums[1]);
-      dw[i][0] = fmaf(d, z, dw[i][0]);
-      db[i][0] += d;
+      next_x[i] = units.load(x + at, t + i * group_threads);
+      next_dy[i] = units.load(dy + at, t + i * group_threads);
     }
-    group.sum<2>(sums);
-    const float mg = sums[0] * inv, mgz = sums[1] * inv;
+    next_mean = a.mean[r][row];
+    next_rstd = a.rstd[r][row];
+  };
+  fetch(row);
+  for (; row < part.hi; row += groups) {
+    uint4 xv[U], dv[U], ev[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const uint32_t c = t + i * group_threads;
-      if (c >= cols) break;
-      float weight;
-      load_weights<WT, 1>(a.weight[r], c, false, &weight);
-      const float z = (one(a.x[r], at + c) - mean) * rstd;
-      float f = (fmaf(one(a.dy[r], at + c), weight, -mg) - z * mgz) * rstd;
-      if (a.extra[r] != nullptr) f += one(a.extra[r], at + c);
-      uint32_t o;
-      pack_out<DT, 1>(&f, &o);
-      store_raw<DT, 1>(a.out[r], at + c, &o);
+      xv[i] = next_x[i];
+      dv[i] = next_dy[i];
+    }
+    const F2 rstd = both(next_rstd), shift = both(-next_mean * next_rstd);
+    const uint64_t at = row * units.row_bytes;
+    if constexpr (EXTRA) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) ev[i] = units.load(extra + at, t + i * group_threads);
+    }
+    fetch(row + groups);
+    F2 sg = both(0.f), sgz = both(0.f);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t u = t + i * group_threads;
+      if (u >= units.count) break;
+      F2 weight[P];
+      load_weights<WT, VEC>(a.weight[r], u * VEC, cols, weights_on_grid, weight);
+      add_unit<DT, P>(xv[i], dv[i], weight, rstd, shift, sg, sgz, dw[i], db[i]);
+    }
+    float sums[2] = {total2(sg), total2(sgz)};
+    group.sum<2>(sums);
+    const F2 mean_g = both(-sums[0] * inv), mean_gz = both(-sums[1] * inv);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t u = t + i * group_threads;
+      F2 weight[P];
+      load_weights<WT, VEC>(a.weight[r], u * VEC, cols, weights_on_grid, weight);
+      uint32_t o[4];
+      grad_unit<DT, P, EXTRA>(xv[i], dv[i], ev[i], weight, rstd, shift, mean_g, mean_gz, o);
+      units.store(static_cast<char*>(a.out[r]) + at, u, o);
     }
   }
-  write_part<1, U>(a, group, groups, group_threads, reinterpret_cast<float*>(ring), dw, db);
+  write_part<VEC, U>(a, group, groups, group_threads, reinterpret_cast<float*>(ring), dw, db);
 }
 
 // A rank's parts added up: a CTA has 32 columns (grid y = rank), each of its warps
@@ -477,23 +587,19 @@ cudaError_t launch_norm(int dt, int weight_dt, bool vec, const NormArgs& args, c
   }
   return by_types(dt, weight_dt, [&](auto d, auto w) {
     constexpr int DT = decltype(d)::value, WT = decltype(w)::value;
-    const auto go = [&](auto ve, auto un) {
-      constexpr int VEC = decltype(ve)::value, U = decltype(un)::value;
-      const int group = whole_warps(a.cols / VEC, U), groups = group >= 256 ? 1 : 256 / group;
+    const uint32_t units = (a.cols * Elem<DT>::kBytes + 15) / 16;
+    const auto go = [&](auto un) {
+      constexpr int U = decltype(un)::value;
+      const int group = whole_warps(units, U), groups = group >= 256 ? 1 : 256 / group;
       // parts small enough that the last ones of a launch end together
       cut_rows(&a.parts, rows, a.p, 152 * 32, groups, false);
-      return launch_norm_kernel(sum ? norm_kernel<DT, WT, VEC, U, true> : norm_kernel<DT, WT, VEC, U, false>, a.parts.first[a.p], group * groups, 0, s,
-                                a, group, grid);
+      return launch_norm_kernel(vec ? (sum ? norm_kernel<DT, WT, U, true, true> : norm_kernel<DT, WT, U, false, true>)
+                                    : (sum ? norm_kernel<DT, WT, U, true, false> : norm_kernel<DT, WT, U, false, false>),
+                                a.parts.first[a.p], group * groups, 0, s, a, group, grid);
     };
-    if (vec) {
-      constexpr int VEC = 16 / Elem<DT>::kBytes;
-      const uint32_t units = a.cols / VEC;
-      if (units <= 32) return go(Int<VEC>{}, Int<1>{});
-      if (units <= 64) return go(Int<VEC>{}, Int<2>{});
-      return units <= 2048 ? go(Int<VEC>{}, Int<4>{}) : go(Int<VEC>{}, Int<8>{});
-    }
-    if (a.cols <= 128) return go(Int<1>{}, Int<4>{});
-    return a.cols <= 8192 ? go(Int<1>{}, Int<16>{}) : go(Int<1>{}, Int<32>{});
+    if (units <= 32) return go(Int<1>{});
+    if (units <= 64) return go(Int<2>{});
+    return units <= 2048 ? go(Int<4>{}) : go(Int<8>{});
   });
 }
 
@@ -518,12 +624,13 @@ cudaError_t launch_norm_grad(int dt, int weight_dt, bool vec, NormArgs* args, cu
     };
     const auto off = [&](auto un) {
       constexpr int U = decltype(un)::value;
-      const int group = whole_warps(a.cols, U), groups = group >= 256 ? 1 : 256 / group;
-      return launch(norm_grad_off_kernel<DT, WT, U>, kNormParts, group, groups, 1, groups > 1 ? a.cols * 8 : 0);
+      const int group = whole_warps((a.cols + VEC - 1) / VEC, U), groups = group >= 256 ? 1 : 256 / group;
+      return launch(extra ? norm_grad_off_kernel<DT, WT, U, true> : norm_grad_off_kernel<DT, WT, U, false>, kNormParts, group, groups, 1,
+                    groups > 1 ? a.cols * 8 : 0, grid);
     };
     const auto any_off = [&] {
-      if (a.cols <= 128) return off(Int<4>{});
-      return a.cols <= 8192 ? off(Int<16>{}) : off(Int<32>{});
+      if (a.cols <= 256) return off(Int<8 / VEC>{});
+      return a.cols <= 8192 ? off(Int<16 / VEC>{}) : off(Int<32 / VEC>{});
     };
     // as many groups of up to 512 threads as leave room for two stages; false where not even one does
     cudaError_t err = cudaSuccess;
