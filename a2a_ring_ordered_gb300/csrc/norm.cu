@@ -9,7 +9,6 @@
 // more warps has a row; a thread has the same columns of every row that its
 // group takes, so that the sums over rows stay in its registers.
 #include "pairs.cuh"
-#include "realign.cuh"
 #include "row_parts.cuh"
 
 namespace ccl {
@@ -18,66 +17,26 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // ------------------------------------------------------------------- units
-// A row goes in units of 16 bytes from its start, thread t of a group having units
-// t, t + threads, ...: the same columns in every row.  GRID: all rows start on 16
-// bytes and are whole units.  Off the grid a unit is cut out of the two aligned
-// granules that hold it, the last unit may be part of one, and aligned granules
-// are put together from neighbouring lanes' units for the stores.
-template <int DT, bool GRID>
-struct Units {
-  static constexpr int kBytes = Elem<DT>::kBytes, kPer = 16 / kBytes;
-  uint32_t row_bytes, count;
-  __device__ __forceinline__ explicit Units(uint32_t cols) : row_bytes(cols * kBytes), count((row_bytes + 15) / 16) {}
-  // The unit's bytes that are the row's.
-  __device__ __forceinline__ uint32_t bytes(uint32_t u) const {
-    if (GRID) return u < count ? 16 : 0;
-    return u < count ? min(16u, row_bytes - 16 * u) : 0;
-  }
-  // The unit, zeros where it is not the row's.
-  __device__ __forceinline__ uint4 load(const char* row, uint32_t u) const {
-    if constexpr (GRID) return u < count ? ld_once16(row + 16 * u) : make_uint4(0, 0, 0, 0);
-    const uint32_t n = bytes(u);
-    const uint4 v = load16_part(row + 16 * u, 0, n);
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) w[k] = n >= 4 * k + 4 ? w[k] : n == 4 * k + 2 ? w[k] & 0xFFFFu : 0;
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  // All lanes of a warp together.
-  __device__ __forceinline__ void store(char* row, uint32_t u, const uint32_t* w) const {
-    const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
-    const uint32_t n = bytes(u), phase = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15;
-    char* to = row + 16 * u;
-    if constexpr (GRID) {
-      if (n) st_stream16(to, v);
-      return;
-    }
-    // `first` bytes of the unit lie in its first granule; the second one takes the rest and the next lane's first
-    const int lane = threadIdx.x & 31;
-    const uint32_t first = 16 - phase;
-    const uint4 next = next_lane(v, make_uint4(0, 0, 0, 0), lane);
-    const uint32_t next_n = __shfl_down_sync(kAll, n, 1);
-    const bool whole = n == 16 && (phase == 0 || (lane < 31 && next_n >= first));
-    if (whole) st_stream16(phase == 0 ? to : to + first, phase == 0 ? v : shift16(v, next, first));
-    // what no lane's granule holds
-    const bool head = phase != 0 && (lane == 0 || n < first);
-    if (!head && whole) return;
-#pragma unroll
-    for (uint32_t e = 0; e < kPer; ++e) {
-      const uint32_t at = e * kBytes;
-      if (at < n && (phase != 0 && at < first ? head : !whole)) store_one<DT>(to, e, w, e);
-    }
-  }
-};
+// On the grid (all rows start on 16 bytes and are multiples of them) a row goes in
+// units of 16 bytes, off it in elements; thread t of a group has units t, t +
+// threads, ...: the same columns in every row.
 
-// The weights of the N columns from c on, zeros from cols on; they are read again
-// for every row and stay in L1.  `grid`: their columns start on 16 bytes.
+// The row's granules into L2, by one instruction: a group asks for its next row
+// while it works on one.
+__device__ __forceinline__ void prefetch_row(const void* base, uint64_t at, uint32_t row_bytes) {
+  const uintptr_t start = reinterpret_cast<uintptr_t>(base) + at, granule = start & ~static_cast<uintptr_t>(15);
+  const uint32_t size = static_cast<uint32_t>((start + row_bytes - granule + 15) & ~static_cast<uintptr_t>(15));
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(granule), "r"(size) : "memory");
+}
+
+// The weights of the N columns from c on; they are read again for every row and
+// stay in L1.  `grid`: they start on 16 bytes.
 template <int WT, int N>
-__device__ __forceinline__ void load_weights(const void* base, uint32_t c, uint32_t cols, bool grid, F2* f) {
+__device__ __forceinline__ void load_weights(const void* base, uint32_t c, bool grid, F2* f) {
   constexpr int B = Elem<WT>::kBytes, kWords = N * B / 4;
   const char* p = static_cast<const char*>(base) + static_cast<size_t>(c) * B;
   uint32_t w[kWords];
-  if (grid && c + N <= cols) {
+  if (grid) {
     if constexpr (kWords >= 4) {
 #pragma unroll
       for (int k = 0; k < kWords / 4; ++k) {
@@ -97,13 +56,59 @@ __device__ __forceinline__ void load_weights(const void* base, uint32_t c, uint3
     for (int k = 0; k < kWords; ++k) w[k] = 0;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      if (c + e >= cols) continue;
       if constexpr (WT == kF32) w[e] = reinterpret_cast<const uint32_t*>(p)[e];
       else w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(p)[e]) << (16 * (e & 1));
     }
   }
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) f[i] = widen2<WT>(w, i);
+}
+
+// Off the grid: how many columns thread t of G has, and its columns of a row, two
+// to a pair, from the first one's place on; zeros behind them.
+template <int G>
+__device__ __forceinline__ int own_columns(uint32_t cols, int t) {
+  return static_cast<int>(cols / G) + (t < static_cast<int>(cols % G) ? 1 : 0);
+}
+template <int DT, int G, int U>
+__device__ __forceinline__ void load_row(const char* at, int mine, F2* f) {
+  float v[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    v[i] = 0.f;
+    if (i < mine) {
+      if constexpr (DT == kF32) v[i] = reinterpret_cast<const float*>(at)[i * G];
+      else v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(at)[i * G]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < U / 2; ++k) f[k] = pair(v[2 * k], v[2 * k + 1]);
+}
+template <int G, int U>
+__device__ __forceinline__ void load_columns(const void* base, int dt, int t, int mine, F2* f) {
+  if (dt == kF32) load_row<kF32, G, U>(static_cast<const char*>(base) + t * 4, mine, f);
+  else load_row<kBF16, G, U>(static_cast<const char*>(base) + t * 2, mine, f);
+}
+template <int DT, int U>
+__device__ __forceinline__ void round_row(F2* f) {
+  if constexpr (DT == kBF16) {
+#pragma unroll
+    for (int k = 0; k < U / 2; ++k) {
+      uint32_t o;
+      pack2<DT, 1>(f + k, &o);
+      f[k] = widen2<DT>(&o, 0);
+    }
+  }
+}
+template <int DT, int G, int U>
+__device__ __forceinline__ void store_row(char* at, int mine, const F2* f) {
+#pragma unroll
+  for (int k = 0; k < U / 2; ++k) {
+    uint32_t o[2];
+    pack2<DT, 1>(f + k, o);
+    if (2 * k < mine) store_one<DT>(at, 2 * k * G, o, 0);
+    if (2 * k + 1 < mine) store_one<DT>(at, (2 * k + 1) * G, o, 1);
+  }
 }
 
 // ------------------------------------------------------------ groups of warps
@@ -150,7 +155,7 @@ struct Group {
 
 // -------------------------------------------------------------------- forward
 // The row stays in registers between its three walks (mean, variance, output).
-template <int DT, int WT, int U, bool SUM, bool GRID>
+template <int DT, int WT, int U, bool SUM>
 __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const __grid_constant__ NormArgs a, int group_threads, uint32_t weights_on_grid) {
   constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2;
   __shared__ float4 slots[2 * kMostWarps];
@@ -158,25 +163,35 @@ __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const _
   Group group(slots, group_threads);
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
   const int r = part.r, groups = blockDim.x / group_threads, t = threadIdx.x - group.id * group_threads;
-  const uint32_t cols = a.cols;
-  const Units<DT, GRID> units(cols);
+  const uint32_t cols = a.cols, units = cols / VEC, row_bytes = cols * Elem<DT>::kBytes;
   const float n = static_cast<float>(cols), eps = static_cast<float>(a.eps);
-  const char *x = static_cast<const char*>(a.x[r]), *extra = static_cast<const char*>(a.extra[r]);
   for (uint32_t row = part.lo + group.id; row < part.hi; row += groups) {
-    const uint64_t at = static_cast<uint64_t>(row) * units.row_bytes;
+    const uint64_t at = static_cast<uint64_t>(row) * row_bytes;
+    if (t == 0 && part.hi - row > static_cast<uint32_t>(groups)) {
+      prefetch_row(a.x[r], at + static_cast<uint64_t>(groups) * row_bytes, row_bytes);
+      if constexpr (SUM) prefetch_row(a.extra[r], at + static_cast<uint64_t>(groups) * row_bytes, row_bytes);
+    }
     F2 f[U][P];
     {
       uint4 v[U];
 #pragma unroll
-      for (int i = 0; i < U; ++i) v[i] = units.load(x + at, t + i * group_threads);
+      for (int i = 0; i < U; ++i) {
+        const uint32_t u = t + i * group_threads;
+        v[i] = u < units ? ld_once16(static_cast<const char*>(a.x[r]) + at + 16 * u) : make_uint4(0, 0, 0, 0);
+      }
       if constexpr (SUM) {
         uint4 q[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) q[i] = units.load(extra + at, t + i * group_threads);
+        for (int i = 0; i < U; ++i) {
+          const uint32_t u = t + i * group_threads;
+          q[i] = u < units ? ld_once16(static_cast<const char*>(a.extra[r]) + at + 16 * u) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
+          const uint32_t u = t + i * group_threads;
           uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, o[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
           if constexpr (DT == kBF16) {
+            // the sum of two bf16 numbers rounded to bf16 at once, or by way of fp32, is the same
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const __nv_bfloat162 h = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&w[k]), *reinterpret_cast<__nv_bfloat162*>(&o[k]));
@@ -186,8 +201,8 @@ __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const _
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) + __uint_as_float(o[k]));
           }
-          units.store(static_cast<char*>(a.sum[r]) + at, t + i * group_threads, w);
           v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (u < units) st_stream16(static_cast<char*>(a.sum[r]) + at + 16 * u, v[i]);
         }
       }
 #pragma unroll
@@ -209,16 +224,10 @@ __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const _
     sum = both(0.f);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const uint32_t left = units.bytes(t + i * group_threads) / Elem<DT>::kBytes;  // elements of the unit
+      if (t + i * group_threads >= units) break;
 #pragma unroll
       for (int k = 0; k < P; ++k) {
         f[i][k] = add2(f[i][k], less);
-        if (GRID) {
-          if (left == 0) f[i][k] = both(0.f);
-        } else {
-          const float2 d = parts(f[i][k]);
-          f[i][k] = pair(left > 2 * k ? d.x : 0.f, left > 2 * k + 1 ? d.y : 0.f);
-        }
         sum = fma2(f[i][k], f[i][k], sum);
       }
     }
@@ -229,11 +238,11 @@ __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const _
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t u = t + i * group_threads;
-      if (GRID && u >= units.count) break;
+      if (u >= units) break;
       F2 w[P], b[P];
-      load_weights<WT, VEC>(a.weight[r], u * VEC, cols, weights_on_grid, w);
+      load_weights<WT, VEC>(a.weight[r], u * VEC, weights_on_grid, w);
       if (a.bias[r] != nullptr) {
-        load_weights<WT, VEC>(a.bias[r], u * VEC, cols, weights_on_grid, b);
+        load_weights<WT, VEC>(a.bias[r], u * VEC, weights_on_grid, b);
 #pragma unroll
         for (int k = 0; k < P; ++k) f[i][k] = fma2(mul2(f[i][k], scale), w[k], b[k]);
       } else {
@@ -242,8 +251,68 @@ __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const _
       }
       uint32_t o[4];
       pack2<DT, P>(f[i], o);
-      units.store(static_cast<char*>(a.out[r]) + at, u, o);
+      st_stream16(static_cast<char*>(a.out[r]) + at + 16 * u, make_uint4(o[0], o[1], o[2], o[3]));
     }
+    if (t == 0 && a.mean[r] != nullptr) {
+      a.mean[r][row] = mean;
+      a.rstd[r][row] = rstd;
+    }
+  }
+}
+
+// Rows off the grid, by elements: thread t of G has columns t + G i, and their
+// weights in registers too.
+template <int DT, int G, int U, bool SUM>
+__global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 2) norm_off_kernel(const __grid_constant__ NormArgs a, int weight_dt) {
+  constexpr int B = Elem<DT>::kBytes, H = U / 2;
+  __shared__ float4 slots[2 * kMostWarps];
+  pdl_enter();
+  Group group(slots, G);
+  const RowPart part = row_part(a.parts, a.p, blockIdx.x);
+  const int r = part.r, groups = blockDim.x / G, t = threadIdx.x % G;
+  const uint32_t cols = a.cols, row_bytes = cols * B;
+  const int mine = own_columns<G>(cols, t);
+  const float n = static_cast<float>(cols), eps = static_cast<float>(a.eps);
+  F2 w[H], b[H];
+  load_columns<G, U>(a.weight[r], weight_dt, t, mine, w);
+  load_columns<G, U>(a.bias[r], weight_dt, t, a.bias[r] != nullptr ? mine : 0, b);
+  for (uint32_t row = part.lo + group.id; row < part.hi; row += groups) {
+    const uint64_t at = static_cast<uint64_t>(row) * row_bytes;
+    if (t == 0 && part.hi - row > static_cast<uint32_t>(groups)) {
+      prefetch_row(a.x[r], at + static_cast<uint64_t>(groups) * row_bytes, row_bytes);
+      if constexpr (SUM) prefetch_row(a.extra[r], at + static_cast<uint64_t>(groups) * row_bytes, row_bytes);
+    }
+    F2 f[H];
+    load_row<DT, G, U>(static_cast<const char*>(a.x[r]) + at + t * B, mine, f);
+    if constexpr (SUM) {
+      F2 q[H];
+      load_row<DT, G, U>(static_cast<const char*>(a.extra[r]) + at + t * B, mine, q);
+#pragma unroll
+      for (int k = 0; k < H; ++k) f[k] = add2(f[k], q[k]);
+      round_row<DT, U>(f);
+      store_row<DT, G, U>(static_cast<char*>(a.sum[r]) + at + t * B, mine, f);
+    }
+    F2 sum = both(0.f);
+#pragma unroll
+    for (int k = 0; k < H; ++k) sum = add2(sum, f[k]);
+    float total[1] = {total2(sum)};
+    group.sum<1>(total);
+    const float mean = total[0] / n;
+    const F2 less = both(-mean);
+    sum = both(0.f);
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+      f[k] = add2(f[k], less);
+      if (2 * k + 2 > mine) f[k] = pair(2 * k < mine ? parts(f[k]).x : 0.f, 0.f);
+      sum = fma2(f[k], f[k], sum);
+    }
+    float square[1] = {total2(sum)};
+    group.sum<1>(square);
+    const float rstd = 1.f / sqrtf(square[0] / n + eps);
+    const F2 scale = both(rstd);
+#pragma unroll
+    for (int k = 0; k < H; ++k) f[k] = fma2(mul2(f[k], scale), w[k], b[k]);
+    store_row<DT, G, U>(static_cast<char*>(a.out[r]) + at + t * B, mine, f);
     if (t == 0 && a.mean[r] != nullptr) {
       a.mean[r][row] = mean;
       a.rstd[r][row] = rstd;
@@ -280,10 +349,20 @@ __device__ __forceinline__ void grad_unit(const uint4& xv, const uint4& dv, cons
   pack2<DT, P>(f, o);
 }
 
+template <int N>
+__device__ __forceinline__ void spread2(const F2* f, float* v) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float2 t = parts(f[k]);
+    v[2 * k] = t.x;
+    v[2 * k + 1] = t.y;
+  }
+}
+
 // The sums over rows of a CTA's groups, group after group, to its part.
 template <int VEC, int U>
 __device__ __forceinline__ void write_part(const NormArgs& a, const Group& group, int groups, int group_threads, float* shared,
-                                           const F2 (&dw)[U][VEC / 2], const F2 (&db)[U][VEC / 2]) {
+                                           const float* dw, const float* db) {
   if (a.partial == nullptr) return;
   const uint32_t cols = a.cols;
   const int t = threadIdx.x - group.id * group_threads;
@@ -299,212 +378,155 @@ __device__ __forceinline__ void write_part(const NormArgs& a, const Group& group
       for (int e = 0; e < VEC; ++e) {
         const uint32_t c = (t + i * group_threads) * VEC + e;
         if (c >= cols) break;
-        const float2 w = parts(dw[i][e / 2]), b = parts(db[i][e / 2]);
-        const float vw = e & 1 ? w.y : w.x, vb = e & 1 ? b.y : b.x;
+        const float vw = dw[i * VEC + e], vb = db[i * VEC + e];
         to[c] = g == 0 ? vw : shared[c] + vw;
         to[cols + c] = g == 0 ? vb : shared[cols + c] + vb;
       }
   }
 }
 
-__device__ __forceinline__ void copy16_async(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-
-// Rows on the 16-byte grid.  R rows at a time come through a ring in shared
-// memory of `depth` stages, in which each thread copies what it reads itself, so
-// that no barrier stands between the copies and their use; both walks over a
-// row (sums, then output) read it there.
-template <int DT, int WT, int U, int R, bool EXTRA>
-__global__ void __launch_bounds__(512) norm_grad_kernel(const __grid_constant__ NormArgs a, int group_threads, int depth, uint32_t weights_on_grid) {
-  constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2, ARRAYS = EXTRA ? 3 : 2, PER_STAGE = R * ARRAYS * U;
-  extern __shared__ uint4 ring[];  // [depth][R][ARRAYS][U][threads]
+// Rows on the 16-byte grid.  A row's units stay in registers between its two
+// walks; with PRE the next row's are on the way there too, and the one after it
+// to L2.
+template <int DT, int WT, int U, bool EXTRA, bool PRE>
+__global__ void __launch_bounds__(512, 1) norm_grad_kernel(const __grid_constant__ NormArgs a, int group_threads, uint32_t weights_on_grid) {
+  constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2, ARRAYS = EXTRA ? 3 : 2;
+  extern __shared__ float shared[];
   __shared__ float4 slots[2 * kMostWarps];
   pdl_enter();
   Group group(slots, group_threads);
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
   const int r = part.r, groups = blockDim.x / group_threads, t = threadIdx.x - group.id * group_threads;
-  const uint32_t cols = a.cols, units = cols / VEC;
-  const uint64_t row_bytes = static_cast<uint64_t>(cols) * Elem<DT>::kBytes;
+  const uint32_t cols = a.cols, row_bytes = cols * Elem<DT>::kBytes, hop = group_threads * 16;
+  const int mine = (static_cast<int>(cols / VEC) - t + group_threads - 1) / group_threads;  // units of the thread
   const float inv = 1.f / static_cast<float>(cols);
-  const uint4* mine = ring + threadIdx.x;
-  const uint32_t mine_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine)), step = blockDim.x * 16;
   F2 dw[U][P], db[U][P];
 #pragma unroll
   for (int i = 0; i < U; ++i)
 #pragma unroll
     for (int k = 0; k < P; ++k) dw[i][k] = db[i][k] = both(0.f);
-
-  const char *x = static_cast<const char*>(a.x[r]) + t * 16, *dy = static_cast<const char*>(a.dy[r]) + t * 16;
-  const char* extra = static_cast<const char*>(a.extra[r]) + t * 16;
-  char* out = static_cast<char*>(a.out[r]) + t * 16;
-  const uint32_t hop = group_threads * 16;
-  const auto fetch = [&](uint64_t row0, int stage) {
+  const void* const from[3] = {a.x[r], a.dy[r], a.extra[r]};
+  uint4 next[ARRAYS][U];
+  const auto fetch = [&](uint32_t row) {
+    const uint64_t at = static_cast<uint64_t>(row) * row_bytes + t * 16;
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (row0 + j >= part.hi) break;
-      const uint64_t at = (row0 + j) * row_bytes;
-      const uint32_t to = mine_at + (stage * PER_STAGE + j * ARRAYS * U) * step;
+    for (int q = 0; q < ARRAYS; ++q)
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        if (t + i * group_threads >= units) break;
-        copy16_async(to + i * step, x + at + i * hop);
-        copy16_async(to + (U + i) * step, dy + at + i * hop);
-        if constexpr (EXTRA) copy16_async(to + (2 * U + i) * step, extra + at + i * hop);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+      for (int i = 0; i < U; ++i) next[q][i] = i < mine ? ld_once16(static_cast<const char*>(from[q]) + at + i * hop) : make_uint4(0, 0, 0, 0);
   };
-  const uint64_t stride = static_cast<uint64_t>(groups) * R;
-  uint64_t ahead = part.lo + static_cast<uint64_t>(group.id) * R, row0 = ahead;
-  for (int d = 0; d < depth - 1; ++d, ahead += stride) fetch(ahead, d);
-  float mean[R], rstd[R];
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const bool there = row0 + j < part.hi;
-    mean[j] = there ? a.mean[r][row0 + j] : 0.f;
-    rstd[j] = there ? a.rstd[r][row0 + j] : 0.f;
-  }
-  for (int stage = 0; row0 < part.hi; row0 += stride) {
-    {
-      const int next = stage + depth - 1;
-      fetch(ahead, next >= depth ? next - depth : next);
-      ahead += stride;
-    }
-    float next_mean[R], next_rstd[R];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const bool there = row0 + stride + j < part.hi;
-      next_mean[j] = there ? a.mean[r][row0 + stride + j] : 0.f;
-      next_rstd[j] = there ? a.rstd[r][row0 + stride + j] : 0.f;
-    }
-    if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else asm volatile("cp.async.wait_group 1;" ::: "memory");
-    const uint4* here = mine + stage * PER_STAGE * blockDim.x;
-    F2 sg[R], sgz[R];
-#pragma unroll
-    for (int j = 0; j < R; ++j) sg[j] = sgz[j] = both(0.f);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const uint32_t u = t + i * group_threads;
-      if (u >= units) break;
-      F2 weight[P];
-      load_weights<WT, VEC>(a.weight[r], u * VEC, cols, weights_on_grid, weight);
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        if (row0 + j >= part.hi) break;
-        add_unit<DT, P>(here[(j * ARRAYS * U + i) * blockDim.x], here[(j * ARRAYS * U + U + i) * blockDim.x], weight, both(rstd[j]),
-                        both(-mean[j] * rstd[j]), sg[j], sgz[j], dw[i], db[i]);
-      }
-    }
-    float sums[2 * R];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      sums[2 * j] = total2(sg[j]);
-      sums[2 * j + 1] = total2(sgz[j]);
-    }
-    group.sum<2 * R>(sums);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const uint32_t u = t + i * group_threads;
-      if (u >= units) break;
-      F2 weight[P];
-      load_weights<WT, VEC>(a.weight[r], u * VEC, cols, weights_on_grid, weight);
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        if (row0 + j >= part.hi) break;
-        uint4 more = make_uint4(0, 0, 0, 0);
-        if constexpr (EXTRA) more = here[(j * ARRAYS * U + 2 * U + i) * blockDim.x];
-        uint32_t o[4];
-        grad_unit<DT, P, EXTRA>(here[(j * ARRAYS * U + i) * blockDim.x], here[(j * ARRAYS * U + U + i) * blockDim.x], more, weight, both(rstd[j]),
-                                both(-mean[j] * rstd[j]), both(-sums[2 * j] * inv), both(-sums[2 * j + 1] * inv), o);
-        st_stream16(out + (row0 + j) * row_bytes + i * hop, make_uint4(o[0], o[1], o[2], o[3]));
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      mean[j] = next_mean[j];
-      rstd[j] = next_rstd[j];
-    }
-    stage = stage + 1 == depth ? 0 : stage + 1;
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  write_part<VEC, U>(a, group, groups, group_threads, reinterpret_cast<float*>(ring), dw, db);
-}
-
-// Rows off the grid, or too long for a ring: a row waits in registers, the next one
-// is on its way there.
-template <int DT, int WT, int U, bool EXTRA>
-__global__ void __launch_bounds__(512) norm_grad_off_kernel(const __grid_constant__ NormArgs a, int group_threads, uint32_t weights_on_grid) {
-  constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2;
-  extern __shared__ uint4 ring[];
-  __shared__ float4 slots[2 * kMostWarps];
-  pdl_enter();
-  Group group(slots, group_threads);
-  const RowPart part = row_part(a.parts, a.p, blockIdx.x);
-  const int r = part.r, groups = blockDim.x / group_threads, t = threadIdx.x - group.id * group_threads;
-  const uint32_t cols = a.cols;
-  const Units<DT, false> units(cols);
-  const float inv = 1.f / static_cast<float>(cols);
-  const char *x = static_cast<const char*>(a.x[r]), *dy = static_cast<const char*>(a.dy[r]), *extra = static_cast<const char*>(a.extra[r]);
-  F2 dw[U][P], db[U][P];
-#pragma unroll
-  for (int i = 0; i < U; ++i)
-#pragma unroll
-    for (int k = 0; k < P; ++k) dw[i][k] = db[i][k] = both(0.f);
-  uint64_t row = part.lo + static_cast<uint64_t>(group.id);
-  uint4 next_x[U], next_dy[U];
+  // rows are below 2^31, groups few
+  uint32_t row = part.lo + group.id;
   float next_mean = 0.f, next_rstd = 0.f;
-  const auto fetch = [&](uint64_t row) {
-    if (row >= part.hi) return;
-    const uint64_t at = row * units.row_bytes;
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      next_x[i] = units.load(x + at, t + i * group_threads);
-      next_dy[i] = units.load(dy + at, t + i * group_threads);
-    }
+  if (row < part.hi) {
+    if constexpr (PRE) fetch(row);
     next_mean = a.mean[r][row];
     next_rstd = a.rstd[r][row];
-  };
-  fetch(row);
+  }
   for (; row < part.hi; row += groups) {
-    uint4 xv[U], dv[U], ev[U];
+    const uint32_t far = row + (PRE ? 2 : 1) * groups;
+    if (t < ARRAYS && far < part.hi) prefetch_row(t == 0 ? from[0] : t == 1 ? from[1] : from[2], static_cast<uint64_t>(far) * row_bytes, row_bytes);
+    if constexpr (!PRE) fetch(row);
+    uint4 now[ARRAYS][U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      xv[i] = next_x[i];
-      dv[i] = next_dy[i];
-    }
+    for (int q = 0; q < ARRAYS; ++q)
+#pragma unroll
+      for (int i = 0; i < U; ++i) now[q][i] = next[q][i];
     const F2 rstd = both(next_rstd), shift = both(-next_mean * next_rstd);
-    const uint64_t at = row * units.row_bytes;
-    if constexpr (EXTRA) {
-#pragma unroll
-      for (int i = 0; i < U; ++i) ev[i] = units.load(extra + at, t + i * group_threads);
+    const uint32_t after = row + groups;
+    if (after < part.hi) {
+      if constexpr (PRE) fetch(after);
+      next_mean = a.mean[r][after];
+      next_rstd = a.rstd[r][after];
     }
-    fetch(row + groups);
     F2 sg = both(0.f), sgz = both(0.f);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const uint32_t u = t + i * group_threads;
-      if (u >= units.count) break;
+      if (i >= mine) break;
       F2 weight[P];
-      load_weights<WT, VEC>(a.weight[r], u * VEC, cols, weights_on_grid, weight);
-      add_unit<DT, P>(xv[i], dv[i], weight, rstd, shift, sg, sgz, dw[i], db[i]);
+      load_weights<WT, VEC>(a.weight[r], (t + i * group_threads) * VEC, weights_on_grid, weight);
+      add_unit<DT, P>(now[0][i], now[1][i], weight, rstd, shift, sg, sgz, dw[i], db[i]);
     }
     float sums[2] = {total2(sg), total2(sgz)};
     group.sum<2>(sums);
     const F2 mean_g = both(-sums[0] * inv), mean_gz = both(-sums[1] * inv);
+    char* out = static_cast<char*>(a.out[r]) + static_cast<uint64_t>(row) * row_bytes + t * 16;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const uint32_t u = t + i * group_threads;
+      if (i >= mine) break;
       F2 weight[P];
-      load_weights<WT, VEC>(a.weight[r], u * VEC, cols, weights_on_grid, weight);
+      load_weights<WT, VEC>(a.weight[r], (t + i * group_threads) * VEC, weights_on_grid, weight);
       uint32_t o[4];
-      grad_unit<DT, P, EXTRA>(xv[i], dv[i], ev[i], weight, rstd, shift, mean_g, mean_gz, o);
-      units.store(static_cast<char*>(a.out[r]) + at, u, o);
+      grad_unit<DT, P, EXTRA>(now[0][i], now[1][i], now[ARRAYS - 1][i], weight, rstd, shift, mean_g, mean_gz, o);
+      st_stream16(out + i * hop, make_uint4(o[0], o[1], o[2], o[3]));
     }
   }
-  write_part<VEC, U>(a, group, groups, group_threads, reinterpret_cast<float*>(ring), dw, db);
+  float all_w[U * VEC], all_b[U * VEC];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    spread2<P>(dw[i], all_w + i * VEC);
+    spread2<P>(db[i], all_b + i * VEC);
+  }
+  write_part<VEC, U>(a, group, groups, group_threads, shared, all_w, all_b);
+}
+
+// Rows off the grid, by elements (thread t of G has columns t + G i): the row stays
+// in registers between its two walks, as do the weights.
+template <int DT, int G, int U, bool EXTRA>
+__global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) norm_grad_off_kernel(const __grid_constant__ NormArgs a, int weight_dt) {
+  constexpr int B = Elem<DT>::kBytes, H = U / 2;
+  extern __shared__ float shared[];
+  __shared__ float4 slots[2 * kMostWarps];
+  pdl_enter();
+  Group group(slots, G);
+  const RowPart part = row_part(a.parts, a.p, blockIdx.x);
+  const int r = part.r, groups = blockDim.x / G, t = threadIdx.x % G;
+  const uint32_t cols = a.cols, row_bytes = cols * B;
+  const int mine = own_columns<G>(cols, t);
+  const float inv = 1.f / static_cast<float>(cols);
+  F2 dw[H], db[H], weight[H];
+#pragma unroll
+  for (int k = 0; k < H; ++k) dw[k] = db[k] = both(0.f);
+  load_columns<G, U>(a.weight[r], weight_dt, t, mine, weight);
+  for (uint32_t row = part.lo + group.id; row < part.hi; row += groups) {
+    const uint64_t at = static_cast<uint64_t>(row) * row_bytes;
+    if (t == 0 && part.hi - row > static_cast<uint32_t>(groups)) {
+      const uint64_t next = at + static_cast<uint64_t>(groups) * row_bytes;
+      prefetch_row(a.x[r], next, row_bytes);
+      prefetch_row(a.dy[r], next, row_bytes);
+      if constexpr (EXTRA) prefetch_row(a.extra[r], next, row_bytes);
+    }
+    F2 z[H], g[H];  // x and dy first
+    load_row<DT, G, U>(static_cast<const char*>(a.x[r]) + at + t * B, mine, z);
+    load_row<DT, G, U>(static_cast<const char*>(a.dy[r]) + at + t * B, mine, g);
+    const F2 rstd = both(a.rstd[r][row]), shift = both(-a.mean[r][row] * a.rstd[r][row]);
+    F2 sg = both(0.f), sgz = both(0.f);
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+      z[k] = fma2(z[k], rstd, shift);
+      dw[k] = fma2(g[k], z[k], dw[k]);
+      db[k] = add2(db[k], g[k]);
+      g[k] = mul2(g[k], weight[k]);
+      sg = add2(sg, g[k]);
+      sgz = fma2(g[k], z[k], sgz);
+    }
+    float sums[2] = {total2(sg), total2(sgz)};
+    group.sum<2>(sums);
+    const F2 mean_g = both(-sums[0] * inv), mean_gz = both(-sums[1] * inv);
+    if constexpr (EXTRA) {
+      F2 more[H];
+      load_row<DT, G, U>(static_cast<const char*>(a.extra[r]) + at + t * B, mine, more);
+#pragma unroll
+      for (int k = 0; k < H; ++k) g[k] = fma2(fma2(z[k], mean_gz, add2(g[k], mean_g)), rstd, more[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < H; ++k) g[k] = mul2(fma2(z[k], mean_gz, add2(g[k], mean_g)), rstd);
+    }
+    store_row<DT, G, U>(static_cast<char*>(a.out[r]) + at + t * B, mine, g);
+  }
+  float all_w[U], all_b[U];
+  spread2<H>(dw, all_w);
+  spread2<H>(db, all_b);
+  write_part<1, U>(a, group, groups, G, shared, all_w, all_b);
 }
 
 // A rank's parts added up: a CTA has 32 columns (grid y = rank), each of its warps
@@ -574,88 +596,101 @@ uint32_t weights_on_grid(const NormArgs& a) {
   return (bits & 15) == 0;
 }
 
+
+// Calls f(G, U) with the threads a row off the grid gets and the columns that each
+// has.
+template <typename F>
+cudaError_t by_columns(uint32_t cols, F f) {
+  if (cols <= 128) return f(Int<32>{}, Int<4>{});
+  if (cols <= 512) return f(Int<32>{}, Int<16>{});
+  if (cols <= 1024) return f(Int<64>{}, Int<16>{});
+  if (cols <= 2048) return f(Int<128>{}, Int<16>{});
+  if (cols <= 4096) return f(Int<256>{}, Int<16>{});
+  if (cols <= 8192) return f(Int<512>{}, Int<16>{});
+  return f(Int<512>{}, Int<32>{});
+}
+
+// The numbers of rows, for cutting them anew; whether a rank has one of the buffers.
+struct Rows {
+  size_t n[kMoeMaxRanks];
+  explicit Rows(const NormArgs& a) {
+    for (int r = 0; r < a.p; ++r) n[r] = a.parts.rows[r];
+  }
+};
+template <typename T>
+bool any_of(const T* const* buffers, int p) {
+  for (int r = 0; r < p; ++r)
+    if (buffers[r] != nullptr) return true;
+  return false;
+}
+
 }  // namespace
 
 cudaError_t launch_norm(int dt, int weight_dt, bool vec, const NormArgs& args, cudaStream_t s) {
-  const uint32_t grid = weights_on_grid(args);
   NormArgs a = args;
-  size_t rows[kMoeMaxRanks];
-  bool sum = false;
-  for (int r = 0; r < a.p; ++r) {
-    rows[r] = a.parts.rows[r];
-    sum = sum || a.sum[r] != nullptr;
+  const Rows rows(a);
+  const bool sum = any_of(a.sum, a.p);
+  const uint32_t grid = weights_on_grid(a);
+  if (!vec) {
+    const auto off = [&](auto d) {
+      constexpr int DT = decltype(d)::value;
+      return by_columns(a.cols, [&](auto gr, auto un) {
+        constexpr int G = decltype(gr)::value, U = decltype(un)::value, groups = G >= 256 ? 1 : 256 / G;
+        // parts that are all there at once, for their weights' loads: 14,006 fp32 rows of 1019 took 29 us in 2 a SM, 41 in 12
+        cut_rows(&a.parts, rows.n, a.p, 152 * 2, groups, false);
+        return launch_norm_kernel(sum ? norm_off_kernel<DT, G, U, true> : norm_off_kernel<DT, G, U, false>, a.parts.first[a.p], G * groups, 0, s, a, weight_dt);
+      });
+    };
+    return dt == kF32 ? off(Int<kF32>{}) : off(Int<kBF16>{});
   }
   return by_types(dt, weight_dt, [&](auto d, auto w) {
     constexpr int DT = decltype(d)::value, WT = decltype(w)::value;
-    const uint32_t units = (a.cols * Elem<DT>::kBytes + 15) / 16;
-    const auto go = [&](auto un) {
+    const auto on = [&](auto un) {
       constexpr int U = decltype(un)::value;
-      const int group = whole_warps(units, U), groups = group >= 256 ? 1 : 256 / group;
-      // parts small enough that the last ones of a launch end together
-      cut_rows(&a.parts, rows, a.p, 152 * 32, groups, false);
-      return launch_norm_kernel(vec ? (sum ? norm_kernel<DT, WT, U, true, true> : norm_kernel<DT, WT, U, false, true>)
-                                    : (sum ? norm_kernel<DT, WT, U, true, false> : norm_kernel<DT, WT, U, false, false>),
-                                a.parts.first[a.p], group * groups, 0, s, a, group, grid);
+      const int group = whole_warps(a.cols / (16 / Elem<DT>::kBytes), U), groups = group >= 256 ? 1 : 256 / group;
+      // parts small enough that the last ones of a launch end together: 8 x 4096 rows of 7168 with a residual took 323 us
+      // in 2 a SM, 306 in 12, 300 in 24
+      cut_rows(&a.parts, rows.n, a.p, 152 * 24, groups, false);
+      return launch_norm_kernel(sum ? norm_kernel<DT, WT, U, true> : norm_kernel<DT, WT, U, false>, a.parts.first[a.p], group * groups, 0, s, a, group, grid);
     };
-    if (units <= 32) return go(Int<1>{});
-    if (units <= 64) return go(Int<2>{});
-    return units <= 2048 ? go(Int<4>{}) : go(Int<8>{});
+    const uint32_t units = a.cols * Elem<DT>::kBytes / 16;
+    if (units <= 32) return on(Int<1>{});
+    if (units <= 64) return on(Int<2>{});
+    return units <= 2048 ? on(Int<4>{}) : on(Int<8>{});
   });
 }
 
 cudaError_t launch_norm_grad(int dt, int weight_dt, bool vec, NormArgs* args, cudaStream_t s) {
-  constexpr size_t kMostRing = 216 * 1024;  // of a SM's shared memory
   NormArgs& a = *args;
+  const Rows rows(a);
+  const bool extra = any_of(a.extra, a.p);
   const uint32_t grid = weights_on_grid(a);
-  size_t rows[kMoeMaxRanks];
-  bool extra = false;
-  for (int r = 0; r < a.p; ++r) {
-    rows[r] = a.parts.rows[r];
-    extra = extra || a.extra[r] != nullptr;
+  // groups of a CTA are joined through shared memory; two of at most 256 threads leave it below 48 KB
+  const auto launch = [&](auto* kernel, uint32_t ctas, int group, int groups, auto... more) {
+    cut_rows(&a.parts, rows.n, a.p, ctas, groups, false);
+    return launch_norm_kernel(kernel, a.parts.first[a.p], group * groups, groups > 1 ? a.cols * 8 : 0, s, static_cast<const NormArgs&>(a), more...);
+  };
+  if (!vec) {
+    const auto off = [&](auto d) {
+      constexpr int DT = decltype(d)::value;
+      return by_columns(a.cols, [&](auto gr, auto un) {
+        constexpr int G = decltype(gr)::value, U = decltype(un)::value, groups = G >= 256 ? 1 : 256 / G;
+        return launch(extra ? norm_grad_off_kernel<DT, G, U, true> : norm_grad_off_kernel<DT, G, U, false>, kNormParts, G, groups, weight_dt);
+      });
+    };
+    return dt == kF32 ? off(Int<kF32>{}) : off(Int<kBF16>{});
   }
   return by_types(dt, weight_dt, [&](auto d, auto w) {
     constexpr int DT = decltype(d)::value, WT = decltype(w)::value, VEC = 16 / Elem<DT>::kBytes;
-    const auto launch = [&](auto* kernel, uint32_t ctas, int group, int groups, int at_once, size_t smem, auto... more) {
-      cut_rows(&a.parts, rows, a.p, ctas, static_cast<uint32_t>(groups) * at_once, false);
-      // the limit belongs to the function, not to the call: always the most that a call may need
-      const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMostRing));
-      if (err != cudaSuccess) return err;
-      return launch_norm_kernel(kernel, a.parts.first[a.p], group * groups, smem, s, static_cast<const NormArgs&>(a), group, more...);
-    };
-    const auto off = [&](auto un) {
+    const auto on = [&](auto un, auto pre, int most_threads, uint32_t ctas) {
       constexpr int U = decltype(un)::value;
-      const int group = whole_warps((a.cols + VEC - 1) / VEC, U), groups = group >= 256 ? 1 : 256 / group;
-      return launch(extra ? norm_grad_off_kernel<DT, WT, U, true> : norm_grad_off_kernel<DT, WT, U, false>, kNormParts, group, groups, 1,
-                    groups > 1 ? a.cols * 8 : 0, grid);
+      constexpr bool PRE = decltype(pre)::value != 0;
+      const int group = whole_warps(a.cols / VEC, U), groups = group >= most_threads ? 1 : most_threads / group;
+      return launch(extra ? norm_grad_kernel<DT, WT, U, true, PRE> : norm_grad_kernel<DT, WT, U, false, PRE>, ctas, group, groups, group, grid);
     };
-    const auto any_off = [&] {
-      if (a.cols <= 256) return off(Int<8 / VEC>{});
-      return a.cols <= 8192 ? off(Int<16 / VEC>{}) : off(Int<32 / VEC>{});
-    };
-    // as many groups of up to 512 threads as leave room for two stages; false where not even one does
-    cudaError_t err = cudaSuccess;
-    const auto on = [&](auto un, auto rs) {
-      constexpr int U = decltype(un)::value, R = decltype(rs)::value;
-      const int group = whole_warps(a.cols / VEC, U);
-      const size_t stage = static_cast<size_t>(group) * 16 * R * (extra ? 3 : 2) * U;
-      const size_t fit = kMostRing / (2 * stage), most = group >= 512 ? 1 : 512 / group;
-      if (fit == 0) return false;
-      const int groups = static_cast<int>(fit < most ? fit : most);
-      const size_t room = kMostRing / (groups * stage), parts = groups > 1 ? a.cols * 8 : 0;
-      const int depth = static_cast<int>(room > 4 ? 4 : room);
-      const size_t ring = depth * groups * stage, smem = ring > parts ? ring : parts;
-      // a CTA a SM, two of the small ones
-      const uint32_t ctas = U * VEC <= 8 && 2 * smem <= kMostRing ? kNormParts : kNormParts / 2;
-      err = launch(extra ? norm_grad_kernel<DT, WT, U, R, true> : norm_grad_kernel<DT, WT, U, R, false>, ctas, group, groups, R, smem, depth, grid);
-      return true;
-    };
-    constexpr int U8 = 8 / VEC, U16 = 16 / VEC, U32 = 32 / VEC;
-    const bool done = vec && (a.cols <= 256    ? on(Int<U8>{}, Int<1>{})
-                              : a.cols <= 512  ? on(Int<U16>{}, Int<1>{})
-                              : a.cols <= 1024 ? on(Int<U32>{}, Int<1>{})
-                              : a.cols <= 8192 ? on(Int<U16>{}, Int<2>{}) || on(Int<U16>{}, Int<1>{})
-                                               : on(Int<U32>{}, Int<1>{}));
-    return done ? err : any_off();
+    if (a.cols <= 256) return on(Int<8 / VEC>{}, Int<1>{}, 256, kNormParts);
+    if (a.cols <= 4096) return on(Int<16 / VEC>{}, Int<1>{}, 256, kNormParts);
+    return a.cols <= 8192 ? on(Int<16 / VEC>{}, Int<1>{}, 512, kNormParts / 2) : on(Int<32 / VEC>{}, Int<0>{}, 512, kNormParts / 2);
   });
 }
 
