@@ -112,44 +112,52 @@ __device__ __forceinline__ void store_row(char* at, int mine, const F2* f) {
 }
 
 // ------------------------------------------------------------ groups of warps
-// Sums over a group, the same for every thread and in a fixed order: by
-// shuffles within the warps, then through shared memory in two sets of slots
-// in turn, so that one barrier of the group does for each sum.
-constexpr int kMostWarps = 32;  // of a CTA
+// One or two sums over a group, the same for every thread and in a fixed order:
+// by shuffles within the warps, then through shared memory in two sets of slots
+// in turn, so that one barrier of the group does for each sum.  Two sums share
+// their shuffles: the lower half of the lanes takes the one, the upper half the
+// other.
+constexpr int kMostWarps = 16;   // of a group
+constexpr int kMostGroups = 8;   // of a CTA, that have more than a warp
 struct Group {
   int warps, warp, lane, id;  // warps of the group, this one among them, the group's number
   int turn = 0;
-  float4* slots;              // 2 x kMostWarps
-  __device__ __forceinline__ Group(float4* s, int group_threads) {
+  float* slots;               // [2][kMostGroups][2 * kMostWarps]; zeros where there is no warp
+  __device__ __forceinline__ Group(float (&s)[2][kMostGroups][2 * kMostWarps], int group_threads) {
     warps = group_threads >> 5;
     id = static_cast<int>(threadIdx.x) / group_threads;
     warp = (static_cast<int>(threadIdx.x) - id * group_threads) >> 5;
     lane = threadIdx.x & 31;
-    slots = s;
+    if (warps == 1) return;
+    slots = s[0][id];
+    if (warp < 2) s[warp][id][lane] = 0.f;
+    sync();
   }
   __device__ __forceinline__ void sync() const {
     asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(warps * 32) : "memory");
   }
-  template <int N>
-  __device__ __forceinline__ void sum(float* v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kAll, v[i], o);
-    if (warps == 1) return;
-    float4* s = slots + turn * kMostWarps + id * warps;
+  __device__ __forceinline__ float across(float v) {
+    float* s = slots + turn * (kMostGroups * 2 * kMostWarps);
     turn ^= 1;
-    if (lane == 0) s[warp] = make_float4(v[0], N > 1 ? v[N > 1 ? 1 : 0] : 0.f, N > 2 ? v[N > 2 ? 2 : 0] : 0.f, N > 3 ? v[N > 3 ? 3 : 0] : 0.f);
+    if ((lane & 15) == 0) s[lane + warp] = v;
     sync();
+    v = s[lane];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.f;
-    for (int w = 0; w < warps; ++w) {
-      const float4 t = s[w];
-      v[0] += t.x;
-      if (N > 1) v[N > 1 ? 1 : 0] += t.y;
-      if (N > 2) v[N > 2 ? 2 : 0] += t.z;
-      if (N > 3) v[N > 3 ? 3 : 0] += t.w;
-    }
+    for (int o = kMostWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+  }
+  __device__ __forceinline__ float2 sum(float a, float b) {
+    const bool upper = lane >= 16;
+    float v = (upper ? b : a) + __shfl_xor_sync(kAll, upper ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    if (warps > 1) v = across(v);
+    return make_float2(__shfl_sync(kAll, v, 0), __shfl_sync(kAll, v, 16));
+  }
+  __device__ __forceinline__ float sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return warps > 1 ? across(v) : v;
   }
 };
 
@@ -158,7 +166,7 @@ struct Group {
 template <int DT, int WT, int U, bool SUM>
 __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const __grid_constant__ NormArgs a, int group_threads, uint32_t weights_on_grid) {
   constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2;
-  __shared__ float4 slots[2 * kMostWarps];
+  __shared__ float slots[2][kMostGroups][2 * kMostWarps];
   pdl_enter();
   Group group(slots, group_threads);
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
@@ -217,9 +225,7 @@ __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const _
     for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int k = 0; k < P; ++k) sum = add2(sum, f[i][k]);
-    float total[1] = {total2(sum)};
-    group.sum<1>(total);
-    const float mean = total[0] / n;
+    const float mean = group.sum(total2(sum)) / n;
     const F2 less = both(-mean);
     sum = both(0.f);
 #pragma unroll
@@ -231,9 +237,7 @@ __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const _
         sum = fma2(f[i][k], f[i][k], sum);
       }
     }
-    float square[1] = {total2(sum)};
-    group.sum<1>(square);
-    const float rstd = 1.f / sqrtf(square[0] / n + eps);
+    const float rstd = 1.f / sqrtf(group.sum(total2(sum)) / n + eps);
     const F2 scale = both(rstd);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -265,7 +269,7 @@ __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const _
 template <int DT, int G, int U, bool SUM>
 __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 2) norm_off_kernel(const __grid_constant__ NormArgs a, int weight_dt) {
   constexpr int B = Elem<DT>::kBytes, H = U / 2;
-  __shared__ float4 slots[2 * kMostWarps];
+  __shared__ float slots[2][kMostGroups][2 * kMostWarps];
   pdl_enter();
   Group group(slots, G);
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
@@ -295,9 +299,7 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 2) norm_off_k
     F2 sum = both(0.f);
 #pragma unroll
     for (int k = 0; k < H; ++k) sum = add2(sum, f[k]);
-    float total[1] = {total2(sum)};
-    group.sum<1>(total);
-    const float mean = total[0] / n;
+    const float mean = group.sum(total2(sum)) / n;
     const F2 less = both(-mean);
     sum = both(0.f);
 #pragma unroll
@@ -306,9 +308,7 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 2) norm_off_k
       if (2 * k + 2 > mine) f[k] = pair(2 * k < mine ? parts(f[k]).x : 0.f, 0.f);
       sum = fma2(f[k], f[k], sum);
     }
-    float square[1] = {total2(sum)};
-    group.sum<1>(square);
-    const float rstd = 1.f / sqrtf(square[0] / n + eps);
+    const float rstd = 1.f / sqrtf(group.sum(total2(sum)) / n + eps);
     const F2 scale = both(rstd);
 #pragma unroll
     for (int k = 0; k < H; ++k) f[k] = fma2(mul2(f[k], scale), w[k], b[k]);
@@ -392,7 +392,7 @@ template <int DT, int WT, int U, bool EXTRA, bool PRE>
 __global__ void __launch_bounds__(512, 1) norm_grad_kernel(const __grid_constant__ NormArgs a, int group_threads, uint32_t weights_on_grid) {
   constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2, ARRAYS = EXTRA ? 3 : 2;
   extern __shared__ float shared[];
-  __shared__ float4 slots[2 * kMostWarps];
+  __shared__ float slots[2][kMostGroups][2 * kMostWarps];
   pdl_enter();
   Group group(slots, group_threads);
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
@@ -446,9 +446,8 @@ __global__ void __launch_bounds__(512, 1) norm_grad_kernel(const __grid_constant
       load_weights<WT, VEC>(a.weight[r], (t + i * group_threads) * VEC, weights_on_grid, weight);
       add_unit<DT, P>(now[0][i], now[1][i], weight, rstd, shift, sg, sgz, dw[i], db[i]);
     }
-    float sums[2] = {total2(sg), total2(sgz)};
-    group.sum<2>(sums);
-    const F2 mean_g = both(-sums[0] * inv), mean_gz = both(-sums[1] * inv);
+    const float2 sums = group.sum(total2(sg), total2(sgz));
+    const F2 mean_g = both(-sums.x * inv), mean_gz = both(-sums.y * inv);
     char* out = static_cast<char*>(a.out[r]) + static_cast<uint64_t>(row) * row_bytes + t * 16;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -475,7 +474,7 @@ template <int DT, int G, int U, bool EXTRA>
 __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) norm_grad_off_kernel(const __grid_constant__ NormArgs a, int weight_dt) {
   constexpr int B = Elem<DT>::kBytes, H = U / 2;
   extern __shared__ float shared[];
-  __shared__ float4 slots[2 * kMostWarps];
+  __shared__ float slots[2][kMostGroups][2 * kMostWarps];
   pdl_enter();
   Group group(slots, G);
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
@@ -509,9 +508,8 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) 
       sg = add2(sg, g[k]);
       sgz = fma2(g[k], z[k], sgz);
     }
-    float sums[2] = {total2(sg), total2(sgz)};
-    group.sum<2>(sums);
-    const F2 mean_g = both(-sums[0] * inv), mean_gz = both(-sums[1] * inv);
+    const float2 sums = group.sum(total2(sg), total2(sgz));
+    const F2 mean_g = both(-sums.x * inv), mean_gz = both(-sums.y * inv);
     if constexpr (EXTRA) {
       F2 more[H];
       load_row<DT, G, U>(static_cast<const char*>(a.extra[r]) + at + t * B, mine, more);
