@@ -29,39 +29,63 @@ __device__ __forceinline__ void prefetch_row(const void* base, uint64_t at, uint
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(granule), "r"(size) : "memory");
 }
 
-// The weights of the N columns from c on; they are read again for every row and
-// stay in L1.  `grid`: they start on 16 bytes.
-template <int WT, int N>
-__device__ __forceinline__ void load_weights(const void* base, uint32_t c, bool grid, F2* f) {
-  constexpr int B = Elem<WT>::kBytes, kWords = N * B / 4;
-  const char* p = static_cast<const char*>(base) + static_cast<size_t>(c) * B;
-  uint32_t w[kWords];
-  if (grid) {
-    if constexpr (kWords >= 4) {
+// The vectors of a call: weight or bias, of fp32 or bf16.
+struct Vector {
+  const void* base;
+  int dt;
+  bool grid;  // starts on 16 bytes
+};
+// The N (4 or 8) columns from c on, a multiple of N.
+template <int N>
+__device__ __forceinline__ void load_columns(const Vector& v, uint32_t c, F2* f) {
+  if (v.dt == kF32) {
+    const float* p = static_cast<const float*>(v.base) + c;
 #pragma unroll
-      for (int k = 0; k < kWords / 4; ++k) {
-        const uint4 v = reinterpret_cast<const uint4*>(p)[k];
-        w[4 * k] = v.x;
-        w[4 * k + 1] = v.y;
-        w[4 * k + 2] = v.z;
-        w[4 * k + 3] = v.w;
-      }
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x;
-      w[1] = v.y;
+    for (int k = 0; k < N / 4; ++k) {
+      const float4 q = v.grid ? reinterpret_cast<const float4*>(p)[k] : make_float4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+      f[2 * k] = pair(q.x, q.y);
+      f[2 * k + 1] = pair(q.z, q.w);
     }
   } else {
+    const unsigned short* p = static_cast<const unsigned short*>(v.base) + c;
+    uint32_t w[N / 2];
+    if (v.grid) {
 #pragma unroll
-    for (int k = 0; k < kWords; ++k) w[k] = 0;
+      for (int k = 0; k < N / 4; ++k) {
+        const uint2 q = reinterpret_cast<const uint2*>(p)[k];
+        w[2 * k] = q.x;
+        w[2 * k + 1] = q.y;
+      }
+    } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      if constexpr (WT == kF32) w[e] = reinterpret_cast<const uint32_t*>(p)[e];
-      else w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(p)[e]) << (16 * (e & 1));
+      for (int k = 0; k < N / 2; ++k) w[k] = p[2 * k] | static_cast<uint32_t>(p[2 * k + 1]) << 16;
+    }
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) f[k] = widen2<kBF16>(w, k);
+  }
+}
+// The same from shared memory, where a vector lies in planes of every unit's first,
+// second, ... four columns: the lanes' 16 bytes are neighbours.
+template <int N>
+__device__ __forceinline__ void staged_columns(const float4* planes, uint32_t units, uint32_t u, F2* f) {
+#pragma unroll
+  for (int k = 0; k < N / 4; ++k) {
+    const float4 q = planes[k * units + u];
+    f[2 * k] = pair(q.x, q.y);
+    f[2 * k + 1] = pair(q.z, q.w);
+  }
+}
+template <int N>
+__device__ __forceinline__ void stage_columns(const Vector& v, float4* planes, uint32_t units) {
+  for (uint32_t u = threadIdx.x; u < units; u += blockDim.x) {
+    F2 f[N / 2];
+    load_columns<N>(v, u * N, f);
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+      const float2 a = parts(f[2 * k]), b = parts(f[2 * k + 1]);
+      planes[k * units + u] = make_float4(a.x, a.y, b.x, b.y);
     }
   }
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) f[i] = widen2<WT>(w, i);
 }
 
 // Off the grid: how many columns thread t of G has, and its columns of a row, two
@@ -85,7 +109,7 @@ __device__ __forceinline__ void load_row(const char* at, int mine, F2* f) {
   for (int k = 0; k < U / 2; ++k) f[k] = pair(v[2 * k], v[2 * k + 1]);
 }
 template <int G, int U>
-__device__ __forceinline__ void load_columns(const void* base, int dt, int t, int mine, F2* f) {
+__device__ __forceinline__ void load_spread(const void* base, int dt, int t, int mine, F2* f) {
   if (dt == kF32) load_row<kF32, G, U>(static_cast<const char*>(base) + t * 4, mine, f);
   else load_row<kBF16, G, U>(static_cast<const char*>(base) + t * 2, mine, f);
 }
@@ -163,15 +187,27 @@ struct Group {
 
 // -------------------------------------------------------------------- forward
 // The row stays in registers between its three walks (mean, variance, output).
-template <int DT, int WT, int U, bool SUM>
-__global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const __grid_constant__ NormArgs a, int group_threads, uint32_t weights_on_grid) {
+// weight and bias come from shared memory where a CTA has rows enough (`stage`):
+// from L1 their reads, of which neighbours' do not lie side by side, take more of
+// its bandwidth than the rows (8.9 M tokens' worth of 7168 bf16 without residual:
+// 80 % of it, and 4.0 TB/s of HBM).
+template <int DT, int U, bool SUM>
+__global__ void __maxnreg__(U * 16 / Elem<DT>::kBytes <= 16 ? 64 : U * 16 / Elem<DT>::kBytes <= 32 ? 80 : 128) norm_kernel(const __grid_constant__ NormArgs a, int group_threads, int weight_dt, uint32_t weights_on_grid, int stage) {
   constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2;
+  extern __shared__ float4 planes[];  // stage: the weight's VEC / 4 planes, then the bias's
   __shared__ float slots[2][kMostGroups][2 * kMostWarps];
   pdl_enter();
   Group group(slots, group_threads);
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
   const int r = part.r, groups = blockDim.x / group_threads, t = threadIdx.x - group.id * group_threads;
   const uint32_t cols = a.cols, units = cols / VEC, row_bytes = cols * Elem<DT>::kBytes;
+  const Vector weight{a.weight[r], weight_dt, weights_on_grid != 0}, bias{a.bias[r], weight_dt, weights_on_grid != 0};
+  float4* const bias_planes = planes + units * (VEC / 4);
+  if (stage) {
+    stage_columns<VEC>(weight, planes, units);
+    if (bias.base != nullptr) stage_columns<VEC>(bias, bias_planes, units);
+    __syncthreads();
+  }
   const float n = static_cast<float>(cols), eps = static_cast<float>(a.eps);
   for (uint32_t row = part.lo + group.id; row < part.hi; row += groups) {
     const uint64_t at = static_cast<uint64_t>(row) * row_bytes;
@@ -244,9 +280,11 @@ __global__ void __maxnreg__(U <= 2 ? 64 : U == 4 ? 80 : 128) norm_kernel(const _
       const uint32_t u = t + i * group_threads;
       if (u >= units) break;
       F2 w[P], b[P];
-      load_weights<WT, VEC>(a.weight[r], u * VEC, weights_on_grid, w);
-      if (a.bias[r] != nullptr) {
-        load_weights<WT, VEC>(a.bias[r], u * VEC, weights_on_grid, b);
+      if (stage) staged_columns<VEC>(planes, units, u, w);
+      else load_columns<VEC>(weight, u * VEC, w);
+      if (bias.base != nullptr) {
+        if (stage) staged_columns<VEC>(bias_planes, units, u, b);
+        else load_columns<VEC>(bias, u * VEC, b);
 #pragma unroll
         for (int k = 0; k < P; ++k) f[i][k] = fma2(mul2(f[i][k], scale), w[k], b[k]);
       } else {
@@ -278,8 +316,8 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 2) norm_off_k
   const int mine = own_columns<G>(cols, t);
   const float n = static_cast<float>(cols), eps = static_cast<float>(a.eps);
   F2 w[H], b[H];
-  load_columns<G, U>(a.weight[r], weight_dt, t, mine, w);
-  load_columns<G, U>(a.bias[r], weight_dt, t, a.bias[r] != nullptr ? mine : 0, b);
+  load_spread<G, U>(a.weight[r], weight_dt, t, mine, w);
+  load_spread<G, U>(a.bias[r], weight_dt, t, a.bias[r] != nullptr ? mine : 0, b);
   for (uint32_t row = part.lo + group.id; row < part.hi; row += groups) {
     const uint64_t at = static_cast<uint64_t>(row) * row_bytes;
     if (t == 0 && part.hi - row > static_cast<uint32_t>(groups)) {
@@ -321,34 +359,6 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 2) norm_off_k
 }
 
 // ------------------------------------------------------------------- backward
-// What a unit of x and dy adds to a row's two sums and to the sums over rows.
-template <int DT, int P>
-__device__ __forceinline__ void add_unit(const uint4& xv, const uint4& dv, const F2* weight, F2 rstd, F2 shift, F2& sg, F2& sgz, F2* dw, F2* db) {
-  const uint32_t x[4] = {xv.x, xv.y, xv.z, xv.w}, dy[4] = {dv.x, dv.y, dv.z, dv.w};
-#pragma unroll
-  for (int k = 0; k < P; ++k) {
-    const F2 z = fma2(widen2<DT>(x, k), rstd, shift), d = widen2<DT>(dy, k), g = mul2(d, weight[k]);
-    sg = add2(sg, g);
-    sgz = fma2(g, z, sgz);
-    dw[k] = fma2(d, z, dw[k]);
-    db[k] = add2(db[k], d);
-  }
-}
-// dx of a unit; means: -mean(g) and -mean(g z).
-template <int DT, int P, bool EXTRA>
-__device__ __forceinline__ void grad_unit(const uint4& xv, const uint4& dv, const uint4& ev, const F2* weight, F2 rstd, F2 shift, F2 mean_g, F2 mean_gz,
-                                          uint32_t* o) {
-  const uint32_t x[4] = {xv.x, xv.y, xv.z, xv.w}, dy[4] = {dv.x, dv.y, dv.z, dv.w}, more[4] = {ev.x, ev.y, ev.z, ev.w};
-  F2 f[P];
-#pragma unroll
-  for (int k = 0; k < P; ++k) {
-    const F2 z = fma2(widen2<DT>(x, k), rstd, shift);
-    f[k] = fma2(z, mean_gz, fma2(widen2<DT>(dy, k), weight[k], mean_g));
-    f[k] = EXTRA ? fma2(f[k], rstd, widen2<DT>(more, k)) : mul2(f[k], rstd);
-  }
-  pack2<DT, P>(f, o);
-}
-
 template <int N>
 __device__ __forceinline__ void spread2(const F2* f, float* v) {
 #pragma unroll
@@ -385,12 +395,12 @@ __device__ __forceinline__ void write_part(const NormArgs& a, const Group& group
   }
 }
 
-// Rows on the 16-byte grid.  A row's units stay in registers between its two
-// walks; with PRE the next row's are on the way there too, and the one after it
-// to L2.
-template <int DT, int WT, int U, bool EXTRA, bool PRE>
-__global__ void __launch_bounds__(512, 1) norm_grad_kernel(const __grid_constant__ NormArgs a, int group_threads, uint32_t weights_on_grid) {
-  constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2, ARRAYS = EXTRA ? 3 : 2;
+// Rows on the 16-byte grid.  z and g stay in registers between the row's two walks;
+// with PRE the next row's units are on the way to registers meanwhile, and the
+// row after it to L2, else the next row to L2.
+template <int DT, int U, bool EXTRA, bool PRE>
+__global__ void __launch_bounds__(512, 1) norm_grad_kernel(const __grid_constant__ NormArgs a, int group_threads, int weight_dt, uint32_t weights_on_grid) {
+  constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2;
   extern __shared__ float shared[];
   __shared__ float slots[2][kMostGroups][2 * kMostWarps];
   pdl_enter();
@@ -400,62 +410,72 @@ __global__ void __launch_bounds__(512, 1) norm_grad_kernel(const __grid_constant
   const uint32_t cols = a.cols, row_bytes = cols * Elem<DT>::kBytes, hop = group_threads * 16;
   const int mine = (static_cast<int>(cols / VEC) - t + group_threads - 1) / group_threads;  // units of the thread
   const float inv = 1.f / static_cast<float>(cols);
+  const Vector weight{a.weight[r], weight_dt, weights_on_grid != 0};
   F2 dw[U][P], db[U][P];
 #pragma unroll
   for (int i = 0; i < U; ++i)
 #pragma unroll
     for (int k = 0; k < P; ++k) dw[i][k] = db[i][k] = both(0.f);
-  const void* const from[3] = {a.x[r], a.dy[r], a.extra[r]};
-  uint4 next[ARRAYS][U];
-  const auto fetch = [&](uint32_t row) {
-    const uint64_t at = static_cast<uint64_t>(row) * row_bytes + t * 16;
+  uint4 x[U], dy[U], extra[U];
+  const auto load = [&](const void* from, uint32_t row, uint4* to) {
+    const char* at = static_cast<const char*>(from) + static_cast<uint64_t>(row) * row_bytes + t * 16;
 #pragma unroll
-    for (int q = 0; q < ARRAYS; ++q)
-#pragma unroll
-      for (int i = 0; i < U; ++i) next[q][i] = i < mine ? ld_once16(static_cast<const char*>(from[q]) + at + i * hop) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < U; ++i) to[i] = i < mine ? ld_once16(at + i * hop) : make_uint4(0, 0, 0, 0);
   };
   // rows are below 2^31, groups few
   uint32_t row = part.lo + group.id;
-  float next_mean = 0.f, next_rstd = 0.f;
-  if (row < part.hi) {
-    if constexpr (PRE) fetch(row);
-    next_mean = a.mean[r][row];
-    next_rstd = a.rstd[r][row];
-  }
+  float mean = 0.f, rstd = 0.f;
+  const auto fetch = [&](uint32_t row) {
+    load(a.x[r], row, x);
+    load(a.dy[r], row, dy);
+    mean = a.mean[r][row];
+    rstd = a.rstd[r][row];
+  };
+  if (PRE && row < part.hi) fetch(row);
   for (; row < part.hi; row += groups) {
-    const uint32_t far = row + (PRE ? 2 : 1) * groups;
-    if (t < ARRAYS && far < part.hi) prefetch_row(t == 0 ? from[0] : t == 1 ? from[1] : from[2], static_cast<uint64_t>(far) * row_bytes, row_bytes);
+    const uint32_t far = row + (PRE ? 2 : 1) * groups, after = row + groups;
+    if (t < (EXTRA ? 3 : 2) && far < part.hi)
+      prefetch_row(t == 0 ? a.x[r] : t == 1 ? a.dy[r] : a.extra[r], static_cast<uint64_t>(far) * row_bytes, row_bytes);
     if constexpr (!PRE) fetch(row);
-    uint4 now[ARRAYS][U];
-#pragma unroll
-    for (int q = 0; q < ARRAYS; ++q)
-#pragma unroll
-      for (int i = 0; i < U; ++i) now[q][i] = next[q][i];
-    const F2 rstd = both(next_rstd), shift = both(-next_mean * next_rstd);
-    const uint32_t after = row + groups;
-    if (after < part.hi) {
-      if constexpr (PRE) fetch(after);
-      next_mean = a.mean[r][after];
-      next_rstd = a.rstd[r][after];
-    }
-    F2 sg = both(0.f), sgz = both(0.f);
+    if constexpr (EXTRA) load(a.extra[r], row, extra);
+    const F2 scale = both(rstd), shift = both(-mean * rstd);
+    F2 z[U][P], g[U][P], sg = both(0.f), sgz = both(0.f);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      if (i >= mine) break;
-      F2 weight[P];
-      load_weights<WT, VEC>(a.weight[r], (t + i * group_threads) * VEC, weights_on_grid, weight);
-      add_unit<DT, P>(now[0][i], now[1][i], weight, rstd, shift, sg, sgz, dw[i], db[i]);
+      F2 w[P];
+      if (i < mine) {
+        load_columns<VEC>(weight, (t + i * group_threads) * VEC, w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < P; ++k) w[k] = both(0.f);
+      }
+      const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, yw[4] = {dy[i].x, dy[i].y, dy[i].z, dy[i].w};
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const F2 d = widen2<DT>(yw, k);
+        z[i][k] = fma2(widen2<DT>(xw, k), scale, shift);
+        dw[i][k] = fma2(d, z[i][k], dw[i][k]);
+        db[i][k] = add2(db[i][k], d);
+        g[i][k] = mul2(d, w[k]);
+        sg = add2(sg, g[i][k]);
+        sgz = fma2(g[i][k], z[i][k], sgz);
+      }
     }
+    if (PRE && after < part.hi) fetch(after);
     const float2 sums = group.sum(total2(sg), total2(sgz));
     const F2 mean_g = both(-sums.x * inv), mean_gz = both(-sums.y * inv);
     char* out = static_cast<char*>(a.out[r]) + static_cast<uint64_t>(row) * row_bytes + t * 16;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (i >= mine) break;
-      F2 weight[P];
-      load_weights<WT, VEC>(a.weight[r], (t + i * group_threads) * VEC, weights_on_grid, weight);
+      const uint32_t more[4] = {extra[i].x, extra[i].y, extra[i].z, extra[i].w};
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        g[i][k] = fma2(z[i][k], mean_gz, add2(g[i][k], mean_g));
+        g[i][k] = EXTRA ? fma2(g[i][k], scale, widen2<DT>(more, k)) : mul2(g[i][k], scale);
+      }
       uint32_t o[4];
-      grad_unit<DT, P, EXTRA>(now[0][i], now[1][i], now[ARRAYS - 1][i], weight, rstd, shift, mean_g, mean_gz, o);
+      pack2<DT, P>(g[i], o);
       st_stream16(out + i * hop, make_uint4(o[0], o[1], o[2], o[3]));
     }
   }
@@ -471,7 +491,7 @@ __global__ void __launch_bounds__(512, 1) norm_grad_kernel(const __grid_constant
 // Rows off the grid, by elements (thread t of G has columns t + G i): the row stays
 // in registers between its two walks, as do the weights.
 template <int DT, int G, int U, bool EXTRA>
-__global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) norm_grad_off_kernel(const __grid_constant__ NormArgs a, int weight_dt) {
+__global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) norm_grad_off_kernel(const __grid_constant__ NormArgs a, int, int weight_dt) {
   constexpr int B = Elem<DT>::kBytes, H = U / 2;
   extern __shared__ float shared[];
   __shared__ float slots[2][kMostGroups][2 * kMostWarps];
@@ -485,7 +505,7 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) 
   F2 dw[H], db[H], weight[H];
 #pragma unroll
   for (int k = 0; k < H; ++k) dw[k] = db[k] = both(0.f);
-  load_columns<G, U>(a.weight[r], weight_dt, t, mine, weight);
+  load_spread<G, U>(a.weight[r], weight_dt, t, mine, weight);
   for (uint32_t row = part.lo + group.id; row < part.hi; row += groups) {
     const uint64_t at = static_cast<uint64_t>(row) * row_bytes;
     if (t == 0 && part.hi - row > static_cast<uint32_t>(groups)) {
@@ -558,13 +578,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid
 }
 
 // ------------------------------------------------------------------ launches
-template <typename F>
-cudaError_t by_types(int dt, int wt, F f) {
-  const auto with = [&](auto d) {
-    return wt == kF32 ? f(d, std::integral_constant<int, kF32>{}) : f(d, std::integral_constant<int, kBF16>{});
-  };
-  return dt == kF32 ? with(std::integral_constant<int, kF32>{}) : with(std::integral_constant<int, kBF16>{});
-}
 template <int N>
 using Int = std::integral_constant<int, N>;
 
@@ -611,8 +624,9 @@ cudaError_t by_columns(uint32_t cols, F f) {
 // The numbers of rows, for cutting them anew; whether a rank has one of the buffers.
 struct Rows {
   size_t n[kMoeMaxRanks];
+  uint64_t total = 0;
   explicit Rows(const NormArgs& a) {
-    for (int r = 0; r < a.p; ++r) n[r] = a.parts.rows[r];
+    for (int r = 0; r < a.p; ++r) total += n[r] = a.parts.rows[r];
   }
 };
 template <typename T>
@@ -641,21 +655,29 @@ cudaError_t launch_norm(int dt, int weight_dt, bool vec, const NormArgs& args, c
     };
     return dt == kF32 ? off(Int<kF32>{}) : off(Int<kBF16>{});
   }
-  return by_types(dt, weight_dt, [&](auto d, auto w) {
-    constexpr int DT = decltype(d)::value, WT = decltype(w)::value;
+  const auto by_type = [&](auto d) {
+    constexpr int DT = decltype(d)::value, VEC = 16 / Elem<DT>::kBytes;
+    const uint32_t units = a.cols / VEC;
     const auto on = [&](auto un) {
       constexpr int U = decltype(un)::value;
-      const int group = whole_warps(a.cols / (16 / Elem<DT>::kBytes), U), groups = group >= 256 ? 1 : 256 / group;
-      // parts small enough that the last ones of a launch end together: 8 x 4096 rows of 7168 with a residual took 323 us
-      // in 2 a SM, 306 in 12, 300 in 24
-      cut_rows(&a.parts, rows.n, a.p, 152 * 24, groups, false);
-      return launch_norm_kernel(sum ? norm_kernel<DT, WT, U, true> : norm_kernel<DT, WT, U, false>, a.parts.first[a.p], group * groups, 0, s, a, group, grid);
+      const int group = whole_warps(units, U), groups = group >= 256 ? 1 : 256 / group;
+      auto* kernel = sum ? norm_kernel<DT, U, true> : norm_kernel<DT, U, false>;
+      // the ends of a launch cost less with small parts, the weights' way into shared memory with large ones: 8 x 4096 rows of
+      // 7168 bf16 with a residual take 303 us in 6 parts a SM, 302 in 12, 298 in 24; 17,438 rows without 206, 214, 227
+      cut_rows(&a.parts, rows.n, a.p, 152 * 12, groups, false);
+      // worth it from four rows a group on
+      const int stage = rows.total >= static_cast<uint64_t>(a.parts.first[a.p]) * groups * 4;
+      const size_t smem = stage ? static_cast<size_t>(a.cols) * 4 * (any_of(a.bias, a.p) ? 2 : 1) : 0;
+      // the limit belongs to the function, not to the call: always the most that a call may need
+      const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kNormMaxCols * 8));
+      if (err != cudaSuccess) return err;
+      return launch_norm_kernel(kernel, a.parts.first[a.p], group * groups, smem, s, a, group, weight_dt, grid, stage);
     };
-    const uint32_t units = a.cols * Elem<DT>::kBytes / 16;
     if (units <= 32) return on(Int<1>{});
     if (units <= 64) return on(Int<2>{});
     return units <= 2048 ? on(Int<4>{}) : on(Int<8>{});
-  });
+  };
+  return dt == kF32 ? by_type(Int<kF32>{}) : by_type(Int<kBF16>{});
 }
 
 cudaError_t launch_norm_grad(int dt, int weight_dt, bool vec, NormArgs* args, cudaStream_t s) {
@@ -663,33 +685,35 @@ cudaError_t launch_norm_grad(int dt, int weight_dt, bool vec, NormArgs* args, cu
   const Rows rows(a);
   const bool extra = any_of(a.extra, a.p);
   const uint32_t grid = weights_on_grid(a);
-  // groups of a CTA are joined through shared memory; two of at most 256 threads leave it below 48 KB
+  // groups of a CTA are joined through shared memory: at most 16 KB, as a row of more has a CTA
   const auto launch = [&](auto* kernel, uint32_t ctas, int group, int groups, auto... more) {
     cut_rows(&a.parts, rows.n, a.p, ctas, groups, false);
-    return launch_norm_kernel(kernel, a.parts.first[a.p], group * groups, groups > 1 ? a.cols * 8 : 0, s, static_cast<const NormArgs&>(a), more...);
+    return launch_norm_kernel(kernel, a.parts.first[a.p], group * groups, groups > 1 ? a.cols * 8 : 0, s, static_cast<const NormArgs&>(a), group, weight_dt, more...);
   };
   if (!vec) {
     const auto off = [&](auto d) {
       constexpr int DT = decltype(d)::value;
       return by_columns(a.cols, [&](auto gr, auto un) {
         constexpr int G = decltype(gr)::value, U = decltype(un)::value, groups = G >= 256 ? 1 : 256 / G;
-        return launch(extra ? norm_grad_off_kernel<DT, G, U, true> : norm_grad_off_kernel<DT, G, U, false>, kNormParts, G, groups, weight_dt);
+        return launch(extra ? norm_grad_off_kernel<DT, G, U, true> : norm_grad_off_kernel<DT, G, U, false>, kNormParts, G, groups);
       });
     };
     return dt == kF32 ? off(Int<kF32>{}) : off(Int<kBF16>{});
   }
-  return by_types(dt, weight_dt, [&](auto d, auto w) {
-    constexpr int DT = decltype(d)::value, WT = decltype(w)::value, VEC = 16 / Elem<DT>::kBytes;
-    const auto on = [&](auto un, auto pre, int most_threads, uint32_t ctas) {
+  const auto by_type = [&](auto d) {
+    constexpr int DT = decltype(d)::value, VEC = 16 / Elem<DT>::kBytes;
+    const auto on = [&](auto un, auto pre, int most) {
       constexpr int U = decltype(un)::value;
       constexpr bool PRE = decltype(pre)::value != 0;
-      const int group = whole_warps(a.cols / VEC, U), groups = group >= most_threads ? 1 : most_threads / group;
-      return launch(extra ? norm_grad_kernel<DT, WT, U, true, PRE> : norm_grad_kernel<DT, WT, U, false, PRE>, ctas, group, groups, group, grid);
+      const int group = whole_warps(a.cols / VEC, U), groups = group >= most ? 1 : most / group;
+      return launch(extra ? norm_grad_kernel<DT, U, true, PRE> : norm_grad_kernel<DT, U, false, PRE>, most == 256 ? kNormParts : kNormParts / 2, group, groups,
+                    grid);
     };
-    if (a.cols <= 256) return on(Int<8 / VEC>{}, Int<1>{}, 256, kNormParts);
-    if (a.cols <= 4096) return on(Int<16 / VEC>{}, Int<1>{}, 256, kNormParts);
-    return a.cols <= 8192 ? on(Int<16 / VEC>{}, Int<1>{}, 512, kNormParts / 2) : on(Int<32 / VEC>{}, Int<0>{}, 512, kNormParts / 2);
-  });
+    if (a.cols <= 256) return on(Int<8 / VEC>{}, Int<1>{}, 256);
+    if (a.cols <= 4096) return on(Int<16 / VEC>{}, Int<1>{}, 256);
+    return a.cols <= 8192 ? on(Int<16 / VEC>{}, Int<1>{}, 512) : on(Int<32 / VEC>{}, Int<0>{}, 512);
+  };
+  return dt == kF32 ? by_type(Int<kF32>{}) : by_type(Int<kBF16>{});
 }
 
 cudaError_t launch_norm_join(int dw_dt, const NormJoinArgs& a, cudaStream_t s) {
