@@ -7,6 +7,7 @@
 // lowest lane has the lowest column.  Columns behind the row are -inf.
 #pragma once
 
+#include "pairs.cuh"
 #include "row_parts.cuh"
 
 namespace ccl {
@@ -83,26 +84,37 @@ __device__ __forceinline__ float lanes_max(float v) {
 }
 template <int L>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
-  if constexpr (L == 32) return __reduce_max_sync(kAllLanes, v);
+  if constexpr (L == 32) {
+    return __reduce_max_sync(kAllLanes, v);
+  } else {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAllLanes, v, o));
-  return v;
+    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAllLanes, v, o));
+    return v;
+  }
 }
 template <int L>
 __device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
-  if constexpr (L == 32) return __reduce_min_sync(kAllLanes, v);
+  if constexpr (L == 32) {
+    return __reduce_min_sync(kAllLanes, v);
+  } else {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(kAllLanes, v, o));
-  return v;
+    for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(kAllLanes, v, o));
+    return v;
+  }
 }
 
 // ------------------------------------------------------------------- scores
-// exp(x), x <= 0: the hardware's power of two of the rounded x log2(e): off by
-// |x| 2^-24 from the product's rounding and two units more, which gates and
-// shares, of fp32, carry on.
-__device__ __forceinline__ float exp_of(float x) {
+// Scores are kept over exp(base), base max(row) for softmax and min(max(row), 0)
+// for sigmoid, so that the row's largest stays away from 0; 0 for a row of -inf.
+//
+// exp(l - base) is the hardware's power of two of the rounded (l - base) log2(e):
+// off by |l - base| 2^-23 and two units more, which gates and shares, of fp32,
+// carry on.  (One fused multiply-add would do for both, but base log2(e) is not
+// finite where a row is masked by the type's lowest value.)
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float power_of_two(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float reciprocal_of(float x) {
@@ -110,23 +122,52 @@ __device__ __forceinline__ float reciprocal_of(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Scores are kept over exp(base), base max(row) for softmax and min(max(row), 0)
-// for sigmoid, so that the row's largest stays away from 0; 0 for a row of -inf.
+// u / v by Markstein's correction of the quotient: u / u is 1 to the bit.
+__device__ __forceinline__ float quotient(float u, float v, float inv) {
+  const float q = u * inv;
+  return fmaf(fmaf(-q, v, u), inv, q);
+}
+__device__ __forceinline__ F2 quotient(F2 u, float v, F2 inv) {
+  const F2 q = mul2(u, inv);
+  return fma2(fma2(q, both(-v), u), inv, q);
+}
 __device__ __forceinline__ float base_of(float top, bool sigmoid) {
   if (top == -INFINITY) return 0.f;
   return sigmoid ? fminf(top, 0.f) : top;
 }
-__device__ __forceinline__ float score_of(float l, float base, bool sigmoid) {
-  if (!sigmoid) return exp_of(l - base);
-  const float t = exp_of(-fabsf(l));
+__device__ __forceinline__ float softmax_score(float l, float base) { return power_of_two((l - base) * kLog2e); }
+__device__ __forceinline__ float sigmoid_score(float l, float base) {
+  const float t = power_of_two(-fabsf(l) * kLog2e);
   // base is 0 for nearly every row
-  const float up = base == 0.f ? (l >= 0.f ? 1.f : t) : exp_of(fminf(l, 0.f) - base);
+  const float up = base == 0.f ? (l >= 0.f ? 1.f : t) : softmax_score(fminf(l, 0.f), base);
   return up * reciprocal_of(1.f + t);
 }
+__device__ __forceinline__ float score_of(float l, float base, bool sigmoid) { return sigmoid ? sigmoid_score(l, base) : softmax_score(l, base); }
 // 1 - sigmoid(l)
 __device__ __forceinline__ float away_of(float l) {
-  const float t = exp_of(-fabsf(l));
+  const float t = power_of_two(-fabsf(l) * kLog2e);
   return (l > 0.f ? t : 1.f) * reciprocal_of(1.f + t);
+}
+// All scores of a lane's columns, in pairs; their sum.
+template <int DT, int NV>
+__device__ __forceinline__ float scores_of(const GateRow<DT, NV>& row, float base, bool sigmoid, F2* u) {
+  F2 sum = both(0.f);
+  if (sigmoid) {
+#pragma unroll
+    for (int k = 0; k < NV / 2; ++k) {
+      u[k] = pair(sigmoid_score(row.value(2 * k), base), sigmoid_score(row.value(2 * k + 1), base));
+      sum = add2(sum, u[k]);
+    }
+  } else {
+    const F2 scale = both(kLog2e), less = both(-base);
+#pragma unroll
+    for (int k = 0; k < NV / 2; ++k) {
+      const float2 x = parts(mul2(add2(pair(row.value(2 * k), row.value(2 * k + 1)), less), scale));
+      u[k] = pair(power_of_two(x.x), power_of_two(x.y));
+      sum = add2(sum, u[k]);
+    }
+  }
+  return total2(sum);
 }
 
 // Lanes of a row that can hold the choices and, eight columns each, the row.

@@ -131,11 +131,11 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
   const int r = part.r;
   int* counts = reinterpret_cast<int*>(shared + kWarps * kRows * L * NV);
-  float sums[NV];
+  F2 sums[NV / 2];
   int live_rows = 0;
   if constexpr (BALANCE) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) sums[i] = 0.f;
+    for (int i = 0; i < NV / 2; ++i) sums[i] = both(0.f);
     for (int i = threadIdx.x; i <= E; i += gate_threads(NV)) counts[i] = 0;
     __syncthreads();
   }
@@ -177,23 +177,18 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
       top = lanes_max<L>(top);
     }
     const float base = base_of(top, sigmoid);
-    float u[NV], total = 0.f;
-    if (BALANCE || !(a.normalize || sigmoid)) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        u[i] = score_of(now.value(i), base, sigmoid);
-        total += u[i];
-      }
-      total = lanes_sum<L>(total);
-    }
+    F2 u[NV / 2];
+    float total = 0.f;
+    if (BALANCE || !(a.normalize || sigmoid)) total = lanes_sum<L>(scores_of<DT, NV>(now, base, sigmoid, u));
     if constexpr (SELECT) {
       float g = 0.f;
       if (a.normalize || !sigmoid) {
         const float own = id >= 0 ? score_of(value, base, sigmoid) : 0.f;
-        const float over = a.normalize ? lanes_sum<L>(own) : total;
-        if (id >= 0) g = over == 0.f ? 0.f : own / over;
+        // no choices from lane KM on
+        const float over = a.normalize ? lanes_sum<(L < KM ? L : KM)>(own) : total;
+        if (id >= 0) g = over == 0.f ? 0.f : quotient(own, over, reciprocal_of(over));
       } else if (id >= 0) {
-        g = score_of(value, 0.f, true);
+        g = sigmoid_score(value, 0.f);
       }
       if (there && lane < k) {
         a.ids[r][item] = id;
@@ -210,14 +205,15 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
         for (int i = 0; i < NV; ++i) live |= !(now.value(i) == -INFINITY);
         live_rows += (__ballot_sync(kAllLanes, live) >> (team * L) & static_cast<unsigned>((1ull << L) - 1)) != 0;
       }
-      const float inv = total == 0.f ? 0.f : 1.f / total;
+      const F2 inv = both(total == 0.f ? 0.f : reciprocal_of(total));
 #pragma unroll
-      for (int i = 0; i < NV; ++i) sums[i] = fmaf(u[i], inv, sums[i]);
+      for (int i = 0; i < NV / 2; ++i) sums[i] = fma2(u[i], inv, sums[i]);
     }
   }
   if constexpr (BALANCE) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) shared[(warp * kRows + team) * (L * NV) + gate_column<L>(lane, i)] = sums[i];
+    for (int i = 0; i < NV; i += 2)
+      *reinterpret_cast<float2*>(shared + (warp * kRows + team) * (L * NV) + gate_column<L>(lane, i)) = parts(sums[i / 2]);
     if (lane == 0) atomicAdd(counts + E, live_rows);
     __syncthreads();
     float* out = a.partial + blockIdx.x * balance_part_words(E);
@@ -233,62 +229,84 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
 }
 
 // One CTA per rank adds up the parts of its own, or of all where the ranks'
-// tokens are one batch: every expert's by as many threads as there are, with the
-// roundings of the additions kept (Knuth's two-sum), then in order; the loss is
-// joined in 64 bits.
+// tokens are one batch: every expert's by as many threads as there are, then in
+// order, and the products with the counts over the experts.  The roundings of all
+// of that are kept beside the sums (Knuth's two-sum, products by a fused
+// multiply-add): additions of 64 bits take 16 times as long here as two of those.
 constexpr int kJoinThreads = 1024;
+struct Kept {
+  float sum = 0.f, rest = 0.f;
+  __device__ __forceinline__ void add(float v) {
+    const float t = sum + v, back = t - sum;
+    rest += (sum - (t - back)) + (v - back);
+    sum = t;
+  }
+  __device__ __forceinline__ void add(const Kept& o) {
+    add(o.sum);
+    rest += o.rest;
+  }
+  __device__ __forceinline__ void add_lanes() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Kept other;
+      other.sum = __shfl_xor_sync(kAllLanes, sum, o);
+      other.rest = __shfl_xor_sync(kAllLanes, rest, o);
+      add(other);
+    }
+  }
+};
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const __grid_constant__ BalanceJoinArgs a) {
-  __shared__ float sums[kJoinThreads], rests[kJoinThreads];
-  __shared__ int numbers[kJoinThreads];
-  __shared__ double warp_sums[kJoinThreads / 32];
-  __shared__ int warp_rows[kJoinThreads / 32];
+  __shared__ Kept sums[kJoinThreads], warp_sums[kJoinThreads / 32];
+  __shared__ int numbers[kJoinThreads], warp_rows[kJoinThreads / 32];
   pdl_enter();
-  const int r = blockIdx.x, E = a.num_experts, tid = threadIdx.x;
+  const int r = blockIdx.x, E = a.num_experts, tid = threadIdx.x, lane = tid & 31;
   const uint32_t lo = a.together ? 0 : a.first[r], hi = a.together ? a.first[a.p] : a.first[r + 1];
   const size_t words = balance_part_words(E);
   const int wide = (E + 31) / 32 * 32, slices = kJoinThreads / wide, e = tid % wide, slice = tid / wide;
-  float s = 0.f, rest = 0.f;
+  Kept s;
   int c = 0;
   if (slice < slices && e < E) {
-#pragma unroll 4
-    for (uint32_t i = lo + slice; i < hi; i += slices) {
-      const float v = a.partial[i * words + e];
-      const float t = s + v, back = t - s;
-      rest += (s - (t - back)) + (v - back);
-      s = t;
-      c += reinterpret_cast<const int*>(a.partial)[i * words + E + e];
+    const float* at = a.partial + (lo + slice) * words + e;
+#pragma unroll 8
+    for (uint32_t i = lo + slice; i < hi; i += slices, at += slices * words) {
+      s.add(at[0]);
+      c += reinterpret_cast<const int*>(at)[E];
     }
   }
-  sums[tid] = s;
-  rests[tid] = rest;
-  numbers[tid] = c;
   int rows = 0;
   for (uint32_t i = lo + tid; i < hi; i += kJoinThreads) rows += reinterpret_cast<const int*>(a.partial)[i * words + 2 * E];
-  rows = __reduce_add_sync(kAllLanes, rows);
-  if ((tid & 31) == 0) warp_rows[tid >> 5] = rows;
+  sums[tid] = s;
+  numbers[tid] = c;
   __syncthreads();
-  double sum = 0.0;
+  Kept product;
   if (tid < E) {
-    c = 0;
-    for (int q = 0; q < slices; ++q) {
-      sum += static_cast<double>(sums[q * wide + tid]) + rests[q * wide + tid];
+    for (int q = 1; q < slices; ++q) {
+      s.add(sums[q * wide + tid]);
       c += numbers[q * wide + tid];
     }
     a.counts[r][tid] = c;
-    sum *= c;
+    // the count in two numbers that are exact
+    const float high = static_cast<float>(c & ~4095), low = static_cast<float>(c & 4095);
+    product.sum = s.sum * high;
+    product.rest = fmaf(s.sum, high, -product.sum) + s.rest * static_cast<float>(c);
+    const float more = s.sum * low;
+    product.rest += fmaf(s.sum, low, -more);
+    product.add(more);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
-  if ((tid & 31) == 0) warp_sums[tid >> 5] = sum;
+  product.add_lanes();
+  rows = __reduce_add_sync(kAllLanes, rows);
+  if (lane == 0) {
+    warp_sums[tid >> 5] = product;
+    warp_rows[tid >> 5] = rows;
+  }
   __syncthreads();
-  if (tid != 0) return;
-  sum = 0.0;
-  rows = 0;
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    sum += warp_sums[w];
-    rows += warp_rows[w];
-  }
+  if (tid >= 32) return;
+  product = warp_sums[lane];
+  product.add_lanes();
+  rows = __reduce_add_sync(kAllLanes, warp_rows[lane]);
+  if (lane != 0) return;
   a.counts[r][E] = rows;
+  const double sum = static_cast<double>(product.sum) + product.rest;
   a.losses[r][0] = rows == 0 ? 0.f : static_cast<float>(sum * E / (static_cast<double>(a.k) * rows * rows));
 }
 

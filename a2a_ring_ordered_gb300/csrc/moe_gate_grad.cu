@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
     for (int i = threadIdx.x & 31; i < 32 * NV; i += 32) spread[warp * 32 * NV + i] = 0.f;
     __syncwarp();
   }
-  float weight[NV];  // a_e, less a constant that changes nothing: E c_e - sum c is exact
+  F2 weight[NV / 2];  // a_e, less a constant that changes nothing: E c_e - sum c is exact
   if constexpr (BALANCE) {
     const int* counts = a.counts[r];
     if (threadIdx.x == 0) {
@@ -44,11 +44,9 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAllLanes, all, o);
     __syncthreads();
+    const auto of = [&](int e) { return e < E ? static_cast<float>(static_cast<long long>(E) * counts[e] - all) * unit : 0.f; };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = gate_column<L>(lane, i);
-      weight[i] = e < E ? static_cast<float>(static_cast<long long>(E) * counts[e] - all) * unit : 0.f;
-    }
+    for (int i = 0; i < NV; i += 2) weight[i / 2] = pair(of(gate_column<L>(lane, i)), of(gate_column<L>(lane, i + 1)));
   }
   uint64_t row0 = part.lo + static_cast<uint64_t>(warp) * kRows;
   GateRow<DT, NV> next;
@@ -78,51 +76,48 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
     }
     float value = -INFINITY;
     if (GATES && id >= 0) value = gate_logit<DT>(a.logits[r], row, E, id);
-    float out[NV], total = 0.f, inv = 0.f, base = 0.f;
+    F2 out[NV / 2];
+    float total = 0.f, inv = 0.f, base = 0.f;
     if (dense) {
       float top = now.value(0);
 #pragma unroll
       for (int i = 1; i < NV; ++i) top = fmaxf(top, now.value(i));
       base = base_of(lanes_max<L>(top), sigmoid);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        out[i] = score_of(now.value(i), base, sigmoid);
-        total += out[i];
-      }
-      total = lanes_sum<L>(total);
-      inv = total == 0.f ? 0.f : 1.f / total;
+      total = lanes_sum<L>(scores_of<DT, NV>(now, base, sigmoid, out));
+      inv = total == 0.f ? 0.f : reciprocal_of(total);
     }
     float own = 0.f, all = 0.f;  // what this lane's choice adds to its column, and to all columns by their shares
     if constexpr (GATES) {
+      constexpr int kMost = L < kMoeMaxK ? L : kMoeMaxK;  // no choices behind them
       if (a.normalize) {
         // over the chosen ones' largest, which may be far below the row's
-        const float chosen_base = base_of(lanes_max<L>(value), sigmoid), u = id >= 0 ? score_of(value, chosen_base, sigmoid) : 0.f;
-        const float over = lanes_sum<L>(u), g = over == 0.f ? 0.f : u / over;
-        const float mean = lanes_sum<L>(g * d);
+        const float chosen_base = base_of(lanes_max<kMost>(value), sigmoid), u = id >= 0 ? score_of(value, chosen_base, sigmoid) : 0.f;
+        const float over = lanes_sum<kMost>(u), g = over == 0.f ? 0.f : quotient(u, over, reciprocal_of(over));
+        const float mean = lanes_sum<kMost>(g * d);
         own = g * (d - mean);
       } else {
-        if (id >= 0) own = sigmoid ? score_of(value, 0.f, true) * d : score_of(value, base, false) * inv * d;
+        if (id >= 0) own = sigmoid ? sigmoid_score(value, 0.f) * d : quotient(softmax_score(value, base), total, inv) * d;
         if (!sigmoid) all = lanes_sum<L>(own);
       }
     }
     if (dense) {
-      // shares; a lone one is 1 to the bit (Markstein's correction of the quotient), so that it has no gradient
-      float mean = 0.f;
+      // shares; a lone one is 1 to the bit, so that it has no gradient
+      F2 mean2 = both(0.f);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const float q = out[i] * inv;
-        out[i] = sigmoid ? fmaf(fmaf(-q, total, out[i]), inv, q) : q;
-        if constexpr (BALANCE) mean = fmaf(out[i], weight[i], mean);
+      for (int i = 0; i < NV / 2; ++i) {
+        out[i] = quotient(out[i], total, both(inv));
+        if constexpr (BALANCE) mean2 = fma2(out[i], weight[i], mean2);
       }
-      if constexpr (BALANCE) mean = lanes_sum<L>(mean);
+      float less = all;
+      if constexpr (BALANCE) less += lanes_sum<L>(total2(mean2));
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if constexpr (BALANCE) out[i] *= (weight[i] - mean) - all;
-        else out[i] *= -all;
+      for (int i = 0; i < NV / 2; ++i) {
+        if constexpr (BALANCE) out[i] = mul2(out[i], add2(weight[i], both(-less)));
+        else out[i] = mul2(out[i], both(-less));
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) out[i] = 0.f;
+      for (int i = 0; i < NV / 2; ++i) out[i] = both(0.f);
     }
     if constexpr (GATES) {
       // an expert that the token has twice is added up by the first lane of it
@@ -141,17 +136,15 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
 #pragma unroll
       for (int i = 0; i < NV; i += 4) {
         const float4 v = *reinterpret_cast<const float4*>(mine + gate_column<L>(lane, i));
-        out[i] += v.x;
-        out[i + 1] += v.y;
-        out[i + 2] += v.z;
-        out[i + 3] += v.w;
+        out[i / 2] = add2(out[i / 2], pair(v.x, v.y));
+        out[i / 2 + 1] = add2(out[i / 2 + 1], pair(v.z, v.w));
       }
       __syncwarp();
       if (first) mine[id] = 0.f;
     }
     if (sigmoid) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) out[i] *= away_of(now.value(i));
+      for (int i = 0; i < NV; i += 2) out[i / 2] = mul2(out[i / 2], pair(away_of(now.value(i)), away_of(now.value(i + 1))));
     }
     if (!there) continue;
     char* to = static_cast<char*>(a.dlogits[r]) + row * E * Elem<DT>::kBytes;
@@ -161,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
       const int c = gate_column<L>(lane, q * kPer);
       if (c >= E) continue;
       uint32_t o[4];
-      pack_out<DT, kPer>(out + q * kPer, o);
+      pack2<DT, kPer / 2>(out + q * kPer / 2, o);
       if (vec) {
         store_raw<DT, kPer>(to, c, o);
       } else {

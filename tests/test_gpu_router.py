@@ -25,13 +25,18 @@ ONE = 2.0 ** -24
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
-def spread(l: np.ndarray) -> float:
-    """A of the tolerances: how far finite logits lie from their row's top, or from 0."""
-    f = np.where(np.isfinite(l), l, 0.0)
-    return float(max(1.0, (f.max(1) - f.min(1)).max(initial=0.0), np.abs(f).max(initial=0.0)))
+def spread(l: np.ndarray) -> np.ndarray:
+    """A of the tolerances, for each row: how far finite logits lie from the row's
+    top, and from 0 (sigmoid); what is further than 104 is 0 in fp32."""
+    finite = np.isfinite(l)
+    top = np.where(finite, l, -np.inf).max(1, initial=-np.inf, keepdims=True)
+    far = np.where(finite, np.where(np.isfinite(top), top, 0.0) - np.where(finite, l, 0.0), 0.0)
+    size = np.where(finite & (np.abs(l) < 104), np.abs(np.where(finite, l, 0.0)), 0.0)
+    return np.maximum(1.0, np.maximum(np.where(far < 104, far, 0.0).max(1, initial=0.0, keepdims=True), size.max(1, initial=0.0, keepdims=True)))
 
 
-def share_tolerance(l: np.ndarray) -> float:
+def share_tolerance(l: np.ndarray) -> np.ndarray:
+    """For each row."""
     return (4 * spread(l) + l.shape[1] / 8 + 32) * ONE
 
 
@@ -111,7 +116,7 @@ def check_losses(losses, logits, n, k, score, together):
         mine = [x for x in logits if x.size] if together else [v]
         want = router.balance_loss(mine, n[r], k, score) if n[r][-1] else 0.0
         rows = max(x.shape[0] for x in logits)
-        tol = max((share_tolerance(x) for x in mine if x.size), default=0.0) + (rows + 8) * ONE
+        tol = max((share_tolerance(x).max() for x in mine if x.size), default=0.0) + (rows + 8) * ONE
         assert abs(losses[r].numpy()[0] - want) <= tol * want
 
 
