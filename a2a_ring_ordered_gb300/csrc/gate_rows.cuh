@@ -136,27 +136,31 @@ __device__ __forceinline__ float base_of(float top, bool sigmoid) {
   return sigmoid ? fminf(top, 0.f) : top;
 }
 __device__ __forceinline__ float softmax_score(float l, float base) { return power_of_two((l - base) * kLog2e); }
-__device__ __forceinline__ float sigmoid_score(float l, float base) {
-  const float t = power_of_two(-fabsf(l) * kLog2e);
-  // base is 0 for nearly every row
-  const float up = base == 0.f ? (l >= 0.f ? 1.f : t) : softmax_score(fminf(l, 0.f), base);
-  return up * reciprocal_of(1.f + t);
-}
+// u, and 1 - sigmoid(l), of one logit; base is 0 for nearly every row.
+struct Sigmoid {
+  float t, r;  // exp(-|l|), 1 / (1 + t)
+  __device__ __forceinline__ explicit Sigmoid(float l) : t(power_of_two(-fabsf(l) * kLog2e)), r(reciprocal_of(1.f + t)) {}
+  __device__ __forceinline__ float score(float l) const { return l >= 0.f ? r : t * r; }
+  __device__ __forceinline__ float score(float l, float base) const { return base == 0.f ? score(l) : softmax_score(fminf(l, 0.f), base) * r; }
+  __device__ __forceinline__ float away(float l) const { return l > 0.f ? t * r : r; }
+};
+__device__ __forceinline__ float sigmoid_score(float l, float base) { return Sigmoid(l).score(l, base); }
 __device__ __forceinline__ float score_of(float l, float base, bool sigmoid) { return sigmoid ? sigmoid_score(l, base) : softmax_score(l, base); }
-// 1 - sigmoid(l)
-__device__ __forceinline__ float away_of(float l) {
-  const float t = power_of_two(-fabsf(l) * kLog2e);
-  return (l > 0.f ? t : 1.f) * reciprocal_of(1.f + t);
-}
-// All scores of a lane's columns, in pairs; their sum.
-template <int DT, int NV>
-__device__ __forceinline__ float scores_of(const GateRow<DT, NV>& row, float base, bool sigmoid, F2* u) {
+// All scores of a lane's columns, in pairs, and their sum; AWAY: and 1 - sigmoid.
+template <int DT, int NV, bool AWAY>
+__device__ __forceinline__ float scores_of(const GateRow<DT, NV>& row, float base, bool sigmoid, F2* u, F2* away) {
   F2 sum = both(0.f);
   if (sigmoid) {
 #pragma unroll
     for (int k = 0; k < NV / 2; ++k) {
-      u[k] = pair(sigmoid_score(row.value(2 * k), base), sigmoid_score(row.value(2 * k + 1), base));
-      sum = add2(sum, u[k]);
+      const float x = row.value(2 * k), y = row.value(2 * k + 1);
+      const Sigmoid a(x), b(y);
+      u[k] = pair(a.score(x), b.score(y));
+      if constexpr (AWAY) away[k] = pair(a.away(x), b.away(y));
+    }
+    if (base != 0.f) {
+#pragma unroll
+      for (int k = 0; k < NV / 2; ++k) u[k] = pair(sigmoid_score(row.value(2 * k), base), sigmoid_score(row.value(2 * k + 1), base));
     }
   } else {
     const F2 scale = both(kLog2e), less = both(-base);
@@ -164,9 +168,10 @@ __device__ __forceinline__ float scores_of(const GateRow<DT, NV>& row, float bas
     for (int k = 0; k < NV / 2; ++k) {
       const float2 x = parts(mul2(add2(pair(row.value(2 * k), row.value(2 * k + 1)), less), scale));
       u[k] = pair(power_of_two(x.x), power_of_two(x.y));
-      sum = add2(sum, u[k]);
     }
   }
+#pragma unroll
+  for (int k = 0; k < NV / 2; ++k) sum = add2(sum, u[k]);
   return total2(sum);
 }
 

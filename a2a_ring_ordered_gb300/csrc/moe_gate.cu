@@ -14,11 +14,11 @@ __host__ __device__ constexpr int gate_threads(int nv) { return nv == 8 ? 512 : 
 
 // A column's place in the order of the choice: the logit's bits made to order as
 // numbers do (-0 as 0, NaN above all), and under them 1023 - column, so that
-// the larger key is the choice's next and keys are unlike.  bf16 fits whole; of
-// fp32 the upper 22 bits do, and choices that these leave open are made again
-// from all bits.  What is below kLeastKey is -inf, and no choice.
+// the larger key is the choice's next and keys are unlike.  bf16 fits whole, into
+// the upper half; of fp32 the upper 22 bits do, and choices that these leave open
+// are made again from all bits.  What is below kLeastKey is -inf, and no choice.
 template <int DT>
-__device__ constexpr uint32_t kLeastKey = DT == kF32 ? 0x2000u << 10 : 0x80u << 10;
+__device__ constexpr uint32_t kLeastKey = DT == kF32 ? 0x2000u << 10 : 0x80u << 16;
 
 __device__ __forceinline__ uint32_t ordered_bits(float l) {
   const uint32_t b = __float_as_uint(l + 0.0f);  // -0 becomes 0, a NaN the canonical one
@@ -36,9 +36,11 @@ __device__ __forceinline__ void make_keys(const GateRow<DT, NV>& row, int lane, 
     for (int i = 0; i < NV; i += 2) {
       const __nv_bfloat162 v = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&row.w[i / 2]), zero);
       const uint32_t b = *reinterpret_cast<const uint32_t*>(&v);
-      const uint32_t o = b ^ (((b >> 15) & 0x00010001u) * 0xFFFFu | 0x80008000u);
-      key[i] = (o & 0xFFFFu) << 10 | static_cast<uint32_t>(1023 - gate_column<L>(lane, i));
-      key[i + 1] = o >> 16 << 10 | static_cast<uint32_t>(1023 - gate_column<L>(lane, i + 1));
+      uint32_t signs;  // of both halves, in all of their bits
+      asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(signs) : "r"(b));
+      const uint32_t o = b ^ (signs | 0x80008000u);
+      key[i] = o * 65536u + static_cast<uint32_t>(1023 - gate_column<L>(lane, i));
+      key[i + 1] = (o & 0xFFFF0000u) | static_cast<uint32_t>(1023 - gate_column<L>(lane, i + 1));
     }
   }
 }
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
         if (__any_sync(kAllLanes, open)) id = choose_exactly<NV, L>(now, lane, k);
         if (id >= 0) value = gate_logit<DT>(a.logits[r], row, E, id);
       } else if (id >= 0) {
-        const uint32_t o = mine >> 10;
+        const uint32_t o = mine >> 16;
         value = __uint_as_float((o & 0x8000u ? o ^ 0x8000u : ~o) << 16);
       }
       top = __shfl_sync(kAllLanes, value, 0, L);
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
     const float base = base_of(top, sigmoid);
     F2 u[NV / 2];
     float total = 0.f;
-    if (BALANCE || !(a.normalize || sigmoid)) total = lanes_sum<L>(scores_of<DT, NV>(now, base, sigmoid, u));
+    if (BALANCE || !(a.normalize || sigmoid)) total = lanes_sum<L>(scores_of<DT, NV, false>(now, base, sigmoid, u, nullptr));
     if constexpr (SELECT) {
       float g = 0.f;
       if (a.normalize || !sigmoid) {
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const __grid
   const int r = blockIdx.x, E = a.num_experts, tid = threadIdx.x, lane = tid & 31;
   const uint32_t lo = a.together ? 0 : a.first[r], hi = a.together ? a.first[a.p] : a.first[r + 1];
   const size_t words = balance_part_words(E);
-  const int wide = (E + 31) / 32 * 32, slices = kJoinThreads / wide, e = tid % wide, slice = tid / wide;
+  const int wide = (E + 31) / 32 * 32, slices = 1 << (31 - __clz(kJoinThreads / wide)), e = tid % wide, slice = tid / wide;
   Kept s;
   int c = 0;
   if (slice < slices && e < E) {
@@ -275,15 +277,20 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const __grid
   }
   int rows = 0;
   for (uint32_t i = lo + tid; i < hi; i += kJoinThreads) rows += reinterpret_cast<const int*>(a.partial)[i * words + 2 * E];
-  sums[tid] = s;
-  numbers[tid] = c;
-  __syncthreads();
+  // halves of the slices onto each other
+  for (int half = slices / 2; half > 0; half /= 2) {
+    if (slice >= half && slice < 2 * half) {
+      sums[tid] = s;
+      numbers[tid] = c;
+    }
+    __syncthreads();
+    if (slice < half) {
+      s.add(sums[tid + half * wide]);
+      c += numbers[tid + half * wide];
+    }
+  }
   Kept product;
   if (tid < E) {
-    for (int q = 1; q < slices; ++q) {
-      s.add(sums[q * wide + tid]);
-      c += numbers[q * wide + tid];
-    }
     a.counts[r][tid] = c;
     // the count in two numbers that are exact
     const float high = static_cast<float>(c & ~4095), low = static_cast<float>(c & 4095);
@@ -306,8 +313,8 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const __grid
   rows = __reduce_add_sync(kAllLanes, warp_rows[lane]);
   if (lane != 0) return;
   a.counts[r][E] = rows;
-  const double sum = static_cast<double>(product.sum) + product.rest;
-  a.losses[r][0] = rows == 0 ? 0.f : static_cast<float>(sum * E / (static_cast<double>(a.k) * rows * rows));
+  const float t = static_cast<float>(rows);
+  a.losses[r][0] = rows == 0 ? 0.f : (product.sum + product.rest) / t * (static_cast<float>(E) / a.k) / t;
 }
 
 }  // namespace

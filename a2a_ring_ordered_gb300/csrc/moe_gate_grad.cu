@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
   // GATES: per warp, what the choices of its rows add to their columns; zeros between rows
   __shared__ __align__(16) float spread[GATES ? kWarps * 32 * NV : 1];
   __shared__ float unit;
+  __shared__ int mean_count, mean_rest;  // sum c = E mean_count + mean_rest
   pdl_enter();
   const int lane = threadIdx.x & (L - 1), warp = threadIdx.x >> 5, team = (threadIdx.x & 31) / L, E = a.num_experts, k = a.k;
   const bool sigmoid = a.score == CCL_SCORE_SIGMOID, vec = a.vec != 0;
@@ -32,19 +33,24 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
     for (int i = threadIdx.x & 31; i < 32 * NV; i += 32) spread[warp * 32 * NV + i] = 0.f;
     __syncwarp();
   }
-  F2 weight[NV / 2];  // a_e, less a constant that changes nothing: E c_e - sum c is exact
+  F2 weight[NV / 2];  // a_e, less a constant that changes nothing: counts near one another do not cancel
   if constexpr (BALANCE) {
     const int* counts = a.counts[r];
-    if (threadIdx.x == 0) {
-      const double t = counts[E] > 0 ? counts[E] : 1.0;
-      unit = static_cast<float>(static_cast<double>(a.dlosses[r] != nullptr ? a.dlosses[r][0] : 1.f) * a.balance_scale / (k * t * t));
-    }
-    long long all = 0;
-    for (int e = threadIdx.x & 31; e < E; e += 32) all += counts[e];
+    if (warp == 0) {
+      long long all = 0;
+      for (int e = threadIdx.x; e < E; e += 32) all += counts[e];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAllLanes, all, o);
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAllLanes, all, o);
+      if (threadIdx.x == 0) {
+        mean_count = static_cast<int>(all / E);
+        mean_rest = static_cast<int>(all - static_cast<long long>(mean_count) * E);
+        const float t = counts[E] > 0 ? static_cast<float>(counts[E]) : 1.f;
+        unit = (a.dlosses[r] != nullptr ? a.dlosses[r][0] : 1.f) * a.balance_scale / t / (t * k);
+      }
+    }
     __syncthreads();
-    const auto of = [&](int e) { return e < E ? static_cast<float>(static_cast<long long>(E) * counts[e] - all) * unit : 0.f; };
+    // E c_e - sum c, times dloss / (k T^2)
+    const auto of = [&](int e) { return e < E ? fmaf(static_cast<float>(counts[e] - mean_count), static_cast<float>(E), -static_cast<float>(mean_rest)) * unit : 0.f; };
 #pragma unroll
     for (int i = 0; i < NV; i += 2) weight[i / 2] = pair(of(gate_column<L>(lane, i)), of(gate_column<L>(lane, i + 1)));
   }
@@ -76,14 +82,14 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
     }
     float value = -INFINITY;
     if (GATES && id >= 0) value = gate_logit<DT>(a.logits[r], row, E, id);
-    F2 out[NV / 2];
+    F2 out[NV / 2], away[NV / 2];
     float total = 0.f, inv = 0.f, base = 0.f;
     if (dense) {
       float top = now.value(0);
 #pragma unroll
       for (int i = 1; i < NV; ++i) top = fmaxf(top, now.value(i));
       base = base_of(lanes_max<L>(top), sigmoid);
-      total = lanes_sum<L>(scores_of<DT, NV>(now, base, sigmoid, out));
+      total = lanes_sum<L>(scores_of<DT, NV, true>(now, base, sigmoid, out, away));
       inv = total == 0.f ? 0.f : reciprocal_of(total);
     }
     float own = 0.f, all = 0.f;  // what this lane's choice adds to its column, and to all columns by their shares
@@ -120,17 +126,19 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
       for (int i = 0; i < NV / 2; ++i) out[i] = both(0.f);
     }
     if constexpr (GATES) {
-      // an expert that the token has twice is added up by the first lane of it
-      const unsigned same = __match_any_sync(kAllLanes, id >= 0 ? team << 16 | id : static_cast<int>(0x80000000u | (threadIdx.x & 31)));
-      const bool first = id >= 0 && __ffs(same) - 1 == static_cast<int>(threadIdx.x & 31);
+      // an expert that the token has twice is added up by the one of its lanes whose number stands there in the end
+      if (id >= 0) mine[id] = __int_as_float(lane);
+      __syncwarp();
+      const bool first = id >= 0 && __float_as_int(mine[id]) == lane;
       if (__any_sync(kAllLanes, id >= 0 && !first)) {
         float s = 0.f;
-        for (int q = 0; q < 32; ++q) {
-          const float v = __shfl_sync(kAllLanes, own, q);
-          if (same >> q & 1) s += v;
+        for (int q = 0; q < L && q < k; ++q) {
+          const float v = __shfl_sync(kAllLanes, own, q, L);
+          if (__shfl_sync(kAllLanes, id, q, L) == id) s += v;
         }
         own = s;
       }
+      __syncwarp();
       if (first) mine[id] = own;
       __syncwarp();
 #pragma unroll
@@ -143,8 +151,13 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
       if (first) mine[id] = 0.f;
     }
     if (sigmoid) {
+      if (!dense) {
 #pragma unroll
-      for (int i = 0; i < NV; i += 2) out[i / 2] = mul2(out[i / 2], pair(away_of(now.value(i)), away_of(now.value(i + 1))));
+        for (int i = 0; i < NV; i += 2)
+          away[i / 2] = pair(Sigmoid(now.value(i)).away(now.value(i)), Sigmoid(now.value(i + 1)).away(now.value(i + 1)));
+      }
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i) out[i] = mul2(out[i], away[i]);
     }
     if (!there) continue;
     char* to = static_cast<char*>(a.dlogits[r]) + row * E * Elem<DT>::kBytes;
