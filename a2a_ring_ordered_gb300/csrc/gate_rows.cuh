@@ -1,7 +1,7 @@
 // gate_rows.cuh -- a token's logits in the registers of a few lanes, shared by
 // the router's kernels.
 //
-// L lanes (a power of two) have a row, NV columns each: eight consecutive ones at
+// L lanes (a power of two), a team, have a row, NV columns each: eight consecutive ones at
 // lane * 8, and where a row has more than 256 columns again at 256, 512, ... of
 // them.  So a lane's columns come by 16-byte loads, and of equal logits the
 // lowest lane has the lowest column.  Columns behind the row are -inf.
@@ -68,6 +68,15 @@ __device__ __forceinline__ float gate_logit(const void* logits, uint64_t row, in
   if constexpr (DT == kF32) return __ldg(static_cast<const float*>(logits) + at);
   else return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const unsigned short*>(logits) + at)) << 16);
 }
+
+// A row's choices have C lanes, so that a warp, which has 32 / L rows at a time,
+// settles the choices of 32 / C rows at once: a batch, of L / C passes.  In pass j a
+// team has the batch's row team * L / C + j, whose choices are in lanes j C .. of the
+// team.  KM: the most choices.
+template <int L, int KM>
+struct GateBatch {
+  static constexpr int kChoices = L < KM ? L : KM, kRows = 32 / kChoices, kPasses = L / kChoices;
+};
 
 // ------------------------------------------------------------ among L lanes
 template <int L>

@@ -60,10 +60,10 @@ __device__ __forceinline__ void sort8(uint32_t* x) {
   order(x[1], x[2]), order(x[3], x[4]), order(x[5], x[6]);
 }
 
-// The key of choice number `lane` (lanes from k on: anything).  `open`: the keys
-// do not tell the choices apart, or the last of them from the next.
+// The key of choice number `slot`, of another slot anything; the largest key.
+// `open`: the keys do not tell the choices apart, or the last of them from the next.
 template <int DT, int NV, int L, int KM>
-__device__ __forceinline__ uint32_t choose(uint32_t* key, int lane, int k, bool& open) {
+__device__ __forceinline__ uint32_t choose(uint32_t* key, int slot, int k, uint32_t& top, bool& open) {
   uint32_t mine = 0, last = 0;
   open = false;
   if constexpr (NV == 8) sort8(key);
@@ -81,7 +81,8 @@ __device__ __forceinline__ uint32_t choose(uint32_t* key, int lane, int k, bool&
     }
     const uint32_t most = lanes_max<L>(head);
     if constexpr (DT == kF32) open |= j > 0 && (most ^ last) < 1024 && most >= kLeastKey<DT>;
-    if (lane == j) mine = most;
+    if (slot == j) mine = most;
+    if (j == 0) top = most;
     last = most;
     if constexpr (NV == 8)
       if (head == most) {
@@ -96,9 +97,9 @@ __device__ __forceinline__ uint32_t choose(uint32_t* key, int lane, int k, bool&
   return mine;
 }
 
-// The same from all 32 bits of each logit.
+// Choice number `slot` from all 32 bits of each logit, or -1.
 template <int NV, int L>
-__device__ __forceinline__ int choose_exactly(const GateRow<kF32, NV>& row, int lane, int k) {
+__device__ __forceinline__ int choose_exactly(const GateRow<kF32, NV>& row, int lane, int slot, int k) {
   uint32_t bits[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) bits[i] = row.value(i) == -INFINITY ? 0 : ordered_bits(row.value(i));
@@ -113,7 +114,7 @@ __device__ __forceinline__ int choose_exactly(const GateRow<kF32, NV>& row, int 
       }
     const uint32_t most = lanes_max<L>(best);
     const uint32_t first = lanes_min<L>(best == most ? at : 0x7FFFFFFF);
-    if (lane == j && most != 0) mine = static_cast<int>(first);
+    if (slot == j && most != 0) mine = static_cast<int>(first);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (gate_column<L>(lane, i) == static_cast<int>(first)) bits[i] = 0;
@@ -121,18 +122,25 @@ __device__ __forceinline__ int choose_exactly(const GateRow<kF32, NV>& row, int 
   return mine;
 }
 
-// VEC (at run time): rows start on 16 bytes.  A warp has 32 / L rows at a time;
-// the next ones are on the way while it works.
+__device__ __forceinline__ float bf16_of_key(uint32_t key) {
+  const uint32_t o = key >> 16;
+  return __uint_as_float((o & 0x8000u ? o ^ 0x8000u : ~o) << 16);
+}
+
+// Every pass chooses in a row and adds its shares; the batch's gates follow, in all
+// lanes.  The next row is on the way meanwhile.
 template <int DT, int L, int NV, int KM, bool SELECT, bool BALANCE>
 __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_constant__ GateArgs a) {
-  constexpr int kRows = 32 / L, kWarps = gate_threads(NV) / 32;
-  extern __shared__ float shared[];  // BALANCE: [kWarps][kRows][L * NV] sums of shares, then E + 1 counts
+  using Batch = GateBatch<L, KM>;
+  constexpr int C = Batch::kChoices, kTeams = 32 / L, kWarps = gate_threads(NV) / 32;
+  extern __shared__ float shared[];  // BALANCE: [kWarps][kTeams][L * NV] sums of shares, then E + 1 counts
   pdl_enter();
   const int lane = threadIdx.x & (L - 1), warp = threadIdx.x >> 5, team = (threadIdx.x & 31) / L, E = a.num_experts, k = a.k;
   const bool sigmoid = a.score == CCL_SCORE_SIGMOID, vec = a.vec != 0;
+  const bool dense = BALANCE || !(a.normalize || sigmoid);  // whether shares, over all of a row, are wanted
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
   const int r = part.r;
-  int* counts = reinterpret_cast<int*>(shared + kWarps * kRows * L * NV);
+  int* counts = reinterpret_cast<int*>(shared + kWarps * kTeams * L * NV);
   F2 sums[NV / 2];
   int live_rows = 0;
   if constexpr (BALANCE) {
@@ -141,88 +149,102 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
     for (int i = threadIdx.x; i <= E; i += gate_threads(NV)) counts[i] = 0;
     __syncthreads();
   }
-  uint64_t row0 = part.lo + static_cast<uint64_t>(warp) * kRows;
+  // rows of the batch that this lane's choice, and this team's pass 0, are in
+  const uint32_t choice_row = (threadIdx.x & 31) / C, team_row = team * Batch::kPasses;
+  uint64_t row0 = part.lo + static_cast<uint64_t>(warp) * Batch::kRows;
   GateRow<DT, NV> next;
-  next.template load<L>(a.logits[r], row0 + team, E, lane, row0 + team < part.hi, vec);
-  for (; row0 < part.hi; row0 += kWarps * kRows) {
-    const uint64_t row = row0 + team, item = row * k + lane;
-    const bool there = row < part.hi;
-    const GateRow<DT, NV> now = next;
-    {
-      const uint64_t ahead = row + kWarps * kRows;
-      next.template load<L>(a.logits[r], ahead, E, lane, ahead < part.hi, vec);
-    }
+  next.template load<L>(a.logits[r], row0 + team_row, E, lane, row0 + team_row < part.hi, vec);
+  for (; row0 < part.hi; row0 += kWarps * Batch::kRows) {
     int id = -1;
-    float value = -INFINITY, top;  // of this lane's choice, of the row
-    if constexpr (SELECT) {
-      uint32_t key[NV];
-      bool open;
-      make_keys<DT, NV, L>(now, lane, key);
-      const uint32_t mine = choose<DT, NV, L, KM>(key, lane, k, open);
-      if (lane < k && mine >= kLeastKey<DT>) id = 1023 - static_cast<int>(mine & 1023u);
-      if constexpr (DT == kF32) {
-        if (__any_sync(kAllLanes, open)) id = choose_exactly<NV, L>(now, lane, k);
-        if (id >= 0) value = gate_logit<DT>(a.logits[r], row, E, id);
-      } else if (id >= 0) {
-        const uint32_t o = mine >> 16;
-        value = __uint_as_float((o & 0x8000u ? o ^ 0x8000u : ~o) << 16);
+    float value = -INFINITY, base = 0.f, total = 0.f;  // of this lane's choice and its row
+#pragma unroll 1
+    for (int j = 0; j < Batch::kPasses; ++j) {
+      const int slot = lane - j * C;  // 0 .. C - 1 in the lanes of this row's choices
+      const GateRow<DT, NV> now = next;
+      {
+        const uint64_t ahead = row0 + team_row + (j + 1 < Batch::kPasses ? j + 1 : kWarps * Batch::kRows);
+        next.template load<L>(a.logits[r], ahead, E, lane, ahead < part.hi, vec);
       }
-      top = __shfl_sync(kAllLanes, value, 0, L);
-    } else {
-      if (there && lane < k) {
-        id = a.ids_in[r][item];
-        if (id >= E) id = -1;
-      }
-      top = now.value(0);
-#pragma unroll
-      for (int i = 1; i < NV; ++i) top = fmaxf(top, now.value(i));
-      top = lanes_max<L>(top);
-    }
-    const float base = base_of(top, sigmoid);
-    F2 u[NV / 2];
-    float total = 0.f;
-    if (BALANCE || !(a.normalize || sigmoid)) total = lanes_sum<L>(scores_of<DT, NV, false>(now, base, sigmoid, u, nullptr));
-    if constexpr (SELECT) {
-      float g = 0.f;
-      if (a.normalize || !sigmoid) {
-        const float own = id >= 0 ? score_of(value, base, sigmoid) : 0.f;
-        // no choices from lane KM on
-        const float over = a.normalize ? lanes_sum<(L < KM ? L : KM)>(own) : total;
-        if (id >= 0) g = over == 0.f ? 0.f : quotient(own, over, reciprocal_of(over));
-      } else if (id >= 0) {
-        g = sigmoid_score(value, 0.f);
-      }
-      if (there && lane < k) {
-        a.ids[r][item] = id;
-        a.gates[r][item] = a.scale * g;
-      }
-    }
-    if constexpr (BALANCE) {
-      if (id >= 0) atomicAdd(counts + id, 1);
+      float top = -INFINITY;
       if constexpr (SELECT) {
-        live_rows += id >= 0;  // counted in lane 0
-      } else {
+        uint32_t key[NV], top_key = 0;
+        bool open;
+        make_keys<DT, NV, L>(now, lane, key);
+        const uint32_t mine = choose<DT, NV, L, KM>(key, slot, k, top_key, open);
+        int chosen = mine >= kLeastKey<DT> ? 1023 - static_cast<int>(mine & 1023u) : -1;
+        if constexpr (DT == kF32)
+          if (__any_sync(kAllLanes, open)) chosen = choose_exactly<NV, L>(now, lane, slot, k);
+        if (slot >= 0 && slot < k) {
+          id = chosen;
+          if constexpr (DT == kBF16)
+            if (id >= 0) value = bf16_of_key(mine);
+        }
+        if constexpr (DT == kBF16) top = top_key >= kLeastKey<DT> ? bf16_of_key(top_key) : -INFINITY;
+        live_rows += top_key >= kLeastKey<DT>;  // counted in lane 0
+      }
+      if (dense) {
+        if constexpr (!SELECT || DT == kF32) {
+          top = now.value(0);
+#pragma unroll
+          for (int i = 1; i < NV; ++i) top = fmaxf(top, now.value(i));
+          top = lanes_max<L>(top);
+        }
+        const float row_base = base_of(top, sigmoid);
+        F2 u[NV / 2];
+        const float row_total = lanes_sum<L>(scores_of<DT, NV, false>(now, row_base, sigmoid, u, nullptr));
+        if (SELECT && slot >= 0 && slot < C) {
+          base = row_base;
+          total = row_total;
+        }
+        if constexpr (BALANCE) {
+          const F2 inv = both(row_total == 0.f ? 0.f : reciprocal_of(row_total));
+#pragma unroll
+          for (int i = 0; i < NV / 2; ++i) sums[i] = fma2(u[i], inv, sums[i]);
+        }
+      }
+      if constexpr (!SELECT) {
         bool live = false;
 #pragma unroll
         for (int i = 0; i < NV; ++i) live |= !(now.value(i) == -INFINITY);
         live_rows += (__ballot_sync(kAllLanes, live) >> (team * L) & static_cast<unsigned>((1ull << L) - 1)) != 0;
       }
-      const F2 inv = both(total == 0.f ? 0.f : reciprocal_of(total));
-#pragma unroll
-      for (int i = 0; i < NV / 2; ++i) sums[i] = fma2(u[i], inv, sums[i]);
     }
+    const int choice = (threadIdx.x & 31) % C;
+    const uint64_t row = row0 + choice_row, item = row * k + choice;
+    const bool there = row < part.hi && choice < k;
+    if constexpr (SELECT) {
+      if constexpr (DT == kF32)
+        if (id >= 0) value = gate_logit<DT>(a.logits[r], row, E, id);
+      float g = 0.f;
+      if (a.normalize) {
+        const float own_base = base_of(__shfl_sync(kAllLanes, value, 0, C), sigmoid), own = id >= 0 ? score_of(value, own_base, sigmoid) : 0.f;
+        const float over = lanes_sum<C>(own);
+        if (id >= 0) g = over == 0.f ? 0.f : quotient(own, over, reciprocal_of(over));
+      } else if (id >= 0) {
+        g = sigmoid ? sigmoid_score(value, 0.f) : quotient(softmax_score(value, base), total, reciprocal_of(total));
+      }
+      if (there) {
+        a.ids[r][item] = id;
+        a.gates[r][item] = a.scale * g;
+      }
+    } else {
+      if (there) id = a.ids_in[r][item];
+      if (id >= E) id = -1;
+    }
+    if constexpr (BALANCE)
+      if (id >= 0) atomicAdd(counts + id, 1);
   }
   if constexpr (BALANCE) {
 #pragma unroll
     for (int i = 0; i < NV; i += 2)
-      *reinterpret_cast<float2*>(shared + (warp * kRows + team) * (L * NV) + gate_column<L>(lane, i)) = parts(sums[i / 2]);
+      *reinterpret_cast<float2*>(shared + (warp * kTeams + team) * (L * NV) + gate_column<L>(lane, i)) = parts(sums[i / 2]);
     if (lane == 0) atomicAdd(counts + E, live_rows);
     __syncthreads();
     float* out = a.partial + blockIdx.x * balance_part_words(E);
     for (int e = threadIdx.x; e <= E; e += gate_threads(NV)) {
       if (e < E) {
         float s = 0.f;
-        for (int w = 0; w < kWarps * kRows; ++w) s += shared[w * (L * NV) + e];
+        for (int w = 0; w < kWarps * kTeams; ++w) s += shared[w * (L * NV) + e];
         out[e] = s;
       }
       reinterpret_cast<int*>(out)[E + e] = counts[e];
@@ -324,18 +346,20 @@ cudaError_t launch_gate(int dt, bool select, bool balance, GateArgs* args, cudaS
   for (int r = 0; r < args->p; ++r) rows[r] = args->parts.rows[r];
   return by_row(dt, args->num_experts, args->k, [&](auto d, auto lanes, auto nv) {
     constexpr int DT = decltype(d)::value, L = decltype(lanes)::value, NV = decltype(nv)::value, kWarps = gate_threads(NV) / 32;
-    // a row of teams at least, then parts for two CTAs a SM
-    cut_rows(&args->parts, rows, args->p, kBalanceParts, kWarps * (32 / L), balance);
     const size_t smem = balance ? (static_cast<size_t>(kWarps) * 32 * NV + args->num_experts + 1) * 4 : 0;
     const auto go = [&](auto km) {
       constexpr int KM = decltype(km)::value;
-      return launch_gate_parts(balance ? gate_kernel<DT, L, NV, KM, true, true> : gate_kernel<DT, L, NV, KM, true, false>, *args, gate_threads(NV), smem, s);
+      // a batch a warp at least, then parts for two CTAs a SM
+      cut_rows(&args->parts, rows, args->p, kBalanceParts, kWarps * GateBatch<L, KM>::kRows, balance);
+      return launch_gate_parts(!select   ? gate_kernel<DT, L, NV, KM, false, true>
+                               : balance ? gate_kernel<DT, L, NV, KM, true, true>
+                                         : gate_kernel<DT, L, NV, KM, true, false>,
+                               *args, gate_threads(NV), smem, s);
     };
-    if (!select) return launch_gate_parts(gate_kernel<DT, L, NV, 0, false, true>, *args, gate_threads(NV), smem, s);
-    if constexpr (NV == 8 && L >= 16) {
+    if constexpr (L >= 16) {
       if (args->k > 8) return go(std::integral_constant<int, 16>{});
     }
-    return go(std::integral_constant<int, NV == 8 ? 8 : 16>{});
+    return go(std::integral_constant<int, 8>{});
   });
 }
 

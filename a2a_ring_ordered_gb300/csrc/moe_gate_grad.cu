@@ -14,10 +14,13 @@
 namespace ccl {
 namespace {
 
-template <int DT, int L, int NV, bool GATES, bool BALANCE>
-__global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_constant__ GateArgs a) {
-  constexpr int kRows = 32 / L, kWarps = kThreads / 32;
-  // GATES: per warp, what the choices of its rows add to their columns; zeros between rows
+// A batch's choices are settled first, in all lanes; then every pass makes a row's
+// gradients.  The next row, and the next batch's choices, are on the way meanwhile.
+template <int DT, int L, int NV, int KM, bool GATES, bool BALANCE>
+__global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : 1) gate_grad_kernel(const __grid_constant__ GateArgs a) {
+  using Batch = GateBatch<L, KM>;
+  constexpr int C = Batch::kChoices, kTeams = 32 / L, kWarps = kThreads / 32;
+  // GATES: of each team, what the choices of its row add to their columns; zeros between rows
   __shared__ __align__(16) float spread[GATES ? kWarps * 32 * NV : 1];
   __shared__ float unit;
   __shared__ int mean_count, mean_rest;  // sum c = E mean_count + mean_rest
@@ -28,7 +31,7 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
   const bool dense = BALANCE || !(a.normalize || sigmoid);
   const RowPart part = row_part(a.parts, a.p, blockIdx.x);
   const int r = part.r;
-  float* mine = spread + (warp * kRows + team) * (L * NV);
+  float* mine = spread + (warp * kTeams + team) * (L * NV);
   if constexpr (GATES) {
     for (int i = threadIdx.x & 31; i < 32 * NV; i += 32) spread[warp * 32 * NV + i] = 0.f;
     __syncwarp();
@@ -54,126 +57,134 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const __grid_consta
 #pragma unroll
     for (int i = 0; i < NV; i += 2) weight[i / 2] = pair(of(gate_column<L>(lane, i)), of(gate_column<L>(lane, i + 1)));
   }
-  uint64_t row0 = part.lo + static_cast<uint64_t>(warp) * kRows;
+  const uint32_t choice_row = (threadIdx.x & 31) / C, choice = (threadIdx.x & 31) % C, team_row = team * Batch::kPasses;
+  uint64_t row0 = part.lo + static_cast<uint64_t>(warp) * Batch::kRows;
   GateRow<DT, NV> next;
-  next.template load<L>(a.logits[r], row0 + team, E, lane, row0 + team < part.hi, vec);
+  next.template load<L>(a.logits[r], row0 + team_row, E, lane, row0 + team_row < part.hi, vec);
   int next_id = -1;
   float next_d = 0.f;
   const auto fetch_choice = [&](uint64_t row) {
     next_id = -1;
     next_d = 0.f;
-    if (lane < k && row < part.hi) {
-      next_id = a.ids_in[r][row * k + lane];
-      next_d = a.dgates[r][row * k + lane];
+    if (choice < k && row < part.hi) {
+      next_id = a.ids_in[r][row * k + choice];
+      next_d = a.dgates[r][row * k + choice];
     }
   };
-  if constexpr (GATES) fetch_choice(row0 + team);
-  for (; row0 < part.hi; row0 += kWarps * kRows) {
-    const uint64_t row = row0 + team, ahead = row + kWarps * kRows;
-    const bool there = row < part.hi;
-    const GateRow<DT, NV> now = next;
+  if constexpr (GATES) fetch_choice(row0 + choice_row);
+  for (; row0 < part.hi; row0 += kWarps * Batch::kRows) {
     int id = next_id;
-    float d = a.scale * next_d;
-    next.template load<L>(a.logits[r], ahead, E, lane, ahead < part.hi, vec);
-    if constexpr (GATES) fetch_choice(ahead);
-    if (id < 0 || id >= E) {
-      id = -1;
-      d = 0.f;  // whatever stands there
-    }
-    float value = -INFINITY;
-    if (GATES && id >= 0) value = gate_logit<DT>(a.logits[r], row, E, id);
-    F2 out[NV / 2], away[NV / 2];
-    float total = 0.f, inv = 0.f, base = 0.f;
-    if (dense) {
-      float top = now.value(0);
-#pragma unroll
-      for (int i = 1; i < NV; ++i) top = fmaxf(top, now.value(i));
-      base = base_of(lanes_max<L>(top), sigmoid);
-      total = lanes_sum<L>(scores_of<DT, NV, true>(now, base, sigmoid, out, away));
-      inv = total == 0.f ? 0.f : reciprocal_of(total);
-    }
-    float own = 0.f, all = 0.f;  // what this lane's choice adds to its column, and to all columns by their shares
+    float own = 0.f, value = -INFINITY, d = 0.f;  // own: what this lane's choice adds to its column
+    bool first = false, twice = false;
     if constexpr (GATES) {
-      constexpr int kMost = L < kMoeMaxK ? L : kMoeMaxK;  // no choices behind them
+      const uint64_t row = row0 + choice_row;
+      if (id < 0 || id >= E) id = -1;
+      if (id >= 0) {
+        d = a.scale * next_d;  // beside a choice that is none stands anything
+        value = gate_logit<DT>(a.logits[r], row, E, id);
+      }
+      fetch_choice(row + kWarps * Batch::kRows);
       if (a.normalize) {
         // over the chosen ones' largest, which may be far below the row's
-        const float chosen_base = base_of(lanes_max<kMost>(value), sigmoid), u = id >= 0 ? score_of(value, chosen_base, sigmoid) : 0.f;
-        const float over = lanes_sum<kMost>(u), g = over == 0.f ? 0.f : quotient(u, over, reciprocal_of(over));
-        const float mean = lanes_sum<kMost>(g * d);
+        const float base = base_of(lanes_max<C>(value), sigmoid), u = id >= 0 ? score_of(value, base, sigmoid) : 0.f;
+        const float over = lanes_sum<C>(u), g = over == 0.f ? 0.f : quotient(u, over, reciprocal_of(over));
+        const float mean = lanes_sum<C>(g * d);
         own = g * (d - mean);
-      } else {
-        if (id >= 0) own = sigmoid ? sigmoid_score(value, 0.f) * d : quotient(softmax_score(value, base), total, inv) * d;
-        if (!sigmoid) all = lanes_sum<L>(own);
+      } else if (sigmoid) {
+        own = id >= 0 ? sigmoid_score(value, 0.f) * d : 0.f;
       }
+      // an expert that the token has twice is added up by the first lane of it
+      bool again = false;
+#pragma unroll
+      for (int o = 1; o < C; ++o) again |= __shfl_xor_sync(kAllLanes, id, o) == id && (choice ^ o) < choice;
+      first = id >= 0 && !again;
+      twice = __any_sync(kAllLanes, id >= 0 && again);
     }
-    if (dense) {
-      // shares; a lone one is 1 to the bit, so that it has no gradient
-      F2 mean2 = both(0.f);
-#pragma unroll
-      for (int i = 0; i < NV / 2; ++i) {
-        out[i] = quotient(out[i], total, both(inv));
-        if constexpr (BALANCE) mean2 = fma2(out[i], weight[i], mean2);
+#pragma unroll 1
+    for (int j = 0; j < Batch::kPasses; ++j) {
+      const uint64_t row = row0 + team_row + j;
+      const int slot = lane - j * C;  // 0 .. C - 1 in the lanes of this row's choices
+      const bool here = slot >= 0 && slot < C, there = row < part.hi;
+      const GateRow<DT, NV> now = next;
+      {
+        const uint64_t ahead = row0 + team_row + (j + 1 < Batch::kPasses ? j + 1 : kWarps * Batch::kRows);
+        next.template load<L>(a.logits[r], ahead, E, lane, ahead < part.hi, vec);
       }
-      float less = all;
-      if constexpr (BALANCE) less += lanes_sum<L>(total2(mean2));
+      F2 out[NV / 2], away[NV / 2];
+      float less = 0.f;  // taken off every column by its share
+      if (dense) {
+        float top = now.value(0);
 #pragma unroll
-      for (int i = 0; i < NV / 2; ++i) {
-        if constexpr (BALANCE) out[i] = mul2(out[i], add2(weight[i], both(-less)));
-        else out[i] = mul2(out[i], both(-less));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV / 2; ++i) out[i] = both(0.f);
-    }
-    if constexpr (GATES) {
-      // an expert that the token has twice is added up by the one of its lanes whose number stands there in the end
-      if (id >= 0) mine[id] = __int_as_float(lane);
-      __syncwarp();
-      const bool first = id >= 0 && __float_as_int(mine[id]) == lane;
-      if (__any_sync(kAllLanes, id >= 0 && !first)) {
-        float s = 0.f;
-        for (int q = 0; q < L && q < k; ++q) {
-          const float v = __shfl_sync(kAllLanes, own, q, L);
-          if (__shfl_sync(kAllLanes, id, q, L) == id) s += v;
+        for (int i = 1; i < NV; ++i) top = fmaxf(top, now.value(i));
+        const float base = base_of(lanes_max<L>(top), sigmoid);
+        const float total = lanes_sum<L>(scores_of<DT, NV, true>(now, base, sigmoid, out, away)), inv = total == 0.f ? 0.f : reciprocal_of(total);
+        if (GATES && !(a.normalize || sigmoid)) {
+          float v = 0.f;
+          if (here && id >= 0) v = own = quotient(softmax_score(value, base), total, inv) * d;
+          less = lanes_sum<L>(v);
         }
-        own = s;
-      }
-      __syncwarp();
-      if (first) mine[id] = own;
-      __syncwarp();
+        // shares; a lone one is 1 to the bit, so that it has no gradient
+        F2 mean = both(0.f);
 #pragma unroll
-      for (int i = 0; i < NV; i += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(mine + gate_column<L>(lane, i));
-        out[i / 2] = add2(out[i / 2], pair(v.x, v.y));
-        out[i / 2 + 1] = add2(out[i / 2 + 1], pair(v.z, v.w));
-      }
-      __syncwarp();
-      if (first) mine[id] = 0.f;
-    }
-    if (sigmoid) {
-      if (!dense) {
+        for (int i = 0; i < NV / 2; ++i) {
+          out[i] = quotient(out[i], total, both(inv));
+          if constexpr (BALANCE) mean = fma2(out[i], weight[i], mean);
+        }
+        if constexpr (BALANCE) less += lanes_sum<L>(total2(mean));
 #pragma unroll
-        for (int i = 0; i < NV; i += 2)
-          away[i / 2] = pair(Sigmoid(now.value(i)).away(now.value(i)), Sigmoid(now.value(i + 1)).away(now.value(i + 1)));
-      }
-#pragma unroll
-      for (int i = 0; i < NV / 2; ++i) out[i] = mul2(out[i], away[i]);
-    }
-    if (!there) continue;
-    char* to = static_cast<char*>(a.dlogits[r]) + row * E * Elem<DT>::kBytes;
-    constexpr int kPer = 16 / Elem<DT>::kBytes;
-#pragma unroll
-    for (int q = 0; q < NV / kPer; ++q) {
-      const int c = gate_column<L>(lane, q * kPer);
-      if (c >= E) continue;
-      uint32_t o[4];
-      pack2<DT, kPer / 2>(out + q * kPer / 2, o);
-      if (vec) {
-        store_raw<DT, kPer>(to, c, o);
+        for (int i = 0; i < NV / 2; ++i) {
+          if constexpr (BALANCE) out[i] = mul2(out[i], add2(weight[i], both(-less)));
+          else out[i] = mul2(out[i], both(-less));
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (c + i < E) store_one<DT>(to, c + i, o, i);
+        for (int i = 0; i < NV / 2; ++i) out[i] = both(0.f);
+      }
+      if constexpr (GATES) {
+        float v = own;
+        if (twice) {
+          v = 0.f;
+          for (int q = 0; q < C; ++q) {
+            const float more = __shfl_sync(kAllLanes, own, q, C);
+            if (__shfl_sync(kAllLanes, id, q, C) == id) v += more;
+          }
+        }
+        if (here && first) mine[id] = v;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+          const float4 more = *reinterpret_cast<const float4*>(mine + gate_column<L>(lane, i));
+          out[i / 2] = add2(out[i / 2], pair(more.x, more.y));
+          out[i / 2 + 1] = add2(out[i / 2 + 1], pair(more.z, more.w));
+        }
+        __syncwarp();
+        if (here && first) mine[id] = 0.f;
+      }
+      if (sigmoid) {
+        if (!dense) {
+#pragma unroll
+          for (int i = 0; i < NV; i += 2)
+            away[i / 2] = pair(Sigmoid(now.value(i)).away(now.value(i)), Sigmoid(now.value(i + 1)).away(now.value(i + 1)));
+        }
+#pragma unroll
+        for (int i = 0; i < NV / 2; ++i) out[i] = mul2(out[i], away[i]);
+      }
+      if (!there) continue;
+      char* to = static_cast<char*>(a.dlogits[r]) + row * E * Elem<DT>::kBytes;
+      constexpr int kPer = 16 / Elem<DT>::kBytes;
+#pragma unroll
+      for (int q = 0; q < NV / kPer; ++q) {
+        const int c = gate_column<L>(lane, q * kPer);
+        if (c >= E) continue;
+        uint32_t o[4];
+        pack2<DT, kPer / 2>(out + q * kPer / 2, o);
+        if (vec) {
+          store_raw<DT, kPer>(to, c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (c + i < E) store_one<DT>(to, c + i, o, i);
+        }
       }
     }
   }
@@ -186,11 +197,18 @@ cudaError_t launch_gate_grad(int dt, bool gates, bool balance, GateArgs* args, c
   for (int r = 0; r < args->p; ++r) rows[r] = args->parts.rows[r];
   return by_row(dt, args->num_experts, gates ? args->k : 1, [&](auto d, auto lanes, auto nv) {
     constexpr int DT = decltype(d)::value, L = decltype(lanes)::value, NV = decltype(nv)::value;
-    cut_rows(&args->parts, rows, args->p, 152 * 8, kThreads / L, false);
-    return launch_gate_parts(!gates    ? gate_grad_kernel<DT, L, NV, false, true>
-                             : balance ? gate_grad_kernel<DT, L, NV, true, true>
-                                       : gate_grad_kernel<DT, L, NV, true, false>,
-                             *args, kThreads, 0, s);
+    const auto go = [&](auto km) {
+      constexpr int KM = decltype(km)::value;
+      cut_rows(&args->parts, rows, args->p, 152 * 8, kThreads / 32 * GateBatch<L, KM>::kRows, false);
+      return launch_gate_parts(!gates    ? gate_grad_kernel<DT, L, NV, KM, false, true>
+                               : balance ? gate_grad_kernel<DT, L, NV, KM, true, true>
+                                         : gate_grad_kernel<DT, L, NV, KM, true, false>,
+                               *args, kThreads, 0, s);
+    };
+    if constexpr (L >= 16) {
+      if (gates && args->k > 8) return go(std::integral_constant<int, 16>{});
+    }
+    return go(std::integral_constant<int, 8>{});
   });
 }
 
