@@ -148,6 +148,10 @@ class _PlainTensors:
         return None
 
     @staticmethod
+    def on_device(device, lists):
+        return None
+
+    @staticmethod
     def places(tuples):
         return [(t.data_ptr(), t.storage_offset(), t.untyped_storage().nbytes(), t.dtype, t.shape, t.stride())
                 for ts in tuples for t in ts]
@@ -912,8 +916,10 @@ def _one_device(first: torch.Tensor, *lists):
     """Refuses lists on another GPU than the first tensor's (a list's own tensors are
     alike, and tensors at all, by the checks that _ranks and _shaped make)."""
     at = first.get_device()
+    if _TENSORS.on_device(at, lists):
+        return
     for ts in lists:
-        if ts and isinstance(ts[0], torch.Tensor) and ts[0].get_device() != at:
+        if ts and isinstance(ts[0], torch.Tensor) and (ts[0].get_device() if ts[0].is_cuda else -1) != at:
             raise ValueError(f"buffers on {ts[0].device} and {first.device} in one call")
 
 
@@ -933,19 +939,18 @@ class _Scratch:
         self.pointer, self.bytes = self.tensor.data_ptr(), self.tensor.numel() * self.tensor.element_size()
 
 
-class _On:
-    """Launches go to the tensors' GPU, whichever is current."""
+_current_gpu = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
-    def __init__(self, first: torch.Tensor):
-        self.guard = torch.cuda.device(first.device) if first.is_cuda and first.get_device() != torch.cuda.current_device() else None
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *error):
-        if self.guard is not None:
-            self.guard.__exit__(*error)
+def _launch(first: torch.Tensor, what: str, function, *args) -> None:
+    """The call, with the tensors' GPU current whichever it was."""
+    if first.get_device() == _current_gpu():
+        status = function(*args)
+    else:
+        with torch.cuda.device(first.device):
+            status = function(*args)
+    if status != CCL_OK:
+        _check(status, what)
 
 
 def _score_code(score: str) -> int:
@@ -980,11 +985,10 @@ def ccl_moe_gate(logits, ids, gates, score: str = "softmax", normalize: bool = T
         counts = _ranks(counts, "counts", p, torch.int32, [experts + 1] * p, 1, True)
         losses = _ranks(losses, "losses", p, torch.float32, [1] * p, 1, True)
     code = _score_code(score)
-    with _On(one):
-        scratch = _Scratch(workspace, ccl_moe_balance_workspace_bytes(p, experts), one, stream) if with_loss else None
-        _check(LIB.ccl_moe_gate(logits, _sizes(tokens), p, k, experts, _dtype_code(one), code, 1 if normalize else 0, scale, packed,
-                                held, 1 if together else 0, counts, losses, scratch and scratch.pointer,
-                                scratch.bytes if scratch else 0, _stream_of(stream, one)), "ccl_moe_gate")
+    scratch = _Scratch(workspace, ccl_moe_balance_workspace_bytes(p, experts), one, stream) if with_loss else None
+    _launch(one, "ccl_moe_gate", LIB.ccl_moe_gate, logits, _sizes(tokens), p, k, experts, _dtype_code(one), code, 1 if normalize else 0, scale,
+            packed, held, 1 if together else 0, counts, losses, scratch and scratch.pointer, scratch.bytes if scratch else 0,
+            _stream_of(stream, one))
 
 
 def ccl_moe_gate_grad(logits, ids, dgates, dlogits, score: str = "softmax", normalize: bool = True, scale: float = 1.0,
@@ -1001,10 +1005,8 @@ def ccl_moe_gate_grad(logits, ids, dgates, dlogits, score: str = "softmax", norm
     _one_device(one, ids, dgates, dlogits, counts, dlosses)
     counts, dlosses = _balance_inputs(counts, dlosses, p, experts)
     code = _score_code(score)
-    with _On(one):
-        _check(LIB.ccl_moe_gate_grad(logits, packed, held, _sizes(tokens), p, k, experts, _dtype_code(one), code,
-                                     1 if normalize else 0, scale, counts, dlosses, balance_scale, out, _stream_of(stream, one)),
-               "ccl_moe_gate_grad")
+    _launch(one, "ccl_moe_gate_grad", LIB.ccl_moe_gate_grad, logits, packed, held, _sizes(tokens), p, k, experts, _dtype_code(one), code,
+            1 if normalize else 0, scale, counts, dlosses, balance_scale, out, _stream_of(stream, one))
 
 
 def _balance_inputs(counts, dlosses, p: int, experts: int):
@@ -1028,10 +1030,9 @@ def ccl_moe_balance(logits, ids, counts, losses, score: str = "softmax", togethe
     counts = _ranks(counts, "counts", p, torch.int32, [experts + 1] * p, 1, True)
     losses = _ranks(losses, "losses", p, torch.float32, [1] * p, 1, True)
     code = _score_code(score)
-    with _On(one):
-        scratch = _Scratch(workspace, ccl_moe_balance_workspace_bytes(p, experts), one, stream)
-        _check(LIB.ccl_moe_balance(logits, packed, _sizes(tokens), p, k, experts, _dtype_code(one), code, 1 if together else 0,
-                                   counts, losses, scratch.pointer, scratch.bytes, _stream_of(stream, one)), "ccl_moe_balance")
+    scratch = _Scratch(workspace, ccl_moe_balance_workspace_bytes(p, experts), one, stream)
+    _launch(one, "ccl_moe_balance", LIB.ccl_moe_balance, logits, packed, _sizes(tokens), p, k, experts, _dtype_code(one), code,
+            1 if together else 0, counts, losses, scratch.pointer, scratch.bytes, _stream_of(stream, one))
 
 
 def ccl_moe_balance_grad(logits, counts, dlogits, k: int, score: str = "softmax", dlosses=None, scale: float = 1.0,
@@ -1044,9 +1045,8 @@ def ccl_moe_balance_grad(logits, counts, dlogits, k: int, score: str = "softmax"
     _one_device(one, counts, dlogits, dlosses)
     counts, dlosses = _balance_inputs(counts, dlosses, p, experts)
     code = _score_code(score)
-    with _On(one):
-        _check(LIB.ccl_moe_balance_grad(logits, counts, dlosses, _sizes(tokens), p, k, experts, _dtype_code(one), code, scale, out,
-                                        _stream_of(stream, one)), "ccl_moe_balance_grad")
+    _launch(one, "ccl_moe_balance_grad", LIB.ccl_moe_balance_grad, logits, counts, dlosses, _sizes(tokens), p, k, experts, _dtype_code(one),
+            code, scale, out, _stream_of(stream, one))
 
 
 # ------------------------------------------------------------------ layer norm
@@ -1072,9 +1072,8 @@ def ccl_layer_norm(x, weight, bias, y, residual=None, sum=None, mean=None, rstd=
     sum = _ranks(sum, "sum", p, dt, rows, cols, True) if sum is not None else None
     mean = _ranks(mean, "mean", p, torch.float32, rows, 1, True) if mean is not None else None
     rstd = _ranks(rstd, "rstd", p, torch.float32, rows, 1, True) if rstd is not None else None
-    with _On(one):
-        _check(LIB.ccl_layer_norm(packed, residual, weight, bias, _sizes(rows), p, cols, eps, _dtype_code(one), _dtype_code(first), out,
-                                  sum, mean, rstd, _stream_of(stream, one)), "ccl_layer_norm")
+    _launch(one, "ccl_layer_norm", LIB.ccl_layer_norm, packed, residual, weight, bias, _sizes(rows), p, cols, eps, _dtype_code(one),
+            _dtype_code(first), out, sum, mean, rstd, _stream_of(stream, one))
 
 
 def ccl_layer_norm_grad_workspace_bytes(p: int, cols: int) -> int:
@@ -1101,11 +1100,10 @@ def ccl_layer_norm_grad(dy, x, weight, mean, rstd, dx, dsum=None, dweight=None, 
     if dbias is not None:
         dbias, held = _vectors(dbias, "dbias", p, cols, None if held is None else held.dtype)
     code = CCL_F32 if held is None else _dtype_code(held)
-    with _On(one):
-        scratch = None if held is None else _Scratch(workspace, ccl_layer_norm_grad_workspace_bytes(p, cols), one, stream)
-        _check(LIB.ccl_layer_norm_grad(grads, dsum, packed, weight, mean, rstd, _sizes(rows), p, cols, _dtype_code(one),
-                                       _dtype_code(first), out, code, dweight, dbias, scratch and scratch.pointer,
-                                       scratch.bytes if scratch else 0, _stream_of(stream, one)), "ccl_layer_norm_grad")
+    scratch = None if held is None else _Scratch(workspace, ccl_layer_norm_grad_workspace_bytes(p, cols), one, stream)
+    _launch(one, "ccl_layer_norm_grad", LIB.ccl_layer_norm_grad, grads, dsum, packed, weight, mean, rstd, _sizes(rows), p, cols, _dtype_code(one),
+            _dtype_code(first), out, code, dweight, dbias, scratch and scratch.pointer, scratch.bytes if scratch else 0,
+            _stream_of(stream, one))
 
 
 # ------------------------------------------------------------------------ AdamW

@@ -351,9 +351,9 @@ struct NormJoinArgs {
 };
 static_assert(sizeof(NormArgs) <= 32764, "norm parameters exceed 32,764 bytes");
 static_assert(sizeof(NormJoinArgs) <= 4096, "norm parameters exceed 4 KB");
-// `vec`: every row starts on 16 bytes
-cudaError_t launch_norm(int dt, int weight_dt, bool vec, const NormArgs& a, cudaStream_t s);
-// Cuts the rows (of which a->parts holds the numbers) into the parts that it leaves in a->parts.
+// Both cut the rows (of which a->parts holds the numbers) into the parts that they
+// leave there.  `vec`: every row starts on 16 bytes.
+cudaError_t launch_norm(int dt, int weight_dt, bool vec, NormArgs* a, cudaStream_t s);
 cudaError_t launch_norm_grad(int dt, int weight_dt, bool vec, NormArgs* a, cudaStream_t s);
 cudaError_t launch_norm_join(int dw_dt, const NormJoinArgs& a, cudaStream_t s);
 

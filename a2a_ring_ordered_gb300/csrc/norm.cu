@@ -638,8 +638,8 @@ bool any_of(const T* const* buffers, int p) {
 
 }  // namespace
 
-cudaError_t launch_norm(int dt, int weight_dt, bool vec, const NormArgs& args, cudaStream_t s) {
-  NormArgs a = args;
+cudaError_t launch_norm(int dt, int weight_dt, bool vec, NormArgs* args, cudaStream_t s) {
+  NormArgs& a = *args;
   const Rows rows(a);
   const bool sum = any_of(a.sum, a.p);
   const uint32_t grid = weights_on_grid(a);
@@ -669,8 +669,10 @@ cudaError_t launch_norm(int dt, int weight_dt, bool vec, const NormArgs& args, c
       const int stage = rows.total >= static_cast<uint64_t>(a.parts.first[a.p]) * groups * 4;
       const size_t smem = stage ? static_cast<size_t>(a.cols) * 4 * (any_of(a.bias, a.p) ? 2 : 1) : 0;
       // the limit belongs to the function, not to the call: always the most that a call may need
-      const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kNormMaxCols * 8));
-      if (err != cudaSuccess) return err;
+      if (smem > 48 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kNormMaxCols * 8));
+        if (err != cudaSuccess) return err;
+      }
       return launch_norm_kernel(kernel, a.parts.first[a.p], group * groups, smem, s, a, group, weight_dt, grid, stage);
     };
     if (units <= 32) return on(Int<1>{});

@@ -337,7 +337,7 @@ extern "C" ccl_status_t ccl_layer_norm(const void* const* x, const void* const* 
   a.cols = static_cast<uint32_t>(cols);
   a.p = p;
   take_rows(&a.parts, rows, p);
-  return launched(launch_norm(dt, weight_dt, on_grid(bits), a, on(stream)), "layer norm kernel");
+  return launched(launch_norm(dt, weight_dt, on_grid(bits), &a, on(stream)), "layer norm kernel");
 }
 
 extern "C" size_t ccl_layer_norm_grad_workspace_bytes(int p, size_t cols) {

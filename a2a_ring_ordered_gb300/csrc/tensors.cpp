@@ -113,6 +113,26 @@ PyObject* shaped(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return all;
 }
 
+// on_device(device, lists) -> whether the first tensor of every list in a tuple
+// of lists (None: no list) is on that GPU; None where one is no such list.
+PyObject* on_device(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 2 || !PyTuple_CheckExact(args[1])) return PyErr_Format(PyExc_TypeError, "on_device() takes a number and a tuple of lists");
+  const Py_ssize_t device = PyLong_AsSsize_t(args[0]);
+  if (PyErr_Occurred() != nullptr) return nullptr;
+  try {
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(args[1]); ++i) {
+      PyObject* ts = PyTuple_GET_ITEM(args[1], i);
+      if (ts == Py_None) continue;
+      if (length(ts) < 0 || !THPVariable_Check(PySequence_Fast_GET_ITEM(ts, 0))) Py_RETURN_NONE;
+      const at::Tensor& t = THPVariable_Unpack(PySequence_Fast_GET_ITEM(ts, 0));
+      if (!t.defined() || !t.is_cuda() || t.get_device() != device) Py_RETURN_FALSE;
+    }
+  } catch (...) {
+    Py_RETURN_NONE;
+  }
+  Py_RETURN_TRUE;
+}
+
 // Where a tensor's elements are, and which.
 struct Place {
   const void* data;  // of its storage
@@ -181,6 +201,7 @@ PyObject* in_place(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {
     {"places", places, METH_O, nullptr},
     {"in_place", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(in_place)), METH_FASTCALL, nullptr},
+    {"on_device", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(on_device)), METH_FASTCALL, nullptr},
     {"ranks", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(ranks)), METH_FASTCALL, nullptr},
     {"shaped", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(shaped)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
