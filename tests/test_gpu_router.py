@@ -266,18 +266,24 @@ def test_same_bits_whatever_the_workspace_held_and_in_a_graph():
     gates = [torch.empty(T + r, k, device="cuda") for r in range(p)]
     counts, losses = [torch.empty(E + 1, dtype=torch.int32, device="cuda") for _ in range(p)], [torch.empty(1, device="cuda") for _ in range(p)]
     ws = torch.full((c.ccl_moe_balance_workspace_bytes(p, E),), 0xFF, dtype=torch.uint8, device="cuda")
-    c.ccl_moe_gate(l, ids, gates, counts=counts, losses=losses, workspace=ws)
-    first = [t.clone() for t in ids + gates + counts + losses]
+    alone = [torch.empty_like(t) for t in counts], [torch.empty_like(t) for t in losses]
+    outs = ids + gates + counts + losses + alone[0] + alone[1]
+
+    def both(**kw):
+        c.ccl_moe_gate(l, ids, gates, counts=counts, losses=losses, **kw)
+        c.ccl_moe_balance(l, ids, *alone)
+
+    both(workspace=ws)
+    first = [t.clone() for t in outs]
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        c.ccl_moe_gate(l, ids, gates, counts=counts, losses=losses, workspace=ws)
-        c.ccl_moe_balance(l, ids, counts, losses)
-    for t in ids + gates + counts + losses:
+        both()
+    for t in outs:
         t.zero_()
     graph.replay()
     graph.replay()
     torch.cuda.synchronize()
-    for a, b in zip(first, ids + gates + counts + losses):
+    for a, b in zip(first, outs):
         assert torch.equal(a, b)
 
 
