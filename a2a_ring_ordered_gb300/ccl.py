@@ -924,18 +924,22 @@ def _one_device(first: torch.Tensor, *lists):
 
 
 class _Scratch:
-    """The workspace of one call: the caller's, or one that torch allocates and
-    keeps until the call's work on `stream` is done."""
+    """The workspace of one call: the caller's, or one that torch allocates for the
+    stream that the call runs on (a block of another stream's may still be in use
+    there)."""
 
     def __init__(self, given, need: int, first: torch.Tensor, stream):
         if given is not None:
             if not given.is_cuda or given.device != first.device or not given.is_contiguous():
                 raise ValueError(f"workspace must be a contiguous tensor on {first.device}")
             self.tensor = given
-        else:
+        elif stream is None:
             self.tensor = torch.empty(need, dtype=torch.uint8, device=first.device)
-            if stream is not None:
-                self.tensor.record_stream(stream)
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=first.device)
+            with torch.cuda.stream(stream):
+                self.tensor = torch.empty(need, dtype=torch.uint8, device=first.device)
         self.pointer, self.bytes = self.tensor.data_ptr(), self.tensor.numel() * self.tensor.element_size()
 
 

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : 1) gate_grad_kernel(co
         next.template load<L>(a.logits[r], ahead, E, lane, ahead < part.hi, vec);
       }
       F2 out[NV / 2], away[NV / 2];
-      float less = 0.f;  // taken off every column by its share
+      float all = 0.f;  // of the gates' part, taken off every column by its share
       if (dense) {
         float top = now.value(0);
 #pragma unroll
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : 1) gate_grad_kernel(co
         if (GATES && !(a.normalize || sigmoid)) {
           float v = 0.f;
           if (here && id >= 0) v = own = quotient(softmax_score(value, base), total, inv) * d;
-          less = lanes_sum<L>(v);
+          all = lanes_sum<L>(v);
         }
         // shares; a lone one is 1 to the bit, so that it has no gradient
         F2 mean = both(0.f);
@@ -130,11 +130,13 @@ __global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : 1) gate_grad_kernel(co
           out[i] = quotient(out[i], total, both(inv));
           if constexpr (BALANCE) mean = fma2(out[i], weight[i], mean);
         }
-        if constexpr (BALANCE) less += lanes_sum<L>(total2(mean));
+        float less = 0.f;
+        if constexpr (BALANCE) less = -lanes_sum<L>(total2(mean));
 #pragma unroll
         for (int i = 0; i < NV / 2; ++i) {
-          if constexpr (BALANCE) out[i] = mul2(out[i], add2(weight[i], both(-less)));
-          else out[i] = mul2(out[i], both(-less));
+          // the loss's part first: of a lone share it is 0, and so is what is left
+          if constexpr (BALANCE) out[i] = mul2(out[i], add2(add2(weight[i], both(less)), both(-all)));
+          else out[i] = mul2(out[i], both(-all));
         }
       } else {
 #pragma unroll

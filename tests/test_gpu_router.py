@@ -234,8 +234,11 @@ def test_one_expert_left_gets_no_gradient():
         out = [torch.empty_like(l)]
         c.ccl_moe_balance_grad([l], counts, out, 3, score=score)
         assert (out[0] == 0).all()
-        c.ccl_moe_gate_grad([l], ids, [torch.randn(40, 3, device="cuda")], out, score=score)
-        assert (out[0] == 0).all()
+        for normalize in (True, False) if score == "softmax" else (True,):
+            c.ccl_moe_gate_grad([l], ids, [torch.randn(40, 3, device="cuda")], out, score=score, normalize=normalize)
+            assert (out[0] == 0).all()
+            c.ccl_moe_gate_grad([l], ids, [torch.randn(40, 3, device="cuda")], out, score=score, normalize=normalize, counts=counts)
+            assert (out[0] == 0).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
