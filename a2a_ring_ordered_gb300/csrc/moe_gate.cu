@@ -64,16 +64,17 @@ __device__ __forceinline__ void sort8(uint32_t* x) {
   order(x[1], x[2]), order(x[3], x[4]), order(x[5], x[6]);
 }
 
-// The key of choice number `slot`, of another slot anything; the largest key.
-// `open`: the keys do not tell the choices apart, or the last of them from the next.
-template <int DT, int NV, int L, int KM>
-__device__ __forceinline__ uint32_t choose(uint32_t* key, int slot, int k, uint32_t& top, bool& open) {
-  uint32_t mine = 0, last = 0;
+// The keys of the k choices, largest first, to `into` (of the team; by the lane whose
+// each is); the largest key.  `open`: the keys do not tell the choices apart, or the
+// last of them from the next.  FULL: k is KM.
+template <int DT, int NV, int L, int KM, bool FULL>
+__device__ __forceinline__ uint32_t choose(uint32_t* key, int k, uint32_t* into, bool& open) {
+  uint32_t top = 0, last = 0;
   open = false;
   if constexpr (NV == 8) sort8(key);
 #pragma unroll
   for (int j = 0; j < KM + (DT == kF32 ? 1 : 0); ++j) {
-    if (j > k || (DT != kF32 && j == k)) break;
+    if (!FULL && (j > k || (DT != kF32 && j == k))) break;
     uint32_t head = key[0];
     if constexpr (NV != 8) {
       // what is left is below the last choice, in every lane
@@ -85,11 +86,11 @@ __device__ __forceinline__ uint32_t choose(uint32_t* key, int slot, int k, uint3
     }
     const uint32_t most = lanes_max<L>(head);
     if constexpr (DT == kF32) open |= j > 0 && (most ^ last) < 1024 && most >= kLeastKey<DT>;
-    if (slot == j) mine = most;
     if (j == 0) top = most;
     last = most;
-    if constexpr (NV == 8)
-      if (head == most) {
+    if (head == most) {
+      if (j < KM && (FULL || DT != kF32 || j < k)) into[j] = most;
+      if constexpr (NV == 8) {
         // no more than the choices that are left can come from here
         constexpr int kLeft = KM + (DT == kF32 ? 1 : 0) - 1;
 #pragma unroll
@@ -97,8 +98,9 @@ __device__ __forceinline__ uint32_t choose(uint32_t* key, int slot, int k, uint3
           if (i < kLeft - j) key[i] = key[i + 1];
         if (7 < KM + 1 - j) key[7] = 0;
       }
+    }
   }
-  return mine;
+  return top;
 }
 
 // Choice number `slot` from all 32 bits of each logit, or -1.
@@ -138,6 +140,7 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
   using Batch = GateBatch<L, KM>;
   constexpr int C = Batch::kChoices, kTeams = 32 / L, kWarps = gate_threads(NV) / 32;
   extern __shared__ float shared[];  // BALANCE: [kWarps][kTeams][L * NV] sums of shares, then E + 1 counts
+  __shared__ uint32_t chosen_keys[SELECT ? kWarps : 1][32];  // of a warp's batch, where its lanes look for their choices
   pdl_enter();
   const int lane = threadIdx.x & (L - 1), warp = threadIdx.x >> 5, team = (threadIdx.x & 31) / L, E = a.num_experts, k = a.k;
   const bool sigmoid = a.score == CCL_SCORE_SIGMOID, vec = a.vec != 0;
@@ -171,19 +174,22 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
       }
       float top = -INFINITY;
       if constexpr (SELECT) {
-        uint32_t key[NV], top_key = 0;
+        uint32_t key[NV];
         bool open;
         make_keys<DT, NV, L>(now, lane, key);
-        const uint32_t mine = choose<DT, NV, L, KM>(key, slot, k, top_key, open);
-        int chosen = mine >= kLeastKey<DT> ? 1023 - static_cast<int>(mine & 1023u) : -1;
-        if constexpr (DT == kF32)
-          if (__any_sync(kAllLanes, open)) chosen = choose_exactly<NV, L>(now, lane, slot, k);
-        if (slot >= 0 && slot < k) {
-          id = chosen;
-          if constexpr (DT == kBF16)
-            if (id >= 0) value = bf16_of_key(mine);
+        uint32_t* const into = chosen_keys[warp] + (threadIdx.x & 31) - lane + j * C;
+        const uint32_t top_key = k == KM ? choose<DT, NV, L, KM, true>(key, k, into, open) : choose<DT, NV, L, KM, false>(key, k, into, open);
+        if constexpr (DT == kF32) {
+          __syncwarp();
+          // by column, as the other way to choose gives them
+          int column = -1;
+          const bool mine = slot >= 0 && slot < k;
+          if (mine && into[slot] >= kLeastKey<DT>) column = 1023 - static_cast<int>(into[slot] & 1023u);
+          if (__any_sync(kAllLanes, open)) column = choose_exactly<NV, L>(now, lane, slot, k);
+          if (mine) id = column;
+        } else {
+          top = top_key >= kLeastKey<DT> ? bf16_of_key(top_key) : -INFINITY;
         }
-        if constexpr (DT == kBF16) top = top_key >= kLeastKey<DT> ? bf16_of_key(top_key) : -INFINITY;
         live_rows += top_key >= kLeastKey<DT>;  // counted in lane 0
       }
       if (dense) {
@@ -217,8 +223,17 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
     const uint64_t row = row0 + choice_row, item = row * k + choice;
     const bool there = row < part.hi && choice < k;
     if constexpr (SELECT) {
-      if constexpr (DT == kF32)
+      if constexpr (DT == kF32) {
         if (id >= 0) value = gate_logit<DT>(a.logits[r], row, E, id);
+      } else {
+        __syncwarp();
+        const uint32_t key = chosen_keys[warp][threadIdx.x & 31];
+        if (choice < k && key >= kLeastKey<DT>) {
+          id = 1023 - static_cast<int>(key & 1023u);
+          value = bf16_of_key(key);
+        }
+        __syncwarp();
+      }
       float g = 0.f;
       if (a.normalize) {
         const float own_base = base_of(__shfl_sync(kAllLanes, value, 0, C), sigmoid), own = id >= 0 ? score_of(value, own_base, sigmoid) : 0.f;

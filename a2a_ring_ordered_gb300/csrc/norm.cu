@@ -309,7 +309,7 @@ __global__ void __maxnreg__(U * 16 / Elem<DT>::kBytes <= 16 ? 64 : U * 16 / Elem
 // Rows off the grid, by elements: thread t of G has columns t + G i, and their
 // weights in registers too.
 template <int DT, int G, int U, bool SUM>
-__global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 2) norm_off_kernel(const __grid_constant__ NormArgs a, int weight_dt) {
+__global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 3) norm_off_kernel(const __grid_constant__ NormArgs a, int weight_dt) {
   constexpr int B = Elem<DT>::kBytes, H = U / 2;
   __shared__ float slots[2][kMostGroups][2 * kMostWarps];
   pdl_enter();
@@ -654,8 +654,9 @@ cudaError_t launch_norm(int dt, int weight_dt, bool vec, NormArgs* args, cudaStr
       constexpr int DT = decltype(d)::value;
       return by_columns(a.cols, [&](auto gr, auto un) {
         constexpr int G = decltype(gr)::value, U = decltype(un)::value, groups = G >= 256 ? 1 : 256 / G;
-        // parts that are all there at once, for their weights' loads: 14,006 fp32 rows of 1019 took 29 us in 2 a SM, 41 in 12
-        cut_rows(&a.parts, rows.n, a.p, 152 * 2, groups, false);
+        // parts that are all there at once, for their weights' loads: 14,006 fp32 rows of 1019 take 22 us in 3 a SM, 28 in 2 or 4,
+        // 41 in 12
+        cut_rows(&a.parts, rows.n, a.p, 152 * 3, groups, false);
         return launch_norm_kernel(sum ? norm_off_kernel<DT, G, U, true> : norm_off_kernel<DT, G, U, false>, a.parts.first[a.p], G * groups, 0, s, a, weight_dt);
       });
     };
