@@ -85,11 +85,30 @@ __device__ __forceinline__ float lanes_sum(float v) {
   for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAllLanes, v, o);
   return v;
 }
+// Two sums by the shuffles of little more than one: half of the lanes take each.
+template <int L>
+__device__ __forceinline__ float2 lanes_sum(float a, float b) {
+  if constexpr (L == 1) {
+    return make_float2(a, b);
+  } else {
+    const bool upper = (threadIdx.x & (L / 2)) != 0;
+    float v = (upper ? b : a) + __shfl_xor_sync(kAllLanes, upper ? a : b, L / 2);
+#pragma unroll
+    for (int o = L / 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAllLanes, v, o);
+    return make_float2(__shfl_sync(kAllLanes, v, 0, L), __shfl_sync(kAllLanes, v, L / 2, L));
+  }
+}
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (L == 32) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(v));  // as fmaxf: numbers before NaN
+    return m;
+  } else {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAllLanes, v, o));
-  return v;
+    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAllLanes, v, o));
+    return v;
+  }
 }
 template <int L>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {

@@ -117,26 +117,50 @@ __global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : 1) gate_grad_kernel(co
 #pragma unroll
         for (int i = 1; i < NV; ++i) top = fmaxf(top, now.value(i));
         const float base = base_of(lanes_max<L>(top), sigmoid);
-        const float total = lanes_sum<L>(scores_of<DT, NV, true>(now, base, sigmoid, out, away)), inv = total == 0.f ? 0.f : reciprocal_of(total);
+        const float part_total = scores_of<DT, NV, true>(now, base, sigmoid, out, away);
+        // The mean of a_e over the shares: for softmax, whose lone score is 1, by a sum over the scores beside theirs
+        F2 product = both(0.f);
+        float total, mean = 0.f, inv;
+        if (BALANCE && !sigmoid) {
+          if constexpr (BALANCE) {
+#pragma unroll
+            for (int i = 0; i < NV / 2; ++i) product = fma2(out[i], weight[i], product);
+          }
+          const float2 sums = lanes_sum<L>(part_total, total2(product));
+          total = sums.x;
+          inv = total == 0.f ? 0.f : reciprocal_of(total);
+          mean = sums.y * inv;
+        } else {
+          total = lanes_sum<L>(part_total);
+          inv = total == 0.f ? 0.f : reciprocal_of(total);
+        }
         if (GATES && !(a.normalize || sigmoid)) {
           float v = 0.f;
-          if (here && id >= 0) v = own = quotient(softmax_score(value, base), total, inv) * d;
+          if (here && id >= 0) v = own = softmax_score(value, base) * inv * d;
           all = lanes_sum<L>(v);
         }
         // shares; a lone one is 1 to the bit, so that it has no gradient
-        F2 mean = both(0.f);
+        if (sigmoid) {
 #pragma unroll
-        for (int i = 0; i < NV / 2; ++i) {
-          out[i] = quotient(out[i], total, both(inv));
-          if constexpr (BALANCE) mean = fma2(out[i], weight[i], mean);
+          for (int i = 0; i < NV / 2; ++i) {
+            out[i] = quotient(out[i], total, both(inv));
+            if constexpr (BALANCE) product = fma2(out[i], weight[i], product);
+          }
+          if constexpr (BALANCE) mean = lanes_sum<L>(total2(product));
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV / 2; ++i) out[i] = mul2(out[i], both(inv));
         }
-        float less = 0.f;
-        if constexpr (BALANCE) less = -lanes_sum<L>(total2(mean));
+        const bool both_parts = GATES && BALANCE && !(a.normalize || sigmoid);
 #pragma unroll
         for (int i = 0; i < NV / 2; ++i) {
-          // the loss's part first: of a lone share it is 0, and so is what is left
-          if constexpr (BALANCE) out[i] = mul2(out[i], add2(add2(weight[i], both(less)), both(-all)));
-          else out[i] = mul2(out[i], both(-all));
+          F2 f = both(-all);
+          if constexpr (BALANCE) {
+            // the loss's part first: of a lone share it is 0, and so is what is left
+            f = add2(weight[i], both(-mean));
+            if (both_parts) f = add2(f, both(-all));
+          }
+          out[i] = mul2(out[i], f);
         }
       } else {
 #pragma unroll
@@ -201,7 +225,8 @@ cudaError_t launch_gate_grad(int dt, bool gates, bool balance, GateArgs* args, c
     constexpr int DT = decltype(d)::value, L = decltype(lanes)::value, NV = decltype(nv)::value;
     const auto go = [&](auto km) {
       constexpr int KM = decltype(km)::value;
-      cut_rows(&args->parts, rows, args->p, 152 * 8, kThreads / 32 * GateBatch<L, KM>::kRows, false);
+      // as many parts as are there at once: 8 x 16384 rows of 256 bf16 took 43 us so, 47 in twice as many, 53 in three quarters
+      cut_rows(&args->parts, rows, args->p, 152 * 4, kThreads / 32 * GateBatch<L, KM>::kRows, false);
       return launch_gate_parts(!gates    ? gate_grad_kernel<DT, L, NV, KM, false, true>
                                : balance ? gate_grad_kernel<DT, L, NV, KM, true, true>
                                          : gate_grad_kernel<DT, L, NV, KM, true, false>,
