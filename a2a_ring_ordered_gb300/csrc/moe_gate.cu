@@ -4,7 +4,11 @@
 // The choice is the k largest logits; gates are u over the chosen ones' sum, or
 // p, or u.  The loss is L = E / (k T^2) sum_e c_e sum_t p_te, c the counts.
 //
-// A row is read once; what bounds this is the instructions of the choice.
+// A row is read once; what bounds this is the instructions of the choice, some 300
+// a row of 256 with top-8 and the loss, half of them on the ALU pipe, which is 80 %
+// busy.  Measured: 8 ranks x 16384 rows of 256 bf16 with the loss 46 us (HBM would
+// take 11), of one rank without it 37; 4 x 20001... rows of 60 fp32, top-6, 10 us; 8 rows
+// 3.0 us in a captured graph.
 #include <cooperative_groups.h>
 
 #include <algorithm>
