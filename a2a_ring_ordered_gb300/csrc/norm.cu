@@ -401,12 +401,15 @@ __device__ __forceinline__ void write_part(const NormArgs& a, const Group& group
 
 // Rows on the 16-byte grid.  z and g stay in registers between the row's two walks;
 // with PRE the next row's units are on the way to registers meanwhile, and the
-// row after it to L2, else the next row to L2.  For 8 x 4096 rows of 7168 bf16 with
-// dsum, 352 us so, a ring of asynchronous copies three rows deep took 410, the
-// second walk from L1 and two rows a SM 447, half the columns a thread 445.
-template <int DT, int U, bool EXTRA, bool PRE>
-__global__ void __launch_bounds__(512, 1) norm_grad_kernel(const __grid_constant__ NormArgs a, int group_threads, int weight_dt, uint32_t weights_on_grid) {
+// row after it to L2, else the next row to L2.  The bounds name the threads that a
+// width takes: the compiler's order of the same instructions for 512 threads cost 15 %
+// at 448.  For 8 x 4096 rows of 7168 bf16 with dsum, 296 us so, a ring of asynchronous
+// copies three rows deep took 410, the second walk from L1 and two rows a SM 447, half
+// the columns a thread 445 (all before the two steps above: 352 us).
+template <int DT, int U, bool EXTRA, bool PRE, int MOST, int PER_SM>
+__global__ void __launch_bounds__(MOST, PER_SM) norm_grad_kernel(const __grid_constant__ NormArgs a, int group_threads, int weight_dt, uint32_t weights_on_grid) {
   constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2;
+  constexpr bool LATE = U * VEC > 8;  // dsum after the first walk, for its registers' sake: 352 -> 323 us
   extern __shared__ float shared[];
   __shared__ float slots[2][kMostGroups][2 * kMostWarps];
   pdl_enter();
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(512, 1) norm_grad_kernel(const __grid_constant
     if (t < (EXTRA ? 3 : 2) && far < part.hi)
       prefetch_row(t == 0 ? a.x[r] : t == 1 ? a.dy[r] : a.extra[r], static_cast<uint64_t>(far) * row_bytes, row_bytes);
     if constexpr (!PRE) fetch(row);
-    if constexpr (EXTRA) load(a.extra[r], row, extra);
+    if (EXTRA && !LATE) load(a.extra[r], row, extra);
     const F2 scale = both(rstd), shift = both(-mean * rstd);
     F2 z[U][P], g[U][P], sg = both(0.f), sgz = both(0.f);
 #pragma unroll
@@ -468,6 +471,7 @@ __global__ void __launch_bounds__(512, 1) norm_grad_kernel(const __grid_constant
       }
     }
     if (PRE && after < part.hi) fetch(after);
+    if (EXTRA && LATE) load(a.extra[r], row, extra);
     const float2 sums = group.sum(total2(sg), total2(sgz));
     const F2 mean_g = both(-sums.x * inv), mean_gz = both(-sums.y * inv);
     char* out = static_cast<char*>(a.out[r]) + static_cast<uint64_t>(row) * row_bytes + t * 16;
@@ -512,7 +516,13 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) 
 #pragma unroll
   for (int k = 0; k < H; ++k) dw[k] = db[k] = both(0.f);
   load_spread<G, U>(a.weight[r], weight_dt, t, mine, weight);
-  for (uint32_t row = part.lo + group.id; row < part.hi; row += groups) {
+  uint32_t row = part.lo + group.id;
+  float next_mean = 0.f, next_rstd = 0.f;
+  if (row < part.hi) {
+    next_mean = a.mean[r][row];
+    next_rstd = a.rstd[r][row];
+  }
+  for (; row < part.hi; row += groups) {
     const uint64_t at = static_cast<uint64_t>(row) * row_bytes;
     if (t == 0 && part.hi - row > static_cast<uint32_t>(groups)) {
       const uint64_t next = at + static_cast<uint64_t>(groups) * row_bytes;
@@ -523,7 +533,11 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) 
     F2 z[H], g[H];  // x and dy first
     load_row<DT, G, U>(static_cast<const char*>(a.x[r]) + at + t * B, mine, z);
     load_row<DT, G, U>(static_cast<const char*>(a.dy[r]) + at + t * B, mine, g);
-    const F2 rstd = both(a.rstd[r][row]), shift = both(-a.mean[r][row] * a.rstd[r][row]);
+    const F2 rstd = both(next_rstd), shift = both(-next_mean * next_rstd);
+    if (part.hi - row > static_cast<uint32_t>(groups)) {
+      next_mean = a.mean[r][row + groups];
+      next_rstd = a.rstd[r][row + groups];
+    }
     F2 sg = both(0.f), sgz = both(0.f);
 #pragma unroll
     for (int k = 0; k < H; ++k) {
@@ -711,16 +725,18 @@ cudaError_t launch_norm_grad(int dt, int weight_dt, bool vec, NormArgs* args, cu
   }
   const auto by_type = [&](auto d) {
     constexpr int DT = decltype(d)::value, VEC = 16 / Elem<DT>::kBytes;
-    const auto on = [&](auto un, auto pre, int most) {
-      constexpr int U = decltype(un)::value;
+    const auto on = [&](auto un, auto pre, auto mt, auto ps) {
+      constexpr int U = decltype(un)::value, MOST = decltype(mt)::value, PER_SM = decltype(ps)::value;
       constexpr bool PRE = decltype(pre)::value != 0;
-      const int group = whole_warps(a.cols / VEC, U), groups = group >= most ? 1 : most / group;
-      return launch(extra ? norm_grad_kernel<DT, U, true, PRE> : norm_grad_kernel<DT, U, false, PRE>, most == 256 ? kNormParts : kNormParts / 2, group, groups,
-                    grid);
+      const int group = whole_warps(a.cols / VEC, U), groups = group >= MOST ? 1 : MOST / group;
+      return launch(extra ? norm_grad_kernel<DT, U, true, PRE, MOST, PER_SM> : norm_grad_kernel<DT, U, false, PRE, MOST, PER_SM>, kNormParts / 2 * PER_SM, group,
+                    groups, grid);
     };
-    if (a.cols <= 256) return on(Int<8 / VEC>{}, Int<1>{}, 256);
-    if (a.cols <= 4096) return on(Int<16 / VEC>{}, Int<1>{}, 256);
-    return a.cols <= 8192 ? on(Int<16 / VEC>{}, Int<1>{}, 512) : on(Int<32 / VEC>{}, Int<0>{}, 512);
+    if (a.cols <= 256) return on(Int<8 / VEC>{}, Int<1>{}, Int<256>{}, Int<2>{});
+    if (a.cols <= 4096) return on(Int<16 / VEC>{}, Int<1>{}, Int<256>{}, Int<2>{});
+    if (a.cols <= 5120) return on(Int<16 / VEC>{}, Int<1>{}, Int<320>{}, Int<1>{});
+    if (a.cols <= 7168) return on(Int<16 / VEC>{}, Int<1>{}, Int<448>{}, Int<1>{});
+    return a.cols <= 8192 ? on(Int<16 / VEC>{}, Int<1>{}, Int<512>{}, Int<1>{}) : on(Int<32 / VEC>{}, Int<0>{}, Int<512>{}, Int<1>{});
   };
   return dt == kF32 ? by_type(Int<kF32>{}) : by_type(Int<kBF16>{});
 }
