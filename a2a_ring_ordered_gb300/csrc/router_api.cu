@@ -413,7 +413,7 @@ extern "C" ccl_status_t ccl_layer_norm_grad(const void* const* dy, const void* c
     spans.add(workspace, need, true);
   }
   if (spans.clash()) return bad("an output overlaps another buffer");
-  a.partial = static_cast<float*>(workspace);
+  a.partial = weights ? static_cast<float*>(workspace) : nullptr;  // one that is not needed has not been looked at
   a.cols = static_cast<uint32_t>(cols);
   a.p = p;
   take_rows(&a.parts, rows, p);

@@ -66,6 +66,37 @@ def test_many_rows(rows, cols, dt):
     assert ((gb.double() - d.sum(0)).abs() <= d.abs().sum(0) * T).all()
 
 
+@pytest.mark.parametrize("dt,wt", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("rows,cols", [(5, 256), (20_011, 512), (3, 7168), (9001, 4096)])
+def test_weights_off_the_grid_of_rows_on_it(rows, cols, dt, wt):
+    """Weight and bias one element off 16 bytes, as a view into a flat buffer may be,
+    few rows and many."""
+    c = ccl()
+    torch.manual_seed(cols)
+    x, dy = torch.randn(rows, cols, device="cuda").to(dt), torch.randn(rows, cols, device="cuda").to(dt)
+    w, b = (torch.randn(cols + 1, device="cuda").to(wt)[1:] for _ in range(2))
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    c.ccl_layer_norm([x], [w], [b], [y], mean=[mean], rstd=[rstd])
+    check_norm(y, x, w, b, 1e-5)
+    c.ccl_layer_norm_grad([dy], [x], [w], [mean], [rstd], [y])
+    check_norm_grad(y, dy, x, w, mean, rstd, None)
+
+
+def test_a_workspace_that_is_not_needed_is_left_alone():
+    """The C call without dweight and dbias takes any workspace, and writes none."""
+    import ctypes
+
+    c = ccl()
+    x, w = torch.randn(40, 64, device="cuda"), torch.ones(64, device="cuda")
+    mean, rstd, dx = torch.zeros(40, device="cuda"), torch.ones(40, device="cuda"), torch.empty(40, 64, device="cuda")
+    held = torch.full((1 << 20,), 5.0, device="cuda")
+    one = lambda t: (ctypes.c_void_p * 1)(t.data_ptr())  # noqa: E731
+    got = c.LIB.ccl_layer_norm_grad(one(x), None, one(x), one(w), one(mean), one(rstd), (ctypes.c_size_t * 1)(40), 1, 64, 0, 0, one(dx), 0, None, None,
+                                    held[1024:].data_ptr(), 16, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert got == c.CCL_OK and (held == 5.0).all()
+
+
 def test_sixty_four_ranks():
     c = ccl()
     torch.manual_seed(0)
