@@ -7,7 +7,7 @@
 // A row is read once; what bounds this is the instructions of the choice, some 300
 // a row of 256 with top-8 and the loss, half of them on the ALU pipe, which is 80 %
 // busy.  Measured: 8 ranks x 16384 rows of 256 bf16 with the loss 46 us (HBM would
-// take 11), of one rank without it 37; 4 x 20001... rows of 60 fp32, top-6, 10 us; 8 rows
+// take 11), of one rank without it 34; 4 x 20001... rows of 60 fp32, top-6, 10 us; 8 rows
 // 3.0 us in a captured graph.
 #include <cooperative_groups.h>
 
@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
           id = 1023 - static_cast<int>(key & 1023u);
           value = bf16_of_key(key);
         }
-        __syncwarp();
       }
+      __syncwarp();  // before the next batch's keys
       float g = 0.f;
       if (a.normalize) {
         const float own_base = base_of(__shfl_sync(kAllLanes, value, 0, C), sigmoid), own = id >= 0 ? score_of(value, own_base, sigmoid) : 0.f;

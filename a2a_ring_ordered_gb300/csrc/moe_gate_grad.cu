@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : 1) gate_grad_kernel(co
         }
         __syncwarp();
         if (here && first) mine[id] = 0.f;
+        __syncwarp();  // before the next row's
       }
       if (sigmoid) {
         if (!dense) {

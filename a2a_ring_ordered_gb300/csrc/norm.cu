@@ -10,8 +10,8 @@
 // between the walks over it; a thread has the same columns of every row that its
 // group takes, so that the sums over rows stay in its registers too.
 // Measured, of 8 ranks x 4096 rows of 7168 bf16 with fp32 weights and a residual:
-// forward 300 us (6.25 TB/s), gradients 352 (5.3); without a residual, 17,438 rows,
-// 214 us (4.7) and 289 (5.2); 14,006 fp32 rows of 1019, off the grid, 28 us (4.0),
+// forward 301 us (6.2 TB/s), gradients 296 (6.35); without a residual, 34,877 rows,
+// 214 us (4.7) and 262 (5.7); 14,006 fp32 rows of 1019, off the grid, 22 us (5.1),
 // gradients of 25,998 bf16 ones 45 us (3.5).
 #include "pairs.cuh"
 #include "row_parts.cuh"
@@ -194,7 +194,7 @@ struct Group {
 // The row stays in registers between its three walks (mean, variance, output).
 // weight and bias come from shared memory where a CTA has rows enough (`stage`):
 // from L1, where a lane's eight fp32 columns lie 32 bytes from its neighbour's, they
-// took 80 % of its bandwidth and 252 us for 17,438 rows of 7168 bf16, 214 so.
+// took 80 % of its bandwidth and 252 us for 34,877 rows of 7168 bf16, 214 so.
 template <int DT, int U, bool SUM>
 __global__ void __maxnreg__(U * 16 / Elem<DT>::kBytes <= 16 ? 64 : U * 16 / Elem<DT>::kBytes <= 32 ? 80 : 128) norm_kernel(const __grid_constant__ NormArgs a, int group_threads, int weight_dt, uint32_t weights_on_grid, int stage) {
   constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2;
@@ -627,7 +627,6 @@ uint32_t weights_on_grid(const NormArgs& a) {
   return (bits & 15) == 0;
 }
 
-
 // Calls f(G, U) with the threads a row off the grid gets and the columns that each
 // has.
 template <typename F>
@@ -684,7 +683,7 @@ cudaError_t launch_norm(int dt, int weight_dt, bool vec, NormArgs* args, cudaStr
       const int group = whole_warps(units, U), groups = group >= 256 ? 1 : 256 / group;
       auto* kernel = sum ? norm_kernel<DT, U, true> : norm_kernel<DT, U, false>;
       // the ends of a launch cost less with small parts, the weights' way into shared memory with large ones: 8 x 4096 rows of
-      // 7168 bf16 with a residual take 303 us in 6 parts a SM, 302 in 12, 298 in 24; 17,438 rows without 206, 214, 227
+      // 7168 bf16 with a residual take 303 us in 6 parts a SM, 302 in 12, 298 in 24; 34,877 rows without 206, 214, 227
       cut_rows(&a.parts, rows.n, a.p, 152 * 12, groups, false);
       // worth it from four rows a group on
       const int stage = rows.total >= static_cast<uint64_t>(a.parts.first[a.p]) * groups * 4;
