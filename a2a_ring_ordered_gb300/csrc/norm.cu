@@ -12,7 +12,7 @@
 // Measured, of 8 ranks x 4096 rows of 7168 bf16 with fp32 weights and a residual:
 // forward 301 us (6.2 TB/s), gradients 296 (6.35); without a residual, 34,877 rows,
 // 214 us (4.7) and 262 (5.7); 14,006 fp32 rows of 1019, off the grid, 22 us (5.1),
-// gradients of 25,998 bf16 ones 45 us (3.5).
+// gradients of 25,998 bf16 ones 47 us (3.4).
 #include "pairs.cuh"
 #include "row_parts.cuh"
 
