@@ -8,11 +8,12 @@
 // Rows move once in each direction, so HBM bounds all of it, where enough loads are
 // under way.  A group of one or more warps has a row, which stays in registers
 // between the walks over it; a thread has the same columns of every row that its
-// group takes, so that the sums over rows stay in its registers too.
+// group takes, so that the sums over rows stay in its registers too, or in its own
+// slots of shared memory where it has 32 columns.
 // Measured, of 8 ranks x 4096 rows of 7168 bf16 with fp32 weights and a residual:
 // forward 301 us (6.2 TB/s), gradients 296 (6.35); without a residual, 34,877 rows,
 // 214 us (4.7) and 262 (5.7); 14,006 fp32 rows of 1019, off the grid, 22 us (5.1),
-// gradients of 25,998 bf16 ones 47 us (3.4).
+// gradients of 25,998 bf16 ones 42 us (3.8).
 #include "pairs.cuh"
 #include "row_parts.cuh"
 
@@ -99,19 +100,41 @@ template <int G>
 __device__ __forceinline__ int own_columns(uint32_t cols, int t) {
   return static_cast<int>(cols / G) + (t < static_cast<int>(cols % G) ? 1 : 0);
 }
+// Of U, as many as every thread has by the choice of G and U (by_columns), which
+// need no look at `mine`: 1019 columns of bf16 forward 3.8 -> 4.2 TB/s.
+template <int G, int U>
+constexpr int kSure = G >= 64 ? U / 2 : U >= 16 ? U / 4 : 0;
 template <int DT, int G, int U>
 __device__ __forceinline__ void load_row(const char* at, int mine, F2* f) {
   float v[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     v[i] = 0.f;
-    if (i < mine) {
+    if (i < kSure<G, U> || i < mine) {
       if constexpr (DT == kF32) v[i] = reinterpret_cast<const float*>(at)[i * G];
       else v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(at)[i * G]);
     }
   }
 #pragma unroll
   for (int k = 0; k < U / 2; ++k) f[k] = pair(v[2 * k], v[2 * k + 1]);
+}
+// The same in two steps: the elements' bits, and the columns of these.
+template <int DT, int G, int U>
+__device__ __forceinline__ void load_bits(const char* at, int mine, uint32_t* v) {
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    v[i] = 0;
+    if (i < kSure<G, U> || i < mine) {
+      if constexpr (DT == kF32) v[i] = reinterpret_cast<const uint32_t*>(at)[i * G];
+      else v[i] = reinterpret_cast<const unsigned short*>(at)[i * G];
+    }
+  }
+}
+template <int DT, int U>
+__device__ __forceinline__ void floats_of(const uint32_t* v, F2* f) {
+  constexpr int kShift = DT == kF32 ? 0 : 16;
+#pragma unroll
+  for (int k = 0; k < U / 2; ++k) f[k] = pair(__uint_as_float(v[2 * k] << kShift), __uint_as_float(v[2 * k + 1] << kShift));
 }
 template <int G, int U>
 __device__ __forceinline__ void load_spread(const void* base, int dt, int t, int mine, F2* f) {
@@ -135,8 +158,8 @@ __device__ __forceinline__ void store_row(char* at, int mine, const F2* f) {
   for (int k = 0; k < U / 2; ++k) {
     uint32_t o[2];
     pack2<DT, 1>(f + k, o);
-    if (2 * k < mine) store_one<DT>(at, 2 * k * G, o, 0);
-    if (2 * k + 1 < mine) store_one<DT>(at, (2 * k + 1) * G, o, 1);
+    if (2 * k < kSure<G, U> || 2 * k < mine) store_one<DT>(at, 2 * k * G, o, 0);
+    if (2 * k + 1 < kSure<G, U> || 2 * k + 1 < mine) store_one<DT>(at, (2 * k + 1) * G, o, 1);
   }
 }
 
@@ -321,7 +344,12 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 ? 1 : 3) norm_off_k
   const float n = static_cast<float>(cols), eps = static_cast<float>(a.eps);
   F2 w[H], b[H];
   load_spread<G, U>(a.weight[r], weight_dt, t, mine, w);
-  load_spread<G, U>(a.bias[r], weight_dt, t, a.bias[r] != nullptr ? mine : 0, b);
+  if (a.bias[r] != nullptr) {
+    load_spread<G, U>(a.bias[r], weight_dt, t, mine, b);
+  } else {
+#pragma unroll
+    for (int k = 0; k < H; ++k) b[k] = both(0.f);
+  }
   for (uint32_t row = part.lo + group.id; row < part.hi; row += groups) {
     const uint64_t at = static_cast<uint64_t>(row) * row_bytes;
     if (t == 0 && part.hi - row > static_cast<uint32_t>(groups)) {
@@ -399,6 +427,37 @@ __device__ __forceinline__ void write_part(const NormArgs& a, const Group& group
   }
 }
 
+// The sums over rows of threads with 32 columns, which registers do not hold beside z
+// and g: four columns to a slot, a thread's own, in planes over the threads.  Only
+// where a CTA is one group.  12,288 columns of bf16 go at 4.2 TB/s so (5.3 with dsum),
+// 10,001 at 2.6; spilled by the compiler, at 3.4 (4.05) and 1.15.
+template <int Q>
+struct SharedSums {
+  float4 *w, *b;
+  int threads;
+  __device__ __forceinline__ SharedSums(float* shared, int group_threads, int t)
+      : w(reinterpret_cast<float4*>(shared) + t), b(w + Q * group_threads), threads(group_threads) {}
+  __device__ __forceinline__ void clear() const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) w[q * threads] = b[q * threads] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void add(int q, F2 d0, F2 d1, F2 z0, F2 z1) const {
+    const float4 sw = w[q * threads], sb = b[q * threads];
+    const float2 w0 = parts(fma2(d0, z0, pair(sw.x, sw.y))), w1 = parts(fma2(d1, z1, pair(sw.z, sw.w)));
+    const float2 b0 = parts(add2(d0, pair(sb.x, sb.y))), b1 = parts(add2(d1, pair(sb.z, sb.w)));
+    w[q * threads] = make_float4(w0.x, w0.y, w1.x, w1.y);
+    b[q * threads] = make_float4(b0.x, b0.y, b1.x, b1.y);
+  }
+  __device__ __forceinline__ void get(float* all_w, float* all_b) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const float4 sw = w[q * threads], sb = b[q * threads];
+      all_w[4 * q] = sw.x, all_w[4 * q + 1] = sw.y, all_w[4 * q + 2] = sw.z, all_w[4 * q + 3] = sw.w;
+      all_b[4 * q] = sb.x, all_b[4 * q + 1] = sb.y, all_b[4 * q + 2] = sb.z, all_b[4 * q + 3] = sb.w;
+    }
+  }
+};
+
 // Rows on the 16-byte grid.  z and g stay in registers between the row's two walks;
 // with PRE the next row's units are on the way to registers meanwhile, and the
 // row after it to L2, else the next row to L2.  The bounds name the threads that a
@@ -420,11 +479,17 @@ __global__ void __launch_bounds__(MOST, PER_SM) norm_grad_kernel(const __grid_co
   const int mine = (static_cast<int>(cols / VEC) - t + group_threads - 1) / group_threads;  // units of the thread
   const float inv = 1.f / static_cast<float>(cols);
   const Vector weight{a.weight[r], weight_dt, weights_on_grid != 0};
-  F2 dw[U][P], db[U][P];
+  constexpr bool HELD = U * VEC <= 16;
+  F2 dw[HELD ? U : 1][P], db[HELD ? U : 1][P];
+  const SharedSums<U * VEC / 4> away(shared, group_threads, t);
+  if constexpr (HELD) {
 #pragma unroll
-  for (int i = 0; i < U; ++i)
+    for (int i = 0; i < U; ++i)
 #pragma unroll
-    for (int k = 0; k < P; ++k) dw[i][k] = db[i][k] = both(0.f);
+      for (int k = 0; k < P; ++k) dw[i][k] = db[i][k] = both(0.f);
+  } else {
+    away.clear();
+  }
   uint4 x[U], dy[U], extra[U];
   const auto load = [&](const void* from, uint32_t row, uint4* to) {
     const char* at = static_cast<const char*>(from) + static_cast<uint64_t>(row) * row_bytes + t * 16;
@@ -463,8 +528,12 @@ __global__ void __launch_bounds__(MOST, PER_SM) norm_grad_kernel(const __grid_co
       for (int k = 0; k < P; ++k) {
         const F2 d = widen2<DT>(yw, k);
         z[i][k] = fma2(widen2<DT>(xw, k), scale, shift);
-        dw[i][k] = fma2(d, z[i][k], dw[i][k]);
-        db[i][k] = add2(db[i][k], d);
+        if constexpr (HELD) {
+          dw[i][k] = fma2(d, z[i][k], dw[i][k]);
+          db[i][k] = add2(db[i][k], d);
+        } else if (k % 2 == 1) {
+          away.add(i * P / 2 + k / 2, widen2<DT>(yw, k - 1), d, z[i][k - 1], z[i][k]);
+        }
         g[i][k] = mul2(d, w[k]);
         sg = add2(sg, g[i][k]);
         sgz = fma2(g[i][k], z[i][k], sgz);
@@ -490,17 +559,25 @@ __global__ void __launch_bounds__(MOST, PER_SM) norm_grad_kernel(const __grid_co
     }
   }
   float all_w[U * VEC], all_b[U * VEC];
+  if constexpr (HELD) {
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    spread2<P>(dw[i], all_w + i * VEC);
-    spread2<P>(db[i], all_b + i * VEC);
+    for (int i = 0; i < U; ++i) {
+      spread2<P>(dw[i], all_w + i * VEC);
+      spread2<P>(db[i], all_b + i * VEC);
+    }
+  } else {
+    away.get(all_w, all_b);
   }
   write_part<VEC, U>(a, group, groups, group_threads, shared, all_w, all_b);
 }
 
 // Rows off the grid, by elements (thread t of G has columns t + G i): the row stays
-// in registers between its two walks, as do the weights.
-template <int DT, int G, int U, bool EXTRA>
+// in registers between its two walks.  With PRE the next row's elements are on the way
+// to registers meanwhile and the weights are in shared memory, to make room: 25,998
+// bf16 rows of 1019 take 42 us so, 47 with the weights in registers.  dsum needs the room
+// itself (4.2 TB/s with PRE, 5.3 without), and fp32 rows of more than a warp lose up
+// to 6 % with PRE.
+template <int DT, int G, int U, bool EXTRA, bool PRE>
 __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) norm_grad_off_kernel(const __grid_constant__ NormArgs a, int, int weight_dt) {
   constexpr int B = Elem<DT>::kBytes, H = U / 2;
   extern __shared__ float shared[];
@@ -512,39 +589,88 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) 
   const uint32_t cols = a.cols, row_bytes = cols * B;
   const int mine = own_columns<G>(cols, t);
   const float inv = 1.f / static_cast<float>(cols);
-  F2 dw[H], db[H], weight[H];
+  constexpr bool HELD = U <= 16, STAGED = PRE || !HELD;
+  F2 dw[HELD ? H : 1], db[HELD ? H : 1], weight[STAGED ? 1 : H];
+  float* const behind = shared + (!HELD ? 2 * U * G : groups > 1 ? 2 * cols : 0);
+  float2* const staged = reinterpret_cast<float2*>(behind);
+  const SharedSums<U / 4> away(shared, G, t);
+  if constexpr (HELD) {
 #pragma unroll
-  for (int k = 0; k < H; ++k) dw[k] = db[k] = both(0.f);
-  load_spread<G, U>(a.weight[r], weight_dt, t, mine, weight);
+    for (int k = 0; k < H; ++k) dw[k] = db[k] = both(0.f);
+  } else {
+    away.clear();
+  }
+  if constexpr (STAGED) {
+    if (group.id == 0) {
+      F2 f[H];
+      load_spread<G, U>(a.weight[r], weight_dt, t, mine, f);
+#pragma unroll
+      for (int k = 0; k < H; ++k) staged[k * G + t] = parts(f[k]);
+    }
+    __syncthreads();
+  } else {
+    load_spread<G, U>(a.weight[r], weight_dt, t, mine, weight);
+  }
   uint32_t row = part.lo + group.id;
   float next_mean = 0.f, next_rstd = 0.f;
+  uint32_t next_x[PRE ? U : 1], next_dy[PRE ? U : 1];
   if (row < part.hi) {
     next_mean = a.mean[r][row];
     next_rstd = a.rstd[r][row];
+    if constexpr (PRE) {
+      const uint64_t at = static_cast<uint64_t>(row) * row_bytes + t * B;
+      load_bits<DT, G, U>(static_cast<const char*>(a.x[r]) + at, mine, next_x);
+      load_bits<DT, G, U>(static_cast<const char*>(a.dy[r]) + at, mine, next_dy);
+    }
   }
   for (; row < part.hi; row += groups) {
-    const uint64_t at = static_cast<uint64_t>(row) * row_bytes;
-    if (t == 0 && part.hi - row > static_cast<uint32_t>(groups)) {
-      const uint64_t next = at + static_cast<uint64_t>(groups) * row_bytes;
+    const uint64_t at = static_cast<uint64_t>(row) * row_bytes, hop = static_cast<uint64_t>(groups) * row_bytes;
+    const uint32_t left = part.hi - row;
+    if (t == 0 && left > static_cast<uint32_t>(groups) * (PRE ? 2 : 1)) {
+      const uint64_t next = at + hop * (PRE ? 2 : 1);
       prefetch_row(a.x[r], next, row_bytes);
       prefetch_row(a.dy[r], next, row_bytes);
       if constexpr (EXTRA) prefetch_row(a.extra[r], next, row_bytes);
     }
     F2 z[H], g[H];  // x and dy first
-    load_row<DT, G, U>(static_cast<const char*>(a.x[r]) + at + t * B, mine, z);
-    load_row<DT, G, U>(static_cast<const char*>(a.dy[r]) + at + t * B, mine, g);
+    if constexpr (PRE) {
+      floats_of<DT, U>(next_x, z);
+      floats_of<DT, U>(next_dy, g);
+    } else {
+      load_row<DT, G, U>(static_cast<const char*>(a.x[r]) + at + t * B, mine, z);
+      load_row<DT, G, U>(static_cast<const char*>(a.dy[r]) + at + t * B, mine, g);
+    }
     const F2 rstd = both(next_rstd), shift = both(-next_mean * next_rstd);
-    if (part.hi - row > static_cast<uint32_t>(groups)) {
+    if (left > static_cast<uint32_t>(groups)) {
       next_mean = a.mean[r][row + groups];
       next_rstd = a.rstd[r][row + groups];
+      if constexpr (PRE) {
+        load_bits<DT, G, U>(static_cast<const char*>(a.x[r]) + at + hop + t * B, mine, next_x);
+        load_bits<DT, G, U>(static_cast<const char*>(a.dy[r]) + at + hop + t * B, mine, next_dy);
+      }
     }
     F2 sg = both(0.f), sgz = both(0.f);
+    if constexpr (!HELD) {
+#pragma unroll
+      for (int k = 0; k < H; k += 2) {
+        z[k] = fma2(z[k], rstd, shift);
+        z[k + 1] = fma2(z[k + 1], rstd, shift);
+        away.add(k / 2, g[k], g[k + 1], z[k], z[k + 1]);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < H; ++k) {
-      z[k] = fma2(z[k], rstd, shift);
-      dw[k] = fma2(g[k], z[k], dw[k]);
-      db[k] = add2(db[k], g[k]);
-      g[k] = mul2(g[k], weight[k]);
+      if constexpr (HELD) {
+        z[k] = fma2(z[k], rstd, shift);
+        dw[k] = fma2(g[k], z[k], dw[k]);
+        db[k] = add2(db[k], g[k]);
+      }
+      if constexpr (STAGED) {
+        const float2 w = staged[k * G + t];
+        g[k] = mul2(g[k], pair(w.x, w.y));
+      } else {
+        g[k] = mul2(g[k], weight[k]);
+      }
       sg = add2(sg, g[k]);
       sgz = fma2(g[k], z[k], sgz);
     }
@@ -562,8 +688,12 @@ __global__ void __launch_bounds__(G > 256 ? G : 256, G > 256 || U > 16 ? 1 : 2) 
     store_row<DT, G, U>(static_cast<char*>(a.out[r]) + at + t * B, mine, g);
   }
   float all_w[U], all_b[U];
-  spread2<H>(dw, all_w);
-  spread2<H>(db, all_b);
+  if constexpr (HELD) {
+    spread2<H>(dw, all_w);
+    spread2<H>(db, all_b);
+  } else {
+    away.get(all_w, all_b);
+  }
   write_part<1, U>(a, group, groups, G, shared, all_w, all_b);
 }
 
@@ -708,16 +838,22 @@ cudaError_t launch_norm_grad(int dt, int weight_dt, bool vec, NormArgs* args, cu
   const bool extra = any_of(a.extra, a.p);
   const uint32_t grid = weights_on_grid(a);
   // groups of a CTA are joined through shared memory: at most 16 KB, as a row of more has a CTA
-  const auto launch = [&](auto* kernel, uint32_t ctas, int group, int groups, auto... more) {
+  const auto launch = [&](auto* kernel, uint32_t ctas, int group, int groups, size_t smem, auto... more) {
     cut_rows(&a.parts, rows.n, a.p, ctas, groups, false);
-    return launch_norm_kernel(kernel, a.parts.first[a.p], group * groups, groups > 1 ? a.cols * 8 : 0, s, static_cast<const NormArgs&>(a), group, weight_dt, more...);
+    if (smem > 32 * 1024) {  // the sums over rows of kNormMaxCols columns, and their weights
+      const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kNormMaxCols * 12));
+      if (err != cudaSuccess) return err;
+    }
+    return launch_norm_kernel(kernel, a.parts.first[a.p], group * groups, smem + (groups > 1 ? a.cols * 8 : 0), s, static_cast<const NormArgs&>(a), group, weight_dt, more...);
   };
   if (!vec) {
     const auto off = [&](auto d) {
       constexpr int DT = decltype(d)::value;
       return by_columns(a.cols, [&](auto gr, auto un) {
         constexpr int G = decltype(gr)::value, U = decltype(un)::value, groups = G >= 256 ? 1 : 256 / G;
-        return launch(extra ? norm_grad_off_kernel<DT, G, U, true> : norm_grad_off_kernel<DT, G, U, false>, kNormParts, G, groups);
+        constexpr bool PRE = U <= 16 && (DT == kBF16 || G == 32);  // of the kernel without dsum
+        const size_t sums = U > 16 ? U * G * 8 : 0, staged = U > 16 || (PRE && !extra) ? U * G * 4 : 0;
+        return launch(extra ? norm_grad_off_kernel<DT, G, U, true, false> : norm_grad_off_kernel<DT, G, U, false, PRE>, kNormParts, G, groups, sums + staged);
       });
     };
     return dt == kF32 ? off(Int<kF32>{}) : off(Int<kBF16>{});
@@ -729,7 +865,7 @@ cudaError_t launch_norm_grad(int dt, int weight_dt, bool vec, NormArgs* args, cu
       constexpr bool PRE = decltype(pre)::value != 0;
       const int group = whole_warps(a.cols / VEC, U), groups = group >= MOST ? 1 : MOST / group;
       return launch(extra ? norm_grad_kernel<DT, U, true, PRE, MOST, PER_SM> : norm_grad_kernel<DT, U, false, PRE, MOST, PER_SM>, kNormParts / 2 * PER_SM, group,
-                    groups, grid);
+                    groups, U * VEC > 16 ? static_cast<size_t>(group) * U * VEC * 8 : 0, grid);
     };
     if (a.cols <= 256) return on(Int<8 / VEC>{}, Int<1>{}, Int<256>{}, Int<2>{});
     if (a.cols <= 4096) return on(Int<16 / VEC>{}, Int<1>{}, Int<256>{}, Int<2>{});

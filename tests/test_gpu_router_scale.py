@@ -66,6 +66,33 @@ def test_many_rows(rows, cols, dt):
     assert ((gb.double() - d.sum(0)).abs() <= d.abs().sum(0) * T).all()
 
 
+@pytest.mark.parametrize("with_sum", [False, True])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(2003, 8193), (2003, 8200), (2003, 12288), (2003, 16383), (2003, 16384), (9001, 61), (9001, 129), (9001, 513), (9001, 1025),
+                                       (4001, 2049), (4001, 4097)])
+def test_sums_over_many_rows(rows, cols, dt, with_sum):
+    """The gradients of rows whose sums are kept in shared memory (more than 8192
+    columns) and of every width of rows off the grid, two of each call the same bits."""
+    c = ccl()
+    torch.manual_seed(cols)
+    x, dy, ds = (torch.randn(rows, cols, device="cuda").to(dt) for _ in range(3))
+    w = torch.randn(cols, device="cuda")
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    c.ccl_layer_norm([x], [w], None, [y], mean=[mean], rstd=[rstd])
+    check_norm(y, x, w, None, 1e-5)
+    extra, got = ds if with_sum else None, []
+    for _ in range(2):
+        out = [torch.full_like(x, 3.0), torch.full((cols,), 3.0, device="cuda"), torch.full((cols,), 3.0, device="cuda")]
+        c.ccl_layer_norm_grad([dy], [x], [w], [mean], [rstd], out[:1], dsum=None if extra is None else [extra], dweight=out[1:2], dbias=out[2:])
+        got.append(out)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    dx, gw, gb = got[0]
+    z, near = check_norm_grad(dx, dy, x, w, mean, rstd, extra)
+    d, T = dy.double(), (rows + 64) * ONE
+    assert ((gw.double() - (d * z).sum(0)).abs() <= (d * z).abs().sum(0) * (T + 8 * ONE) + (d.abs() * near).sum(0) + ONE * gw.double().abs()).all()
+    assert ((gb.double() - d.sum(0)).abs() <= d.abs().sum(0) * T).all()
+
+
 @pytest.mark.parametrize("dt,wt", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16), (torch.float32, torch.float32)])
 @pytest.mark.parametrize("rows,cols", [(5, 256), (20_011, 512), (3, 7168), (9001, 4096)])
 def test_weights_off_the_grid_of_rows_on_it(rows, cols, dt, wt):
