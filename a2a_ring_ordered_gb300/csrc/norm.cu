@@ -9,7 +9,7 @@
 // under way.  A group of one or more warps has a row, which stays in registers
 // between the walks over it; a thread has the same columns of every row that its
 // group takes, so that the sums over rows stay in its registers too, or in its own
-// slots of shared memory where it has 32 columns.
+// slots of shared memory.
 // Measured, of 8 ranks x 4096 rows of 7168 bf16 with fp32 weights and a residual:
 // forward 301 us (6.2 TB/s), gradients 296 (6.35); without a residual, 34,877 rows,
 // 214 us (4.7) and 262 (5.7); 14,006 fp32 rows of 1019, off the grid, 22 us (5.1),
@@ -427,10 +427,11 @@ __device__ __forceinline__ void write_part(const NormArgs& a, const Group& group
   }
 }
 
-// The sums over rows of threads with 32 columns, which registers do not hold beside z
-// and g: four columns to a slot, a thread's own, in planes over the threads.  Only
-// where a CTA is one group.  12,288 columns of bf16 go at 4.2 TB/s so (5.3 with dsum),
-// 10,001 at 2.6; spilled by the compiler, at 3.4 (4.05) and 1.15.
+// The sums over rows where registers do not hold them beside z and g (32 columns a
+// thread), or are wanted for other things: four columns to a slot, a thread's own, in
+// planes over the threads.  Only where a CTA is one group.  12,288 columns of bf16 go
+// at 4.2 TB/s so (5.3 with dsum), 10,001 at 2.6; spilled by the compiler, at 3.4 (4.05)
+// and 1.15.
 template <int Q>
 struct SharedSums {
   float4 *w, *b;
@@ -460,12 +461,13 @@ struct SharedSums {
 
 // Rows on the 16-byte grid.  z and g stay in registers between the row's two walks;
 // with PRE the next row's units are on the way to registers meanwhile, and the
-// row after it to L2, else the next row to L2.  The bounds name the threads that a
+// row after it to L2, else the next row to L2; HELD: the sums over rows are in
+// registers.  The bounds name the threads that a
 // width takes: the compiler's order of the same instructions for 512 threads cost 15 %
 // at 448.  For 8 x 4096 rows of 7168 bf16 with dsum, 296 us so, a ring of asynchronous
 // copies three rows deep took 410, the second walk from L1 and two rows a SM 447, half
 // the columns a thread 445 (all before the two steps above: 352 us).
-template <int DT, int U, bool EXTRA, bool PRE, int MOST, int PER_SM>
+template <int DT, int U, bool EXTRA, bool PRE, bool HELD, int MOST, int PER_SM>
 __global__ void __launch_bounds__(MOST, PER_SM) norm_grad_kernel(const __grid_constant__ NormArgs a, int group_threads, int weight_dt, uint32_t weights_on_grid) {
   constexpr int VEC = 16 / Elem<DT>::kBytes, P = VEC / 2;
   constexpr bool LATE = U * VEC > 8;  // dsum after the first walk, for its registers' sake: 352 -> 323 us
@@ -479,7 +481,6 @@ __global__ void __launch_bounds__(MOST, PER_SM) norm_grad_kernel(const __grid_co
   const int mine = (static_cast<int>(cols / VEC) - t + group_threads - 1) / group_threads;  // units of the thread
   const float inv = 1.f / static_cast<float>(cols);
   const Vector weight{a.weight[r], weight_dt, weights_on_grid != 0};
-  constexpr bool HELD = U * VEC <= 16;
   F2 dw[HELD ? U : 1][P], db[HELD ? U : 1][P];
   const SharedSums<U * VEC / 4> away(shared, group_threads, t);
   if constexpr (HELD) {
@@ -860,18 +861,22 @@ cudaError_t launch_norm_grad(int dt, int weight_dt, bool vec, NormArgs* args, cu
   }
   const auto by_type = [&](auto d) {
     constexpr int DT = decltype(d)::value, VEC = 16 / Elem<DT>::kBytes;
-    const auto on = [&](auto un, auto pre, auto mt, auto ps) {
+    const auto on = [&](auto un, auto pre, auto held, auto mt, auto ps) {
       constexpr int U = decltype(un)::value, MOST = decltype(mt)::value, PER_SM = decltype(ps)::value;
-      constexpr bool PRE = decltype(pre)::value != 0;
+      constexpr bool PRE = decltype(pre)::value != 0, HELD = decltype(held)::value != 0;
       const int group = whole_warps(a.cols / VEC, U), groups = group >= MOST ? 1 : MOST / group;
-      return launch(extra ? norm_grad_kernel<DT, U, true, PRE, MOST, PER_SM> : norm_grad_kernel<DT, U, false, PRE, MOST, PER_SM>, kNormParts / 2 * PER_SM, group,
-                    groups, U * VEC > 16 ? static_cast<size_t>(group) * U * VEC * 8 : 0, grid);
+      return launch(extra ? norm_grad_kernel<DT, U, true, PRE, HELD, MOST, PER_SM> : norm_grad_kernel<DT, U, false, PRE, HELD, MOST, PER_SM>, kNormParts / 2 * PER_SM, group,
+                    groups, HELD ? 0 : static_cast<size_t>(group) * U * VEC * 8, grid);
     };
-    if (a.cols <= 256) return on(Int<8 / VEC>{}, Int<1>{}, Int<256>{}, Int<2>{});
-    if (a.cols <= 4096) return on(Int<16 / VEC>{}, Int<1>{}, Int<256>{}, Int<2>{});
-    if (a.cols <= 5120) return on(Int<16 / VEC>{}, Int<1>{}, Int<320>{}, Int<1>{});
-    if (a.cols <= 7168) return on(Int<16 / VEC>{}, Int<1>{}, Int<448>{}, Int<1>{});
-    return a.cols <= 8192 ? on(Int<16 / VEC>{}, Int<1>{}, Int<512>{}, Int<1>{}) : on(Int<32 / VEC>{}, Int<0>{}, Int<512>{}, Int<1>{});
+    if (a.cols <= 256) return on(Int<8 / VEC>{}, Int<1>{}, Int<1>{}, Int<256>{}, Int<2>{});
+    if (a.cols <= 4096) return on(Int<16 / VEC>{}, Int<1>{}, Int<1>{}, Int<256>{}, Int<2>{});
+    // sums in shared memory where that leaves room for a second CTA, or for what is spilled otherwise: gradients of 5120 bf16
+    // columns without and with dsum 4.6 and 5.0 TB/s -> 5.0 and 6.1 (fp32 6.45, 6.8 -> 6.1, 5.8), of 7168 fp32 ones 6.1, 5.5 ->
+    // 6.25, 6.65 (bf16 5.7, 6.4 -> 4.5, 5.5)
+    constexpr bool B = DT == kBF16;
+    if (a.cols <= 5120) return on(Int<16 / VEC>{}, Int<1>{}, Int<!B>{}, Int<320>{}, Int<B ? 2 : 1>{});
+    if (a.cols <= 7168) return on(Int<16 / VEC>{}, Int<1>{}, Int<B>{}, Int<448>{}, Int<1>{});
+    return a.cols <= 8192 ? on(Int<16 / VEC>{}, Int<1>{}, Int<B>{}, Int<512>{}, Int<1>{}) : on(Int<32 / VEC>{}, Int<0>{}, Int<0>{}, Int<512>{}, Int<1>{});
   };
   return dt == kF32 ? by_type(Int<kF32>{}) : by_type(Int<kBF16>{});
 }

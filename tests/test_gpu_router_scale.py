@@ -69,10 +69,10 @@ def test_many_rows(rows, cols, dt):
 @pytest.mark.parametrize("with_sum", [False, True])
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,cols", [(2003, 8193), (2003, 8200), (2003, 12288), (2003, 16383), (2003, 16384), (9001, 61), (9001, 129), (9001, 513), (9001, 1025),
-                                       (4001, 2049), (4001, 4097)])
+                                       (4001, 2049), (4001, 4097), (4001, 4104), (4001, 5120), (4001, 5128), (4001, 7168), (4001, 8192)])
 def test_sums_over_many_rows(rows, cols, dt, with_sum):
-    """The gradients of rows whose sums are kept in shared memory (more than 8192
-    columns) and of every width of rows off the grid, two of each call the same bits."""
+    """The gradients of rows whose sums are kept in shared memory, and of every width of
+    rows off the grid; two of each call give the same bits."""
     c = ccl()
     torch.manual_seed(cols)
     x, dy, ds = (torch.randn(rows, cols, device="cuda").to(dt) for _ in range(3))
