@@ -98,15 +98,26 @@ __device__ __forceinline__ float2 lanes_sum(float a, float b) {
     return make_float2(__shfl_sync(kAllLanes, v, 0, L), __shfl_sync(kAllLanes, v, L / 2, L));
   }
 }
+// Of two numbers; NaN where one of them is.
+__device__ __forceinline__ float larger(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+__device__ __forceinline__ float smaller(float a, float b) {
+  float m;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
   if constexpr (L == 32) {
     float m;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(v));  // as fmaxf: numbers before NaN
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(v));
     return m;
   } else {
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAllLanes, v, o));
+    for (int o = L / 2; o > 0; o >>= 1) v = larger(v, __shfl_xor_sync(kAllLanes, v, o));
     return v;
   }
 }
@@ -135,20 +146,52 @@ __device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
 // Scores are kept over exp(base), base max(row) for softmax and min(max(row), 0)
 // for sigmoid, so that the row's largest stays away from 0; 0 for a row of -inf.
 //
-// exp(l - base) is the hardware's power of two of the rounded (l - base) log2(e):
-// off by |l - base| 2^-23 and two units more, which gates and shares, of fp32,
-// carry on.  (One fused multiply-add would do for both, but base log2(e) is not
-// finite where a row is masked by the type's lowest value.)
-constexpr float kLog2e = 1.4426950408889634f;
+// exp(x) of x = l - base <= 0 is the hardware's power of two of t = x log2(e), which
+// is rounded: by itself that is off by |x| 2^-23, and so is a gate or a share of a
+// logit far from its row's top.  Times 1 + r, r = x - t ln 2 (below 2^-16) being what
+// the rounding left, it is off by some four roundings of 2^-24, and |x| 2^-28 more
+// because ln 2 is rounded too.  A sum of scores goes without: by the weight of the
+// scores in it, the mean of |x| is at most the logarithm of their number.
+//
+// (One fused multiply-add would do for x and t both, but base log2(e) is not finite
+// where a row is masked by the type's lowest value.)
+constexpr float kLog2e = static_cast<float>(1.4426950408889634), kLn2 = static_cast<float>(0.6931471805599453);
 __device__ __forceinline__ float power_of_two(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float reciprocal_of(float x) {
+__device__ __forceinline__ float rough_exp(float x) { return power_of_two(x * kLog2e); }
+__device__ __forceinline__ F2 rough_exp(F2 x) {
+  const float2 t = parts(mul2(x, both(kLog2e)));
+  return pair(power_of_two(t.x), power_of_two(t.y));
+}
+__device__ __forceinline__ float exp_of(float x) {
+  x = larger(x, -128.f);  // -inf has no r; NaN stays
+  const float t = __fmul_rn(x, kLog2e), y = power_of_two(t);
+  return fmaf(y, fmaf(t, -kLn2, x), y);
+}
+// Of a row: 0 for -inf, and for NaN, which the row's base tells of.
+__device__ __forceinline__ float fma_sat(float a, float b, float c) {  // within 0 and 1, NaN as 0
+  float d;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ F2 exp_of(F2 x) {
+  const F2 t = mul2(x, both(kLog2e));
+  const float2 e = parts(t), r = parts(fma2(t, both(-kLn2), x));
+  const float a = power_of_two(e.x), b = power_of_two(e.y);
+  return pair(fma_sat(a, r.x, a), fma_sat(b, r.y, b));
+}
+__device__ __forceinline__ float rough_reciprocal(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// That, and a step of Newton's method.
+__device__ __forceinline__ float reciprocal_of(float x) {
+  const float y = rough_reciprocal(x);
+  return fmaf(fmaf(-x, y, 1.f), y, y);
 }
 // u / v by Markstein's correction of the quotient: u / u is 1 to the bit.
 __device__ __forceinline__ float quotient(float u, float v, float inv) {
@@ -159,43 +202,64 @@ __device__ __forceinline__ F2 quotient(F2 u, float v, F2 inv) {
   const F2 q = mul2(u, inv);
   return fma2(fma2(q, both(-v), u), inv, q);
 }
+// NaN where the row has one (sigmoid: where its largest is one).
 __device__ __forceinline__ float base_of(float top, bool sigmoid) {
   if (top == -INFINITY) return 0.f;
-  return sigmoid ? fminf(top, 0.f) : top;
+  return sigmoid ? smaller(top, 0.f) : top;
 }
-__device__ __forceinline__ float softmax_score(float l, float base) { return power_of_two((l - base) * kLog2e); }
+__device__ __forceinline__ float softmax_score(float l, float base) { return exp_of(l - base); }
 // u, and 1 - sigmoid(l), of one logit; base is 0 for nearly every row.
 struct Sigmoid {
   float t, r;  // exp(-|l|), 1 / (1 + t)
-  __device__ __forceinline__ explicit Sigmoid(float l) : t(power_of_two(-fabsf(l) * kLog2e)), r(reciprocal_of(1.f + t)) {}
+  __device__ __forceinline__ Sigmoid(float t, float r) : t(t), r(r) {}
+  __device__ __forceinline__ explicit Sigmoid(float l) : t(exp_of(-fabsf(l))), r(reciprocal_of(1.f + t)) {}
   __device__ __forceinline__ float score(float l) const { return l >= 0.f ? r : t * r; }
   __device__ __forceinline__ float score(float l, float base) const { return base == 0.f ? score(l) : softmax_score(fminf(l, 0.f), base) * r; }
   __device__ __forceinline__ float away(float l) const { return l > 0.f ? t * r : r; }
 };
+// Of two, of a row.
+struct Sigmoids {
+  Sigmoid a, b;
+};
+template <bool EACH>
+__device__ __forceinline__ Sigmoids sigmoids(float x, float y) {
+  float2 t;
+  if constexpr (EACH) t = parts(exp_of(pair(-fabsf(x), -fabsf(y))));
+  else t = make_float2(rough_exp(-fabsf(x)), rough_exp(-fabsf(y)));
+  return {Sigmoid(t.x, rough_reciprocal(1.f + t.x)), Sigmoid(t.y, rough_reciprocal(1.f + t.y))};
+}
 __device__ __forceinline__ float sigmoid_score(float l, float base) { return Sigmoid(l).score(l, base); }
 __device__ __forceinline__ float score_of(float l, float base, bool sigmoid) { return sigmoid ? sigmoid_score(l, base) : softmax_score(l, base); }
-// All scores of a lane's columns, in pairs, and their sum; AWAY: and 1 - sigmoid.
-template <int DT, int NV, bool AWAY>
+// A score of a row whose logits are all below 0.
+template <bool EACH>
+__device__ __forceinline__ float far_sigmoid(float l, float base) {
+  if constexpr (EACH) return sigmoid_score(l, base);
+  else return rough_exp(fminf(l, 0.f) - base) * rough_reciprocal(1.f + rough_exp(-fabsf(l)));
+}
+// All scores of a lane's columns, in pairs, and their sum.  EACH: each is wanted as it is,
+// not the sum alone; AWAY: and 1 - sigmoid.
+template <int DT, int NV, bool EACH, bool AWAY>
 __device__ __forceinline__ float scores_of(const GateRow<DT, NV>& row, float base, bool sigmoid, F2* u, F2* away) {
-  F2 sum = both(0.f);
+  F2 sum = pair(EACH ? base - base : 0.f, 0.f);  // NaN where the base is
   if (sigmoid) {
 #pragma unroll
     for (int k = 0; k < NV / 2; ++k) {
       const float x = row.value(2 * k), y = row.value(2 * k + 1);
-      const Sigmoid a(x), b(y);
-      u[k] = pair(a.score(x), b.score(y));
-      if constexpr (AWAY) away[k] = pair(a.away(x), b.away(y));
+      const Sigmoids v = sigmoids<EACH>(x, y);
+      u[k] = pair(v.a.score(x), v.b.score(y));
+      if constexpr (AWAY) away[k] = pair(v.a.away(x), v.b.away(y));
     }
     if (base != 0.f) {
 #pragma unroll
-      for (int k = 0; k < NV / 2; ++k) u[k] = pair(sigmoid_score(row.value(2 * k), base), sigmoid_score(row.value(2 * k + 1), base));
+      for (int k = 0; k < NV / 2; ++k) u[k] = pair(far_sigmoid<EACH>(row.value(2 * k), base), far_sigmoid<EACH>(row.value(2 * k + 1), base));
     }
   } else {
-    const F2 scale = both(kLog2e), less = both(-base);
+    const F2 less = both(-base);
 #pragma unroll
     for (int k = 0; k < NV / 2; ++k) {
-      const float2 x = parts(mul2(add2(pair(row.value(2 * k), row.value(2 * k + 1)), less), scale));
-      u[k] = pair(power_of_two(x.x), power_of_two(x.y));
+      const F2 x = add2(pair(row.value(2 * k), row.value(2 * k + 1)), less);
+      if constexpr (EACH) u[k] = exp_of(x);
+      else u[k] = rough_exp(x);
     }
   }
 #pragma unroll

@@ -19,6 +19,7 @@ namespace ccl {
 namespace {
 
 __host__ __device__ constexpr int gate_threads(int nv) { return nv == 8 ? 512 : 256; }
+constexpr size_t kCapSharedBytes = 80 * 1024;  // more than a third of a SM's, more than any row needs
 
 // A column's place in the order of the choice: the logit's bits made to order as
 // numbers do (-0 as 0, NaN above all), and under them 1023 - column, so that
@@ -200,18 +201,18 @@ __global__ void __launch_bounds__(gate_threads(NV)) gate_kernel(const __grid_con
         if constexpr (!SELECT || DT == kF32) {
           top = now.value(0);
 #pragma unroll
-          for (int i = 1; i < NV; ++i) top = fmaxf(top, now.value(i));
+          for (int i = 1; i < NV; ++i) top = larger(top, now.value(i));
           top = lanes_max<L>(top);
         }
         const float row_base = base_of(top, sigmoid);
         F2 u[NV / 2];
-        const float row_total = lanes_sum<L>(scores_of<DT, NV, false>(now, row_base, sigmoid, u, nullptr));
+        const float row_total = lanes_sum<L>(scores_of<DT, NV, !SELECT, false>(now, row_base, sigmoid, u, nullptr));
         if (SELECT && slot >= 0 && slot < C) {
           base = row_base;
           total = row_total;
         }
         if constexpr (BALANCE) {
-          const F2 inv = both(row_total == 0.f ? 0.f : reciprocal_of(row_total));
+          const F2 inv = both(row_total == 0.f ? 0.f : rough_reciprocal(row_total));
 #pragma unroll
           for (int i = 0; i < NV / 2; ++i) sums[i] = fma2(u[i], inv, sums[i]);
         }
@@ -393,16 +394,21 @@ cudaError_t launch_gate(int dt, bool select, bool balance, GateArgs* args, cudaS
   for (int r = 0; r < args->p; ++r) rows[r] = args->parts.rows[r];
   return by_row(dt, args->num_experts, args->k, [&](auto d, auto lanes, auto nv) {
     constexpr int DT = decltype(d)::value, L = decltype(lanes)::value, NV = decltype(nv)::value, kWarps = gate_threads(NV) / 32;
-    const size_t smem = balance ? (static_cast<size_t>(kWarps) * 32 * NV + args->num_experts + 1) * 4 : 0;
+    size_t smem = balance ? (static_cast<size_t>(kWarps) * 32 * NV + args->num_experts + 1) * 4 : 0;
     const auto go = [&](auto km) {
       constexpr int KM = decltype(km)::value;
       // a batch a warp at least, then parts for two CTAs a SM: six without the loss, where they would fit, took 12.1 us for 61,998 rows of 60
       // fp32 instead of 9.8
       cut_rows(&args->parts, rows, args->p, kBalanceParts, kWarps * GateBatch<L, KM>::kRows, balance);
-      return launch_gate_parts(!select   ? gate_kernel<DT, L, NV, KM, false, true>
-                               : balance ? gate_kernel<DT, L, NV, KM, true, true>
-                                         : gate_kernel<DT, L, NV, KM, true, false>,
-                               *args, gate_threads(NV), smem, s);
+      auto* kernel = !select ? gate_kernel<DT, L, NV, KM, false, true> : balance ? gate_kernel<DT, L, NV, KM, true, true> : gate_kernel<DT, L, NV, KM, true, false>;
+      // no third CTA on a SM, where registers would let one on: the parts are two a SM, and while the call before still has some SMs
+      // it would be missing from another.  The loss of given ids of 4 x 16384 rows of 384 bf16, call after call, 32 us -> 26
+      if (NV == 16 && !select) {
+        smem = kCapSharedBytes;
+        const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (err != cudaSuccess) return err;
+      }
+      return launch_gate_parts(kernel, *args, gate_threads(NV), smem, s);
     };
     if constexpr (L >= 16) {
       if (args->k > 8) return go(std::integral_constant<int, 16>{});

@@ -20,7 +20,7 @@ namespace {
 // A batch's choices are settled first, in all lanes; then every pass makes a row's
 // gradients.  The next row, and the next batch's choices, are on the way meanwhile.
 template <int DT, int L, int NV, int KM, bool GATES, bool BALANCE>
-__global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : 1) gate_grad_kernel(const __grid_constant__ GateArgs a) {
+__global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : NV == 16 && !(GATES && BALANCE) ? 2 : 1) gate_grad_kernel(const __grid_constant__ GateArgs a) {
   using Batch = GateBatch<L, KM>;
   constexpr int C = Batch::kChoices, kTeams = 32 / L, kWarps = kThreads / 32;
   // GATES: of each team, what the choices of its row add to their columns; zeros between rows
@@ -118,9 +118,9 @@ __global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : 1) gate_grad_kernel(co
       if (dense) {
         float top = now.value(0);
 #pragma unroll
-        for (int i = 1; i < NV; ++i) top = fmaxf(top, now.value(i));
+        for (int i = 1; i < NV; ++i) top = larger(top, now.value(i));
         const float base = base_of(lanes_max<L>(top), sigmoid);
-        const float part_total = scores_of<DT, NV, true>(now, base, sigmoid, out, away);
+        const float part_total = scores_of<DT, NV, true, true>(now, base, sigmoid, out, away);
         // The mean of a_e over the shares: for softmax, whose lone score is 1, by a sum over the scores beside theirs
         F2 product = both(0.f);
         float total, mean = 0.f, inv;
@@ -193,8 +193,10 @@ __global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : 1) gate_grad_kernel(co
       if (sigmoid) {
         if (!dense) {
 #pragma unroll
-          for (int i = 0; i < NV; i += 2)
-            away[i / 2] = pair(Sigmoid(now.value(i)).away(now.value(i)), Sigmoid(now.value(i + 1)).away(now.value(i + 1)));
+          for (int i = 0; i < NV; i += 2) {
+            const Sigmoids v = sigmoids<true>(now.value(i), now.value(i + 1));
+            away[i / 2] = pair(v.a.away(now.value(i)), v.b.away(now.value(i + 1)));
+          }
         }
 #pragma unroll
         for (int i = 0; i < NV / 2; ++i) out[i] = mul2(out[i], away[i]);

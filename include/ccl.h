@@ -507,7 +507,10 @@ ccl_status_t ccl_moe_product_grad_weight(const void* const* dy, const void* cons
  *   `together` counts each rank gets its own tokens' part of the one loss.
  * ccl_moe_balance_grad: dlogits[r] = the gradient of scale * dlosses[r] * L alone.
  *
- * A masked logit (-inf) gets gradient 0.  Scores, sums and gradients are fp32;
+ * A masked logit (-inf) gets gradient 0.  Scores, sums and gradients are fp32: a
+ * score that a gate, a gradient or a loss of given ids takes is off by at most 12
+ * roundings of 2^-24 of it, and by |l - top| 2^-24 where the distance of fp32 logits
+ * from their row's largest has to be rounded;
  * column sums over tokens are added in a fixed order, joined in 64 bits.
  * workspace (device, 16-byte aligned, ccl_moe_balance_workspace_bytes) is
  * scratch of one call at a time; it may hold anything.  No output may overlap
