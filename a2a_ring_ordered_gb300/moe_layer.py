@@ -125,18 +125,22 @@ class Router:
         return ids, gates, losses
 
     def backward(self, dgates: Sequence[torch.Tensor], dweight: Sequence[torch.Tensor], dlosses: Sequence[torch.Tensor] | None = None,
-                 balance_scale: float = 0.0) -> list[torch.Tensor]:
+                 balance_scale: float | None = None) -> list[torch.Tensor]:
         """The gradient for x of the last forward: of the gates', and of
-        balance_scale * dlosses[r] * losses[r] (dlosses None: ones); writes each rank's
-        weight gradient (experts, hidden), fp32 or bf16, into dweight[r]."""
+        balance_scale * dlosses[r] * losses[r]; writes each rank's weight gradient
+        (experts, hidden), fp32 or bf16, into dweight[r].  dlosses None are ones;
+        balance_scale None is 1 where dlosses is given, else 0, at which the losses
+        have no part."""
         if self.saved is None:
             raise RuntimeError("backward() without a forward()")
         x, ends, logits, ids, counts = self.saved
         self.saved = None
         p = len(x)
         dlogits = [torch.empty_like(v) for v in logits]
-        ccl.ccl_moe_gate_grad(logits, ids, list(dgates), dlogits, **self.how, counts=counts, dlosses=None if dlosses is None else list(dlosses),
-                              balance_scale=balance_scale)
+        if balance_scale is None:
+            balance_scale = 0.0 if dlosses is None else 1.0
+        loss = {} if balance_scale == 0 else {"counts": counts, "dlosses": None if dlosses is None else list(dlosses), "balance_scale": balance_scale}
+        ccl.ccl_moe_gate_grad(logits, ids, list(dgates), dlogits, **self.how, **loss)
         ccl.ccl_moe_product_grad_weight(dlogits, x, ends, [w[None] for w in dweight])
         dx = [torch.empty_like(v) for v in x]
         ccl.ccl_moe_product_grad_input(dlogits, ends, [self.weight[None]] * p, dx)
@@ -172,7 +176,7 @@ class MoEBlock:
 
     def backward(self, dy: Sequence[torch.Tensor], ds: Sequence[torch.Tensor] | None, dw_up: Sequence[torch.Tensor], dw_down: Sequence[torch.Tensor],
                  dw_router: Sequence[torch.Tensor], dw_norm: Sequence[torch.Tensor], db_norm: Sequence[torch.Tensor] | None = None,
-                 dlosses: Sequence[torch.Tensor] | None = None, balance_scale: float = 0.0) -> list[torch.Tensor]:
+                 dlosses: Sequence[torch.Tensor] | None = None, balance_scale: float | None = None) -> list[torch.Tensor]:
         """The gradient for x (and for residual alike) of the last forward, ds being the
         gradient that reaches s past this block; writes each rank's weight gradients
         where the caller wants them (``ExpertLayer.backward``, ``Router.backward``, the
