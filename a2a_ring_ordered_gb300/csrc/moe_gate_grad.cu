@@ -233,10 +233,11 @@ cudaError_t launch_gate_grad(int dt, bool gates, bool balance, GateArgs* args, c
       constexpr int KM = decltype(km)::value;
       // as many parts as are there at once: 8 x 16384 rows of 256 bf16 took 43 us so, 47 in twice as many, 53 in three quarters
       cut_rows(&args->parts, rows, args->p, 152 * 4, kThreads / 32 * GateBatch<L, KM>::kRows, false);
-      return launch_gate_parts(!gates    ? gate_grad_kernel<DT, L, NV, KM, false, true>
-                               : balance ? gate_grad_kernel<DT, L, NV, KM, true, true>
-                                         : gate_grad_kernel<DT, L, NV, KM, true, false>,
-                               *args, kThreads, 0, s);
+      auto* kernel = balance ? gate_grad_kernel<DT, L, NV, KM, true, true> : gate_grad_kernel<DT, L, NV, KM, true, false>;
+      if constexpr (KM == 8) {
+        if (!gates) kernel = gate_grad_kernel<DT, L, NV, KM, false, true>;
+      }
+      return launch_gate_parts(kernel, *args, kThreads, 0, s);
     };
     if constexpr (L >= 16) {
       if (gates && args->k > 8) return go(std::integral_constant<int, 16>{});

@@ -837,7 +837,10 @@ cudaError_t launch_norm(int dt, int weight_dt, bool vec, NormArgs* args, cudaStr
     };
     if (units <= 32) return on(Int<1>{});
     if (units <= 64) return on(Int<2>{});
-    return units <= 2048 ? on(Int<4>{}) : on(Int<8>{});
+    if constexpr (kNormMaxCols / VEC > 2048) {  // fp32 rows
+      if (units > 2048) return on(Int<8>{});
+    }
+    return on(Int<4>{});
   };
   return dt == kF32 ? by_type(Int<kF32>{}) : by_type(Int<kBF16>{});
 }
