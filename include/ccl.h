@@ -511,7 +511,8 @@ ccl_status_t ccl_moe_product_grad_weight(const void* const* dy, const void* cons
  * score that a gate, a gradient or a loss of given ids takes is off by at most 12
  * roundings of 2^-24 of it, and by |l - top| 2^-24 where the distance of fp32 logits
  * from their row's largest has to be rounded;
- * column sums over tokens are added in a fixed order, joined in 64 bits.
+ * sums over tokens are made in a fixed order, a warp's rows of a column by plain
+ * fp32 additions, then the parts with the additions' roundings kept beside the sum.
  * workspace (device, 16-byte aligned, ccl_moe_balance_workspace_bytes) is
  * scratch of one call at a time; it may hold anything.  No output may overlap
  * an input or another output of its rank. */
