@@ -91,6 +91,11 @@ class Router:
 
     weight  (experts, hidden) bf16, shared by the ranks.  score, normalize and scale
     as in ``ccl_moe_gate``; ``together``: the balance loss is over all ranks' tokens.
+
+    Logits and their gradients are held in bf16, as ``ccl_moe_product`` makes and takes
+    them: of 256 normal ones, four rows in ten have equal ones among the largest nine (one
+    in thirteen where eight end), which the lower index wins.  Logits of fp32 go to
+    ``ccl_moe_gate`` directly.
     """
 
     def __init__(self, weight: torch.Tensor, k: int, score: str = "softmax", normalize: bool = True, scale: float = 1.0,

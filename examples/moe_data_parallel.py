@@ -1,7 +1,7 @@
 """Trains one mixture-of-experts layer on p data-parallel virtual ranks.
 
-Every rank routes its own tokens to the same experts; the expert layer's weight
-gradients are written straight into the DDP buckets, each bucket's ring-ordered
+Every rank routes its own tokens to the same experts; the router's and the experts'
+weight gradients are written straight into the DDP buckets, each bucket's ring-ordered
 all-reduce averages them over the ranks and rounds them to bf16, and AdamW, with
 its moments in 8 bits, updates fp32 master weights and the bf16 copies that the
 next forward pass reads.
@@ -23,7 +23,7 @@ def train(ranks: int = 4, steps: int = 60, tokens: int = 512, hidden: int = 256,
           state_bits: int = 8, seed: int = 0) -> list[float]:
     """Losses of each step: the layer learns another layer of its shape."""
     from a2a_ring_ordered_gb300.ddp import GradBuckets
-    from a2a_ring_ordered_gb300.moe_layer import ExpertLayer
+    from a2a_ring_ordered_gb300.moe_layer import ExpertLayer, Router
     from a2a_ring_ordered_gb300.optim import AdamW
 
     dev = torch.device("cuda")
@@ -38,27 +38,20 @@ def train(ranks: int = 4, steps: int = 60, tokens: int = 512, hidden: int = 256,
     buckets = GradBuckets(shapes, ranks, dev)
     optimizer = AdamW(masters, [buckets.averaged(0, i) for i in range(3)], lr=2e-3, betas=(0.9, 0.98), weight_decay=0.0,
                       state_bits=state_bits, copies=weights)
-    layer = ExpertLayer(weights[1], weights[2])
+    router, layer = Router(weights[0], k), ExpertLayer(weights[1], weights[2])
     target = ExpertLayer(normal(*shapes[1], scale=hidden ** -0.5).bfloat16(), normal(*shapes[2], scale=width ** -0.5).bfloat16())
 
-    def route(x, w):
-        logits, ids = (x.float() @ w.float().T).topk(k, dim=1)
-        return torch.softmax(logits, dim=1), ids.to(torch.int32).contiguous()
-
     x = [normal(tokens, hidden).bfloat16() for _ in range(ranks)]
-    want = target.forward(x, *zip(*[(i, w.contiguous()) for w, i in (route(v, normal(experts, hidden)) for v in x)]))
+    want = target.forward(x, *Router(normal(experts, hidden).bfloat16(), k).forward(x)[:2])
     losses = []
     for _ in range(steps):
-        router = weights[0].float().requires_grad_()
-        gates, ids = zip(*[route(v, router) for v in x])
-        out = layer.forward(x, ids, [w.detach().contiguous() for w in gates])
+        ids, gates, _ = router.forward(x)
+        out = layer.forward(x, ids, gates)
         errors = [o.float() - t.float() for o, t in zip(out, want)]
         losses.append(sum(e.square().mean() for e in errors) / ranks)
         dout = [(e * (2.0 / e.numel())).bfloat16() for e in errors]
         _, dgates = layer.backward(dout, [buckets.grad(r, 1) for r in range(ranks)], [buckets.grad(r, 2) for r in range(ranks)])
-        for r in range(ranks):  # the router's share by autograd
-            (dr,) = torch.autograd.grad(gates[r], router, dgates[r], retain_graph=r + 1 < ranks)
-            buckets.grad(r, 0).copy_(dr)
+        router.backward(dgates, [buckets.grad(r, 0) for r in range(ranks)])
         for b in range(buckets.num_buckets):
             buckets.reduce_bucket(b)
         optimizer.step()
