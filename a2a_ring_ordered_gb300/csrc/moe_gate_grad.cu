@@ -9,9 +9,9 @@
 // and all of it times 1 - sigmoid(l_e) for sigmoid scores.
 //
 // Logits are read once and gradients written once; beside HBM, instructions bound
-// it, some 280 a row of 256 with both parts.  Measured: 8 ranks x 16384 rows of 256 bf16,
-// top-8 and the loss, 43 us (3.3 TB/s); the loss alone, fp32 and sigmoid, 46 us (5.8
-// TB/s); 4 x 20001... rows of 60 fp32, top-6, 8.3 us.
+// it, some 270 a row of 256 with both parts.  Measured: 8 ranks x 16384 rows of 256 bf16,
+// top-8 and the loss, 45 us (3.2 TB/s); the loss alone, fp32 and sigmoid, 46 us (5.8
+// TB/s); 4 x 20001... rows of 60 fp32, top-6, 8.7 us.
 #include "gate_rows.cuh"
 
 namespace ccl {
@@ -19,6 +19,8 @@ namespace {
 
 // A batch's choices are settled first, in all lanes; then every pass makes a row's
 // gradients.  The next row, and the next batch's choices, are on the way meanwhile.
+// Two CTAs a SM of 257 to 512 columns, but with both parts, which need more registers:
+// the loss's gradient of 4 x 16384 rows of 384 fp32, sigmoid, takes 46 us so, 66 in one.
 template <int DT, int L, int NV, int KM, bool GATES, bool BALANCE>
 __global__ void __launch_bounds__(kThreads, NV == 8 ? 4 : NV == 16 && !(GATES && BALANCE) ? 2 : 1) gate_grad_kernel(const __grid_constant__ GateArgs a) {
   using Batch = GateBatch<L, KM>;

@@ -11,8 +11,8 @@
 // group takes, so that the sums over rows stay in its registers too, or in its own
 // slots of shared memory.
 // Measured, of 8 ranks x 4096 rows of 7168 bf16 with fp32 weights and a residual:
-// forward 301 us (6.2 TB/s), gradients 296 (6.35); without a residual, 34,877 rows,
-// 214 us (4.7) and 262 (5.7); 14,006 fp32 rows of 1019, off the grid, 22 us (5.1),
+// forward 301 us (6.2 TB/s), gradients 301 (6.2); without a residual, 34,877 rows,
+// 214 us (4.7) and 267 (5.6); 14,006 fp32 rows of 1019, off the grid, 22 us (5.1),
 // gradients of 25,998 bf16 ones 42 us (3.8).
 #include "pairs.cuh"
 #include "row_parts.cuh"
@@ -440,7 +440,7 @@ __device__ __forceinline__ void write_part(const NormArgs& a, const Group& group
 // The sums over rows where registers do not hold them beside z and g (32 columns a
 // thread), or are wanted for other things: four columns to a slot, a thread's own, in
 // planes over the threads.  Only where a CTA is one group.  12,288 columns of bf16 go
-// at 4.2 TB/s so (5.3 with dsum), 10,001 at 2.6; spilled by the compiler, at 3.4 (4.05)
+// at 4.2 TB/s so (5.5 with dsum), 10,001 at 2.65; spilled by the compiler, at 3.4 (4.05)
 // and 1.15.
 template <int Q>
 struct SharedSums {
@@ -474,7 +474,7 @@ struct SharedSums {
 // row after it to L2, else the next row to L2; HELD: the sums over rows are in
 // registers.  The bounds name the threads that a
 // width takes: the compiler's order of the same instructions for 512 threads cost 15 %
-// at 448.  For 8 x 4096 rows of 7168 bf16 with dsum, 296 us so, a ring of asynchronous
+// at 448.  For 8 x 4096 rows of 7168 bf16 with dsum, 301 us so, a ring of asynchronous
 // copies three rows deep took 410, the second walk from L1 and two rows a SM 447, half
 // the columns a thread 445 (all before the two steps above: 352 us).
 template <int DT, int U, bool EXTRA, bool PRE, bool HELD, int MOST, int PER_SM>

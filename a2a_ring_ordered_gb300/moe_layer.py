@@ -192,7 +192,7 @@ class MoEBlock:
         self.saved = None
         dnormed, dgates = self.experts.backward(dy, dw_up, dw_down)
         for d, more in zip(dnormed, self.router.backward(dgates, dw_router, dlosses, balance_scale)):
-            d.add_(more)
+            d.add_(more)  # both are bf16 already; their sum is rounded to it once more, as the norm takes its gradient
         dx = [torch.empty_like(v) for v in s]
         ccl.ccl_layer_norm_grad(dnormed, s, [self.norm_weight] * len(s), mean, rstd, dx, dsum=None if ds is None else list(ds), dweight=list(dw_norm),
                                 dbias=None if db_norm is None else list(db_norm))

@@ -510,8 +510,8 @@ ccl_status_t ccl_moe_product_grad_weight(const void* const* dy, const void* cons
  * A masked logit (-inf) gets gradient 0.  Scores, sums and gradients are fp32: a
  * score that a gate, a gradient or a loss of given ids takes is off by at most 12
  * roundings of 2^-24 of it, and by |l - top| 2^-24 where the distance of fp32 logits
- * from their row's largest has to be rounded;
- * sums over tokens are made in a fixed order, a warp's rows of a column by plain
+ * from their row's largest has to be rounded; below 2^-126 it is 0.
+ * Sums over tokens are made in a fixed order, a warp's rows of a column by plain
  * fp32 additions, then the parts with the additions' roundings kept beside the sum.
  * workspace (device, 16-byte aligned, ccl_moe_balance_workspace_bytes) is
  * scratch of one call at a time; it may hold anything.  No output may overlap
