@@ -66,6 +66,32 @@ def test_far_apart(experts, k, dtype, score, top):
     assert (np.abs(out.numpy() - want) <= 2 * tol * size + step * np.abs(want) + 2.0 ** -124).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("experts", [8, 60, 256, 384])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_nan_stays_a_nan(score, experts):
+    """Shares of a row with a NaN are NaN, and so are the loss and gradients made of them;
+    the gradient of sigmoid gates is NaN in its column (times 1 - sigmoid), chosen or not."""
+    c = ccl()
+    torch.manual_seed(0)
+    l = torch.randn(30, experts, device="cuda")
+    l[3, 1], l[4, 5:] = float("nan"), float("nan")
+    ids, d = torch.tensor([[0, 2]] * 30, dtype=torch.int32, device="cuda"), torch.randn(30, 2, device="cuda")
+    n, loss, out = torch.empty(experts + 1, dtype=torch.int32, device="cuda"), torch.empty(1, device="cuda"), torch.empty_like(l)
+    rest = [r for r in range(30) if r not in (3, 4)]
+    c.ccl_moe_balance([l], [ids], [n], [loss], score=score)
+    assert loss.isnan().all()
+    c.ccl_moe_balance_grad([l], [n], [out], 2, score=score)
+    assert out[3:5].isnan().all() and out[rest].isfinite().all()
+    for normalize in (True, False):
+        c.ccl_moe_gate_grad([l], [ids], [d], [out], score=score, normalize=normalize)
+        assert out[rest].isfinite().all()
+        if score == "sigmoid":
+            assert torch.equal(out[3:5].isnan(), l[3:5].isnan())
+        else:
+            assert out[3:5].isnan().all() if not normalize else out[3:5].isfinite().all()
+
+
 def test_distances_are_exact():
     """What the tolerances rest on: no difference of a row's logits is rounded in fp32."""
     rng = np.random.default_rng(0)
