@@ -11,7 +11,7 @@
 // group takes, so that the sums over rows stay in its registers too, or in its own
 // slots of shared memory.
 // Measured, of 8 ranks x 4096 rows of 7168 bf16 with fp32 weights and a residual:
-// forward 301 us (6.2 TB/s), gradients 301 (6.2); without a residual, 34,877 rows,
+// forward 301 us (6.2 TB/s), gradients 300 (6.25); without a residual, 34,877 rows,
 // 214 us (4.7) and 267 (5.6); 14,006 fp32 rows of 1019, off the grid, 22 us (5.1),
 // gradients of 25,998 bf16 ones 42 us (3.8).
 #include "pairs.cuh"
@@ -474,7 +474,7 @@ struct SharedSums {
 // row after it to L2, else the next row to L2; HELD: the sums over rows are in
 // registers.  The bounds name the threads that a
 // width takes: the compiler's order of the same instructions for 512 threads cost 15 %
-// at 448.  For 8 x 4096 rows of 7168 bf16 with dsum, 301 us so, a ring of asynchronous
+// at 448.  For 8 x 4096 rows of 7168 bf16 with dsum, 300 us so, a ring of asynchronous
 // copies three rows deep took 410, the second walk from L1 and two rows a SM 447, half
 // the columns a thread 445 (all before the two steps above: 352 us).
 template <int DT, int U, bool EXTRA, bool PRE, bool HELD, int MOST, int PER_SM>
