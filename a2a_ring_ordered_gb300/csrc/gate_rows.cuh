@@ -171,12 +171,13 @@ __device__ __forceinline__ float exp_of(float x) {
   const float t = __fmul_rn(x, kLog2e), y = power_of_two(t);
   return fmaf(y, fmaf(t, -kLn2, x), y);
 }
-// Of a row: 0 for -inf, and for NaN, which the row's base tells of.
-__device__ __forceinline__ float fma_sat(float a, float b, float c) {  // within 0 and 1, NaN as 0
+// a b + c within 0 and 1, NaN as 0.
+__device__ __forceinline__ float fma_sat(float a, float b, float c) {
   float d;
   asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// Of a row's columns: 0 for -inf, and for a NaN too, of which the row's base tells.
 __device__ __forceinline__ F2 exp_of(F2 x) {
   const F2 t = mul2(x, both(kLog2e));
   const float2 e = parts(t), r = parts(fma2(t, both(-kLn2), x));
